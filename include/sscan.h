@@ -507,6 +507,151 @@ SSCAN_API int sscan_scan_plan(int64_t batch, int64_t dim, int64_t len, int64_t d
  * SSCAN_ERR_UNSUPPORTED (dstate != 16). */
 SSCAN_API int sscan_bwd_plan(int64_t batch, int64_t dim, int64_t len, int64_t dstate, int bidir, int64_t* out);
 
+/* ---- The gated delta rule -----------------------------------------------------------
+ * A matrix-state recurrence.  Per batch row and value head, with a float32 state
+ * S [dk, dv] (0 before the first token, or h0):
+ *   S' = exp(g_t) S                     decay (g_t: log decay, normally <= 0; -inf resets S)
+ *   u_t = beta_t (v_t - S'^T k_t)       what the state does not yet answer for k_t
+ *   S  = S' + k_t u_t^T
+ *   o_t = scale * S^T q_t
+ * With qk_norm != 0, q_t and k_t are first divided by sqrt(sum of squares + 1e-6).
+ * v_heads is a multiple of qk_heads: value head j uses query/key head
+ * j / (v_heads / qk_heads).
+ *
+ * Layouts: q, k [batch, len, qk_heads, dk], v [batch, len, v_heads, dv] (io_dtype) and
+ * g, beta [batch, len, v_heads] (float32), each with its own element strides between
+ * batch rows, tokens and heads (>= 0); dk and dv are contiguous.  out [batch, len,
+ * v_heads, dv] io_dtype and the states [batch, v_heads, dk, dv] float32 are contiguous.
+ * lengths (optional, device int32 [batch]): tokens of each row, clamped to 0..len; later
+ * tokens are not read, their outputs and gradients are 0 and they leave the state alone.
+ * dk in 1..128, dv in 1..256, len <= 2^30.  States and accumulators are float32; bf16
+ * outputs round to nearest even.  Sequences are walked in chunks of 64 tokens by matrix
+ * products: a non-finite q, k, v or beta makes the outputs of its whole chunk (and the
+ * state after it) non-finite. */
+typedef struct sscan_delta_params {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* beta;
+  const int32_t* lengths;   /* optional */
+  const float* h0;          /* optional, 16-byte aligned; not used by sscan_delta_step */
+  int64_t q_stride[3];      /* elements between batch rows, tokens, heads */
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t g_stride[3];
+  int64_t beta_stride[3];
+  int64_t batch, len, qk_heads, v_heads, dk, dv;
+  float scale;
+  int qk_norm;              /* 0 or 1 */
+  int io_dtype;             /* of q, k, v, out and their gradients */
+} sscan_delta_params;
+
+/* Gradients (device pointers, contiguous, in the inputs' layouts).  All but dh0 are
+ * required when they have elements. */
+typedef struct sscan_delta_grads {
+  void* dq;                 /* [batch, len, qk_heads, dk] io_dtype */
+  void* dk;
+  void* dv;                 /* [batch, len, v_heads, dv] io_dtype */
+  float* dg;                /* [batch, len, v_heads] */
+  float* dbeta;
+  float* dh0;               /* optional, [batch, v_heads, dk, dv] */
+} sscan_delta_grads;
+
+/* Whole sequences.  h_last (required, 16-byte aligned) receives the state after each
+ * row's last token; it may be h0 itself.  out and h_last must not overlap each other,
+ * any other input or the workspace.  Workspace: sscan_delta_workspace_bytes(...) bytes,
+ * 256-byte aligned.  len == 0 copies the entry state (or zeros) to h_last. */
+SSCAN_API int sscan_delta_fwd(const sscan_delta_params* p, void* out, float* h_last, void* stream, void* workspace,
+                    size_t workspace_bytes);
+
+/* One token from a stored state, updated in place (p->len must be 1 and p->h0 NULL; a
+ * row of lengths 0 keeps its state and answers 0).  No workspace. */
+SSCAN_API int sscan_delta_step(const sscan_delta_params* p, float* state, void* out, void* stream);
+
+/* Gradients of sum(dout * out) + sum(dh_last * h_last) (dout [batch, len, v_heads, dv]
+ * io_dtype, contiguous; dh_last optional).  The forward states are recomputed; nothing
+ * from the forward call is needed.  No atomics: results are bitwise reproducible.
+ * Gradients of heads that are shared are summed in float32 and rounded once.  Outputs must not
+ * overlap each other, any input or the workspace (sscan_delta_bwd_workspace_bytes). */
+SSCAN_API int sscan_delta_bwd(const sscan_delta_params* p, const void* dout, const float* dh_last,
+                    const sscan_delta_grads* grads, void* stream, void* workspace, size_t workspace_bytes);
+
+SSCAN_API size_t sscan_delta_workspace_bytes(int64_t batch, int64_t len, int64_t qk_heads, int64_t v_heads, int64_t dk,
+                                   int64_t dv, int io_dtype);
+SSCAN_API size_t sscan_delta_bwd_workspace_bytes(int64_t batch, int64_t len, int64_t qk_heads, int64_t v_heads,
+                                       int64_t dk, int64_t dv, int io_dtype);
+
+/* The checks of the three calls above, without touching the GPU. */
+SSCAN_API int sscan_validate_delta_fwd(const sscan_delta_params* p, const void* out, const float* h_last,
+                             const void* workspace, size_t workspace_bytes);
+SSCAN_API int sscan_validate_delta_step(const sscan_delta_params* p, const float* state, const void* out);
+SSCAN_API int sscan_validate_delta_bwd(const sscan_delta_params* p, const void* dout, const float* dh_last,
+                             const sscan_delta_grads* grads, const void* workspace, size_t workspace_bytes);
+
+/* ---- RMS norms around a mixer ---------------------------------------------------------
+ * The norm of a mixer's output fused with its silu gate, per row and head over `size`
+ * elements (rms(x) = sqrt(mean(x^2) + eps)):
+ *   out = x / rms(x) * weight * silu(z)               (gate_first == 0)
+ *   out = m / rms(m) * weight, m = x * silu(z)        (gate_first != 0)
+ * x, z [rows, heads, size] io_dtype with strides between rows and heads (elements,
+ * >= 0); out contiguous; weight float32 [size], or [heads, size] with per_head != 0
+ * (optional unless per_head: NULL = 1).  size in 1..8192. */
+typedef struct sscan_gated_norm_params {
+  const void* x;
+  const void* z;
+  const float* weight;
+  int64_t x_stride[2];
+  int64_t z_stride[2];
+  int64_t rows, heads, size;
+  float eps;
+  int gate_first, per_head, io_dtype;
+} sscan_gated_norm_params;
+
+SSCAN_API int sscan_gated_norm(const sscan_gated_norm_params* p, void* out, void* stream);
+/* dout, dx, dz contiguous; dweight float32 in weight's shape (optional).  Sums run in a
+ * fixed order.  Workspace: sscan_gated_norm_bwd_workspace_bytes, 16-byte aligned. */
+SSCAN_API int sscan_gated_norm_bwd(const sscan_gated_norm_params* p, const void* dout, void* dx, void* dz, float* dweight,
+                         void* stream, void* workspace, size_t workspace_bytes);
+SSCAN_API size_t sscan_gated_norm_bwd_workspace_bytes(int64_t rows, int64_t heads, int64_t size);
+SSCAN_API int sscan_validate_gated_norm(const sscan_gated_norm_params* p, const void* out);
+SSCAN_API int sscan_validate_gated_norm_bwd(const sscan_gated_norm_params* p, const void* dout, const void* dx,
+                                  const void* dz, const float* dweight, const void* workspace,
+                                  size_t workspace_bytes);
+
+/* A block's output added to the residual stream, and the next block's norm:
+ *   residual_out = residual + scale * a,  a = x, or x / rms(x) * post_weight
+ *   out = residual_out / rms(residual_out) * weight
+ * x, out [rows, size] io_dtype; residual, residual_out [rows, size] residual_dtype
+ * (residual NULL: 0); weight, scale, post_weight float32 [size] (each optional: NULL
+ * weight or scale = 1, NULL post_weight: x is not normed).  The norm is that of
+ * residual_out as stored (rounded to residual_dtype).  residual_out may be residual
+ * itself.  All contiguous; size in 1..8192. */
+typedef struct sscan_add_norm_params {
+  const void* x;
+  const void* residual;     /* backward: residual_out of the forward call */
+  const float* weight;
+  const float* scale;
+  const float* post_weight;
+  int64_t rows, size;
+  float eps;
+  int io_dtype, residual_dtype;
+} sscan_add_norm_params;
+
+SSCAN_API int sscan_add_norm(const sscan_add_norm_params* p, void* out, void* residual_out, void* stream);
+/* From dout (io_dtype) and dresidual_out (residual_dtype, optional): dx (io_dtype),
+ * dresidual (residual_dtype; may be dresidual_out itself), and the optional float32
+ * dweight, dscale, dpost_weight [size] (dpost_weight only with post_weight).  Sums run
+ * in a fixed order.  Workspace: sscan_add_norm_bwd_workspace_bytes, 16-byte aligned. */
+SSCAN_API int sscan_add_norm_bwd(const sscan_add_norm_params* p, const void* dout, const void* dresidual_out, void* dx,
+                       void* dresidual, float* dweight, float* dscale, float* dpost_weight, void* stream,
+                       void* workspace, size_t workspace_bytes);
+SSCAN_API size_t sscan_add_norm_bwd_workspace_bytes(int64_t rows, int64_t size);
+SSCAN_API int sscan_validate_add_norm(const sscan_add_norm_params* p, const void* out, const void* residual_out);
+SSCAN_API int sscan_validate_add_norm_bwd(const sscan_add_norm_params* p, const void* dout, const void* dresidual_out,
+                                const void* dx, const void* dresidual, const float* dweight, const float* dscale,
+                                const float* dpost_weight, const void* workspace, size_t workspace_bytes);
+
 /* Static description of a status code; never NULL. */
 SSCAN_API const char* sscan_strerror(int status);
 

@@ -1,0 +1,179 @@
+// sscan_delta_device.h -- device helpers shared by the gated delta rule's kernels.
+//
+// Matrix products run on v_mfma_f32_16x16x32_bf16 with float32 accumulators.  Its
+// operands are bf16, so a float32 factor is cut into three bf16 terms that hold its
+// 24 significand bits exactly (x = t0 + t1 + t2, each term 8 bits), and a product
+// keeps the terms whose magnitude reaches 2^-24 of the leading one: three products
+// against an exact bf16 factor, six against another float32 one.  The result is as
+// exact as a float32 FMA chain at 3/8 of the float32 matrix instruction's cost.
+//
+// Lane layout of the instruction (lane = 16 * qd + i): A holds row i, contraction
+// indices 8 qd .. 8 qd + 7; B holds column i and the same indices; the result holds
+// column i and rows 4 qd .. 4 qd + 3.  A result becomes the B factor of the next
+// product without leaving its lane when two result tiles p = 0, 1 of a group of 32
+// rows are given the rows  32 s + 8 (i >> 2) + 4 p + (i & 3)  at tile row i: lane
+// group qd then holds rows 32 s + 8 qd + 4 p + r, its own eight contraction indices.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+namespace sscan {
+namespace delta {
+
+typedef __bf16 bf16;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kC = 64;      // tokens per chunk
+constexpr int kTerms = 3;   // bf16 terms of a float32 factor
+constexpr int kFrags = 6;   // non-zero 16 x 32 fragments of a lower (or upper) triangular 64 x 64 matrix
+constexpr int kFragBytes = 1024;
+constexpr int kVecFloats = 4 * kC;  // per-token factors of a chunk: c, d, e, and (last, beta)
+
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// N-term factor: N = 1 an exact bf16 value, N = 3 a float32 value.
+template <int N>
+struct Frag {
+  bf16x8 t[N];
+};
+
+__device__ __forceinline__ Frag<3> split(f32x8 x) {
+  Frag<3> f;
+  f.t[0] = __builtin_convertvector(x, bf16x8);
+  x -= __builtin_convertvector(f.t[0], f32x8);
+  f.t[1] = __builtin_convertvector(x, bf16x8);
+  x -= __builtin_convertvector(f.t[1], f32x8);
+  f.t[2] = __builtin_convertvector(x, bf16x8);
+  return f;
+}
+
+__device__ __forceinline__ Frag<3> split(f32x4 lo, f32x4 hi) {
+  return split(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// c + a b, dropping the products below 2^-24 of the leading one; the small products
+// are added first.  kUse caps the terms used (2 where the result is rounded to bf16).
+template <int kUse = 3, int NA, int NB>
+__device__ __forceinline__ f32x4 mul(const Frag<NA>& a, const Frag<NB>& b, f32x4 c) {
+#pragma unroll
+  for (int sum = kUse - 1; sum >= 0; --sum)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (sum - i >= 0 && sum - i < NB) c = mfma(a.t[i], b.t[sum - i], c);
+  return c;
+}
+
+// Token (or state row) of tile m, tile row i, in the chained order above.
+__device__ __forceinline__ int chained(int m, int i) { return 32 * (m >> 1) + 8 * (i >> 2) + 4 * (m & 1) + (i & 3); }
+
+// Index of the fragment (tile m, contraction step s) of a triangular matrix, or -1.
+__device__ constexpr int lower_frag(int m, int s) { return m < 2 ? (s == 0 ? m : -1) : 2 * m - 2 + s; }
+__device__ constexpr int upper_frag(int m, int s) { return m < 2 ? 2 * m + s : (s == 1 ? m + 2 : -1); }
+
+__device__ __forceinline__ int lane_id() { return int(threadIdx.x) & 63; }
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T x) {
+  return float(x);
+}
+
+// Eight consecutive elements from p, of which those at `left` and beyond read as 0.
+// wide: p is aligned to 8 elements' natural width (16 bytes bf16, 32 bytes as two
+// 16-byte loads float32) and left is 0 or at least 8.
+__device__ __forceinline__ bf16x8 load8(const bf16* p, int left, bool wide) {
+  bf16x8 x = {};
+  if (wide) {
+    if (left > 0) x = *reinterpret_cast<const bf16x8*>(p);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) x[j] = p[j];
+  }
+  return x;
+}
+
+__device__ __forceinline__ f32x8 load8(const float* p, int left, bool wide) {
+  f32x8 x = {};
+  if (wide) {
+    if (left > 0) {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+      x = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) x[j] = p[j];
+  }
+  return x;
+}
+
+__device__ __forceinline__ Frag<1> as_frag(bf16x8 x) { return Frag<1>{{x}}; }
+__device__ __forceinline__ Frag<3> as_frag(f32x8 x) { return split(x); }
+
+template <typename T>
+struct Io;
+template <>
+struct Io<bf16> {
+  static constexpr int kN = 1;       // bf16 terms of an input
+  static constexpr int kOutTerms = 2;  // terms used where only the rounded output depends on them
+  typedef bf16x8 V8;
+};
+template <>
+struct Io<float> {
+  static constexpr int kN = 3;
+  static constexpr int kOutTerms = 3;
+  typedef f32x8 V8;
+};
+
+// LDS tiles of bf16 rows, padded by 16 bytes so that sixteen rows read at one column
+// start at different banks.
+template <int KP>
+struct Tile {
+  static constexpr int kLd = KP + 8;             // elements between rows
+  static constexpr int kElems = kC * kLd;        // of one term
+};
+
+// Fragment of 8 contraction indices along a row.
+__device__ __forceinline__ bf16x8 row_frag(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
+
+// Four rows of sixteen columns, transposed: lane i of each group of sixteen receives
+// column i.  The caller passes row (i >> 2), columns 4 (i & 3) .. + 3 of the group.
+__device__ __forceinline__ bf16x4 read_tr(const bf16* p) {
+  const s16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) s16x4*)(p));
+  return __builtin_bit_cast(bf16x4, r);
+}
+
+// Fragment whose row i (or column i) is a column of the LDS tile and whose eight
+// contraction indices are tile rows r0 .. r0 + 7: col4 is where columns
+// 4 (i & 3) .. + 3 of the sixteen start (four consecutive ones).
+__device__ __forceinline__ bf16x8 col_frag(const bf16* tile, int ld, int r0, int col4) {
+  const int i = lane_id() & 15;
+  const bf16* p = tile + (r0 + (i >> 2)) * ld + col4;
+  const bf16x4 a = read_tr(p), b = read_tr(p + 4 * ld);
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+__device__ __forceinline__ int row_len(const int32_t* lengths, int64_t b, int64_t len) {
+  // lengths outside 0..len are clamped
+  if (!lengths) return int(len);
+  const int64_t n = lengths[b];
+  return int(n < 0 ? 0 : (n > len ? len : n));
+}
+
+// Decays below exp(-104) are zero in float32; the clamp keeps the running sums (and
+// differences of them) finite for g = -inf, a reset of the state.  NaN passes.
+__device__ __forceinline__ float clamp_decay(float g) { return g < -104.0f ? -104.0f : g; }
+
+}  // namespace delta
+}  // namespace sscan

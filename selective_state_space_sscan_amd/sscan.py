@@ -48,6 +48,35 @@ class DirGrads(ctypes.Structure):
                 ("dB", ctypes.c_void_p), ("dC", ctypes.c_void_p), ("dD", ctypes.c_void_p)]
 
 
+class DeltaParams(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("g", ctypes.c_void_p),
+                ("beta", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("h0", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("g_stride", ctypes.c_int64 * 3), ("beta_stride", ctypes.c_int64 * 3), ("batch", ctypes.c_int64),
+                ("len", ctypes.c_int64), ("qk_heads", ctypes.c_int64), ("v_heads", ctypes.c_int64),
+                ("dk", ctypes.c_int64), ("dv", ctypes.c_int64), ("scale", ctypes.c_float), ("qk_norm", ctypes.c_int),
+                ("io_dtype", ctypes.c_int)]
+
+
+class DeltaGrads(ctypes.Structure):
+    _fields_ = [("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p), ("dg", ctypes.c_void_p),
+                ("dbeta", ctypes.c_void_p), ("dh0", ctypes.c_void_p)]
+
+
+class GatedNormParams(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("z", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64 * 2), ("z_stride", ctypes.c_int64 * 2), ("rows", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("size", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("gate_first", ctypes.c_int), ("per_head", ctypes.c_int), ("io_dtype", ctypes.c_int)]
+
+
+class AddNormParams(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("post_weight", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("size", ctypes.c_int64), ("eps", ctypes.c_float), ("io_dtype", ctypes.c_int),
+                ("residual_dtype", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -157,6 +186,31 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.sscan_scan_plan.restype = I
     lib.sscan_bwd_plan.argtypes = [I64, I64, I64, I64, I, ctypes.POINTER(ctypes.c_int64)]
     lib.sscan_bwd_plan.restype = I
+    PP, GP, NP, AP = (ctypes.POINTER(c) for c in (DeltaParams, DeltaGrads, GatedNormParams, AddNormParams))
+    lib.sscan_delta_fwd.argtypes = [PP, V, V, V, V, SZ]
+    lib.sscan_delta_step.argtypes = [PP, V, V, V]
+    lib.sscan_delta_bwd.argtypes = [PP, V, V, GP, V, V, SZ]
+    lib.sscan_validate_delta_fwd.argtypes = [PP, V, V, V, SZ]
+    lib.sscan_validate_delta_step.argtypes = [PP, V, V]
+    lib.sscan_validate_delta_bwd.argtypes = [PP, V, V, GP, V, SZ]
+    lib.sscan_gated_norm.argtypes = [NP, V, V]
+    lib.sscan_gated_norm_bwd.argtypes = [NP, V, V, V, V, V, V, SZ]
+    lib.sscan_validate_gated_norm.argtypes = [NP, V]
+    lib.sscan_validate_gated_norm_bwd.argtypes = [NP, V, V, V, V, V, SZ]
+    lib.sscan_add_norm.argtypes = [AP, V, V, V]
+    lib.sscan_add_norm_bwd.argtypes = [AP, V, V, V, V, V, V, V, V, V, SZ]
+    lib.sscan_validate_add_norm.argtypes = [AP, V, V]
+    lib.sscan_validate_add_norm_bwd.argtypes = [AP, V, V, V, V, V, V, V, V, SZ]
+    for name in ("delta_fwd", "delta_step", "delta_bwd", "gated_norm", "gated_norm_bwd", "add_norm", "add_norm_bwd"):
+        getattr(lib, "sscan_" + name).restype = I
+        getattr(lib, "sscan_validate_" + name).restype = I
+    for name in ("sscan_delta_workspace_bytes", "sscan_delta_bwd_workspace_bytes"):
+        getattr(lib, name).argtypes = [I64] * 6 + [I]
+        getattr(lib, name).restype = SZ
+    lib.sscan_gated_norm_bwd_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.sscan_gated_norm_bwd_workspace_bytes.restype = SZ
+    lib.sscan_add_norm_bwd_workspace_bytes.argtypes = [I64, I64]
+    lib.sscan_add_norm_bwd_workspace_bytes.restype = SZ
     lib.sscan_strerror.argtypes = [I]
     lib.sscan_strerror.restype = ctypes.c_char_p
     lib.sscan_version.argtypes = []
@@ -1022,3 +1076,345 @@ def selective_scan_bidir(u, z, fwd_params: dict, rev_params: dict, softplus: boo
     f, r = fwd_params, rev_params
     return _BidirFn.apply(u, z, f["delta"], f["A"], f["B"], f["C"], f.get("D"), f.get("delta_bias"),
                           r["delta"], r["A"], r["B"], r["C"], r.get("D"), r.get("delta_bias"), softplus)
+
+
+# ---- the gated delta rule ---------------------------------------------------------
+
+def _strided(t, name: str, device, dtype, shape, unit: bool = True):
+    """A tensor the kernels read through its own strides: only the last dimension has
+    to be contiguous (``unit``; the gates have none)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if unit and shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _delta_params(what, q, k, v, g, beta, h0, lengths, scale, qk_norm):
+    """Checks the inputs of a delta call and returns (params, device)."""
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError(f"sscan.{what} needs CUDA (HIP) tensors")
+    if q.dtype not in _DT_CODE:
+        raise TypeError("q/k/v must be float32 or bfloat16")
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k are [batch, len, qk_heads, dk] and v is [batch, len, v_heads, dv]")
+    b, L, hk, dk = q.shape
+    hv, dv = v.shape[2:]
+    if hv % max(hk, 1) or (hk == 0) != (hv == 0):
+        raise ValueError(f"v_heads ({hv}) must be a multiple of qk_heads ({hk})")
+    _strided(q, "q", dev, q.dtype, (b, L, hk, dk))
+    _strided(k, "k", dev, q.dtype, (b, L, hk, dk))
+    _strided(v, "v", dev, q.dtype, (b, L, hv, dv))
+    _strided(g, "g", dev, torch.float32, (b, L, hv), unit=False)
+    _strided(beta, "beta", dev, torch.float32, (b, L, hv), unit=False)
+    _check(h0, "h0", dev, torch.float32, (b, hv, dk, dv))
+    _check(lengths, "lengths", dev, torch.int32, (b,))
+    if scale is None:
+        scale = float(dk) ** -0.5 if dk else 1.0
+    I3 = ctypes.c_int64 * 3
+    p = DeltaParams(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                    None if lengths is None else lengths.data_ptr(), None if h0 is None else h0.data_ptr(),
+                    I3(*q.stride()[:3]), I3(*k.stride()[:3]), I3(*v.stride()[:3]), I3(*g.stride()),
+                    I3(*beta.stride()), b, L, hk, hv, dk, dv, scale, int(bool(qk_norm)), _DT_CODE[q.dtype])
+    return p, dev
+
+
+def delta_workspace_bytes(batch: int, length: int, qk_heads: int, v_heads: int, dk: int, dv: int,
+                          io_dtype=torch.bfloat16, backward: bool = False) -> int:
+    lib = load_library()
+    f = lib.sscan_delta_bwd_workspace_bytes if backward else lib.sscan_delta_workspace_bytes
+    return int(f(batch, length, qk_heads, v_heads, dk, dv, _DT_CODE[io_dtype]))
+
+
+def delta_fwd(q, k, v, g, beta, h0: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+              scale: Optional[float] = None, qk_norm: bool = False, out: Optional[torch.Tensor] = None,
+              h_last: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """The gated delta rule over whole sequences (``sscan_delta_fwd``).  q, k: [batch,
+    len, qk_heads, dk], v: [batch, len, v_heads, dv], f32/bf16; g (log decay), beta:
+    [batch, len, v_heads] f32; any strides with the last dimension of q, k, v
+    contiguous.  h0: [batch, v_heads, dk, dv] f32; lengths: int32 [batch].  scale
+    defaults to dk ** -0.5.  Returns (out, h_last); h_last may be given as h0."""
+    lib = load_library()
+    p, dev = _delta_params("delta_fwd", q, k, v, g, beta, h0, lengths, scale, qk_norm)
+    b, L, hk, dk = q.shape
+    hv, dv = v.shape[2:]
+    if out is None:
+        out = torch.empty((b, L, hv, dv), dtype=q.dtype, device=dev)
+    _check(out, "out", dev, q.dtype, (b, L, hv, dv))
+    if h_last is None:
+        h_last = torch.empty((b, hv, dk, dv), dtype=torch.float32, device=dev)
+    _check(h_last, "h_last", dev, torch.float32, (b, hv, dk, dv))
+    if b * hv == 0:
+        return out, h_last
+    ws, ws_bytes = _workspace(lib.sscan_delta_workspace_bytes(b, L, hk, hv, dk, dv, p.io_dtype), dev, workspace)
+    st = lib.sscan_delta_fwd(ctypes.byref(p), _ptr(out), _ptr(h_last), _stream(dev), _ptr(ws), ws_bytes)
+    if st != 0:
+        raise SScanError(st, "sscan_delta_fwd")
+    return out, h_last
+
+
+def delta_step(state, q, k, v, g, beta, lengths: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+               qk_norm: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token from a stored state (``sscan_delta_step``), updating ``state``
+    [batch, v_heads, dk, dv] f32 in place.  q, k: [batch, qk_heads, dk]; v: [batch,
+    v_heads, dv]; g, beta: [batch, v_heads] f32.  Rows of ``lengths`` 0 keep their
+    state and answer 0.  Returns [batch, v_heads, dv] in q's dtype."""
+    lib = load_library()
+    for name, t, n in (("q", q, 3), ("k", k, 3), ("v", v, 3), ("g", g, 2), ("beta", beta, 2)):
+        if t.dim() != n:
+            raise ValueError(f"{name} must have {n} dimensions for one token")
+    p, dev = _delta_params("delta_step", q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), g.unsqueeze(1),
+                           beta.unsqueeze(1), None, lengths, scale, qk_norm)
+    b, hk, dk = q.shape
+    hv, dv = v.shape[1:]
+    if state is None:
+        raise ValueError("state is required")
+    _check(state, "state", dev, torch.float32, (b, hv, dk, dv))
+    if out is None:
+        out = torch.empty((b, hv, dv), dtype=q.dtype, device=dev)
+    _check(out, "out", dev, q.dtype, (b, hv, dv))
+    if b * hv == 0:
+        return out
+    st = lib.sscan_delta_step(ctypes.byref(p), _ptr(state), _ptr(out), _stream(dev))
+    if st != 0:
+        raise SScanError(st, "sscan_delta_step")
+    return out
+
+
+def delta_bwd(q, k, v, g, beta, dout, h0: Optional[torch.Tensor] = None, dh_last: Optional[torch.Tensor] = None,
+              lengths: Optional[torch.Tensor] = None, scale: Optional[float] = None, qk_norm: bool = False,
+              workspace: Optional[torch.Tensor] = None) -> dict:
+    """Backward pass of ``delta_fwd`` (``sscan_delta_bwd``): the gradients of
+    sum(dout * out) + sum(dh_last * h_last) as {"dq", "dk", "dv" (q's dtype), "dg",
+    "dbeta", "dh0" (f32)}, contiguous; the states are recomputed."""
+    lib = load_library()
+    p, dev = _delta_params("delta_bwd", q, k, v, g, beta, h0, lengths, scale, qk_norm)
+    b, L, hk, dk = q.shape
+    hv, dv = v.shape[2:]
+    _check(dout, "dout", dev, q.dtype, (b, L, hv, dv))
+    _check(dh_last, "dh_last", dev, torch.float32, (b, hv, dk, dv))
+
+    def new(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+    r = dict(dq=new((b, L, hk, dk), q.dtype), dk=new((b, L, hk, dk), q.dtype), dv=new((b, L, hv, dv), q.dtype),
+             dg=new((b, L, hv), torch.float32), dbeta=new((b, L, hv), torch.float32),
+             dh0=new((b, hv, dk, dv), torch.float32))
+    if b * hv == 0:
+        return r
+    ws, ws_bytes = _workspace(lib.sscan_delta_bwd_workspace_bytes(b, L, hk, hv, dk, dv, p.io_dtype), dev, workspace)
+    gst = DeltaGrads(*(r[n].data_ptr() for n in ("dq", "dk", "dv", "dg", "dbeta", "dh0")))
+    st = lib.sscan_delta_bwd(ctypes.byref(p), _ptr(dout), _ptr(dh_last), ctypes.byref(gst), _stream(dev), _ptr(ws),
+                             ws_bytes)
+    if st != 0:
+        raise SScanError(st, "sscan_delta_bwd")
+    return r
+
+
+class _DeltaFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, h0, lengths, scale, qk_norm):
+        ctx.save_for_backward(q, k, v, g, beta, h0, lengths)
+        ctx.scale, ctx.qk_norm = scale, qk_norm
+        ctx.set_materialize_grads(False)
+        return delta_fwd(q, k, v, g, beta, h0, lengths, scale, qk_norm)
+
+    @staticmethod
+    def backward(ctx, dout, dh_last):
+        q, k, v, g, beta, h0, lengths = ctx.saved_tensors
+        if dout is None:
+            dout = torch.zeros(v.shape, dtype=v.dtype, device=v.device)
+        r = delta_bwd(q, k, v, g, beta, dout.contiguous(), h0, None if dh_last is None else dh_last.contiguous(),
+                      lengths, ctx.scale, ctx.qk_norm)
+        return (r["dq"], r["dk"], r["dv"], r["dg"], r["dbeta"], None if h0 is None else r["dh0"], None, None, None)
+
+
+def gated_delta(q, k, v, g, beta, h0: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                scale: Optional[float] = None, qk_norm: bool = False):
+    """``delta_fwd`` with gradients in q, k, v, g, beta and h0 (``sscan_delta_bwd`` in
+    the backward pass).  Returns (out, h_last)."""
+    return _DeltaFn.apply(q, k, v, g, beta, h0, lengths, scale, qk_norm)
+
+
+# ---- RMS norms around a mixer -----------------------------------------------------
+
+def _gated_params(what, x, z, weight, eps, gate_first):
+    """(params, device, per_head): x and z are [..., size] or [..., heads, size]; all
+    leading dimensions but the last one (the heads, where there are two or more)
+    collapse to rows."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError(f"sscan.{what} needs CUDA (HIP) tensors")
+    if x.dtype not in _DT_CODE:
+        raise TypeError("x/z must be float32 or bfloat16")
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    size = x.shape[-1]
+    _strided(x, "x", dev, x.dtype, x.shape)
+    _strided(z, "z", dev, x.dtype, x.shape)
+    heads = x.shape[-2] if x.dim() >= 3 else 1
+    per_head = weight is not None and weight.dim() == 2
+    _check(weight, "weight", dev, torch.float32, (heads, size) if per_head else (size,))
+    rows = x.numel() // max(heads * size, 1) if x.numel() else 0
+
+    def strides(t, name):
+        lead = [(n, s) for n, s in zip(t.shape[:-2] if t.dim() >= 3 else t.shape[:-1], t.stride()) if n > 1]
+        for (n0, s0), (n1, s1) in zip(lead, lead[1:]):
+            if s0 != n1 * s1:
+                raise ValueError(f"the leading dimensions of {name} must collapse to rows of one stride")
+        return (ctypes.c_int64 * 2)(lead[-1][1] if lead else 0, t.stride(-2) if t.dim() >= 3 else 0)
+
+    p = GatedNormParams(x.data_ptr(), z.data_ptr(), None if weight is None else weight.data_ptr(), strides(x, "x"),
+                        strides(z, "z"), rows, heads, size, eps, int(bool(gate_first)), int(per_head),
+                        _DT_CODE[x.dtype])
+    return p, dev
+
+
+def gated_norm(x, z, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, gate_first: bool = False,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """RMS norm over the last dimension fused with a silu gate (``sscan_gated_norm``):
+    x / rms(x) * weight * silu(z), or with ``gate_first`` m / rms(m) * weight of m = x *
+    silu(z).  x, z: [..., size] or [..., heads, size] f32/bf16 (rows and heads may be
+    strided); weight: [size] or [heads, size] f32.  Returns a contiguous tensor."""
+    lib = load_library()
+    p, dev = _gated_params("gated_norm", x, z, weight, eps, gate_first)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    _check(out, "out", dev, x.dtype, x.shape)
+    st = lib.sscan_gated_norm(ctypes.byref(p), _ptr(out), _stream(dev))
+    if st != 0:
+        raise SScanError(st, "sscan_gated_norm")
+    return out
+
+
+def gated_norm_bwd(x, z, dout, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, gate_first: bool = False,
+                   workspace: Optional[torch.Tensor] = None) -> dict:
+    """Backward pass of ``gated_norm`` (``sscan_gated_norm_bwd``): {"dx", "dz",
+    "dweight" (f32, None without a weight)}."""
+    lib = load_library()
+    p, dev = _gated_params("gated_norm_bwd", x, z, weight, eps, gate_first)
+    _check(dout, "dout", dev, x.dtype, x.shape)
+    dx, dz = (torch.empty(x.shape, dtype=x.dtype, device=dev) for _ in range(2))
+    dw = None if weight is None else torch.empty_like(weight)
+    ws, ws_bytes = _workspace(lib.sscan_gated_norm_bwd_workspace_bytes(p.rows, p.heads, p.size), dev, workspace)
+    st = lib.sscan_gated_norm_bwd(ctypes.byref(p), _ptr(dout), _ptr(dx), _ptr(dz), _ptr(dw), _stream(dev), _ptr(ws),
+                                  ws_bytes)
+    if st != 0:
+        raise SScanError(st, "sscan_gated_norm_bwd")
+    return dict(dx=dx, dz=dz, dweight=dw)
+
+
+def _add_params(what, x, residual, residual_dtype, weight, scale, post_weight, eps):
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError(f"sscan.{what} needs CUDA (HIP) tensors")
+    if x.dtype not in _DT_CODE or residual_dtype not in _DT_CODE:
+        raise TypeError("x and the residual must be float32 or bfloat16")
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    size = x.shape[-1]
+    _check(x, "x", dev)
+    _check(residual, "residual", dev, residual_dtype, x.shape)
+    for name, t in (("weight", weight), ("scale", scale), ("post_weight", post_weight)):
+        _check(t, name, dev, torch.float32, (size,))
+    addr = [None if t is None else t.data_ptr() for t in (x, residual, weight, scale, post_weight)]
+    rows = x.numel() // size if size else 0
+    return AddNormParams(*addr, rows, size, eps, _DT_CODE[x.dtype], _DT_CODE[residual_dtype]), dev
+
+
+def add_norm(x, residual: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+             scale: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             residual_dtype=None, out: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None):
+    """A block's output added to the residual stream, and the next block's RMS norm
+    (``sscan_add_norm``): total = residual + scale * x (x normed by ``post_weight``
+    first where given), out = total / rms(total) * weight.  x: [..., size] f32/bf16;
+    residual: f32/bf16 of the same shape (None: 0, stored as ``residual_dtype`` or x's
+    dtype); weight, scale, post_weight: [size] f32 or None.  Returns (out, total);
+    ``residual_out`` may be ``residual`` itself."""
+    lib = load_library()
+    if residual_dtype is None:
+        residual_dtype = x.dtype if residual is None else residual.dtype
+    p, dev = _add_params("add_norm", x, residual, residual_dtype, weight, scale, post_weight, eps)
+    if out is None:
+        out = torch.empty_like(x)
+    if residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=residual_dtype, device=dev)
+    _check(out, "out", dev, x.dtype, x.shape)
+    _check(residual_out, "residual_out", dev, residual_dtype, x.shape)
+    st = lib.sscan_add_norm(ctypes.byref(p), _ptr(out), _ptr(residual_out), _stream(dev))
+    if st != 0:
+        raise SScanError(st, "sscan_add_norm")
+    return out, residual_out
+
+
+def add_norm_bwd(x, residual_out, dout, weight: Optional[torch.Tensor] = None,
+                 dresidual_out: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                 post_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 workspace: Optional[torch.Tensor] = None) -> dict:
+    """Backward pass of ``add_norm`` (``sscan_add_norm_bwd``) from the total it stored:
+    {"dx", "dresidual", "dweight", "dscale", "dpost_weight"} (the last three f32, None
+    for a vector that was not given)."""
+    lib = load_library()
+    p, dev = _add_params("add_norm_bwd", x, residual_out, residual_out.dtype, weight, scale, post_weight, eps)
+    _check(dout, "dout", dev, x.dtype, x.shape)
+    _check(dresidual_out, "dresidual_out", dev, residual_out.dtype, x.shape)
+    dx, dres = torch.empty_like(x), torch.empty_like(residual_out)
+    dw, ds, dp = (None if t is None else torch.empty_like(t) for t in (weight, scale, post_weight))
+    ws, ws_bytes = _workspace(lib.sscan_add_norm_bwd_workspace_bytes(p.rows, p.size), dev, workspace)
+    st = lib.sscan_add_norm_bwd(ctypes.byref(p), _ptr(dout), _ptr(dresidual_out), _ptr(dx), _ptr(dres), _ptr(dw),
+                                _ptr(ds), _ptr(dp), _stream(dev), _ptr(ws), ws_bytes)
+    if st != 0:
+        raise SScanError(st, "sscan_add_norm_bwd")
+    return dict(dx=dx, dresidual=dres, dweight=dw, dscale=ds, dpost_weight=dp)
+
+
+class _GatedNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, z, weight, eps, gate_first):
+        ctx.save_for_backward(x, z, weight)
+        ctx.eps, ctx.gate_first = eps, gate_first
+        return gated_norm(x, z, weight, eps, gate_first)
+
+    @staticmethod
+    def backward(ctx, dout):
+        x, z, weight = ctx.saved_tensors
+        r = gated_norm_bwd(x, z, dout.contiguous(), weight, ctx.eps, ctx.gate_first)
+        return r["dx"], r["dz"], r["dweight"], None, None
+
+
+def gated_rms_norm(x, z, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, gate_first: bool = False):
+    """``gated_norm`` with gradients in x, z and weight."""
+    return _GatedNormFn.apply(x, z, weight, eps, gate_first)
+
+
+class _AddNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, scale, post_weight, eps, residual_dtype):
+        out, total = add_norm(x, residual, weight, scale, post_weight, eps, residual_dtype)
+        ctx.save_for_backward(x, total, weight, scale, post_weight)
+        ctx.eps, ctx.has_residual = eps, residual is not None
+        ctx.set_materialize_grads(False)
+        return out, total
+
+    @staticmethod
+    def backward(ctx, dout, dtotal):
+        x, total, weight, scale, post_weight = ctx.saved_tensors
+        dout = torch.zeros_like(x) if dout is None else dout.contiguous()
+        r = add_norm_bwd(x, total, dout, weight, None if dtotal is None else dtotal.contiguous(), scale, post_weight,
+                         ctx.eps)
+        return (r["dx"], r["dresidual"] if ctx.has_residual else None, r["dweight"], r["dscale"], r["dpost_weight"],
+                None, None)
+
+
+def add_rms_norm(x, residual: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                 scale: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 residual_dtype=None):
+    """``add_norm`` with gradients in x, residual, weight, scale and post_weight.
+    Returns (out, total)."""
+    return _AddNormFn.apply(x, residual, weight, scale, post_weight, eps, residual_dtype)
