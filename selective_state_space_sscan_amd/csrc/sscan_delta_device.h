@@ -35,7 +35,11 @@ constexpr int kC = 64;      // tokens per chunk
 constexpr int kTerms = 3;   // bf16 terms of a float32 factor
 constexpr int kFrags = 6;   // non-zero 16 x 32 fragments of a lower (or upper) triangular 64 x 64 matrix
 constexpr int kFragBytes = 1024;
-constexpr int kVecFloats = 4 * kC;  // per-token factors of a chunk: c, d, e, and (last, beta)
+// Per-token factors of a chunk, kC floats each (G the running sum of g, rk and rq the
+// inverse norms of k and q): c = exp(G) rk, d = exp(G_C - G) rk, e = scale exp(G) rq,
+// exp(G_C) (repeated); for the backward pass also beta, rk, rq.
+constexpr int kVecFloats = 4 * kC;
+constexpr int kVecFloatsBwd = 7 * kC;
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);

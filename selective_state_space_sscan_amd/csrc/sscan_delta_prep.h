@@ -1,7 +1,7 @@
 // sscan_delta_prep.h -- chunk-local factors of the gated delta rule, shared by its
 // forward and backward passes: T diag(beta) = (I + A)^-1 diag(beta), the masked and
-// decayed P = scale (Q K^T . D), and the per-token factors, laid out as the matrix
-// instruction's A fragments.
+// decayed P = scale (Q K^T . D) (backward: T^T and P^T too), and the per-token factors,
+// laid out as the matrix instruction's A fragments.
 #pragma once
 
 #include "sscan_delta.h"
@@ -160,11 +160,16 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int nchunk
       gsum[lane] = sum;
       sbeta[lane] = beta;
       const float into = expf(float(sum)), rest = expf(float(end - sum));
-      float* v = vec + idx * kVecFloats;
+      float* v = vec + idx * (BWD ? kVecFloatsBwd : kVecFloats);
       v[lane] = into * srk[lane];
       v[kC + lane] = rest * srk[lane];
       v[2 * kC + lane] = a.scale * into * srq[lane];
       v[3 * kC + lane] = expf(float(end));
+      if constexpr (BWD) {
+        v[4 * kC + lane] = beta;
+        v[5 * kC + lane] = srk[lane];
+        v[6 * kC + lane] = srq[lane];
+      }
     }
     __syncthreads();
     for (int e = tid; e < kC * kC; e += 256) {
@@ -190,7 +195,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int nchunk
         if (kind == 1)
           x[j] = q <= r ? a.scale * srq[r] * srk[q] * expf(float(gsum[r] - gsum[q])) * qk[r * kLdM + q] : 0.0f;
         else
-          x[j] = mat[r * kLdM + q] * sbeta[q];
+          x[j] = kind == 0 ? mat[r * kLdM + q] * sbeta[q] : mat[r * kLdM + q];
       }
       const Frag<3> fr = split(x);
       const int terms = kind == 1 ? NP : 3;
