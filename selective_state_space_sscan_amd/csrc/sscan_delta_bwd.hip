@@ -33,24 +33,25 @@ __global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, i
                                                               const char* frag_tt, const char* frag_pt,
                                                               const float* vec, float* adjoints, float* xgrad,
                                                               int dvp, int wide) {
-  constexpr int N = Io<IO>::kN, kTiles = KP / 16, kSteps = KP / 32, kLdD = 72;
+  constexpr int N = Io<IO>::kN, kTiles = KP / 16, kSteps = KP / 32, kBytes = kFrags * 3 * kFragBytes;
   typedef Tile<KP> TileK;
   __shared__ __attribute__((aligned(16))) bf16 sk[N][TileK::kElems];
   __shared__ __attribute__((aligned(16))) bf16 sq[N][TileK::kElems];
-  __shared__ __attribute__((aligned(16))) bf16 sd[N][kC * kLdD];
+  __shared__ __attribute__((aligned(16))) char st[kBytes];
+  __shared__ __attribute__((aligned(16))) char sp[kBytes];
   __shared__ __attribute__((aligned(16))) float svec[kVecFloatsBwd];
 
   const DeltaArgs& a = b_.f;
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, i = lane & 15, qd = lane >> 4;
   const int64_t bh = int64_t(blockIdx.x) / nvb, b = bh / a.hv;
   const int h = int(bh % a.hv), hq = h / (a.hv / a.hk);
-  const int col_blk = int(int64_t(blockIdx.x) % nvb) * 64, col = col_blk + 16 * wave + i;
+  const int col = int(int64_t(blockIdx.x) % nvb) * 64 + 16 * wave + i;
   const int Lb = row_len(a.lengths, b, a.len), live_chunks = (Lb + kC - 1) / kC;
   const IO* kp = static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h;
   const IO* qp = static_cast<const IO*>(a.q) + b * a.sq.b + hq * a.sq.h;
-  const IO* dp = static_cast<const IO*>(b_.dout) + (b * a.len * a.hv + h) * a.dv;
+  const IO* dp = static_cast<const IO*>(b_.dout) + (b * a.len * a.hv + h) * a.dv + col;
   const int64_t out_t = int64_t(a.hv) * a.dv;
-  const bool wide_qk = wide & 1, wide_d = wide & 4;
+  const bool wide_qk = wide & 1, live_col = col < a.dv;
 
   f32x4 E[kTiles];
 #pragma unroll
@@ -58,48 +59,59 @@ __global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, i
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int dim = chained(m, 4 * qd + r);
-      E[m][r] = (b_.dh_last && dim < a.dk && col < a.dv) ? b_.dh_last[(bh * a.dk + dim) * a.dv + col] : 0.0f;
+      E[m][r] = (b_.dh_last && dim < a.dk && live_col) ? b_.dh_last[(bh * a.dk + dim) * a.dv + col] : 0.0f;
     }
 
-  for (int c = live_chunks - 1; c >= 0; --c) {
-    const int t0 = c * kC;
+  RowsAhead<IO, KP> next_k, next_q;
+  BytesAhead<kBytes> next_t, next_p;
+  typename Io<IO>::V8 next_d[2];  // dO of this lane's column, tokens 32 s + 8 qd ..
+  float next_vec[2] = {};
+  const auto load_ahead = [&](int c) {
     const int64_t idx = bh * nchunk + c;
+    const int t0 = c * kC;
+    next_k.load(kp, a.sk.t, t0, Lb, a.dk, wide_qk);
+    next_q.load(qp, a.sq.t, t0, Lb, a.dk, wide_qk);
+    next_p.load(frag_pt + idx * kBytes);
+    next_t.load(frag_tt + idx * kBytes);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      if (tid + 256 * n < kVecFloatsBwd) next_vec[n] = vec[idx * kVecFloatsBwd + tid + 256 * n];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int t = t0 + 32 * s + 8 * qd + j;
+        next_d[s][j] = t < Lb && live_col ? dp[t * out_t] : IO(0.0f);
+      }
+  };
+  if (live_chunks > 0) load_ahead(live_chunks - 1);
+
+  for (int c = live_chunks - 1; c >= 0; --c) {
+    const int64_t idx = bh * nchunk + c;
+    __syncthreads();  // the last chunk's readers of the tiles are done
+    next_k.store(sk);
+    next_q.store(sq);
+    next_p.store(sp);
+    next_t.store(st);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      if (tid + 256 * n < kVecFloatsBwd) svec[tid + 256 * n] = next_vec[n];
+    const Frag<N> df[2] = {as_frag(next_d[0]), as_frag(next_d[1])};
+    f32x8 dof[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dof[s][j] = to_f32(next_d[s][j]);
+    __syncthreads();
+    if (c > 0) load_ahead(c - 1);
     if (col < dvp) {
 #pragma unroll
       for (int m = 0; m < kTiles; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r) adjoints[(idx * KP + chained(m, 4 * qd + r)) * dvp + col] = E[m][r];
     }
-    __syncthreads();
-    for (int u = tid; u < kC * KP / 8; u += 256) {
-      const int row = u / (KP / 8), d8 = (u % (KP / 8)) * 8;
-      const bool in = t0 + row < Lb;
-      const auto fk = as_frag(load8(kp + (t0 + row) * a.sk.t + d8, in ? a.dk - d8 : 0, wide_qk));
-      const auto fq = as_frag(load8(qp + (t0 + row) * a.sq.t + d8, in ? a.dk - d8 : 0, wide_qk));
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        *reinterpret_cast<bf16x8*>(&sk[n][row * TileK::kLd + d8]) = fk.t[n];
-        *reinterpret_cast<bf16x8*>(&sq[n][row * TileK::kLd + d8]) = fq.t[n];
-      }
-    }
-    for (int u = tid; u < kC * 8; u += 256) {
-      const int row = u / 8, c8 = (u % 8) * 8;
-      const bool in = t0 + row < Lb;
-      const auto f = as_frag(load8(dp + (t0 + row) * out_t + col_blk + c8, in ? a.dv - col_blk - c8 : 0, wide_d));
-#pragma unroll
-      for (int n = 0; n < N; ++n) *reinterpret_cast<bf16x8*>(&sd[n][row * kLdD + c8]) = f.t[n];
-    }
-    for (int u = tid; u < kVecFloatsBwd; u += 256) svec[u] = vec[idx * kVecFloatsBwd + u];
-    __syncthreads();
 
-    const char* ft = frag_tt + idx * kFrags * 3 * kFragBytes;
-    const char* fp = frag_pt + idx * kFrags * 3 * kFragBytes;
     // du = P^T do + d (K E)
-    Frag<N> df[2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int n = 0; n < N; ++n) df[s].t[n] = col_frag(sd[n], kLdD, 32 * s + 8 * qd, 16 * wave + 4 * (i & 3));
     Frag<3> ef[kSteps];
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) ef[s] = split(E[2 * s], E[2 * s + 1]);
@@ -122,7 +134,7 @@ __global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, i
         Frag<3> f;
 #pragma unroll
         for (int n = 0; n < 3; ++n)
-          f.t[n] = *reinterpret_cast<const bf16x8*>(fp + ((upper_frag(m, s) * 3 + n) * 64 + lane) * 16);
+          f.t[n] = *reinterpret_cast<const bf16x8*>(sp + ((upper_frag(m, s) * 3 + n) * 64 + lane) * 16);
         x[m] = mul(f, df[s], x[m]);
       }
     }
@@ -137,7 +149,7 @@ __global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, i
         Frag<3> f;
 #pragma unroll
         for (int n = 0; n < 3; ++n)
-          f.t[n] = *reinterpret_cast<const bf16x8*>(ft + ((upper_frag(m, s) * 3 + n) * 64 + lane) * 16);
+          f.t[n] = *reinterpret_cast<const bf16x8*>(st + ((upper_frag(m, s) * 3 + n) * 64 + lane) * 16);
         x[m] = mul(f, xf[s], x[m]);
       }
       const int tok = chained(m, 4 * qd);
@@ -151,12 +163,8 @@ __global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, i
     const Frag<3> yf[2] = {split(x[0], x[1]), split(x[2], x[3])};
     Frag<3> gf[2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      f32x8 d = __builtin_convertvector(df[s].t[0], f32x8);
-#pragma unroll
-      for (int n = 1; n < N; ++n) d += __builtin_convertvector(df[s].t[n], f32x8);
-      gf[s] = split(d * *reinterpret_cast<const f32x8*>(&svec[2 * kC + 32 * s + 8 * qd]));
-    }
+    for (int s = 0; s < 2; ++s)
+      gf[s] = split(dof[s] * *reinterpret_cast<const f32x8*>(&svec[2 * kC + 32 * s + 8 * qd]));
     const float last = svec[3 * kC];
 #pragma unroll
     for (int m = 0; m < kTiles; ++m) {
@@ -180,7 +188,7 @@ __global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, i
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int dim = chained(m, 4 * qd + r);
-      if (dim < a.dk && col < a.dv) b_.dh0[(bh * a.dk + dim) * a.dv + col] = E[m][r];
+      if (dim < a.dk && live_col) b_.dh0[(bh * a.dk + dim) * a.dv + col] = E[m][r];
     }
 }
 
