@@ -23,6 +23,7 @@ namespace sscan {
 constexpr int kDeltaChunk = 64;
 constexpr int kDeltaMaxK = 128;      // key size (a state's rows, held in registers)
 constexpr int kDeltaMaxV = 256;      // value size
+constexpr int64_t kDeltaMaxStride = 1 << 23;  // elements between tokens: a chunk's rows stay within 2^31 bytes
 // Sequences of at most this many tokens take the token-by-token kernel.
 constexpr int kDeltaRecurrentMax = 8;
 

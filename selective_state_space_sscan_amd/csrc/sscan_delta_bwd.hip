@@ -49,9 +49,10 @@ __global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, i
   const int Lb = row_len(a.lengths, b, a.len), live_chunks = (Lb + kC - 1) / kC;
   const IO* kp = static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h;
   const IO* qp = static_cast<const IO*>(a.q) + b * a.sq.b + hq * a.sq.h;
-  const IO* dp = static_cast<const IO*>(b_.dout) + (b * a.len * a.hv + h) * a.dv + col;
+  const IO* dp = static_cast<const IO*>(b_.dout) + (b * a.len * a.hv + h) * a.dv;
   const int64_t out_t = int64_t(a.hv) * a.dv;
   const bool wide_qk = wide & 1, live_col = col < a.dv;
+  const int d_lane = (8 * qd * int(out_t) + col) * int(sizeof(IO)), d_row = int(out_t) * int(sizeof(IO));
 
   f32x4 E[kTiles];
 #pragma unroll
@@ -76,12 +77,14 @@ __global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, i
 #pragma unroll
     for (int n = 0; n < 2; ++n)
       if (tid + 256 * n < kVecFloatsBwd) next_vec[n] = vec[idx * kVecFloatsBwd + tid + 256 * n];
+    const Buffer rows = rows_of(dp + t0 * out_t, Lb - t0 < kC ? Lb - t0 : kC, out_t, a.dv);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int t = t0 + 32 * s + 8 * qd + j;
-        next_d[s][j] = t < Lb && live_col ? dp[t * out_t] : IO(0.0f);
+        IO x;
+        load1(rows, live_col ? d_lane + (32 * s + j) * d_row : kOutside, &x);
+        next_d[s][j] = x;
       }
   };
   if (live_chunks > 0) load_ahead(live_chunks - 1);

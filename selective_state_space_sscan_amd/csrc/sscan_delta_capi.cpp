@@ -101,6 +101,10 @@ int view_delta(const sscan_delta_params* p, DeltaView* w) {
   if (!aligned(p->q, w->esz) || !aligned(p->k, w->esz) || !aligned(p->v, w->esz) || !aligned(p->g, 4) ||
       !aligned(p->beta, 4) || !aligned(p->lengths, 4) || !aligned(p->h0, 16))
     return SSCAN_ERR_ALIGN;
+  // a chunk's rows are addressed by 32-bit byte offsets
+  if (p->q_stride[1] >= sscan::kDeltaMaxStride || p->k_stride[1] >= sscan::kDeltaMaxStride ||
+      p->v_stride[1] >= sscan::kDeltaMaxStride || p->v_heads * p->dv >= sscan::kDeltaMaxStride)
+    return SSCAN_ERR_UNSUPPORTED;
   const int64_t qd[3] = {p->batch, p->len, p->qk_heads}, vd[3] = {p->batch, p->len, p->v_heads};
   const int64_t eq = extent(qd, p->q_stride, 3, p->dk), ek = extent(qd, p->k_stride, 3, p->dk),
                 ev = extent(vd, p->v_stride, 3, p->dv), eg = extent(vd, p->g_stride, 3, 1),

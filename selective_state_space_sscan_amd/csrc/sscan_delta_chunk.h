@@ -16,10 +16,11 @@ struct RowsAhead {
   typename Io<IO>::V8 x[kUnits];
 
   __device__ __forceinline__ void load(const IO* p, int64_t stride, int t0, int len, int dk, bool wide) {
+    const Buffer rows = rows_of(p + t0 * stride, len - t0 < kC ? len - t0 : kC, stride, dk);
 #pragma unroll
     for (int n = 0; n < kUnits; ++n) {
       const int u = int(threadIdx.x) + 256 * n, row = u / (KP / 8), d8 = (u % (KP / 8)) * 8;
-      x[n] = load8(p + (t0 + row) * stride + d8, t0 + row < len ? dk - d8 : 0, wide);
+      load8<IO>(rows, (row * int(stride) + d8) * int(sizeof(IO)), dk - d8, wide, &x[n]);
     }
   }
 
@@ -89,10 +90,14 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs a, int nchun
   const int live_chunks = (Lb + kC - 1) / kC;
   const IO* kp = static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h;
   const IO* qp = static_cast<const IO*>(a.q) + b * a.sq.b + hq * a.sq.h;
-  const IO* vp = static_cast<const IO*>(a.v) + b * a.sv.b + h * a.sv.h + col;
-  IO* op = static_cast<IO*>(a.out) + (b * a.len * a.hv + h) * a.dv + col;
+  const IO* vp = static_cast<const IO*>(a.v) + b * a.sv.b + h * a.sv.h;
+  IO* op = static_cast<IO*>(a.out) + (b * a.len * a.hv + h) * a.dv;
   const int64_t out_t = int64_t(a.hv) * a.dv;
   const bool wide_qk = wide & 1, live_col = col < a.dv;
+  // byte offset of this lane's first token (8 qd) and column in a chunk's rows, and the
+  // rows from there to token 32 (m >> 1) + 4 (m & 1) + r
+  const int v_lane = (8 * qd * int(a.sv.t) + col) * int(sizeof(IO)), v_row = int(a.sv.t) * int(sizeof(IO));
+  const int o_lane = (8 * qd * int(out_t) + col) * int(sizeof(IO)), o_row = int(out_t) * int(sizeof(IO));
 
   f32x4 S[kTiles];
 #pragma unroll
@@ -118,13 +123,12 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs a, int nchun
       next_p.load(frag_p + idx * kBytesP);
     }
     next_vec = vec[idx * kVecs + tid];
+    const Buffer rows = rows_of(vp + t0 * a.sv.t, Lb - t0 < kC ? Lb - t0 : kC, a.sv.t, a.dv);
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = t0 + chained(m, 4 * qd + r);
-        next_v[m][r] = t < Lb && live_col ? vp[t * a.sv.t] : IO(0.0f);
-      }
+      for (int r = 0; r < 4; ++r)
+        load1(rows, live_col ? v_lane + (32 * (m >> 1) + 4 * (m & 1) + r) * v_row : kOutside, &next_v[m][r]);
   };
   if (live_chunks > 0) load_ahead(0);
 
@@ -207,13 +211,12 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs a, int nchun
             fp.t[n] = *reinterpret_cast<const bf16x8*>(sp + ((lower_frag(m, s) * NO + n) * 64 + lane) * 16);
           o[m] = mul<NO>(fp, uf[s], o[m]);
         }
+      const Buffer rows = rows_of(op + t0 * out_t, L - t0 < kC ? L - t0 : kC, out_t, a.dv);
 #pragma unroll
       for (int m = 0; m < 4; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = t0 + chained(m, 4 * qd + r);
-          if (t < L && live_col) op[t * out_t] = IO(o[m][r]);
-        }
+        for (int r = 0; r < 4; ++r)
+          store1(rows, live_col ? o_lane + (32 * (m >> 1) + 4 * (m & 1) + r) * o_row : kOutside, IO(o[m][r]));
     } else if (col < dvp) {
 #pragma unroll
       for (int m = 0; m < 4; ++m)
@@ -240,7 +243,7 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs a, int nchun
   if constexpr (STATES) return;
   // tokens past the row's length: zeros (those of its last chunk were written above)
   if (live_col)
-    for (int t = live_chunks * kC + qd; t < L; t += 4) op[t * out_t] = IO(0.0f);
+    for (int t = live_chunks * kC + qd; t < L; t += 4) op[t * out_t + col] = IO(0.0f);
 #pragma unroll
   for (int m = 0; m < kTiles; ++m)
 #pragma unroll

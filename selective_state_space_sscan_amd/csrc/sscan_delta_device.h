@@ -121,6 +121,60 @@ __device__ __forceinline__ f32x8 load8(const float* p, int left, bool wide) {
   return x;
 }
 
+// Chunk rows are read and written through buffer descriptors whose size ends with the
+// last row: an access past it reads 0 or is dropped, so tails cost no branches.  Offsets
+// are bytes from the chunk's first row, in 32 bits (the callers' token strides are
+// limited to kDeltaMaxStride elements).
+typedef __amdgpu_buffer_rsrc_t Buffer;
+constexpr int kOutside = int(0x80000000u);  // an offset beyond every buffer
+
+__device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, int(bytes), 0x00020000);
+}
+
+// `rows` rows of `size` elements `stride` apart, from p.
+template <typename T>
+__device__ __forceinline__ Buffer rows_of(const T* p, int rows, int64_t stride, int size) {
+  return buffer_of(p, rows > 0 ? uint32_t(((rows - 1) * stride + size) * int64_t(sizeof(T))) : 0u);
+}
+
+__device__ __forceinline__ void load1(Buffer b, int off, bf16* x) {
+  *x = __builtin_bit_cast(bf16, __builtin_amdgcn_raw_buffer_load_b16(b, off, 0, 0));
+}
+__device__ __forceinline__ void load1(Buffer b, int off, float* x) {
+  *x = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, off, 0, 0));
+}
+__device__ __forceinline__ void store1(Buffer b, int off, bf16 x) {
+  __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, x), b, off, 0, 0);
+}
+__device__ __forceinline__ void store1(Buffer b, int off, float x) {
+  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, x), b, off, 0, 0);
+}
+__device__ __forceinline__ void load_wide(Buffer b, int off, bf16x8* x) {
+  *x = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
+}
+__device__ __forceinline__ void load_wide(Buffer b, int off, f32x8* x) {
+  const auto lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
+  const auto hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off + 16, 0, 0));
+  *x = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Eight consecutive elements at byte offset off, of which those at `left` and beyond
+// read as 0 (wide: 16-byte accesses; left is then at most 0 or at least 8).
+template <typename T, typename V8>
+__device__ __forceinline__ void load8(Buffer b, int off, int left, bool wide, V8* x) {
+  if (wide) {
+    load_wide(b, left > 0 ? off : kOutside, x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      T y;
+      load1(b, j < left ? off + j * int(sizeof(T)) : kOutside, &y);
+      (*x)[j] = y;
+    }
+  }
+}
+
 __device__ __forceinline__ Frag<1> as_frag(bf16x8 x) { return Frag<1>{{x}}; }
 __device__ __forceinline__ Frag<3> as_frag(f32x8 x) { return split(x); }
 
@@ -169,10 +223,10 @@ __device__ __forceinline__ bf16x8 col_frag(const bf16* tile, int ld, int r0, int
 }
 
 __device__ __forceinline__ int row_len(const int32_t* lengths, int64_t b, int64_t len) {
-  // lengths outside 0..len are clamped
+  // lengths outside 0..len are clamped; one value for the whole wave
   if (!lengths) return int(len);
   const int64_t n = lengths[b];
-  return int(n < 0 ? 0 : (n > len ? len : n));
+  return __builtin_amdgcn_readfirstlane(int(n < 0 ? 0 : (n > len ? len : n)));
 }
 
 // Decays below exp(-104) are zero in float32; the clamp keeps the running sums (and
