@@ -118,6 +118,19 @@ __global__ __launch_bounds__(256) void delta_recurrent_kernel(DeltaArgs a, int n
   }
 }
 
+// KP: dk rounded up; W: waves (sixteen value columns each) of a walk's block.
+template <typename IO, int KP, int W>
+hipError_t launch_walk(const DeltaArgs& a, const DeltaPlan& p, char* ws, hipStream_t stream) {
+  const int wide = wide_flags<IO>(a), nvb = (a.dv + 16 * W - 1) / (16 * W), n = int(p.nchunk);
+  char *ft = ws + p.off_t, *fp = ws + p.off_p;
+  float* vec = reinterpret_cast<float*>(ws + p.off_vec);
+  delta_prep_kernel<IO, KP, false>
+      <<<dim3(unsigned(a.batch * a.hk * n)), 256, 0, stream>>>(a, n, ft, fp, nullptr, vec, wide);
+  delta_chunk_kernel<IO, KP, W, false>
+      <<<dim3(unsigned(a.batch * a.hv * nvb)), 64 * W, 0, stream>>>(a, n, nvb, ft, fp, vec, nullptr, nullptr, 0, wide);
+  return hipGetLastError();
+}
+
 template <typename IO>
 hipError_t launch_fwd(const DeltaArgs& a, const DeltaPlan& p, char* ws, hipStream_t stream) {
   const int wide = wide_flags<IO>(a);
@@ -131,18 +144,8 @@ hipError_t launch_fwd(const DeltaArgs& a, const DeltaPlan& p, char* ws, hipStrea
       delta_recurrent_kernel<IO, 16><<<grid, 256, 0, stream>>>(a, ncol, waves, wide);
     return hipGetLastError();
   }
-  const int nvb = (a.dv + 63) / 64, n = int(p.nchunk);
-  char *ft = ws + p.off_t, *fp = ws + p.off_p;
-  float* vec = reinterpret_cast<float*>(ws + p.off_vec);
-  const dim3 prep{unsigned(a.batch * a.hk * n)}, grid{unsigned(a.batch * a.hv * nvb)};
-  if (a.dk <= 64) {
-    delta_prep_kernel<IO, 64, false><<<prep, 256, 0, stream>>>(a, n, ft, fp, nullptr, vec, wide);
-    delta_chunk_kernel<IO, 64, false><<<grid, 256, 0, stream>>>(a, n, nvb, ft, fp, vec, nullptr, nullptr, 0, wide);
-  } else {
-    delta_prep_kernel<IO, 128, false><<<prep, 256, 0, stream>>>(a, n, ft, fp, nullptr, vec, wide);
-    delta_chunk_kernel<IO, 128, false><<<grid, 256, 0, stream>>>(a, n, nvb, ft, fp, vec, nullptr, nullptr, 0, wide);
-  }
-  return hipGetLastError();
+  if (a.dk <= 64) return a.dv > 64 ? launch_walk<IO, 64, 8>(a, p, ws, stream) : launch_walk<IO, 64, 4>(a, p, ws, stream);
+  return a.dv > 64 ? launch_walk<IO, 128, 8>(a, p, ws, stream) : launch_walk<IO, 128, 4>(a, p, ws, stream);
 }
 
 }  // namespace delta

@@ -28,77 +28,90 @@ namespace delta {
 // ---- the walk back over chunks ------------------------------------------------------
 //
 // As the forward walk: a wave owns sixteen columns of the adjoint state.
-template <typename IO, int KP>
-__global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, int nchunk, int nvb,
-                                                              const char* frag_tt, const char* frag_pt,
-                                                              const float* vec, float* adjoints, float* xgrad,
-                                                              int dvp, int wide) {
-  constexpr int N = Io<IO>::kN, kTiles = KP / 16, kSteps = KP / 32, kBytes = kFrags * 3 * kFragBytes;
+template <typename IO, int KP, int W>
+__global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, int nchunk, int nvb,
+                                                                 const char* frag_tt, const char* frag_pt,
+                                                                 const float* vec, float* adjoints, float* xgrad,
+                                                                 int dvp, int wide) {
+  constexpr int N = Io<IO>::kN, kTiles = KP / 16, kSteps = KP / 32, kThreads = 64 * W, kVecs = 5 * kC;
   typedef Tile<KP> TileK;
-  __shared__ __attribute__((aligned(16))) bf16 sk[N][TileK::kElems];
-  __shared__ __attribute__((aligned(16))) bf16 sq[N][TileK::kElems];
-  __shared__ __attribute__((aligned(16))) char st[kBytes];
-  __shared__ __attribute__((aligned(16))) char sp[kBytes];
-  __shared__ __attribute__((aligned(16))) float svec[kVecFloatsBwd];
+  typedef WalkLds<IO, KP, true, 3, kVecs> Lds;
+  __shared__ __attribute__((aligned(256))) char lds[Lds::kSets * Lds::kSet];
 
   const DeltaArgs& a = b_.f;
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, i = lane & 15, qd = lane >> 4;
   const int64_t bh = int64_t(blockIdx.x) / nvb, b = bh / a.hv;
   const int h = int(bh % a.hv), hq = h / (a.hv / a.hk);
-  const int col = int(int64_t(blockIdx.x) % nvb) * 64 + 16 * wave + i;
+  const int col = int(int64_t(blockIdx.x) % nvb) * (16 * W) + 16 * wave + i;
   const int Lb = row_len(a.lengths, b, a.len), live_chunks = (Lb + kC - 1) / kC;
   const IO* kp = static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h;
   const IO* qp = static_cast<const IO*>(a.q) + b * a.sq.b + hq * a.sq.h;
   const IO* dp = static_cast<const IO*>(b_.dout) + (b * a.len * a.hv + h) * a.dv;
   const int64_t out_t = int64_t(a.hv) * a.dv;
   const bool wide_qk = wide & 1, live_col = col < a.dv;
-  const int d_lane = (8 * qd * int(out_t) + col) * int(sizeof(IO)), d_row = int(out_t) * int(sizeof(IO));
-
-  f32x4 E[kTiles];
+  const int d_lane = live_col ? (8 * qd * int(out_t) + col) * int(sizeof(IO)) : kOutside;
+  const int d_row = int(out_t) * int(sizeof(IO));
+  int at_row[kSteps], at_col[kSteps];
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int dim = chained(m, 4 * qd + r);
-      E[m][r] = (b_.dh_last && dim < a.dk && live_col) ? b_.dh_last[(bh * a.dk + dim) * a.dv + col] : 0.0f;
-    }
+  for (int s = 0; s < kSteps; ++s) {
+    at_row[s] = TileK::unit_at(chained(0, i), 4 * s + qd);
+    at_col[s] = TileK::unit_at(8 * qd + (i >> 2), 4 * s + (i & 3));
+  }
 
-  RowsAhead<IO, KP> next_k, next_q;
-  BytesAhead<kBytes> next_t, next_p;
+  const int s_lane = live_col ? (8 * qd * a.dv + col) * 4 : kOutside;
+  const int w_lane = col < dvp ? (8 * qd * dvp + col) * 4 : kOutside;
+  const uint32_t state_bytes = uint32_t(a.dk * a.dv * 4);
+
+  f32x4 E[kTiles] = {};
+  if (b_.dh_last) load_state(buffer_of(b_.dh_last + bh * a.dk * a.dv, state_bytes), s_lane, a.dv, E);
+
+  RowsAhead<IO, KP, kThreads> next_k, next_q;
+  BytesAhead<Lds::kBytesT, kThreads> next_t, next_p;
   typename Io<IO>::V8 next_d[2];  // dO of this lane's column, tokens 32 s + 8 qd ..
-  float next_vec[2] = {};
-  const auto load_ahead = [&](int c) {
-    const int64_t idx = bh * nchunk + c;
+  f32x4 next_vec = {};
+  const auto load_rows = [&](int c) {
     const int t0 = c * kC;
     next_k.load(kp, a.sk.t, t0, Lb, a.dk, wide_qk);
     next_q.load(qp, a.sq.t, t0, Lb, a.dk, wide_qk);
-    next_p.load(frag_pt + idx * kBytes);
-    next_t.load(frag_tt + idx * kBytes);
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-      if (tid + 256 * n < kVecFloatsBwd) next_vec[n] = vec[idx * kVecFloatsBwd + tid + 256 * n];
     const Buffer rows = rows_of(dp + t0 * out_t, Lb - t0 < kC ? Lb - t0 : kC, out_t, a.dv);
+    const int at = here(d_lane);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         IO x;
-        load1(rows, live_col ? d_lane + (32 * s + j) * d_row : kOutside, &x);
+        load1(rows, at + (32 * s + j) * d_row, &x);
         next_d[s][j] = x;
       }
   };
-  if (live_chunks > 0) load_ahead(live_chunks - 1);
+  const auto load_frags = [&](int c) {
+    const int64_t idx = bh * nchunk + c;
+    next_p.load(frag_pt + idx * Lds::kBytesT);
+    next_t.load(frag_tt + idx * Lds::kBytesT);
+    if (tid < kVecs / 4) next_vec = reinterpret_cast<const f32x4*>(vec + idx * kVecFloatsBwd)[tid];
+  };
+  const auto store_rows = [&](char* set) {
+    next_k.store(reinterpret_cast<bf16*>(set));
+    next_q.store(reinterpret_cast<bf16*>(set + Lds::kQ));
+  };
+  const auto store_frags = [&](char* set) {
+    next_p.store(set + Lds::kP);
+    next_t.store(set + Lds::kT);
+    if (tid < kVecs / 4) reinterpret_cast<f32x4*>(set + Lds::kVec)[tid] = next_vec;
+  };
+  if (live_chunks > 0) {
+    load_rows(live_chunks - 1);
+    load_frags(live_chunks - 1);
+    if (Lds::kSets == 2) {
+      store_rows(lds + ((live_chunks - 1) & 1) * Lds::kSet);
+      store_frags(lds + ((live_chunks - 1) & 1) * Lds::kSet);
+    }
+  }
 
   for (int c = live_chunks - 1; c >= 0; --c) {
     const int64_t idx = bh * nchunk + c;
-    __syncthreads();  // the last chunk's readers of the tiles are done
-    next_k.store(sk);
-    next_q.store(sq);
-    next_p.store(sp);
-    next_t.store(st);
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-      if (tid + 256 * n < kVecFloatsBwd) svec[tid + 256 * n] = next_vec[n];
+    const char* set = lds + (Lds::kSets == 2 ? (c & 1) * Lds::kSet : 0);
+    char* other = lds + (Lds::kSets == 2 ? (~c & 1) * Lds::kSet : 0);
     const Frag<N> df[2] = {as_frag(next_d[0]), as_frag(next_d[1])};
     f32x8 dof[2];
 #pragma unroll
@@ -106,13 +119,19 @@ __global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, i
 #pragma unroll
       for (int j = 0; j < 8; ++j) dof[s][j] = to_f32(next_d[s][j]);
     __syncthreads();
-    if (c > 0) load_ahead(c - 1);
-    if (col < dvp) {
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) adjoints[(idx * KP + chained(m, 4 * qd + r)) * dvp + col] = E[m][r];
+    if (Lds::kSets == 1) {
+      store_rows(lds);
+      store_frags(lds);
+      __syncthreads();
     }
+    if (c > 0) {
+      load_rows(c - 1);
+      if (Lds::kSets == 1) load_frags(c - 1);
+    }
+    store_state(buffer_of(adjoints + idx * KP * dvp, KP * dvp * 4), w_lane, dvp, E);
+    const bf16 *sk = reinterpret_cast<const bf16*>(set), *sq = reinterpret_cast<const bf16*>(set + Lds::kQ);
+    const char *st = set + Lds::kT + lane * 16, *sp = set + Lds::kP + lane * 16;
+    const float* svec = reinterpret_cast<const float*>(set + Lds::kVec);
 
     // du = P^T do + d (K E)
     Frag<3> ef[kSteps];
@@ -122,12 +141,11 @@ __global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, i
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       f32x4 ke = {};
-      const int row = chained(m, i) * TileK::kLd + 8 * qd;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         Frag<N> fk;
 #pragma unroll
-        for (int n = 0; n < N; ++n) fk.t[n] = row_frag(&sk[n][row + 32 * s]);
+        for (int n = 0; n < N; ++n) fk.t[n] = row_frag(sk + n * TileK::kElems + chained(m, 0) * KP + at_row[s]);
         ke = mul(fk, ef[s], ke);
       }
       x[m] = ke * *reinterpret_cast<const f32x4*>(&svec[kC + chained(m, 4 * qd)]);
@@ -137,9 +155,13 @@ __global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, i
         Frag<3> f;
 #pragma unroll
         for (int n = 0; n < 3; ++n)
-          f.t[n] = *reinterpret_cast<const bf16x8*>(sp + ((upper_frag(m, s) * 3 + n) * 64 + lane) * 16);
+          f.t[n] = *reinterpret_cast<const bf16x8*>(sp + (upper_frag(m, s) * 3 + n) * kFragBytes);
         x[m] = mul(f, df[s], x[m]);
       }
+    }
+    if (Lds::kSets == 2 && c > 0) {
+      store_rows(other);
+      load_frags(c - 1);
     }
     // x~ = T^T du
     const Frag<3> xf[2] = {split(x[0], x[1]), split(x[2], x[3])};
@@ -152,14 +174,14 @@ __global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, i
         Frag<3> f;
 #pragma unroll
         for (int n = 0; n < 3; ++n)
-          f.t[n] = *reinterpret_cast<const bf16x8*>(st + ((upper_frag(m, s) * 3 + n) * 64 + lane) * 16);
+          f.t[n] = *reinterpret_cast<const bf16x8*>(st + (upper_frag(m, s) * 3 + n) * kFragBytes);
         x[m] = mul(f, xf[s], x[m]);
       }
-      const int tok = chained(m, 4 * qd);
-      if (col < dvp) {
+    }
+    store_state(buffer_of(xgrad + idx * kC * dvp, kC * dvp * 4), w_lane, dvp, x);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) xgrad[(idx * kC + tok + r) * dvp + col] = x[m][r];
-      }
+    for (int m = 0; m < 4; ++m) {
+      const int tok = chained(m, 4 * qd);
       x[m] *= *reinterpret_cast<const f32x4*>(&svec[tok]) * *reinterpret_cast<const f32x4*>(&svec[4 * kC + tok]) * -1.0f;
     }
     // E = last E + Q^T (e do) - K^T (c beta x~)
@@ -174,25 +196,20 @@ __global__ __launch_bounds__(256) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, i
       E[m] *= last;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
+        const int at = 32 * s * KP + at_col[m >> 1] + 4 * (m & 1);
         Frag<N> fk, fq;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-          fk.t[n] = col_frag(sk[n], TileK::kLd, 32 * s + 8 * qd, chained(m, 4 * (i & 3)));
-          fq.t[n] = col_frag(sq[n], TileK::kLd, 32 * s + 8 * qd, chained(m, 4 * (i & 3)));
+          fk.t[n] = col_frag(sk + n * TileK::kElems + at, KP);
+          fq.t[n] = col_frag(sq + n * TileK::kElems + at, KP);
         }
         E[m] = mul(fk, yf[s], E[m]);
         E[m] = mul(fq, gf[s], E[m]);
       }
     }
+    if (Lds::kSets == 2 && c > 0) store_frags(other);
   }
-  if (!b_.dh0) return;
-#pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int dim = chained(m, 4 * qd + r);
-      if (dim < a.dk && live_col) b_.dh0[(bh * a.dk + dim) * a.dv + col] = E[m][r];
-    }
+  if (b_.dh0) store_state(buffer_of(b_.dh0 + bh * a.dk * a.dv, state_bytes), s_lane, a.dv, E);
 }
 
 // ---- the gradients of a chunk --------------------------------------------------------
@@ -259,14 +276,14 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs b_, int nc
     const auto fq = as_frag(load8(qp + (t0 + row) * a.sq.t + d8, in ? a.dk - d8 : 0, wide_qk));
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      *reinterpret_cast<bf16x8*>(&sk[n][row * TileK::kLd + d8]) = fk.t[n];
-      *reinterpret_cast<bf16x8*>(&sq[n][row * TileK::kLd + d8]) = fq.t[n];
+      *reinterpret_cast<bf16x8*>(&sk[n][TileK::unit_at(row, d8 / 8)]) = fk.t[n];
+      *reinterpret_cast<bf16x8*>(&sq[n][TileK::unit_at(row, d8 / 8)]) = fq.t[n];
     }
   }
   const auto at_tile = [](const bf16 (&s)[N][TileK::kElems], int row, int dim) {
     float x = 0.0f;
 #pragma unroll
-    for (int n = N - 1; n >= 0; --n) x += float(s[n][row * TileK::kLd + dim]);
+    for (int n = N - 1; n >= 0; --n) x += float(s[n][TileK::at(row, dim)]);
     return x;
   };
 
@@ -426,7 +443,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs b_, int nc
             Frag<N> fb;
 #pragma unroll
             for (int t = 0; t < N; ++t)
-              fb.t[t] = col_frag(tile[t], TileK::kLd, 32 * s + 8 * qd, 16 * (wave + 4 * n) + 4 * (i & 3));
+              fb.t[t] = col_frag<KP>(tile[t], 32 * s + 8 * qd, 16 * (wave + 4 * n) + 4 * (i & 3));
             acc[m][n] = mul(fg, fb, acc[m][n]);
           }
         }
@@ -440,7 +457,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs b_, int nc
           Frag<3> fg;
 #pragma unroll
           for (int n = 0; n < 3; ++n) {
-            fg.t[n] = col_frag(sg[n], kLdG, 32 * s + 8 * qd, 16 * m + 4 * (i & 3));
+            fg.t[n] = col_frag(&sg[n][(32 * s + 8 * qd + (i >> 2)) * kLdG + 16 * m + 4 * (i & 3)], kLdG);
             if (minus) fg.t[n] = -fg.t[n];
           }
 #pragma unroll
@@ -448,7 +465,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs b_, int nc
             Frag<N> fb;
 #pragma unroll
             for (int t = 0; t < N; ++t)
-              fb.t[t] = col_frag(tile[t], TileK::kLd, 32 * s + 8 * qd, 16 * (wave + 4 * n) + 4 * (i & 3));
+              fb.t[t] = col_frag<KP>(tile[t], 32 * s + 8 * qd, 16 * (wave + 4 * n) + 4 * (i & 3));
             acc[m][n] = mul(fg, fb, acc[m][n]);
           }
         }
@@ -554,13 +571,13 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs b_, int nc
     }
 }
 
-template <typename IO, int KP>
+template <typename IO, int KP, int W>
 hipError_t launch_bwd(const DeltaBwdArgs& b, const DeltaBwdPlan& p, char* ws, hipStream_t stream) {
   const DeltaArgs& a = b.f;
   int wide = wide_flags<IO>(a) & ~4;
   if (a.dv % 8 == 0 && reinterpret_cast<uintptr_t>(b.dout) % 16 == 0) wide |= 4;
   if (a.dv % 8 == 0 && reinterpret_cast<uintptr_t>(b.dv) % 16 == 0) wide |= 16;
-  const int n = int(p.nchunk), nvb = (p.dvp + 63) / 64;
+  const int n = int(p.nchunk), nvb = (p.dvp + 16 * W - 1) / (16 * W);
   char *ft = ws + p.off_t, *ftt = ws + p.off_tt, *fpt = ws + p.off_pt;
   float *vec = reinterpret_cast<float*>(ws + p.off_vec), *u = reinterpret_cast<float*>(ws + p.off_u),
         *x = reinterpret_cast<float*>(ws + p.off_y), *s = reinterpret_cast<float*>(ws + p.off_s),
@@ -568,11 +585,18 @@ hipError_t launch_bwd(const DeltaBwdArgs& b, const DeltaBwdPlan& p, char* ws, hi
   const dim3 per_key{unsigned(a.batch * a.hk * n)}, walk{unsigned(a.batch * a.hv * nvb)};
   if (n > 0) {
     delta_prep_kernel<IO, KP, true><<<per_key, 256, 0, stream>>>(a, n, ft, fpt, ftt, vec, wide);
-    delta_chunk_kernel<IO, KP, true><<<walk, 256, 0, stream>>>(a, n, nvb, ft, nullptr, vec, s, u, p.dvp, wide);
+    delta_chunk_kernel<IO, KP, W, true><<<walk, 64 * W, 0, stream>>>(a, n, nvb, ft, nullptr, vec, s, u, p.dvp, wide);
   }
-  delta_chunk_bwd_kernel<IO, KP><<<walk, 256, 0, stream>>>(b, n, nvb, ftt, fpt, vec, e, x, p.dvp, wide);
+  delta_chunk_bwd_kernel<IO, KP, W><<<walk, 64 * W, 0, stream>>>(b, n, nvb, ftt, fpt, vec, e, x, p.dvp, wide);
   if (n > 0) delta_grad_kernel<IO, KP><<<per_key, 256, 0, stream>>>(b, n, vec, s, e, u, x, p.dvp, wide);
   return hipGetLastError();
+}
+
+template <typename IO>
+hipError_t launch_bwd(const DeltaBwdArgs& b, const DeltaBwdPlan& p, char* ws, hipStream_t stream) {
+  if (p.kp == 64)
+    return p.dvp > 64 ? launch_bwd<IO, 64, 8>(b, p, ws, stream) : launch_bwd<IO, 64, 4>(b, p, ws, stream);
+  return p.dvp > 64 ? launch_bwd<IO, 128, 8>(b, p, ws, stream) : launch_bwd<IO, 128, 4>(b, p, ws, stream);
 }
 
 }  // namespace delta
@@ -606,11 +630,7 @@ DeltaBwdPlan make_delta_bwd_plan(int64_t batch, int64_t len, int hk, int hv, int
 }
 
 hipError_t launch_delta_bwd(const DeltaBwdArgs& b, const DeltaBwdPlan& p, char* ws, hipStream_t stream) {
-  if (b.f.io_bf16)
-    return p.kp == 64 ? delta::launch_bwd<delta::bf16, 64>(b, p, ws, stream)
-                      : delta::launch_bwd<delta::bf16, 128>(b, p, ws, stream);
-  return p.kp == 64 ? delta::launch_bwd<float, 64>(b, p, ws, stream)
-                    : delta::launch_bwd<float, 128>(b, p, ws, stream);
+  return b.f.io_bf16 ? delta::launch_bwd<delta::bf16>(b, p, ws, stream) : delta::launch_bwd<float>(b, p, ws, stream);
 }
 
 }  // namespace sscan

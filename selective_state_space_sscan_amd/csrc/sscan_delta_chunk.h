@@ -8,84 +8,92 @@
 namespace sscan {
 namespace delta {
 
-// A chunk's rows of K (or Q) on their way from memory to the LDS tile: loaded into
-// registers while the chunk before is computed.
-template <typename IO, int KP>
+// A chunk's rows of K (or Q) on their way from memory to the LDS tile, by kThreads
+// threads, held in registers meanwhile.
+template <typename IO, int KP, int kThreads>
 struct RowsAhead {
-  static constexpr int kUnits = kC * KP / 8 / 256;
+  static constexpr int kUnits = kC * KP / 8 / kThreads;
   typename Io<IO>::V8 x[kUnits];
 
   __device__ __forceinline__ void load(const IO* p, int64_t stride, int t0, int len, int dk, bool wide) {
     const Buffer rows = rows_of(p + t0 * stride, len - t0 < kC ? len - t0 : kC, stride, dk);
 #pragma unroll
     for (int n = 0; n < kUnits; ++n) {
-      const int u = int(threadIdx.x) + 256 * n, row = u / (KP / 8), d8 = (u % (KP / 8)) * 8;
-      load8<IO>(rows, (row * int(stride) + d8) * int(sizeof(IO)), dk - d8, wide, &x[n]);
+      const int u = int(threadIdx.x) + kThreads * n, row = u / (KP / 8), unit = u % (KP / 8);
+      load8<IO>(rows, (row * int(stride) + 8 * unit) * int(sizeof(IO)), dk - 8 * unit, wide, &x[n]);
     }
   }
 
-  template <int N>
-  __device__ __forceinline__ void store(bf16 (&tile)[N][Tile<KP>::kElems]) const {
+  // Terms follow each other Tile<KP>::kElems apart.
+  __device__ __forceinline__ void store(bf16* tile) const {
 #pragma unroll
     for (int n = 0; n < kUnits; ++n) {
-      const int u = int(threadIdx.x) + 256 * n, row = u / (KP / 8), d8 = (u % (KP / 8)) * 8;
+      const int u = int(threadIdx.x) + kThreads * n;
+      bf16* at = tile + Tile<KP>::unit_at(u / (KP / 8), u % (KP / 8));
       const auto f = as_frag(x[n]);
 #pragma unroll
-      for (int k = 0; k < N; ++k) *reinterpret_cast<bf16x8*>(&tile[k][row * Tile<KP>::kLd + d8]) = f.t[k];
+      for (int k = 0; k < Io<IO>::kN; ++k) *reinterpret_cast<bf16x8*>(at + k * Tile<KP>::kElems) = f.t[k];
     }
   }
 };
 
 // A contiguous block of kBytes, likewise.
-template <int kBytes>
+template <int kBytes, int kThreads>
 struct BytesAhead {
-  static constexpr int kUnits = (kBytes / 16 + 255) / 256;
-  u32x4 x[kUnits];
+  static constexpr int kUnits = (kBytes / 16 + kThreads - 1) / kThreads;
+  u32x4 x[kUnits > 0 ? kUnits : 1];
 
   __device__ __forceinline__ void load(const char* p) {
+    const Buffer b = buffer_of(p, kBytes);
 #pragma unroll
-    for (int n = 0; n < kUnits; ++n) {
-      const int u = int(threadIdx.x) + 256 * n;
-      if (u < kBytes / 16) x[n] = reinterpret_cast<const u32x4*>(p)[u];
-    }
+    for (int n = 0; n < kUnits; ++n)
+      x[n] = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int(threadIdx.x) + kThreads * n) * 16, 0, 0));
   }
 
   __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
     for (int n = 0; n < kUnits; ++n) {
-      const int u = int(threadIdx.x) + 256 * n;
-      if (u < kBytes / 16) reinterpret_cast<u32x4*>(lds)[u] = x[n];
+      const int u = int(threadIdx.x) + kThreads * n;
+      if ((n + 1) * kThreads <= kBytes / 16 || u < kBytes / 16) reinterpret_cast<u32x4*>(lds)[u] = x[n];
     }
   }
+};
+
+// LDS of a walk: per chunk the K tile, the Q tile, the fragments of two triangular
+// matrices and the per-token factors.  bf16: two sets, the next chunk's being filled
+// while one is read (one barrier a chunk); float32 has room for one (two barriers).
+template <typename IO, int KP, bool kWithQ, int kTermsP, int kVecs>
+struct WalkLds {
+  static constexpr int kTileBytes = Io<IO>::kN * Tile<KP>::kElems * 2;
+  static constexpr int kBytesT = kFrags * 3 * kFragBytes, kBytesP = kWithQ ? kFrags * kTermsP * kFragBytes : 0;
+  static constexpr int kQ = kTileBytes, kT = kQ + (kWithQ ? kTileBytes : 0), kP = kT + kBytesT, kVec = kP + kBytesP;
+  static constexpr int kSet = kVec + kVecs * 4, kSets = std::is_same<IO, bf16>::value ? 2 : 1;
 };
 
 // A wave owns sixteen columns of S for the whole sequence (KP x 16, in the accumulator
 // layout) and walks the chunks in order; columns are independent, so waves never
 // exchange data: every product's result is the next product's B factor in the same
-// lane.  A block is four waves (64 columns) that share the chunk's K and Q tiles and
-// the fragments of T and P through LDS; the next chunk's are loaded into registers
-// while a chunk is computed.  V and the output move between memory and the lanes that
-// own them (32-byte runs of a row that the block's four waves complete to a line).
+// lane.  A block is W waves (16 W columns) that share the chunk's K and Q tiles and
+// the fragments of T and P through LDS; the next chunk's come in while a chunk is
+// computed.  V and the output move between memory and the lanes that own them (32-byte
+// runs of a row that the block's waves complete to whole lines).
 // STATES: the backward pass's recomputation, which leaves every chunk's entry state
 // [KP][dvp] and U [64][dvp] in float32 instead of the output and the last state.
-template <typename IO, int KP, bool STATES>
-__global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs a, int nchunk, int nvb, const char* frag_t,
-                                                          const char* frag_p, const float* vec, float* states,
-                                                          float* values, int dvp, int wide) {
-  constexpr int N = Io<IO>::kN, NO = Io<IO>::kOutTerms;
+template <typename IO, int KP, int W, bool STATES>
+__global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nchunk, int nvb, const char* frag_t,
+                                                             const char* frag_p, const float* vec, float* states,
+                                                             float* values, int dvp, int wide) {
+  constexpr int N = Io<IO>::kN, NO = Io<IO>::kOutTerms, kThreads = 64 * W;
   constexpr int kTiles = KP / 16, kSteps = KP / 32, kVecs = STATES ? kVecFloatsBwd : kVecFloats;
-  constexpr int kBytesT = kFrags * 3 * kFragBytes, kBytesP = STATES ? 16 : kFrags * NO * kFragBytes;
   typedef Tile<KP> TileK;
-  __shared__ __attribute__((aligned(16))) bf16 sk[N][TileK::kElems];
-  __shared__ __attribute__((aligned(16))) bf16 sq[STATES ? 1 : N][STATES ? 8 : TileK::kElems];
-  __shared__ __attribute__((aligned(16))) char st[kBytesT];
-  __shared__ __attribute__((aligned(16))) char sp[kBytesP];
-  __shared__ __attribute__((aligned(16))) float svec[kVecFloats];
+  typedef WalkLds<IO, KP, !STATES, NO, kVecFloats> Lds;
+  __shared__ __attribute__((aligned(256))) char lds[Lds::kSets * Lds::kSet];
 
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, i = lane & 15, qd = lane >> 4;
   const int64_t bh = int64_t(blockIdx.x) / nvb, b = bh / a.hv;
   const int h = int(bh % a.hv), hq = h / (a.hv / a.hk);
-  const int col = int(int64_t(blockIdx.x) % nvb) * 64 + 16 * wave + i;
+  const int col = int(int64_t(blockIdx.x) % nvb) * (16 * W) + 16 * wave + i;
   const int L = int(a.len), Lb = row_len(a.lengths, b, a.len);
   const int live_chunks = (Lb + kC - 1) / kC;
   const IO* kp = static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h;
@@ -96,66 +104,89 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs a, int nchun
   const bool wide_qk = wide & 1, live_col = col < a.dv;
   // byte offset of this lane's first token (8 qd) and column in a chunk's rows, and the
   // rows from there to token 32 (m >> 1) + 4 (m & 1) + r
-  const int v_lane = (8 * qd * int(a.sv.t) + col) * int(sizeof(IO)), v_row = int(a.sv.t) * int(sizeof(IO));
-  const int o_lane = (8 * qd * int(out_t) + col) * int(sizeof(IO)), o_row = int(out_t) * int(sizeof(IO));
-
-  f32x4 S[kTiles];
+  const int v_lane = live_col ? (8 * qd * int(a.sv.t) + col) * int(sizeof(IO)) : kOutside;
+  const int o_lane = live_col ? (8 * qd * int(out_t) + col) * int(sizeof(IO)) : kOutside;
+  const int v_row = int(a.sv.t) * int(sizeof(IO)), o_row = int(out_t) * int(sizeof(IO));
+  // this lane's elements in a tile: rows by contraction step, columns by pairs of tiles
+  int at_row[kSteps], at_col[kSteps];
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int dim = chained(m, 4 * qd + r);
-      S[m][r] = (a.h0 && dim < a.dk && live_col) ? a.h0[(bh * a.dk + dim) * a.dv + col] : 0.0f;
-    }
+  for (int s = 0; s < kSteps; ++s) {
+    at_row[s] = TileK::unit_at(chained(0, i), 4 * s + qd);
+    at_col[s] = TileK::unit_at(8 * qd + (i >> 2), 4 * s + (i & 3));
+  }
 
-  RowsAhead<IO, KP> next_k, next_q;
-  BytesAhead<kBytesT> next_t;
-  BytesAhead<kBytesP> next_p;
+  const int s_lane = live_col ? (8 * qd * a.dv + col) * 4 : kOutside;
+  const int w_lane = STATES && col < dvp ? (8 * qd * dvp + col) * 4 : kOutside;
+  const uint32_t state_bytes = uint32_t(a.dk * a.dv * 4);
+
+  f32x4 S[kTiles] = {};
+  if (a.h0) load_state(buffer_of(a.h0 + bh * a.dk * a.dv, state_bytes), s_lane, a.dv, S);
+
+  RowsAhead<IO, KP, kThreads> next_k, next_q;
+  BytesAhead<Lds::kBytesT, kThreads> next_t;
+  BytesAhead<Lds::kBytesP, kThreads> next_p;
   IO next_v[4][4];
-  float next_vec = 0.0f;
-  const auto load_ahead = [&](int c) {
-    const int64_t idx = bh * nchunk + c;
+  f32x4 next_vec = {};
+  const auto load_rows = [&](int c) {
     const int t0 = c * kC;
     next_k.load(kp, a.sk.t, t0, Lb, a.dk, wide_qk);
-    next_t.load(frag_t + idx * kBytesT);
-    if constexpr (!STATES) {
-      next_q.load(qp, a.sq.t, t0, Lb, a.dk, wide_qk);
-      next_p.load(frag_p + idx * kBytesP);
-    }
-    next_vec = vec[idx * kVecs + tid];
+    if constexpr (!STATES) next_q.load(qp, a.sq.t, t0, Lb, a.dk, wide_qk);
     const Buffer rows = rows_of(vp + t0 * a.sv.t, Lb - t0 < kC ? Lb - t0 : kC, a.sv.t, a.dv);
+    const int at = here(v_lane);
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        load1(rows, live_col ? v_lane + (32 * (m >> 1) + 4 * (m & 1) + r) * v_row : kOutside, &next_v[m][r]);
+      for (int r = 0; r < 4; ++r) load1(rows, at + (32 * (m >> 1) + 4 * (m & 1) + r) * v_row, &next_v[m][r]);
   };
-  if (live_chunks > 0) load_ahead(0);
+  const auto load_frags = [&](int c) {
+    const int64_t idx = bh * nchunk + c;
+    next_t.load(frag_t + idx * Lds::kBytesT);
+    if constexpr (!STATES) next_p.load(frag_p + idx * Lds::kBytesP);
+    if (tid < kVecFloats / 4) next_vec = reinterpret_cast<const f32x4*>(vec + idx * kVecs)[tid];
+  };
+  const auto store_rows = [&](char* set) {
+    next_k.store(reinterpret_cast<bf16*>(set));
+    if constexpr (!STATES) next_q.store(reinterpret_cast<bf16*>(set + Lds::kQ));
+  };
+  const auto store_frags = [&](char* set) {
+    next_t.store(set + Lds::kT);
+    if constexpr (!STATES) next_p.store(set + Lds::kP);
+    if (tid < kVecFloats / 4) reinterpret_cast<f32x4*>(set + Lds::kVec)[tid] = next_vec;
+  };
+  if (live_chunks > 0) {
+    load_rows(0);
+    load_frags(0);
+    if (Lds::kSets == 2) {
+      store_rows(lds);
+      store_frags(lds);
+    }
+  }
 
   for (int c = 0; c < live_chunks; ++c) {
     const int t0 = c * kC;
     const int64_t idx = bh * nchunk + c;
-    __syncthreads();  // the last chunk's readers of the tiles are done
-    next_k.store(sk);
-    next_t.store(st);
-    if constexpr (!STATES) {
-      next_q.store(sq);
-      next_p.store(sp);
-    }
-    svec[tid] = next_vec;
+    const char* set = lds + (Lds::kSets == 2 ? (c & 1) * Lds::kSet : 0);
+    char* other = lds + (Lds::kSets == 2 ? (~c & 1) * Lds::kSet : 0);
     f32x4 x[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) x[m][r] = to_f32(next_v[m][r]);
     __syncthreads();
-    if (c + 1 < live_chunks) load_ahead(c + 1);
-    if (STATES && col < dvp) {
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) states[(idx * KP + chained(m, 4 * qd + r)) * dvp + col] = S[m][r];
+    if (Lds::kSets == 1) {
+      store_rows(lds);
+      store_frags(lds);
+      __syncthreads();
     }
+    const bool more = c + 1 < live_chunks;
+    if (more) {
+      load_rows(c + 1);
+      if (Lds::kSets == 1) load_frags(c + 1);
+    }
+    if constexpr (STATES) store_state(buffer_of(states + idx * KP * dvp, KP * dvp * 4), w_lane, dvp, S);
+    const bf16 *sk = reinterpret_cast<const bf16*>(set), *sq = reinterpret_cast<const bf16*>(set + Lds::kQ);
+    const char *st = set + Lds::kT + lane * 16, *sp = set + Lds::kP + lane * 16;
+    const float* svec = reinterpret_cast<const float*>(set + Lds::kVec);
 
     Frag<3> sf[kSteps];
 #pragma unroll
@@ -165,14 +196,14 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs a, int nchun
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       f32x4 ks = {}, qs = {};
-      const int row = chained(m, i) * TileK::kLd + 8 * qd;
+      const int row = chained(m, 0) * KP;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         Frag<N> fk, fq;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-          fk.t[n] = row_frag(&sk[n][row + 32 * s]);
-          if constexpr (!STATES) fq.t[n] = row_frag(&sq[n][row + 32 * s]);
+          fk.t[n] = row_frag(sk + n * TileK::kElems + row + at_row[s]);
+          if constexpr (!STATES) fq.t[n] = row_frag(sq + n * TileK::kElems + row + at_row[s]);
         }
         ks = mul(fk, sf[s], ks);
         if constexpr (!STATES) qs = mul<NO>(fq, sf[s], qs);
@@ -180,6 +211,10 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs a, int nchun
       const int tok = chained(m, 4 * qd);
       x[m] -= *reinterpret_cast<const f32x4*>(&svec[tok]) * ks;
       o[m] = *reinterpret_cast<const f32x4*>(&svec[2 * kC + tok]) * qs;
+    }
+    if (Lds::kSets == 2 && more) {
+      store_rows(other);
+      load_frags(c + 1);
     }
     // u = (T diag(beta)) x
     const Frag<3> xf[2] = {split(x[0], x[1]), split(x[2], x[3])};
@@ -193,7 +228,7 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs a, int nchun
         Frag<3> ft;
 #pragma unroll
         for (int n = 0; n < 3; ++n)
-          ft.t[n] = *reinterpret_cast<const bf16x8*>(st + ((lower_frag(m, s) * 3 + n) * 64 + lane) * 16);
+          ft.t[n] = *reinterpret_cast<const bf16x8*>(st + (lower_frag(m, s) * 3 + n) * kFragBytes);
         u[m] = mul(ft, xf[s], u[m]);
       }
     }
@@ -208,20 +243,17 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs a, int nchun
           Frag<NO> fp;
 #pragma unroll
           for (int n = 0; n < NO; ++n)
-            fp.t[n] = *reinterpret_cast<const bf16x8*>(sp + ((lower_frag(m, s) * NO + n) * 64 + lane) * 16);
+            fp.t[n] = *reinterpret_cast<const bf16x8*>(sp + (lower_frag(m, s) * NO + n) * kFragBytes);
           o[m] = mul<NO>(fp, uf[s], o[m]);
         }
       const Buffer rows = rows_of(op + t0 * out_t, L - t0 < kC ? L - t0 : kC, out_t, a.dv);
+      const int at = here(o_lane);
 #pragma unroll
       for (int m = 0; m < 4; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          store1(rows, live_col ? o_lane + (32 * (m >> 1) + 4 * (m & 1) + r) * o_row : kOutside, IO(o[m][r]));
-    } else if (col < dvp) {
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) values[(idx * kC + chained(m, 4 * qd + r)) * dvp + col] = u[m][r];
+        for (int r = 0; r < 4; ++r) store1(rows, at + (32 * (m >> 1) + 4 * (m & 1) + r) * o_row, IO(o[m][r]));
+    } else {
+      store_state(buffer_of(values + idx * kC * dvp, kC * dvp * 4), w_lane, dvp, u);
     }
     // S = last S + K^T (d u)
 #pragma unroll
@@ -235,22 +267,18 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs a, int nchun
       for (int s = 0; s < 2; ++s) {
         Frag<N> fk;
 #pragma unroll
-        for (int n = 0; n < N; ++n) fk.t[n] = col_frag(sk[n], TileK::kLd, 32 * s + 8 * qd, chained(m, 4 * (i & 3)));
+        for (int n = 0; n < N; ++n)
+          fk.t[n] = col_frag(sk + n * TileK::kElems + 32 * s * KP + at_col[m >> 1] + 4 * (m & 1), KP);
         S[m] = mul(fk, df[s], S[m]);
       }
     }
+    if (Lds::kSets == 2 && more) store_frags(other);
   }
   if constexpr (STATES) return;
   // tokens past the row's length: zeros (those of its last chunk were written above)
   if (live_col)
     for (int t = live_chunks * kC + qd; t < L; t += 4) op[t * out_t + col] = IO(0.0f);
-#pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int dim = chained(m, 4 * qd + r);
-      if (dim < a.dk && live_col) a.h_last[(bh * a.dk + dim) * a.dv + col] = S[m][r];
-    }
+  store_state(buffer_of(a.h_last + bh * a.dk * a.dv, state_bytes), s_lane, a.dv, S);
 }
 
 }  // namespace delta

@@ -128,8 +128,14 @@ __device__ __forceinline__ f32x8 load8(const float* p, int left, bool wide) {
 typedef __amdgpu_buffer_rsrc_t Buffer;
 constexpr int kOutside = int(0x80000000u);  // an offset beyond every buffer
 
+// p and bytes are the same in all lanes (read from the first, so that the descriptor is
+// held in scalar registers).
 __device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, int(bytes), 0x00020000);
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  const uint64_t lo = uint32_t(__builtin_amdgcn_readfirstlane(int(at)));
+  const uint64_t hi = uint32_t(__builtin_amdgcn_readfirstlane(int(at >> 32)));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(hi << 32 | lo), 0,
+                                           __builtin_amdgcn_readfirstlane(int(bytes)), 0x00020000);
 }
 
 // `rows` rows of `size` elements `stride` apart, from p.
@@ -159,6 +165,13 @@ __device__ __forceinline__ void load_wide(Buffer b, int off, f32x8* x) {
   *x = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// x, computed here and not before: keeps the compiler from holding the sums of x and
+// many constants in registers across a whole loop instead of adding them where used.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // Eight consecutive elements at byte offset off, of which those at `left` and beyond
 // read as 0 (wide: 16-byte accesses; left is then at most 0 or at least 8).
 template <typename T, typename V8>
@@ -166,6 +179,8 @@ __device__ __forceinline__ void load8(Buffer b, int off, int left, bool wide, V8
   if (wide) {
     load_wide(b, left > 0 ? off : kOutside, x);
   } else {
+    off = here(off);
+    left = here(left);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       T y;
@@ -173,6 +188,30 @@ __device__ __forceinline__ void load8(Buffer b, int off, int left, bool wide, V8
       (*x)[j] = y;
     }
   }
+}
+
+// A state's columns in the accumulator layout, from or to rows of `ld` floats: lane_at
+// is the byte offset of the lane's row 8 qd and column, or kOutside.
+template <int kTiles>
+__device__ __forceinline__ void load_state(Buffer b, int lane_at, int ld, f32x4 (&S)[kTiles]) {
+  lane_at = here(lane_at);
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float x;
+      load1(b, lane_at + (32 * (m >> 1) + 4 * (m & 1) + r) * ld * 4, &x);
+      S[m][r] = x;
+    }
+}
+
+template <int kTiles>
+__device__ __forceinline__ void store_state(Buffer b, int lane_at, int ld, const f32x4 (&S)[kTiles]) {
+  lane_at = here(lane_at);
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) store1(b, lane_at + (32 * (m >> 1) + 4 * (m & 1) + r) * ld * 4, S[m][r]);
 }
 
 __device__ __forceinline__ Frag<1> as_frag(bf16x8 x) { return Frag<1>{{x}}; }
@@ -193,16 +232,20 @@ struct Io<float> {
   typedef f32x8 V8;
 };
 
-// LDS tiles of bf16 rows, padded by 16 bytes so that sixteen rows read at one column
-// start at different banks.
+// LDS tile of bf16 rows of KP elements, in units of eight (16 bytes).  A row's units are
+// permuted by its index, so that both ways of reading the tile touch every bank once:
+// sixteen chained rows at one unit (row_at), and four consecutive rows at four units
+// (the transposing reads of col_frag).
 template <int KP>
 struct Tile {
-  static constexpr int kLd = KP + 8;             // elements between rows
-  static constexpr int kElems = kC * kLd;        // of one term
-};
+  static constexpr int kElems = kC * KP;  // of one term
 
-// Fragment of 8 contraction indices along a row.
-__device__ __forceinline__ bf16x8 row_frag(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
+  __device__ static __forceinline__ int swizzle(int row) {
+    return KP == 64 ? 4 * ((row >> 1) & 1) + ((row >> 3) & 3) : 4 * (row & 3) + ((row >> 3) & 3);
+  }
+  __device__ static __forceinline__ int unit_at(int row, int unit) { return row * KP + ((unit ^ swizzle(row)) << 3); }
+  __device__ static __forceinline__ int at(int row, int dim) { return unit_at(row, dim >> 3) + (dim & 7); }
+};
 
 // Four rows of sixteen columns, transposed: lane i of each group of sixteen receives
 // column i.  The caller passes row (i >> 2), columns 4 (i & 3) .. + 3 of the group.
@@ -212,15 +255,23 @@ __device__ __forceinline__ bf16x4 read_tr(const bf16* p) {
   return __builtin_bit_cast(bf16x4, r);
 }
 
-// Fragment whose row i (or column i) is a column of the LDS tile and whose eight
-// contraction indices are tile rows r0 .. r0 + 7: col4 is where columns
-// 4 (i & 3) .. + 3 of the sixteen start (four consecutive ones).
-__device__ __forceinline__ bf16x8 col_frag(const bf16* tile, int ld, int r0, int col4) {
-  const int i = lane_id() & 15;
-  const bf16* p = tile + (r0 + (i >> 2)) * ld + col4;
+// Fragment whose row i (or column i) is a column of rows `ld` elements apart, and whose
+// eight contraction indices are eight consecutive rows: p is where columns
+// 4 (i & 3) .. + 3 of the sixteen start in row (i >> 2) of them.
+__device__ __forceinline__ bf16x8 col_frag(const bf16* p, int ld) {
   const bf16x4 a = read_tr(p), b = read_tr(p + 4 * ld);
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
+
+// The same of a tile: rows r0 .. r0 + 7 (r0 a multiple of eight: their units are
+// permuted alike), columns from col4.
+template <int KP>
+__device__ __forceinline__ bf16x8 col_frag(const bf16* tile, int r0, int col4) {
+  const int row = r0 + ((lane_id() & 15) >> 2);
+  return col_frag(tile + Tile<KP>::unit_at(row, col4 >> 3) + (col4 & 4), KP);
+}
+
+__device__ __forceinline__ bf16x8 row_frag(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
 
 __device__ __forceinline__ int row_len(const int32_t* lengths, int64_t b, int64_t len) {
   // lengths outside 0..len are clamped; one value for the whole wave
