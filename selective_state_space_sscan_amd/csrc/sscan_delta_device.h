@@ -51,14 +51,27 @@ struct Frag {
   bf16x8 t[N];
 };
 
+// Pairs are rounded together and widened again from the packed word (a shift and a
+// mask): eleven instructions for the three terms of two values.
 __device__ __forceinline__ Frag<3> split(f32x8 x) {
-  Frag<3> f;
-  f.t[0] = __builtin_convertvector(x, bf16x8);
-  x -= __builtin_convertvector(f.t[0], f32x8);
-  f.t[1] = __builtin_convertvector(x, bf16x8);
-  x -= __builtin_convertvector(f.t[1], f32x8);
-  f.t[2] = __builtin_convertvector(x, bf16x8);
-  return f;
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  u32x4 w[3];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    f32x2 y = {x[2 * p], x[2 * p + 1]};
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      uint32_t packed = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, bf16x2));
+      asm("" : "+v"(packed));  // keeps the widening below from becoming a second rounding
+      w[n][p] = packed;
+      if (n < 2) {
+        y[0] -= __builtin_bit_cast(float, packed << 16);
+        y[1] -= __builtin_bit_cast(float, packed & 0xffff0000u);
+      }
+    }
+  }
+  return Frag<3>{{__builtin_bit_cast(bf16x8, w[0]), __builtin_bit_cast(bf16x8, w[1]), __builtin_bit_cast(bf16x8, w[2])}};
 }
 
 __device__ __forceinline__ Frag<3> split(f32x4 lo, f32x4 hi) {
