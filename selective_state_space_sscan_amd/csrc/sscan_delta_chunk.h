@@ -60,6 +60,59 @@ struct BytesAhead {
   }
 };
 
+// A wave's sixteen columns of V of a chunk, in the accumulator layout.  bf16: a row of
+// them is 32 bytes, lane = token loads them whole, and the wave turns them around in 2 KB
+// of LDS of its own (against sixteen 2-byte loads a lane: 0.7 us less a chunk of eight
+// waves).  float32: each lane loads its own elements.
+template <typename IO>
+struct ColumnsAhead {
+  static constexpr int kLds = 16;
+  IO x[4][4];
+
+  __device__ __forceinline__ void load(Buffer rows, int64_t stride, int col0, int dv, bool) {
+    const int i = lane_id() & 15, qd = lane_id() >> 4;
+    const int at = here(col0 + i < dv ? (8 * qd * int(stride) + col0 + i) * int(sizeof(IO)) : kOutside);
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        load1(rows, at + (32 * (m >> 1) + 4 * (m & 1) + r) * int(stride) * int(sizeof(IO)), &x[m][r]);
+  }
+
+  __device__ __forceinline__ void get(char*, f32x4 (&v)[4]) const {
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[m][r] = to_f32(x[m][r]);
+  }
+};
+
+template <>
+struct ColumnsAhead<bf16> {
+  static constexpr int kLds = kC * 16 * 2;  // bytes a wave
+  bf16x8 x[2];
+
+  __device__ __forceinline__ void load(Buffer rows, int64_t stride, int col0, int dv, bool wide) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      load8<bf16>(rows, (lane_id() * int(stride) + col0 + 8 * n) * 2, dv - col0 - 8 * n, wide, &x[n]);
+  }
+
+  __device__ __forceinline__ void get(char* own, f32x4 (&v)[4]) const {
+    const int lane = lane_id(), i = lane & 15, qd = lane >> 4;
+    bf16* tile = reinterpret_cast<bf16*>(own);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) *reinterpret_cast<bf16x8*>(tile + 16 * lane + 8 * n) = x[n];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int row = 32 * (m >> 1) + 8 * qd + 4 * (m & 1) + (i >> 2);
+      v[m] = __builtin_convertvector(read_tr(tile + 16 * row + 4 * (i & 3)), f32x4);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+};
+
 // LDS of a walk: per chunk the K tile, the Q tile, the fragments of two triangular
 // matrices and the per-token factors.  bf16: two sets, the next chunk's being filled
 // while one is read (one barrier a chunk); float32 has room for one (two barriers).
@@ -84,11 +137,12 @@ template <typename IO, int KP, int W, bool STATES>
 __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nchunk, int nvb, const char* frag_t,
                                                              const char* frag_p, const float* vec, float* states,
                                                              float* values, int dvp, int wide) {
-  constexpr int N = Io<IO>::kN, NO = Io<IO>::kOutTerms, kThreads = 64 * W;
+  constexpr int N = Io<IO>::kN, NO = Io<IO>::kOutTerms, kThreads = 64 * W, kRing = N == 1 ? 5 : 2;
   constexpr int kTiles = KP / 16, kSteps = KP / 32, kVecs = STATES ? kVecFloatsBwd : kVecFloats;
   typedef Tile<KP> TileK;
   typedef WalkLds<IO, KP, !STATES, NO, kVecFloats> Lds;
   __shared__ __attribute__((aligned(256))) char lds[Lds::kSets * Lds::kSet];
+  __shared__ __attribute__((aligned(16))) char lds_v[W * ColumnsAhead<IO>::kLds];
 
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, i = lane & 15, qd = lane >> 4;
   const int64_t bh = int64_t(blockIdx.x) / nvb, b = bh / a.hv;
@@ -101,12 +155,11 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
   const IO* vp = static_cast<const IO*>(a.v) + b * a.sv.b + h * a.sv.h;
   IO* op = static_cast<IO*>(a.out) + (b * a.len * a.hv + h) * a.dv;
   const int64_t out_t = int64_t(a.hv) * a.dv;
-  const bool wide_qk = wide & 1, live_col = col < a.dv;
-  // byte offset of this lane's first token (8 qd) and column in a chunk's rows, and the
-  // rows from there to token 32 (m >> 1) + 4 (m & 1) + r
-  const int v_lane = live_col ? (8 * qd * int(a.sv.t) + col) * int(sizeof(IO)) : kOutside;
+  const bool wide_qk = wide & 1, wide_v = wide & 2, live_col = col < a.dv;
+  // byte offset of this lane's first token (8 qd) and column in a chunk's output rows; its
+  // other tokens are 32 (m >> 1) + 4 (m & 1) + r rows on
   const int o_lane = live_col ? (8 * qd * int(out_t) + col) * int(sizeof(IO)) : kOutside;
-  const int v_row = int(a.sv.t) * int(sizeof(IO)), o_row = int(out_t) * int(sizeof(IO));
+  const int o_row = int(out_t) * int(sizeof(IO));
   // this lane's elements in a tile: rows by contraction step, columns by pairs of tiles
   int at_row[kSteps], at_col[kSteps];
 #pragma unroll
@@ -125,18 +178,13 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
   RowsAhead<IO, KP, kThreads> next_k, next_q;
   BytesAhead<Lds::kBytesT, kThreads> next_t;
   BytesAhead<Lds::kBytesP, kThreads> next_p;
-  IO next_v[4][4];
+  ColumnsAhead<IO> next_v;
   f32x4 next_vec = {};
   const auto load_rows = [&](int c) {
     const int t0 = c * kC;
     next_k.load(kp, a.sk.t, t0, Lb, a.dk, wide_qk);
     if constexpr (!STATES) next_q.load(qp, a.sq.t, t0, Lb, a.dk, wide_qk);
-    const Buffer rows = rows_of(vp + t0 * a.sv.t, Lb - t0 < kC ? Lb - t0 : kC, a.sv.t, a.dv);
-    const int at = here(v_lane);
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) load1(rows, at + (32 * (m >> 1) + 4 * (m & 1) + r) * v_row, &next_v[m][r]);
+    next_v.load(rows_of(vp + t0 * a.sv.t, Lb - t0 < kC ? Lb - t0 : kC, a.sv.t, a.dv), a.sv.t, col - i, a.dv, wide_v);
   };
   const auto load_frags = [&](int c) {
     const int64_t idx = bh * nchunk + c;
@@ -168,10 +216,7 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
     const char* set = lds + (Lds::kSets == 2 ? (c & 1) * Lds::kSet : 0);
     char* other = lds + (Lds::kSets == 2 ? (~c & 1) * Lds::kSet : 0);
     f32x4 x[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[m][r] = to_f32(next_v[m][r]);
+    next_v.get(lds_v + wave * ColumnsAhead<IO>::kLds, x);
     __syncthreads();
     if (Lds::kSets == 1) {
       store_rows(lds);
@@ -188,64 +233,69 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
     const char *st = set + Lds::kT + lane * 16, *sp = set + Lds::kP + lane * 16;
     const float* svec = reinterpret_cast<const float*>(set + Lds::kVec);
 
+    // fragments of rows of K and Q, in the order of the products
+    struct Rows {
+      Frag<N> k, q;
+    };
+    const auto read_rows = [&](int j, Rows& f) {
+      const int at = chained(j / kSteps, 0) * KP + at_row[j % kSteps];
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        f.k.t[n] = row_frag(sk + n * TileK::kElems + at);
+        if constexpr (!STATES) f.q.t[n] = row_frag(sq + n * TileK::kElems + at);
+      }
+    };
+    constexpr int kRingT = 4;
+    const auto read_t = [&](int j, Frag<3>& f) {
+#pragma unroll
+      for (int n = 0; n < 3; ++n) f.t[n] = *reinterpret_cast<const bf16x8*>(st + (j * 3 + n) * kFragBytes);
+    };
+    const auto read_p = [&](int j, Frag<NO>& f) {
+#pragma unroll
+      for (int n = 0; n < NO; ++n) f.t[n] = *reinterpret_cast<const bf16x8*>(sp + (j * NO + n) * kFragBytes);
+    };
+    const auto read_cols = [&](int j, Frag<N>& f) {
+      const int m = j >> 1, s = j & 1;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        f.t[n] = col_frag(sk + n * TileK::kElems + 32 * s * KP + at_col[m >> 1] + 4 * (m & 1), KP);
+    };
+
+    // x = v - c (K S), o = e (Q S), per tile of sixteen tokens in chained order
+    Rows rows_ring[kRing];
+    ring_start<4 * kSteps>(rows_ring, read_rows);
     Frag<3> sf[kSteps];
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) sf[s] = split(S[2 * s], S[2 * s + 1]);
-    // x = v - c (K S), o = e (Q S), per tile of sixteen tokens in chained order
-    f32x4 o[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      f32x4 ks = {}, qs = {};
-      const int row = chained(m, 0) * KP;
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        Frag<N> fk, fq;
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          fk.t[n] = row_frag(sk + n * TileK::kElems + row + at_row[s]);
-          if constexpr (!STATES) fq.t[n] = row_frag(sq + n * TileK::kElems + row + at_row[s]);
-        }
-        ks = mul(fk, sf[s], ks);
-        if constexpr (!STATES) qs = mul<NO>(fq, sf[s], qs);
+    f32x4 o[4] = {}, ks = {};
+    ring_run<4 * kSteps>(rows_ring, read_rows, [&](int j, const Rows& f) {
+      const int m = j / kSteps, s = j % kSteps, tok = chained(m, 4 * qd);
+      ks = mul(f.k, sf[s], s == 0 ? f32x4{} : ks);
+      if constexpr (!STATES) o[m] = mul<NO>(f.q, sf[s], o[m]);
+      if (s == kSteps - 1) {
+        x[m] -= *reinterpret_cast<const f32x4*>(&svec[tok]) * ks;
+        if constexpr (!STATES) o[m] *= *reinterpret_cast<const f32x4*>(&svec[2 * kC + tok]);
       }
-      const int tok = chained(m, 4 * qd);
-      x[m] -= *reinterpret_cast<const f32x4*>(&svec[tok]) * ks;
-      o[m] = *reinterpret_cast<const f32x4*>(&svec[2 * kC + tok]) * qs;
-    }
+    });
+    Frag<3> t_ring[kRingT];
+    ring_start<kFrags>(t_ring, read_t);
     if (Lds::kSets == 2 && more) {
       store_rows(other);
       load_frags(c + 1);
     }
     // u = (T diag(beta)) x
     const Frag<3> xf[2] = {split(x[0], x[1]), split(x[2], x[3])};
-    f32x4 u[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      u[m] = f32x4{};
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (lower_frag(m, s) < 0) continue;
-        Frag<3> ft;
-#pragma unroll
-        for (int n = 0; n < 3; ++n)
-          ft.t[n] = *reinterpret_cast<const bf16x8*>(st + (lower_frag(m, s) * 3 + n) * kFragBytes);
-        u[m] = mul(ft, xf[s], u[m]);
-      }
-    }
+    f32x4 u[4] = {};
+    ring_run<kFrags>(t_ring, read_t,
+                     [&](int j, const Frag<3>& f) { u[lower_m(j)] = mul(f, xf[lower_s(j)], u[lower_m(j)]); });
     // o += P u
     if constexpr (!STATES) {
+      Frag<NO> p_ring[kRingT];
+      ring_start<kFrags>(p_ring, read_p);
       const Frag<3> uf[2] = {split(u[0], u[1]), split(u[2], u[3])};
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (lower_frag(m, s) < 0) continue;
-          Frag<NO> fp;
-#pragma unroll
-          for (int n = 0; n < NO; ++n)
-            fp.t[n] = *reinterpret_cast<const bf16x8*>(sp + (lower_frag(m, s) * NO + n) * kFragBytes);
-          o[m] = mul<NO>(fp, uf[s], o[m]);
-        }
+      ring_run<kFrags>(p_ring, read_p, [&](int j, const Frag<NO>& f) {
+        o[lower_m(j)] = mul<NO>(f, uf[lower_s(j)], o[lower_m(j)]);
+      });
       const Buffer rows = rows_of(op + t0 * out_t, L - t0 < kC ? L - t0 : kC, out_t, a.dv);
       const int at = here(o_lane);
 #pragma unroll
@@ -256,22 +306,15 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
       store_state(buffer_of(values + idx * kC * dvp, kC * dvp * 4), w_lane, dvp, u);
     }
     // S = last S + K^T (d u)
+    Frag<N> c_ring[kRing];
+    ring_start<2 * kTiles>(c_ring, read_cols);
 #pragma unroll
     for (int m = 0; m < 4; ++m) u[m] *= *reinterpret_cast<const f32x4*>(&svec[kC + chained(m, 4 * qd)]);
     const Frag<3> df[2] = {split(u[0], u[1]), split(u[2], u[3])};
     const float last = svec[3 * kC];
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m) {
-      S[m] *= last;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        Frag<N> fk;
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-          fk.t[n] = col_frag(sk + n * TileK::kElems + 32 * s * KP + at_col[m >> 1] + 4 * (m & 1), KP);
-        S[m] = mul(fk, df[s], S[m]);
-      }
-    }
+    for (int m = 0; m < kTiles; ++m) S[m] *= last;
+    ring_run<2 * kTiles>(c_ring, read_cols, [&](int j, const Frag<N>& f) { S[j >> 1] = mul(f, df[j & 1], S[j >> 1]); });
     if (Lds::kSets == 2 && more) store_frags(other);
   }
   if constexpr (STATES) return;

@@ -286,6 +286,33 @@ __device__ __forceinline__ bf16x8 col_frag(const bf16* tile, int r0, int col4) {
 
 __device__ __forceinline__ bf16x8 row_frag(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
 
+// A sequence of J products whose fragments come from LDS through a ring of R sets: a
+// set is read R - 1 products before it is used, since one read takes as long as several
+// products.  load(j, set) reads, use(j, set) multiplies; the barrier keeps the compiler
+// from moving LDS reads back to their uses.
+template <int J, int R, typename Set, typename Load>
+__device__ __forceinline__ void ring_start(Set (&ring)[R], Load load) {
+#pragma unroll
+  for (int j = 0; j < R - 1 && j < J; ++j) load(j, ring[j]);
+  __builtin_amdgcn_sched_barrier(0x7f);
+}
+
+template <int J, int R, typename Set, typename Load, typename Use>
+__device__ __forceinline__ void ring_run(Set (&ring)[R], Load load, Use use) {
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    if (j + R - 1 < J) load(j + R - 1, ring[(j + R - 1) % R]);
+    __builtin_amdgcn_sched_barrier(0x7f);
+    use(j, ring[j % R]);
+  }
+}
+
+// The j-th non-zero fragment of a lower (upper) triangular matrix: tile and step.
+__device__ constexpr int lower_m(int j) { return j < 2 ? j : (j + 2) >> 1; }
+__device__ constexpr int lower_s(int j) { return j < 2 ? 0 : j & 1; }
+__device__ constexpr int upper_m(int j) { return j < 4 ? j >> 1 : j - 2; }
+__device__ constexpr int upper_s(int j) { return j < 4 ? j & 1 : 1; }
+
 __device__ __forceinline__ int row_len(const int32_t* lengths, int64_t b, int64_t len) {
   // lengths outside 0..len are clamped; one value for the whole wave
   if (!lengths) return int(len);
