@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -75,6 +76,13 @@ class AddNormParams(ctypes.Structure):
                 ("scale", ctypes.c_void_p), ("post_weight", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("size", ctypes.c_int64), ("eps", ctypes.c_float), ("io_dtype", ctypes.c_int),
                 ("residual_dtype", ctypes.c_int)]
+
+
+# The parameter structs packed in one go: small calls are bound by the host, and a
+# ctypes.Structure of thirty fields takes several microseconds to fill.
+_DELTA = struct.Struct("7P21qfii4x")
+_GATED = struct.Struct("3P7qfiii")
+_ADD = struct.Struct("5P2qfii4x")
 
 
 _lib = None
@@ -186,7 +194,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.sscan_scan_plan.restype = I
     lib.sscan_bwd_plan.argtypes = [I64, I64, I64, I64, I, ctypes.POINTER(ctypes.c_int64)]
     lib.sscan_bwd_plan.restype = I
-    PP, GP, NP, AP = (ctypes.POINTER(c) for c in (DeltaParams, DeltaGrads, GatedNormParams, AddNormParams))
+    PP = NP = AP = V  # packed bytes, or a reference to the struct
+    GP = ctypes.POINTER(DeltaGrads)
     lib.sscan_delta_fwd.argtypes = [PP, V, V, V, V, SZ]
     lib.sscan_delta_step.argtypes = [PP, V, V, V]
     lib.sscan_delta_bwd.argtypes = [PP, V, V, GP, V, V, SZ]
@@ -337,7 +346,10 @@ def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]):
 
 
 def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if device.index is None:
+        return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # the handle alone, without a Stream object: 2 us less a call
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
 
 
 def fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus: bool = True, reverse: bool = False,
@@ -1095,34 +1107,58 @@ def _strided(t, name: str, device, dtype, shape, unit: bool = True):
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
-def _delta_params(what, q, k, v, g, beta, h0, lengths, scale, qk_norm):
-    """Checks the inputs of a delta call and returns (params, device)."""
+def _delta_check(what, q, k, v, g, beta, lengths, tokens: bool):
+    """Raises what is wrong with the inputs of a delta call (its fast test failed)."""
+    for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
     dev = q.device
     if dev.type != "cuda":
         raise ValueError(f"sscan.{what} needs CUDA (HIP) tensors")
     if q.dtype not in _DT_CODE:
         raise TypeError("q/k/v must be float32 or bfloat16")
-    if q.dim() != 4 or v.dim() != 4:
-        raise ValueError("q, k are [batch, len, qk_heads, dk] and v is [batch, len, v_heads, dv]")
-    b, L, hk, dk = q.shape
-    hv, dv = v.shape[2:]
+    if q.dim() != 3 + tokens or v.dim() != 3 + tokens:
+        raise ValueError("q, k are [batch, len, qk_heads, dk] and v is [batch, len, v_heads, dv]" if tokens else
+                         "q, k are [batch, qk_heads, dk] and v is [batch, v_heads, dv]")
+    lead, (hk, dk), (hv, dv) = q.shape[:-2], q.shape[-2:], v.shape[-2:]
     if hv % max(hk, 1) or (hk == 0) != (hv == 0):
         raise ValueError(f"v_heads ({hv}) must be a multiple of qk_heads ({hk})")
-    _strided(q, "q", dev, q.dtype, (b, L, hk, dk))
-    _strided(k, "k", dev, q.dtype, (b, L, hk, dk))
-    _strided(v, "v", dev, q.dtype, (b, L, hv, dv))
-    _strided(g, "g", dev, torch.float32, (b, L, hv), unit=False)
-    _strided(beta, "beta", dev, torch.float32, (b, L, hv), unit=False)
-    _check(h0, "h0", dev, torch.float32, (b, hv, dk, dv))
-    _check(lengths, "lengths", dev, torch.int32, (b,))
+    _strided(q, "q", dev, q.dtype, (*lead, hk, dk))
+    _strided(k, "k", dev, q.dtype, (*lead, hk, dk))
+    _strided(v, "v", dev, q.dtype, (*lead, hv, dv))
+    _strided(g, "g", dev, torch.float32, (*lead, hv), unit=False)
+    _strided(beta, "beta", dev, torch.float32, (*lead, hv), unit=False)
+    _check(lengths, "lengths", dev, torch.int32, (q.shape[0],))
+
+
+def _delta_pack(what, q, k, v, g, beta, h0, lengths, scale, qk_norm, tokens: bool = True):
+    """Checks the inputs of a delta call; (packed params, device, sizes (b, L, hk, hv, dk, dv), dtype code)."""
+    qs, vs, dt, di = q.shape, v.shape, q.dtype, q.get_device()
+    qt, kt, vt, gt, bt = q.stride(), k.stride(), v.stride(), g.stride(), beta.stride()
+    code = _DT_CODE.get(dt)
+    # one test of everything that is wrong only in a wrong call; _delta_check says what
+    if not (code is not None and di >= 0 and len(qs) == 3 + tokens and k.shape == qs and len(vs) == len(qs)
+            and vs[:-2] == qs[:-2] and g.shape == vs[:-1] and beta.shape == g.shape and k.dtype == dt
+            and v.dtype == dt and g.dtype == torch.float32 and beta.dtype == torch.float32
+            and k.get_device() == di and v.get_device() == di and g.get_device() == di and beta.get_device() == di
+            and qt[-1] == 1 and kt[-1] == 1 and vt[-1] == 1 and lengths is None and qs[-2] and not vs[-2] % qs[-2]):
+        _delta_check(what, q, k, v, g, beta, lengths, tokens)
+    dev = q.device
+    if tokens:
+        b, L, hk, dk = qs
+        strides = (*qt[:3], *kt[:3], *vt[:3], *gt, *bt)
+    else:
+        (b, hk, dk), L = qs, 1
+        strides = (qt[0], 0, qt[1], kt[0], 0, kt[1], vt[0], 0, vt[1], gt[0], 0, gt[1], bt[0], 0, bt[1])
+    hv, dv = vs[-2:]
+    if h0 is not None:
+        _check(h0, "h0", dev, torch.float32, (b, hv, dk, dv))
     if scale is None:
-        scale = float(dk) ** -0.5 if dk else 1.0
-    I3 = ctypes.c_int64 * 3
-    p = DeltaParams(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                    None if lengths is None else lengths.data_ptr(), None if h0 is None else h0.data_ptr(),
-                    I3(*q.stride()[:3]), I3(*k.stride()[:3]), I3(*v.stride()[:3]), I3(*g.stride()),
-                    I3(*beta.stride()), b, L, hk, hv, dk, dv, scale, int(bool(qk_norm)), _DT_CODE[q.dtype])
-    return p, dev
+        scale = dk ** -0.5 if dk else 1.0
+    p = _DELTA.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                    0 if lengths is None else lengths.data_ptr(), 0 if h0 is None else h0.data_ptr(), *strides,
+                    b, L, hk, hv, dk, dv, scale, 1 if qk_norm else 0, code)
+    return p, dev, (b, L, hk, hv, dk, dv), code
 
 
 def delta_workspace_bytes(batch: int, length: int, qk_heads: int, v_heads: int, dk: int, dv: int,
@@ -1141,19 +1177,19 @@ def delta_fwd(q, k, v, g, beta, h0: Optional[torch.Tensor] = None, lengths: Opti
     contiguous.  h0: [batch, v_heads, dk, dv] f32; lengths: int32 [batch].  scale
     defaults to dk ** -0.5.  Returns (out, h_last); h_last may be given as h0."""
     lib = load_library()
-    p, dev = _delta_params("delta_fwd", q, k, v, g, beta, h0, lengths, scale, qk_norm)
-    b, L, hk, dk = q.shape
-    hv, dv = v.shape[2:]
+    p, dev, (b, L, hk, hv, dk, dv), code = _delta_pack("delta_fwd", q, k, v, g, beta, h0, lengths, scale, qk_norm)
     if out is None:
         out = torch.empty((b, L, hv, dv), dtype=q.dtype, device=dev)
-    _check(out, "out", dev, q.dtype, (b, L, hv, dv))
+    else:
+        _check(out, "out", dev, q.dtype, (b, L, hv, dv))
     if h_last is None:
         h_last = torch.empty((b, hv, dk, dv), dtype=torch.float32, device=dev)
-    _check(h_last, "h_last", dev, torch.float32, (b, hv, dk, dv))
+    else:
+        _check(h_last, "h_last", dev, torch.float32, (b, hv, dk, dv))
     if b * hv == 0:
         return out, h_last
-    ws, ws_bytes = _workspace(lib.sscan_delta_workspace_bytes(b, L, hk, hv, dk, dv, p.io_dtype), dev, workspace)
-    st = lib.sscan_delta_fwd(ctypes.byref(p), _ptr(out), _ptr(h_last), _stream(dev), _ptr(ws), ws_bytes)
+    ws, ws_bytes = _workspace(lib.sscan_delta_workspace_bytes(b, L, hk, hv, dk, dv, code), dev, workspace)
+    st = lib.sscan_delta_fwd(p, out.data_ptr(), h_last.data_ptr(), _stream(dev), _ptr(ws), ws_bytes)
     if st != 0:
         raise SScanError(st, "sscan_delta_fwd")
     return out, h_last
@@ -1166,22 +1202,18 @@ def delta_step(state, q, k, v, g, beta, lengths: Optional[torch.Tensor] = None, 
     v_heads, dv]; g, beta: [batch, v_heads] f32.  Rows of ``lengths`` 0 keep their
     state and answer 0.  Returns [batch, v_heads, dv] in q's dtype."""
     lib = load_library()
-    for name, t, n in (("q", q, 3), ("k", k, 3), ("v", v, 3), ("g", g, 2), ("beta", beta, 2)):
-        if t.dim() != n:
-            raise ValueError(f"{name} must have {n} dimensions for one token")
-    p, dev = _delta_params("delta_step", q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), g.unsqueeze(1),
-                           beta.unsqueeze(1), None, lengths, scale, qk_norm)
-    b, hk, dk = q.shape
-    hv, dv = v.shape[1:]
+    p, dev, (b, _, hk, hv, dk, dv), code = _delta_pack("delta_step", q, k, v, g, beta, None, lengths, scale, qk_norm,
+                                                       tokens=False)
     if state is None:
         raise ValueError("state is required")
     _check(state, "state", dev, torch.float32, (b, hv, dk, dv))
     if out is None:
         out = torch.empty((b, hv, dv), dtype=q.dtype, device=dev)
-    _check(out, "out", dev, q.dtype, (b, hv, dv))
+    else:
+        _check(out, "out", dev, q.dtype, (b, hv, dv))
     if b * hv == 0:
         return out
-    st = lib.sscan_delta_step(ctypes.byref(p), _ptr(state), _ptr(out), _stream(dev))
+    st = lib.sscan_delta_step(p, state.data_ptr(), out.data_ptr(), _stream(dev))
     if st != 0:
         raise SScanError(st, "sscan_delta_step")
     return out
@@ -1194,9 +1226,7 @@ def delta_bwd(q, k, v, g, beta, dout, h0: Optional[torch.Tensor] = None, dh_last
     sum(dout * out) + sum(dh_last * h_last) as {"dq", "dk", "dv" (q's dtype), "dg",
     "dbeta", "dh0" (f32)}, contiguous; the states are recomputed."""
     lib = load_library()
-    p, dev = _delta_params("delta_bwd", q, k, v, g, beta, h0, lengths, scale, qk_norm)
-    b, L, hk, dk = q.shape
-    hv, dv = v.shape[2:]
+    p, dev, (b, L, hk, hv, dk, dv), code = _delta_pack("delta_bwd", q, k, v, g, beta, h0, lengths, scale, qk_norm)
     _check(dout, "dout", dev, q.dtype, (b, L, hv, dv))
     _check(dh_last, "dh_last", dev, torch.float32, (b, hv, dk, dv))
 
@@ -1208,9 +1238,9 @@ def delta_bwd(q, k, v, g, beta, dout, h0: Optional[torch.Tensor] = None, dh_last
              dh0=new((b, hv, dk, dv), torch.float32))
     if b * hv == 0:
         return r
-    ws, ws_bytes = _workspace(lib.sscan_delta_bwd_workspace_bytes(b, L, hk, hv, dk, dv, p.io_dtype), dev, workspace)
+    ws, ws_bytes = _workspace(lib.sscan_delta_bwd_workspace_bytes(b, L, hk, hv, dk, dv, code), dev, workspace)
     gst = DeltaGrads(*(r[n].data_ptr() for n in ("dq", "dk", "dv", "dg", "dbeta", "dh0")))
-    st = lib.sscan_delta_bwd(ctypes.byref(p), _ptr(dout), _ptr(dh_last), ctypes.byref(gst), _stream(dev), _ptr(ws),
+    st = lib.sscan_delta_bwd(p, _ptr(dout), _ptr(dh_last), ctypes.byref(gst), _stream(dev), _ptr(ws),
                              ws_bytes)
     if st != 0:
         raise SScanError(st, "sscan_delta_bwd")
@@ -1245,35 +1275,44 @@ def gated_delta(q, k, v, g, beta, h0: Optional[torch.Tensor] = None, lengths: Op
 # ---- RMS norms around a mixer -----------------------------------------------------
 
 def _gated_params(what, x, z, weight, eps, gate_first):
-    """(params, device, per_head): x and z are [..., size] or [..., heads, size]; all
+    """(packed params, device, (rows, heads, size)): x and z are [..., size] or [..., heads, size]; all
     leading dimensions but the last one (the heads, where there are two or more)
     collapse to rows."""
-    dev = x.device
+    dev, xs, dt = x.device, x.shape, x.dtype
     if dev.type != "cuda":
         raise ValueError(f"sscan.{what} needs CUDA (HIP) tensors")
-    if x.dtype not in _DT_CODE:
+    if dt not in _DT_CODE:
         raise TypeError("x/z must be float32 or bfloat16")
-    if x.dim() < 1:
+    if not xs:
         raise ValueError("x needs at least one dimension")
-    size = x.shape[-1]
-    _strided(x, "x", dev, x.dtype, x.shape)
-    _strided(z, "z", dev, x.dtype, x.shape)
-    heads = x.shape[-2] if x.dim() >= 3 else 1
+    size = xs[-1]
+    _strided(x, "x", dev, dt, xs)
+    _strided(z, "z", dev, dt, xs)
+    heads = xs[-2] if len(xs) >= 3 else 1
     per_head = weight is not None and weight.dim() == 2
-    _check(weight, "weight", dev, torch.float32, (heads, size) if per_head else (size,))
-    rows = x.numel() // max(heads * size, 1) if x.numel() else 0
+    if weight is not None:
+        _check(weight, "weight", dev, torch.float32, (heads, size) if per_head else (size,))
+    n = x.numel()
+    rows = n // (heads * size) if n else 0
 
     def strides(t, name):
-        lead = [(n, s) for n, s in zip(t.shape[:-2] if t.dim() >= 3 else t.shape[:-1], t.stride()) if n > 1]
-        for (n0, s0), (n1, s1) in zip(lead, lead[1:]):
-            if s0 != n1 * s1:
+        st = t.stride()
+        keep = len(xs) - 2 if len(xs) >= 3 else len(xs) - 1
+        row = reach = None
+        for i in range(keep - 1, -1, -1):  # innermost first: each must continue the one inside
+            if xs[i] <= 1:
+                continue
+            if row is None:
+                row = st[i]
+            elif st[i] != reach:
                 raise ValueError(f"the leading dimensions of {name} must collapse to rows of one stride")
-        return (ctypes.c_int64 * 2)(lead[-1][1] if lead else 0, t.stride(-2) if t.dim() >= 3 else 0)
+            reach = st[i] * xs[i]
+        return row or 0, st[-2] if len(xs) >= 3 else 0
 
-    p = GatedNormParams(x.data_ptr(), z.data_ptr(), None if weight is None else weight.data_ptr(), strides(x, "x"),
-                        strides(z, "z"), rows, heads, size, eps, int(bool(gate_first)), int(per_head),
-                        _DT_CODE[x.dtype])
-    return p, dev
+    p = _GATED.pack(x.data_ptr(), z.data_ptr(), 0 if weight is None else weight.data_ptr(), *strides(x, "x"),
+                    *strides(z, "z"), rows, heads, size, eps, 1 if gate_first else 0, 1 if per_head else 0,
+                    _DT_CODE[dt])
+    return p, dev, (rows, heads, size)
 
 
 def gated_norm(x, z, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, gate_first: bool = False,
@@ -1283,11 +1322,12 @@ def gated_norm(x, z, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, g
     silu(z).  x, z: [..., size] or [..., heads, size] f32/bf16 (rows and heads may be
     strided); weight: [size] or [heads, size] f32.  Returns a contiguous tensor."""
     lib = load_library()
-    p, dev = _gated_params("gated_norm", x, z, weight, eps, gate_first)
+    p, dev, _ = _gated_params("gated_norm", x, z, weight, eps, gate_first)
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _check(out, "out", dev, x.dtype, x.shape)
-    st = lib.sscan_gated_norm(ctypes.byref(p), _ptr(out), _stream(dev))
+    else:
+        _check(out, "out", dev, x.dtype, x.shape)
+    st = lib.sscan_gated_norm(p, out.data_ptr(), _stream(dev))
     if st != 0:
         raise SScanError(st, "sscan_gated_norm")
     return out
@@ -1298,12 +1338,12 @@ def gated_norm_bwd(x, z, dout, weight: Optional[torch.Tensor] = None, eps: float
     """Backward pass of ``gated_norm`` (``sscan_gated_norm_bwd``): {"dx", "dz",
     "dweight" (f32, None without a weight)}."""
     lib = load_library()
-    p, dev = _gated_params("gated_norm_bwd", x, z, weight, eps, gate_first)
+    p, dev, sizes = _gated_params("gated_norm_bwd", x, z, weight, eps, gate_first)
     _check(dout, "dout", dev, x.dtype, x.shape)
     dx, dz = (torch.empty(x.shape, dtype=x.dtype, device=dev) for _ in range(2))
     dw = None if weight is None else torch.empty_like(weight)
-    ws, ws_bytes = _workspace(lib.sscan_gated_norm_bwd_workspace_bytes(p.rows, p.heads, p.size), dev, workspace)
-    st = lib.sscan_gated_norm_bwd(ctypes.byref(p), _ptr(dout), _ptr(dx), _ptr(dz), _ptr(dw), _stream(dev), _ptr(ws),
+    ws, ws_bytes = _workspace(lib.sscan_gated_norm_bwd_workspace_bytes(*sizes), dev, workspace)
+    st = lib.sscan_gated_norm_bwd(p, _ptr(dout), _ptr(dx), _ptr(dz), _ptr(dw), _stream(dev), _ptr(ws),
                                   ws_bytes)
     if st != 0:
         raise SScanError(st, "sscan_gated_norm_bwd")
@@ -1319,13 +1359,18 @@ def _add_params(what, x, residual, residual_dtype, weight, scale, post_weight, e
     if x.dim() < 1:
         raise ValueError("x needs at least one dimension")
     size = x.shape[-1]
-    _check(x, "x", dev)
-    _check(residual, "residual", dev, residual_dtype, x.shape)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if residual is not None and not (residual.dtype == residual_dtype and residual.shape == x.shape
+                                     and residual.is_contiguous() and residual.device == dev):
+        _check(residual, "residual", dev, residual_dtype, x.shape)
     for name, t in (("weight", weight), ("scale", scale), ("post_weight", post_weight)):
-        _check(t, name, dev, torch.float32, (size,))
-    addr = [None if t is None else t.data_ptr() for t in (x, residual, weight, scale, post_weight)]
+        if t is not None and not (t.dtype == torch.float32 and t.dim() == 1 and t.shape[0] == size
+                                  and t.is_contiguous() and t.device == dev):
+            _check(t, name, dev, torch.float32, (size,))
+    addr = [0 if t is None else t.data_ptr() for t in (x, residual, weight, scale, post_weight)]
     rows = x.numel() // size if size else 0
-    return AddNormParams(*addr, rows, size, eps, _DT_CODE[x.dtype], _DT_CODE[residual_dtype]), dev
+    return _ADD.pack(*addr, rows, size, eps, _DT_CODE[x.dtype], _DT_CODE[residual_dtype]), dev, (rows, size)
 
 
 def add_norm(x, residual: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
@@ -1340,14 +1385,16 @@ def add_norm(x, residual: Optional[torch.Tensor] = None, weight: Optional[torch.
     lib = load_library()
     if residual_dtype is None:
         residual_dtype = x.dtype if residual is None else residual.dtype
-    p, dev = _add_params("add_norm", x, residual, residual_dtype, weight, scale, post_weight, eps)
+    p, dev, _ = _add_params("add_norm", x, residual, residual_dtype, weight, scale, post_weight, eps)
     if out is None:
         out = torch.empty_like(x)
+    else:
+        _check(out, "out", dev, x.dtype, x.shape)
     if residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=residual_dtype, device=dev)
-    _check(out, "out", dev, x.dtype, x.shape)
-    _check(residual_out, "residual_out", dev, residual_dtype, x.shape)
-    st = lib.sscan_add_norm(ctypes.byref(p), _ptr(out), _ptr(residual_out), _stream(dev))
+        residual_out = torch.empty_like(x if residual is None else residual, dtype=residual_dtype)
+    else:
+        _check(residual_out, "residual_out", dev, residual_dtype, x.shape)
+    st = lib.sscan_add_norm(p, out.data_ptr(), residual_out.data_ptr(), _stream(dev))
     if st != 0:
         raise SScanError(st, "sscan_add_norm")
     return out, residual_out
@@ -1361,13 +1408,13 @@ def add_norm_bwd(x, residual_out, dout, weight: Optional[torch.Tensor] = None,
     {"dx", "dresidual", "dweight", "dscale", "dpost_weight"} (the last three f32, None
     for a vector that was not given)."""
     lib = load_library()
-    p, dev = _add_params("add_norm_bwd", x, residual_out, residual_out.dtype, weight, scale, post_weight, eps)
+    p, dev, sizes = _add_params("add_norm_bwd", x, residual_out, residual_out.dtype, weight, scale, post_weight, eps)
     _check(dout, "dout", dev, x.dtype, x.shape)
     _check(dresidual_out, "dresidual_out", dev, residual_out.dtype, x.shape)
     dx, dres = torch.empty_like(x), torch.empty_like(residual_out)
     dw, ds, dp = (None if t is None else torch.empty_like(t) for t in (weight, scale, post_weight))
-    ws, ws_bytes = _workspace(lib.sscan_add_norm_bwd_workspace_bytes(p.rows, p.size), dev, workspace)
-    st = lib.sscan_add_norm_bwd(ctypes.byref(p), _ptr(dout), _ptr(dresidual_out), _ptr(dx), _ptr(dres), _ptr(dw),
+    ws, ws_bytes = _workspace(lib.sscan_add_norm_bwd_workspace_bytes(*sizes), dev, workspace)
+    st = lib.sscan_add_norm_bwd(p, _ptr(dout), _ptr(dresidual_out), _ptr(dx), _ptr(dres), _ptr(dw),
                                 _ptr(ds), _ptr(dp), _stream(dev), _ptr(ws), ws_bytes)
     if st != 0:
         raise SScanError(st, "sscan_add_norm_bwd")

@@ -119,6 +119,10 @@ def test_gated_norm_of_strided_views():
     close(r["dweight"], r2["dweight"].cpu(), "dweight")
     with pytest.raises(ValueError):  # batch and token strides that no single row stride covers
         sscan.gated_norm(x.transpose(0, 1), z.transpose(0, 1), w)
+    with pytest.raises(ValueError):  # one row broadcast over an inner dimension
+        sscan.gated_norm(x[:, :1].expand(2, 9, 4, 64), z)
+    one = sscan.gated_norm(x[:1, :1].expand(2, 9, 4, 64), z)  # over all of them: rows of stride 0
+    close(one, sscan.gated_norm(x[:1, :1].expand(2, 9, 4, 64).contiguous(), z).cpu().double(), "broadcast")
     # a weight that is not 16-byte aligned
     y3 = sscan.gated_norm(x, z, torch.cat([w[:1], w])[1:])
     close(y3, y2.cpu().double(), "unaligned weight")
