@@ -125,7 +125,7 @@ hipError_t launch_walk(const DeltaArgs& a, const DeltaPlan& p, char* ws, hipStre
   char *ft = ws + p.off_t, *fp = ws + p.off_p;
   float* vec = reinterpret_cast<float*>(ws + p.off_vec);
   delta_prep_kernel<IO, KP, false>
-      <<<dim3(unsigned(a.batch * a.hk * n)), 256, 0, stream>>>(a, n, ft, fp, nullptr, vec, wide);
+      <<<dim3(unsigned(a.batch * a.hv * n)), 256, 0, stream>>>(a, n, ft, fp, nullptr, vec, wide);
   delta_chunk_kernel<IO, KP, W, false>
       <<<dim3(unsigned(a.batch * a.hv * nvb)), 64 * W, 0, stream>>>(a, n, nvb, ft, fp, vec, nullptr, nullptr, 0, wide);
   return hipGetLastError();

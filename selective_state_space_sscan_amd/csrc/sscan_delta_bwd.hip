@@ -39,7 +39,7 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_
   __shared__ __attribute__((aligned(256))) char lds[Lds::kSets * Lds::kSet];
 
   const DeltaArgs& a = b_.f;
-  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, i = lane & 15, qd = lane >> 4;
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = wave_id(), i = lane & 15, qd = lane >> 4;
   const int64_t bh = int64_t(blockIdx.x) / nvb, b = bh / a.hv;
   const int h = int(bh % a.hv), hq = h / (a.hv / a.hk);
   const int col = int(int64_t(blockIdx.x) % nvb) * (16 * W) + 16 * wave + i;
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs b_, int nc
   __shared__ float sdot[4][4][kC], sxv[kC], sse[4];
 
   const DeltaArgs& a = b_.f;
-  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, i = lane & 15, qd = lane >> 4;
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = wave_id(), i = lane & 15, qd = lane >> 4;
   const int c = int(blockIdx.x % unsigned(nchunk));
   const int64_t bhk = blockIdx.x / unsigned(nchunk), b = bhk / a.hk;
   const int hq = int(bhk % a.hk), share = a.hv / a.hk;
@@ -584,7 +584,7 @@ hipError_t launch_bwd(const DeltaBwdArgs& b, const DeltaBwdPlan& p, char* ws, hi
         *e = reinterpret_cast<float*>(ws + p.off_ds);
   const dim3 per_key{unsigned(a.batch * a.hk * n)}, walk{unsigned(a.batch * a.hv * nvb)};
   if (n > 0) {
-    delta_prep_kernel<IO, KP, true><<<per_key, 256, 0, stream>>>(a, n, ft, fpt, ftt, vec, wide);
+    delta_prep_kernel<IO, KP, true><<<dim3(unsigned(a.batch * a.hv * n)), 256, 0, stream>>>(a, n, ft, fpt, ftt, vec, wide);
     delta_chunk_kernel<IO, KP, W, true><<<walk, 64 * W, 0, stream>>>(a, n, nvb, ft, nullptr, vec, s, u, p.dvp, wide);
   }
   delta_chunk_bwd_kernel<IO, KP, W><<<walk, 64 * W, 0, stream>>>(b, n, nvb, ftt, fpt, vec, e, x, p.dvp, wide);

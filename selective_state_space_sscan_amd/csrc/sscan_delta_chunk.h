@@ -144,7 +144,7 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
   __shared__ __attribute__((aligned(256))) char lds[Lds::kSets * Lds::kSet];
   __shared__ __attribute__((aligned(16))) char lds_v[W * ColumnsAhead<IO>::kLds];
 
-  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, i = lane & 15, qd = lane >> 4;
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = wave_id(), i = lane & 15, qd = lane >> 4;
   const int64_t bh = int64_t(blockIdx.x) / nvb, b = bh / a.hv;
   const int h = int(bh % a.hv), hq = h / (a.hv / a.hk);
   const int col = int(int64_t(blockIdx.x) % nvb) * (16 * W) + 16 * wave + i;

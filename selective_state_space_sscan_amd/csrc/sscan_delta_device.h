@@ -98,6 +98,8 @@ __device__ constexpr int lower_frag(int m, int s) { return m < 2 ? (s == 0 ? m :
 __device__ constexpr int upper_frag(int m, int s) { return m < 2 ? 2 * m + s : (s == 1 ? m + 2 : -1); }
 
 __device__ __forceinline__ int lane_id() { return int(threadIdx.x) & 63; }
+// In a scalar register, so that what depends on it branches without masks.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6); }
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T x) {

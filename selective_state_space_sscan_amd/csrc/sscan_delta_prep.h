@@ -12,6 +12,11 @@ namespace delta {
 
 constexpr int kLdM = 68;  // floats between rows of a 64 x 64 LDS matrix
 
+__device__ __forceinline__ f32x8 read8(const float* p) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
 // c + M[r0.., c0..] b for 16 x 16 blocks in float32, b in the result layout.
 __device__ __forceinline__ f32x4 block_mul(const float* M, int r0, int c0, f32x4 b, f32x4 c) {
   const int i = lane_id() & 15, qd = lane_id() >> 4;
@@ -41,14 +46,20 @@ __device__ __forceinline__ void block_write(float* M, int r0, int c0, f32x4 b) {
 // T_ij = -T_ii (sum_{j <= k < i} A_ik T_kj), 32-row halves last.
 __device__ __forceinline__ void invert_unit_lower(float* M, int wave) {
   const int i = lane_id() & 15, qd = lane_id() >> 4, d0 = 16 * wave;
-  float t[16];  // column i of the block's inverse
+  // column i of the block's inverse; a row's coefficients are the same in every lane,
+  // and a value is subtracted from all later rows as soon as it is known
+  float t[16];
+  f32x4 row[16][4];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    float x = r == i ? 1.0f : 0.0f;
+  for (int r = 1; r < 16; ++r)
 #pragma unroll
-    for (int k = 0; k < r; ++k) x -= M[(d0 + r) * kLdM + d0 + k] * t[k];
-    t[r] = x;
-  }
+    for (int k = 0; k < r; k += 4) row[r][k / 4] = *reinterpret_cast<const f32x4*>(&M[(d0 + r) * kLdM + d0 + k]);
+#pragma unroll
+  for (int r = 0; r < 16; ++r) t[r] = r == i ? 1.0f : 0.0f;
+#pragma unroll
+  for (int k = 0; k < 15; ++k)
+#pragma unroll
+    for (int r = k + 1; r < 16; ++r) t[r] -= row[r][k / 4][k % 4] * t[k];
   // all of this wave's reads of its block come before its writes (one wave, in order)
   __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -63,7 +74,9 @@ __device__ __forceinline__ void invert_unit_lower(float* M, int wave) {
   __syncthreads();
   const int I = 2 + (wave >> 1), J = wave & 1;
   f32x4 y2 = {}, y3 = {};
-  for (int k = J; k < 2; ++k) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (k < J) continue;
     const f32x4 t_kj = block_read(M, 16 * k, 16 * J);
     y2 = block_mul(M, 32, 16 * k, t_kj, y2);
     if (I == 3) y3 = block_mul(M, 48, 16 * k, t_kj, y3);
@@ -75,135 +88,177 @@ __device__ __forceinline__ void invert_unit_lower(float* M, int wave) {
   __syncthreads();
 }
 
+// x of another lane by a DPP control; 0 where the control names none.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double dpp(double x) {
+  const uint64_t w = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(w), kCtrl, kRows, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(w >> 32), kCtrl, kRows, 0xf, false);
+  return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+
 // Inclusive sum over the wave's 64 lanes in double: decays are exponentials of
 // differences of these sums, which float32 sums of large negative g would lose.
 __device__ __forceinline__ double wave_running_sum(double x) {
-  const int lane = lane_id();
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) {
-    const double y = __shfl_up(x, m);
-    if (lane >= m) x += y;
-  }
+  x += dpp<0x111, 0xf>(x);  // row_shr 1, 2, 4, 8
+  x += dpp<0x112, 0xf>(x);
+  x += dpp<0x114, 0xf>(x);
+  x += dpp<0x118, 0xf>(x);
+  x += dpp<0x142, 0xa>(x);  // lane 15 of the row before, into rows 1 and 3
+  x += dpp<0x143, 0xc>(x);  // lane 31, into rows 2 and 3
   return x;
 }
 
-// One block per (batch row, key head, chunk); the value heads that share the key head
-// reuse its K K^T and Q K^T.  BWD: the transposed fragments as well, three terms each.
+__device__ __forceinline__ double lane_of(double x, int lane) {
+  const uint64_t w = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane(int(w), lane), hi = __builtin_amdgcn_readlane(int(w >> 32), lane);
+  return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+
+// One block per (batch row, value head, chunk).  Wave w computes rows 16 w .. + 15 of
+// K K^T and Q K^T against the tokens up to them.  The decay of a pair in one tile of
+// sixteen is its own exponential; of a pair in two tiles the product of two, through the
+// last token of the earlier tile, both at most 1 (for g <= 0) and never smaller than the
+// product: seven exponentials a lane instead of thirty-two.  BWD: T, T^T and P^T.
 template <typename IO, int KP, bool BWD>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int nchunk, char* frag_t, char* frag_p,
                                                          char* frag_tt, float* vec, int wide) {
   constexpr int N = Io<IO>::kN, NP = BWD ? 3 : Io<IO>::kOutTerms, kSteps = KP / 32;
-  __shared__ __attribute__((aligned(16))) float kk[kC * kLdM];
-  __shared__ __attribute__((aligned(16))) float qk[kC * kLdM];
-  __shared__ __attribute__((aligned(16))) float mat[kC * kLdM];
+  __shared__ __attribute__((aligned(16))) float pmat[kC * kLdM];
+  __shared__ __attribute__((aligned(16))) float tmat[kC * kLdM];
   __shared__ double gsum[kC];
-  __shared__ float sbeta[kC], srk[kC], srq[kC];
+  __shared__ __attribute__((aligned(16))) float sbeta[kC];
+  __shared__ float srk[kC], srq[kC], from[3][kC], to_end[kC];
 
-  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, i = lane & 15, qd = lane >> 4;
+  const int tid = int(threadIdx.x), lane = tid & 63, wave = wave_id(), i = lane & 15, qd = lane >> 4;
   const int c = int(blockIdx.x % unsigned(nchunk));
-  const int64_t bhk = blockIdx.x / unsigned(nchunk);
-  const int64_t b = bhk / a.hk;
-  const int hq = int(bhk % a.hk), share = a.hv / a.hk;
+  const int64_t idx = blockIdx.x, bh = blockIdx.x / unsigned(nchunk), b = bh / a.hv;
+  const int h = int(bh % a.hv), hq = h / (a.hv / a.hk);
   const int Lb = row_len(a.lengths, b, a.len), t0 = c * kC;
   if (t0 >= Lb) return;
   const bool wide_qk = wide & 1;
-  const IO* kp = static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h;
-  const IO* qp = static_cast<const IO*>(a.q) + b * a.sq.b + hq * a.sq.h;
+  const int rows = Lb - t0 < kC ? Lb - t0 : kC;
+  const Buffer kb = rows_of(static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h + t0 * a.sk.t, rows, a.sk.t, a.dk);
+  const Buffer qb = rows_of(static_cast<const IO*>(a.q) + b * a.sq.b + hq * a.sq.h + t0 * a.sq.t, rows, a.sq.t, a.dk);
 
-  // K K^T and Q K^T: wave w takes tokens 16 w .. 16 w + 15 against all earlier ones
+  typename Io<IO>::V8 xk[kSteps], xq[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int d8 = 32 * s + 8 * qd, row = 16 * wave + i;
+    load8<IO>(kb, (row * int(a.sk.t) + d8) * int(sizeof(IO)), a.dk - d8, wide_qk, &xk[s]);
+    load8<IO>(qb, (row * int(a.sq.t) + d8) * int(sizeof(IO)), a.dk - d8, wide_qk, &xq[s]);
+  }
+  // every wave has all tokens' running sums of g, and computes one of the tables
+  const int t = t0 + lane;
+  float g = 0.0f, beta = 0.0f;
+  if (t < Lb) {
+    g = clamp_decay(a.g[b * a.sg.b + t * a.sg.t + h * a.sg.h]);
+    beta = a.beta[b * a.sb.b + t * a.sb.t + h * a.sb.h];
+  }
+  const double sum = wave_running_sum(double(g));
+  if (wave < 3) {
+    const double ref = lane_of(sum, 16 * wave + 15);
+    from[wave][lane] = lane > 16 * wave + 15 ? expf(float(sum - ref)) : 0.0f;
+  } else {
+    const double ref = lane < 16 ? lane_of(sum, 15) : lane < 32 ? lane_of(sum, 31) : lane < 48 ? lane_of(sum, 47)
+                                                                                              : lane_of(sum, 63);
+    to_end[lane] = expf(float(ref - sum));
+    gsum[lane] = sum;
+    sbeta[lane] = beta;
+  }
+
+  f32x4 kk[4], qk[4];
   {
-    const int tok = t0 + 16 * wave + i;
-    const bool in = tok < Lb;
     Frag<N> fk[kSteps], fq[kSteps];
     float ssq = 0.0f;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const int d8 = 32 * s + 8 * qd;
-      fk[s] = as_frag(load8(kp + tok * a.sk.t + d8, in ? a.dk - d8 : 0, wide_qk));
-      const auto q8 = load8(qp + tok * a.sq.t + d8, in ? a.dk - d8 : 0, wide_qk);
-      fq[s] = as_frag(q8);
+      fk[s] = as_frag(xk[s]);
+      fq[s] = as_frag(xq[s]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ssq += to_f32(q8[j]) * to_f32(q8[j]);
+      for (int j = 0; j < 8; ++j) ssq += to_f32(xq[s][j]) * to_f32(xq[s][j]);
     }
     ssq += __shfl_xor(ssq, 16);
     ssq += __shfl_xor(ssq, 32);
     if (qd == 0) srq[16 * wave + i] = a.qk_norm ? 1.0f / sqrtf(ssq + 1e-6f) : 1.0f;
-    for (int ct = 0; ct <= wave; ++ct) {
-      const int tc = t0 + 16 * ct + i;
-      f32x4 xk = {}, xq = {};
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) {
+      kk[ct] = qk[ct] = f32x4{};
+      if (ct > wave) continue;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const int d8 = 32 * s + 8 * qd;
-        const auto fb = as_frag(load8(kp + tc * a.sk.t + d8, tc < Lb ? a.dk - d8 : 0, wide_qk));
-        xk = mul(fk[s], fb, xk);
-        xq = mul(fq[s], fb, xq);
+        Frag<N> fb = fk[s];
+        if (ct != wave) {
+          const int d8 = 32 * s + 8 * qd;
+          typename Io<IO>::V8 x;
+          load8<IO>(kb, ((16 * ct + i) * int(a.sk.t) + d8) * int(sizeof(IO)), a.dk - d8, wide_qk, &x);
+          fb = as_frag(x);
+        }
+        kk[ct] = mul(fk[s], fb, kk[ct]);
+        qk[ct] = mul(fq[s], fb, qk[ct]);
       }
-      block_write(kk, 16 * wave, 16 * ct, xk);
-      block_write(qk, 16 * wave, 16 * ct, xq);
+      if (ct == wave) {  // the diagonal holds the keys' squares
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (4 * qd + r == i) srk[16 * wave + i] = a.qk_norm ? 1.0f / sqrtf(kk[ct][r] + 1e-6f) : 1.0f;
+      }
     }
   }
   __syncthreads();
-  if (tid < kC) srk[tid] = a.qk_norm ? 1.0f / sqrtf(kk[tid * kLdM + tid] + 1e-6f) : 1.0f;
-
-  for (int hh = 0; hh < share; ++hh) {
-    const int h = hq * share + hh;
-    const int64_t idx = (b * a.hv + h) * nchunk + c;
-    __syncthreads();
-    if (wave == 0) {
-      const int t = t0 + lane;
-      float g = 0.0f, beta = 0.0f;
-      if (t < Lb) {
-        g = clamp_decay(a.g[b * a.sg.b + t * a.sg.t + h * a.sg.h]);
-        beta = a.beta[b * a.sb.b + t * a.sb.t + h * a.sb.h];
-      }
-      const double sum = wave_running_sum(double(g)), end = __shfl(sum, 63);
-      gsum[lane] = sum;
-      sbeta[lane] = beta;
-      const float into = expf(float(sum)), rest = expf(float(end - sum));
-      float* v = vec + idx * (BWD ? kVecFloatsBwd : kVecFloats);
-      v[lane] = into * srk[lane];
-      v[kC + lane] = rest * srk[lane];
-      v[2 * kC + lane] = a.scale * into * srq[lane];
-      v[3 * kC + lane] = expf(float(end));
-      if constexpr (BWD) {
-        v[4 * kC + lane] = beta;
-        v[5 * kC + lane] = srk[lane];
-        v[6 * kC + lane] = srq[lane];
-      }
+  if (wave == 0) {
+    const float into = expf(float(sum)), rest = expf(float(lane_of(sum, 63) - sum));
+    float* v = vec + idx * (BWD ? kVecFloatsBwd : kVecFloats);
+    v[lane] = into * srk[lane];
+    v[kC + lane] = rest * srk[lane];
+    v[2 * kC + lane] = a.scale * into * srq[lane];
+    v[3 * kC + lane] = expf(float(lane_of(sum, 63)));
+    if constexpr (BWD) {
+      v[4 * kC + lane] = beta;
+      v[5 * kC + lane] = srk[lane];
+      v[6 * kC + lane] = srq[lane];
     }
-    __syncthreads();
-    for (int e = tid; e < kC * kC; e += 256) {
-      const int r = e / kC, j = e % kC;
-      float x = 0.0f;
-      if (j < r) x = sbeta[r] * expf(float(gsum[r] - gsum[j])) * srk[r] * srk[j] * kk[r * kLdM + j];
-      mat[r * kLdM + j] = x;
-    }
-    __syncthreads();
-    invert_unit_lower(mat, wave);
-
-    constexpr int kKinds = BWD ? 3 : 2;
-    for (int task = wave; task < kKinds * kFrags; task += 4) {
-      const int kind = task / kFrags, f = task % kFrags;  // 0: T, 1: P (BWD: P^T), 2: T^T
-      const bool upper = BWD && kind > 0;
-      const int m = upper ? (f < 4 ? f >> 1 : f - 2) : (f < 2 ? f : (f + 2) >> 1);
-      const int s = upper ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : f & 1);
-      const int row = chained(m, i), k0 = 32 * s + 8 * qd;
-      f32x8 x;
+  }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = upper ? k0 + j : row, q = upper ? row : k0 + j;  // matrix row (later token), column
-        if (kind == 1)
-          x[j] = q <= r ? a.scale * srq[r] * srk[q] * expf(float(gsum[r] - gsum[q])) * qk[r * kLdM + q] : 0.0f;
-        else
-          x[j] = kind == 0 ? mat[r * kLdM + q] * sbeta[q] : mat[r * kLdM + q];
-      }
-      const Frag<3> fr = split(x);
-      const int terms = kind == 1 ? NP : 3;
-      char* dst = (kind == 0 ? frag_t : kind == 1 ? frag_p : frag_tt) + (idx * kFrags + f) * terms * kFragBytes;
+  for (int ct = 0; ct < 4; ++ct) {
+    const int tj = 16 * ct + i;
 #pragma unroll
-      for (int n = 0; n < 3; ++n)
-        if (n < terms) *reinterpret_cast<bf16x8*>(dst + (n * 64 + lane) * 16) = fr.t[n];
+    for (int r = 0; r < 4; ++r) {
+      const int ti = 16 * wave + 4 * qd + r;
+      float decay = 0.0f;
+      if (ct < wave) decay = from[ct < 3 ? ct : 0][ti] * to_end[tj];
+      if (ct == wave && tj <= ti) decay = expf(float(gsum[ti] - gsum[tj]));
+      decay *= srk[tj];
+      tmat[ti * kLdM + tj] = tj < ti ? sbeta[ti] * decay * srk[ti] * kk[ct][r] : 0.0f;
+      pmat[ti * kLdM + tj] = tj <= ti ? a.scale * decay * srq[ti] * qk[ct][r] : 0.0f;
     }
+  }
+  __syncthreads();
+  invert_unit_lower(tmat, wave);
+
+  constexpr int kKinds = BWD ? 3 : 2;
+#pragma unroll
+  for (int n = 0; n < (kKinds * kFrags + 3) / 4; ++n) {
+    const int task = wave + 4 * n;
+    if (task >= kKinds * kFrags) break;
+    const int kind = task / kFrags, f = task % kFrags;  // 0: T, 1: P (BWD: P^T), 2: T^T
+    const bool upper = BWD && kind > 0;
+    const int m = upper ? upper_m(f) : lower_m(f), s = upper ? upper_s(f) : lower_s(f);
+    const int row = chained(m, i), k0 = 32 * s + 8 * qd;
+    const float* from_mat = kind == 1 ? pmat : tmat;
+    f32x8 x;
+    if (upper) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = from_mat[(k0 + j) * kLdM + row];
+    } else {
+      x = read8(&from_mat[row * kLdM + k0]);
+    }
+    if (kind == 0) x *= read8(&sbeta[k0]);
+    const Frag<3> fr = split(x);
+    const int terms = kind == 1 ? NP : 3;
+    char* dst = (kind == 0 ? frag_t : kind == 1 ? frag_p : frag_tt) + (idx * kFrags + f) * terms * kFragBytes;
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (k < terms) *reinterpret_cast<bf16x8*>(dst + (k * 64 + lane) * 16) = fr.t[k];
   }
 }
 
