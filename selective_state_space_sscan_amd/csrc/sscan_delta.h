@@ -58,18 +58,21 @@ struct DeltaBwdArgs {
 struct DeltaPlan {
   int64_t nchunk;                    // chunks per row
   int recurrent;                     // token-by-token kernel, no workspace
+  int kp;                            // dk rounded up to 64 or 128
+  int dvp;                           // dv rounded up to 32
+  int waves;                         // waves (sixteen value columns each) of a walk's block
+  int nseg, seg_chunks;              // segments of a row walked at once, chunks in each
   size_t off_t, off_p, off_vec;      // forward: fragments of T and of the masked Q K^T; per-token factors
+  size_t off_ends, off_moves;        // segments' end (entry) states and transitions
   size_t workspace_bytes;
 };
 
-// Backward: the transposed fragments as well, the corrected values U and the adjoint
-// Y = diag(1/beta)-free gradient of V in float32, and the state and its adjoint at
-// every chunk's edge.
+// Backward: the transposed fragments as well, the corrected values U and the adjoint X~
+// in float32, the state and its adjoint at every chunk's edge, and the adjoints between
+// segments.
 struct DeltaBwdPlan {
-  int64_t nchunk;
-  int dvp;                           // dv rounded up to 32
-  int kp;                            // dk rounded up to 64
-  size_t off_t, off_tt, off_pt, off_vec, off_u, off_y, off_s, off_ds;
+  DeltaPlan f;
+  size_t off_tt, off_pt, off_u, off_y, off_s, off_ds, off_back;
   size_t workspace_bytes;
 };
 

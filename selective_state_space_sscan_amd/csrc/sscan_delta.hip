@@ -118,16 +118,25 @@ __global__ __launch_bounds__(256) void delta_recurrent_kernel(DeltaArgs a, int n
   }
 }
 
-// KP: dk rounded up; W: waves (sixteen value columns each) of a walk's block.
 template <typename IO, int KP, int W>
 hipError_t launch_walk(const DeltaArgs& a, const DeltaPlan& p, char* ws, hipStream_t stream) {
   const int wide = wide_flags<IO>(a), nvb = (a.dv + 16 * W - 1) / (16 * W), n = int(p.nchunk);
   char *ft = ws + p.off_t, *fp = ws + p.off_p;
   float* vec = reinterpret_cast<float*>(ws + p.off_vec);
+  const int64_t bh = a.batch * a.hv;
   delta_prep_kernel<IO, KP, false>
-      <<<dim3(unsigned(a.batch * a.hv * n)), 256, 0, stream>>>(a, n, ft, fp, nullptr, vec, wide);
-  delta_chunk_kernel<IO, KP, W, false>
-      <<<dim3(unsigned(a.batch * a.hv * nvb)), 64 * W, 0, stream>>>(a, n, nvb, ft, fp, vec, nullptr, nullptr, 0, wide);
+      <<<dim3(unsigned(bh * n)), 256, 0, stream>>>(a, n, ft, fp, nullptr, vec, wide);
+  const WalkArgs w{n, nvb, p.nseg, p.seg_chunks, p.dvp, wide, ft, fp, vec, nullptr, nullptr,
+                   reinterpret_cast<float*>(ws + p.off_ends), reinterpret_cast<float*>(ws + p.off_moves)};
+  if (p.nseg > 1) {
+    constexpr int kIdent = (KP + 16 * W - 1) / (16 * W);
+    delta_chunk_kernel<IO, KP, W, kEnds>
+        <<<dim3(unsigned(bh * p.nseg * (nvb + kIdent))), 64 * W, 0, stream>>>(a, w, kVecFloats);
+  }
+  if (p.nseg > 2)
+    delta_carry_kernel<KP, 4, false>
+        <<<dim3(unsigned(bh * ((p.dvp + 63) / 64))), 256, 0, stream>>>(w.moves, w.ends, p.nseg, p.dvp, (p.dvp + 63) / 64);
+  delta_chunk_kernel<IO, KP, W, kOut><<<dim3(unsigned(bh * p.nseg * nvb)), 64 * W, 0, stream>>>(a, w, kVecFloats);
   return hipGetLastError();
 }
 
@@ -144,27 +153,58 @@ hipError_t launch_fwd(const DeltaArgs& a, const DeltaPlan& p, char* ws, hipStrea
       delta_recurrent_kernel<IO, 16><<<grid, 256, 0, stream>>>(a, ncol, waves, wide);
     return hipGetLastError();
   }
-  if (a.dk <= 64) return a.dv > 64 ? launch_walk<IO, 64, 8>(a, p, ws, stream) : launch_walk<IO, 64, 4>(a, p, ws, stream);
-  return a.dv > 64 ? launch_walk<IO, 128, 8>(a, p, ws, stream) : launch_walk<IO, 128, 4>(a, p, ws, stream);
+  if (p.kp == 64)
+    return p.waves == 8 ? launch_walk<IO, 64, 8>(a, p, ws, stream) : launch_walk<IO, 64, 4>(a, p, ws, stream);
+  return p.waves == 8 ? launch_walk<IO, 128, 8>(a, p, ws, stream) : launch_walk<IO, 128, 4>(a, p, ws, stream);
 }
 
 }  // namespace delta
 
 static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Segments a row is walked in.  One CU holds one block of a walk, so a walk takes
+// ceil(blocks / CUs) times its chunks; in units of the time of one chunk of the output
+// walk, a chunk of the transitions' walk takes 3/4 and a step of the chain between
+// segments 1/2.
+static int choose_segments(int64_t heads, int64_t nchunk, int nvb, int nkb) {
+  constexpr int64_t kCus = 256;
+  const auto rounds = [](int64_t blocks) { return double((blocks + kCus - 1) / kCus); };
+  int best = 1;
+  double least = rounds(heads * nvb) * double(nchunk);
+  for (int n = 2; n <= 64 && nchunk / n >= 4; ++n) {
+    const double chunks = double((nchunk + n - 1) / n);
+    const double cost = rounds(heads * nvb * n) * chunks +
+                        0.75 * rounds(heads * (nvb * (n - 1) + nkb * (n - 2))) * chunks + 0.5 * (n - 2) + 2.0;
+    if (cost < 0.9 * least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
 DeltaPlan make_delta_plan(int64_t batch, int64_t len, int hk, int hv, int dk, int dv, bool io_bf16) {
   (void)hk;
-  (void)dk;
-  (void)dv;
   DeltaPlan p{};
   p.nchunk = (len + kDeltaChunk - 1) / kDeltaChunk;
   p.recurrent = len <= kDeltaRecurrentMax;
+  p.kp = dk <= 64 ? 64 : 128;
+  p.dvp = (dv + 31) / 32 * 32;
+  p.waves = dv > 64 ? 8 : 4;
   if (p.recurrent) return p;
-  const size_t n = size_t(batch) * size_t(hv) * size_t(p.nchunk);
+  const int cols = 16 * p.waves;
+  const int64_t heads = batch * hv;
+  p.nseg = choose_segments(heads, p.nchunk, (dv + cols - 1) / cols, (p.kp + cols - 1) / cols);
+  p.seg_chunks = int((p.nchunk + p.nseg - 1) / p.nseg);
+  p.nseg = int((p.nchunk + p.seg_chunks - 1) / p.seg_chunks);
+  const size_t n = size_t(heads) * size_t(p.nchunk);
   p.off_t = 0;
   p.off_p = p.off_t + round256(n * delta::kFrags * 3 * delta::kFragBytes);
   p.off_vec = p.off_p + round256(n * delta::kFrags * (io_bf16 ? 2 : 3) * delta::kFragBytes);
-  p.workspace_bytes = p.off_vec + round256(n * delta::kVecFloats * 4);
+  p.off_ends = p.off_vec + round256(n * delta::kVecFloats * 4);
+  const size_t segs = p.nseg > 1 ? size_t(heads) * size_t(p.nseg) * size_t(p.kp) * 4 : 0;
+  p.off_moves = p.off_ends + round256(segs * size_t(p.dvp));
+  p.workspace_bytes = p.off_moves + round256(segs * size_t(p.kp));
   return p;
 }
 

@@ -27,12 +27,19 @@ namespace delta {
 
 // ---- the walk back over chunks ------------------------------------------------------
 //
-// As the forward walk: a wave owns sixteen columns of the adjoint state.
-template <typename IO, int KP, int W>
-__global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, int nchunk, int nvb,
-                                                                 const char* frag_tt, const char* frag_pt,
-                                                                 const float* vec, float* adjoints, float* xgrad,
-                                                                 int dvp, int wide) {
+// As the forward walk: a wave owns sixteen columns of the adjoint state, and segments
+// are walked at once.  ENDS: only the adjoint that a segment hands to the one before it,
+// started from zero (the last segment: from dh_last); the transitions between them are
+// the forward walk's, transposed.
+struct WalkBackArgs {
+  int nchunk, nvb, nseg, seg_chunks, dvp, wide;
+  const char *frag_tt, *frag_pt;
+  const float* vec;
+  float *adjoints, *xgrad, *back;
+};
+
+template <typename IO, int KP, int W, bool ENDS>
+__global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, WalkBackArgs w) {
   constexpr int N = Io<IO>::kN, kTiles = KP / 16, kSteps = KP / 32, kThreads = 64 * W, kVecs = 5 * kC;
   typedef Tile<KP> TileK;
   typedef WalkLds<IO, KP, true, 3, kVecs> Lds;
@@ -40,15 +47,19 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_
 
   const DeltaArgs& a = b_.f;
   const int tid = int(threadIdx.x), lane = tid & 63, wave = wave_id(), i = lane & 15, qd = lane >> 4;
-  const int64_t bh = int64_t(blockIdx.x) / nvb, b = bh / a.hv;
+  const int vb = int(blockIdx.x % unsigned(w.nvb)), seg = int(blockIdx.x / unsigned(w.nvb) % unsigned(w.nseg));
+  const int64_t bh = blockIdx.x / unsigned(w.nvb) / unsigned(w.nseg), b = bh / a.hv, at_seg = bh * w.nseg + seg;
+  if (ENDS && seg == 0) return;  // nobody reads it
   const int h = int(bh % a.hv), hq = h / (a.hv / a.hk);
-  const int col = int(int64_t(blockIdx.x) % nvb) * (16 * W) + 16 * wave + i;
+  const int col = vb * (16 * W) + 16 * wave + i, dvp = w.dvp;
   const int Lb = row_len(a.lengths, b, a.len), live_chunks = (Lb + kC - 1) / kC;
+  const int first = seg * w.seg_chunks;
+  const int past = live_chunks < first + w.seg_chunks ? live_chunks : first + w.seg_chunks;  // chunks past - 1 .. first
   const IO* kp = static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h;
   const IO* qp = static_cast<const IO*>(a.q) + b * a.sq.b + hq * a.sq.h;
   const IO* dp = static_cast<const IO*>(b_.dout) + (b * a.len * a.hv + h) * a.dv;
   const int64_t out_t = int64_t(a.hv) * a.dv;
-  const bool wide_qk = wide & 1, live_col = col < a.dv;
+  const bool wide_qk = w.wide & 1, live_col = col < a.dv;
   const int d_lane = live_col ? (8 * qd * int(out_t) + col) * int(sizeof(IO)) : kOutside;
   const int d_row = int(out_t) * int(sizeof(IO));
   int at_row[kSteps], at_col[kSteps];
@@ -63,7 +74,11 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_
   const uint32_t state_bytes = uint32_t(a.dk * a.dv * 4);
 
   f32x4 E[kTiles] = {};
-  if (b_.dh_last) load_state(buffer_of(b_.dh_last + bh * a.dk * a.dv, state_bytes), s_lane, a.dv, E);
+  if (seg == w.nseg - 1) {
+    if (b_.dh_last) load_state(buffer_of(b_.dh_last + bh * a.dk * a.dv, state_bytes), s_lane, a.dv, E);
+  } else if (!ENDS) {
+    load_state(buffer_of(w.back + (at_seg + 1) * KP * dvp, KP * dvp * 4), w_lane, dvp, E);
+  }
 
   RowsAhead<IO, KP, kThreads> next_k, next_q;
   BytesAhead<Lds::kBytesT, kThreads> next_t, next_p;
@@ -85,10 +100,10 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_
       }
   };
   const auto load_frags = [&](int c) {
-    const int64_t idx = bh * nchunk + c;
-    next_p.load(frag_pt + idx * Lds::kBytesT);
-    next_t.load(frag_tt + idx * Lds::kBytesT);
-    if (tid < kVecs / 4) next_vec = reinterpret_cast<const f32x4*>(vec + idx * kVecFloatsBwd)[tid];
+    const int64_t idx = bh * w.nchunk + c;
+    next_p.load(w.frag_pt + idx * Lds::kBytesT);
+    next_t.load(w.frag_tt + idx * Lds::kBytesT);
+    if (tid < kVecs / 4) next_vec = reinterpret_cast<const f32x4*>(w.vec + idx * kVecFloatsBwd)[tid];
   };
   const auto store_rows = [&](char* set) {
     next_k.store(reinterpret_cast<bf16*>(set));
@@ -99,17 +114,17 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_
     next_t.store(set + Lds::kT);
     if (tid < kVecs / 4) reinterpret_cast<f32x4*>(set + Lds::kVec)[tid] = next_vec;
   };
-  if (live_chunks > 0) {
-    load_rows(live_chunks - 1);
-    load_frags(live_chunks - 1);
+  if (first < past) {
+    load_rows(past - 1);
+    load_frags(past - 1);
     if (Lds::kSets == 2) {
-      store_rows(lds + ((live_chunks - 1) & 1) * Lds::kSet);
-      store_frags(lds + ((live_chunks - 1) & 1) * Lds::kSet);
+      store_rows(lds + ((past - 1) & 1) * Lds::kSet);
+      store_frags(lds + ((past - 1) & 1) * Lds::kSet);
     }
   }
 
-  for (int c = live_chunks - 1; c >= 0; --c) {
-    const int64_t idx = bh * nchunk + c;
+  for (int c = past - 1; c >= first; --c) {
+    const int64_t idx = bh * w.nchunk + c;
     const char* set = lds + (Lds::kSets == 2 ? (c & 1) * Lds::kSet : 0);
     char* other = lds + (Lds::kSets == 2 ? (~c & 1) * Lds::kSet : 0);
     const Frag<N> df[2] = {as_frag(next_d[0]), as_frag(next_d[1])};
@@ -124,11 +139,11 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_
       store_frags(lds);
       __syncthreads();
     }
-    if (c > 0) {
+    if (c > first) {
       load_rows(c - 1);
       if (Lds::kSets == 1) load_frags(c - 1);
     }
-    store_state(buffer_of(adjoints + idx * KP * dvp, KP * dvp * 4), w_lane, dvp, E);
+    if constexpr (!ENDS) store_state(buffer_of(w.adjoints + idx * KP * dvp, KP * dvp * 4), w_lane, dvp, E);
     const bf16 *sk = reinterpret_cast<const bf16*>(set), *sq = reinterpret_cast<const bf16*>(set + Lds::kQ);
     const char *st = set + Lds::kT + lane * 16, *sp = set + Lds::kP + lane * 16;
     const float* svec = reinterpret_cast<const float*>(set + Lds::kVec);
@@ -159,7 +174,7 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_
         x[m] = mul(f, df[s], x[m]);
       }
     }
-    if (Lds::kSets == 2 && c > 0) {
+    if (Lds::kSets == 2 && c > first) {
       store_rows(other);
       load_frags(c - 1);
     }
@@ -178,7 +193,7 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_
         x[m] = mul(f, xf[s], x[m]);
       }
     }
-    store_state(buffer_of(xgrad + idx * kC * dvp, kC * dvp * 4), w_lane, dvp, x);
+    if constexpr (!ENDS) store_state(buffer_of(w.xgrad + idx * kC * dvp, kC * dvp * 4), w_lane, dvp, x);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const int tok = chained(m, 4 * qd);
@@ -207,9 +222,11 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_
         E[m] = mul(fq, gf[s], E[m]);
       }
     }
-    if (Lds::kSets == 2 && c > 0) store_frags(other);
+    if (Lds::kSets == 2 && c > first) store_frags(other);
   }
-  if (b_.dh0) store_state(buffer_of(b_.dh0 + bh * a.dk * a.dv, state_bytes), s_lane, a.dv, E);
+  if constexpr (ENDS) store_state(buffer_of(w.back + at_seg * KP * dvp, KP * dvp * 4), w_lane, dvp, E);
+  if (!ENDS && seg == 0 && b_.dh0)
+    store_state(buffer_of(b_.dh0 + bh * a.dk * a.dv, state_bytes), s_lane, a.dv, E);
 }
 
 // ---- the gradients of a chunk --------------------------------------------------------
@@ -577,26 +594,41 @@ hipError_t launch_bwd(const DeltaBwdArgs& b, const DeltaBwdPlan& p, char* ws, hi
   int wide = wide_flags<IO>(a) & ~4;
   if (a.dv % 8 == 0 && reinterpret_cast<uintptr_t>(b.dout) % 16 == 0) wide |= 4;
   if (a.dv % 8 == 0 && reinterpret_cast<uintptr_t>(b.dv) % 16 == 0) wide |= 16;
-  const int n = int(p.nchunk), nvb = (p.dvp + 16 * W - 1) / (16 * W);
-  char *ft = ws + p.off_t, *ftt = ws + p.off_tt, *fpt = ws + p.off_pt;
-  float *vec = reinterpret_cast<float*>(ws + p.off_vec), *u = reinterpret_cast<float*>(ws + p.off_u),
-        *x = reinterpret_cast<float*>(ws + p.off_y), *s = reinterpret_cast<float*>(ws + p.off_s),
-        *e = reinterpret_cast<float*>(ws + p.off_ds);
-  const dim3 per_key{unsigned(a.batch * a.hk * n)}, walk{unsigned(a.batch * a.hv * nvb)};
+  const DeltaPlan& f = p.f;
+  const int n = int(f.nchunk), nvb = (f.dvp + 16 * W - 1) / (16 * W);
+  const auto floats = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+  char *ft = ws + f.off_t, *ftt = ws + p.off_tt, *fpt = ws + p.off_pt;
+  float *vec = floats(f.off_vec), *u = floats(p.off_u), *x = floats(p.off_y), *s = floats(p.off_s),
+        *e = floats(p.off_ds), *ends = floats(f.off_ends), *moves = floats(f.off_moves), *back = floats(p.off_back);
+  const WalkArgs w{n, nvb, f.nseg, f.seg_chunks, f.dvp, wide, ft, nullptr, vec, s, u, ends, moves};
+  const WalkBackArgs wb{n, nvb, f.nseg, f.seg_chunks, f.dvp, wide, ftt, fpt, vec, e, x, back};
+  const int64_t bh = a.batch * a.hv;
+  const dim3 walk{unsigned(bh * f.nseg * nvb)}, chain{unsigned(bh * ((f.dvp + 63) / 64))};
   if (n > 0) {
-    delta_prep_kernel<IO, KP, true><<<dim3(unsigned(a.batch * a.hv * n)), 256, 0, stream>>>(a, n, ft, fpt, ftt, vec, wide);
-    delta_chunk_kernel<IO, KP, W, true><<<walk, 64 * W, 0, stream>>>(a, n, nvb, ft, nullptr, vec, s, u, p.dvp, wide);
+    delta_prep_kernel<IO, KP, true><<<dim3(unsigned(bh * n)), 256, 0, stream>>>(a, n, ft, fpt, ftt, vec, wide);
+    if (f.nseg > 1) {
+      constexpr int kIdent = (KP + 16 * W - 1) / (16 * W);
+      delta_chunk_kernel<IO, KP, W, kEnds>
+          <<<dim3(unsigned(bh * f.nseg * (nvb + kIdent))), 64 * W, 0, stream>>>(a, w, kVecFloatsBwd);
+      delta_chunk_bwd_kernel<IO, KP, W, true><<<walk, 64 * W, 0, stream>>>(b, wb);
+    }
+    if (f.nseg > 2) {
+      delta_carry_kernel<KP, 4, false><<<chain, 256, 0, stream>>>(moves, ends, f.nseg, f.dvp, (f.dvp + 63) / 64);
+      delta_carry_kernel<KP, 4, true><<<chain, 256, 0, stream>>>(moves, back, f.nseg, f.dvp, (f.dvp + 63) / 64);
+    }
+    delta_chunk_kernel<IO, KP, W, kStates><<<walk, 64 * W, 0, stream>>>(a, w, kVecFloatsBwd);
   }
-  delta_chunk_bwd_kernel<IO, KP, W><<<walk, 64 * W, 0, stream>>>(b, n, nvb, ftt, fpt, vec, e, x, p.dvp, wide);
-  if (n > 0) delta_grad_kernel<IO, KP><<<per_key, 256, 0, stream>>>(b, n, vec, s, e, u, x, p.dvp, wide);
+  delta_chunk_bwd_kernel<IO, KP, W, false><<<walk, 64 * W, 0, stream>>>(b, wb);
+  if (n > 0)
+    delta_grad_kernel<IO, KP><<<dim3(unsigned(a.batch * a.hk * n)), 256, 0, stream>>>(b, n, vec, s, e, u, x, f.dvp, wide);
   return hipGetLastError();
 }
 
 template <typename IO>
 hipError_t launch_bwd(const DeltaBwdArgs& b, const DeltaBwdPlan& p, char* ws, hipStream_t stream) {
-  if (p.kp == 64)
-    return p.dvp > 64 ? launch_bwd<IO, 64, 8>(b, p, ws, stream) : launch_bwd<IO, 64, 4>(b, p, ws, stream);
-  return p.dvp > 64 ? launch_bwd<IO, 128, 8>(b, p, ws, stream) : launch_bwd<IO, 128, 4>(b, p, ws, stream);
+  if (p.f.kp == 64)
+    return p.f.waves == 8 ? launch_bwd<IO, 64, 8>(b, p, ws, stream) : launch_bwd<IO, 64, 4>(b, p, ws, stream);
+  return p.f.waves == 8 ? launch_bwd<IO, 128, 8>(b, p, ws, stream) : launch_bwd<IO, 128, 4>(b, p, ws, stream);
 }
 
 }  // namespace delta
@@ -604,27 +636,32 @@ hipError_t launch_bwd(const DeltaBwdArgs& b, const DeltaBwdPlan& p, char* ws, hi
 static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 DeltaBwdPlan make_delta_bwd_plan(int64_t batch, int64_t len, int hk, int hv, int dk, int dv, bool io_bf16) {
-  (void)hk;
-  (void)io_bf16;
   DeltaBwdPlan p{};
-  p.nchunk = (len + kDeltaChunk - 1) / kDeltaChunk;
-  p.dvp = (dv + 31) / 32 * 32;
-  p.kp = dk <= 64 ? 64 : 128;
-  const size_t n = size_t(batch) * size_t(hv) * size_t(p.nchunk);
+  p.f = make_delta_plan(batch, len, hk, hv, dk, dv, io_bf16);
+  if (p.f.recurrent) {  // the gradients always go by chunks, and these rows have at most one
+    p.f.recurrent = 0;
+    p.f.nseg = p.f.seg_chunks = 1;
+  }
+  const size_t n = size_t(batch) * size_t(hv) * size_t(p.f.nchunk), segs = size_t(batch) * size_t(hv) * size_t(p.f.nseg);
+  const size_t kp = size_t(p.f.kp), dvp = size_t(p.f.dvp);
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     const size_t off = at;
-    at += round256(n * bytes);
+    at += round256(bytes);
     return off;
   };
-  p.off_t = take(delta::kFrags * 3 * delta::kFragBytes);
-  p.off_tt = take(delta::kFrags * 3 * delta::kFragBytes);
-  p.off_pt = take(delta::kFrags * 3 * delta::kFragBytes);
-  p.off_vec = take(delta::kVecFloatsBwd * 4);
-  p.off_u = take(size_t(kDeltaChunk) * p.dvp * 4);
-  p.off_y = take(size_t(kDeltaChunk) * p.dvp * 4);
-  p.off_s = take(size_t(p.kp) * p.dvp * 4);
-  p.off_ds = take(size_t(p.kp) * p.dvp * 4);
+  p.f.off_t = take(n * delta::kFrags * 3 * delta::kFragBytes);
+  p.off_tt = take(n * delta::kFrags * 3 * delta::kFragBytes);
+  p.off_pt = take(n * delta::kFrags * 3 * delta::kFragBytes);
+  p.f.off_vec = take(n * delta::kVecFloatsBwd * 4);
+  p.off_u = take(n * kDeltaChunk * dvp * 4);
+  p.off_y = take(n * kDeltaChunk * dvp * 4);
+  p.off_s = take(n * kp * dvp * 4);
+  p.off_ds = take(n * kp * dvp * 4);
+  const bool split = p.f.nseg > 1;
+  p.f.off_ends = take(split ? segs * kp * dvp * 4 : 0);
+  p.f.off_moves = take(split ? segs * kp * kp * 4 : 0);
+  p.off_back = take(split ? segs * kp * dvp * 4 : 0);
   p.workspace_bytes = at;
   return p;
 }

@@ -131,31 +131,50 @@ struct WalkLds {
 // the fragments of T and P through LDS; the next chunk's come in while a chunk is
 // computed.  V and the output move between memory and the lanes that own them (32-byte
 // runs of a row that the block's waves complete to whole lines).
-// STATES: the backward pass's recomputation, which leaves every chunk's entry state
-// [KP][dvp] and U [64][dvp] in float32 instead of the output and the last state.
-template <typename IO, int KP, int W, bool STATES>
-__global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nchunk, int nvb, const char* frag_t,
-                                                             const char* frag_p, const float* vec, float* states,
-                                                             float* values, int dvp, int wide) {
+//
+// A row is walked in nseg segments at once.  kOut: the output walk, and with the last
+// segment the last state; kStates: the backward pass's recomputation, which leaves every
+// chunk's entry state [KP][dvp] and U [64][dvp] in float32 instead.  kEnds: the
+// segments' transitions S -> M S + N, walked before those two where nseg > 1: the state
+// columns from zero (segment 0: from h0) give N, and the columns of the identity without
+// values give M.  Blocks nvb .. of a segment hold the identity's columns.
+enum WalkMode { kOut, kStates, kEnds };
+
+struct WalkArgs {
+  int nchunk, nvb, nseg, seg_chunks, dvp, wide;
+  const char *frag_t, *frag_p;
+  const float* vec;
+  float *states, *values;   // kStates
+  float *ends, *moves;      // N [row, head][nseg][KP][dvp] (as carried: entry states), M [..][KP][KP]
+};
+
+template <typename IO, int KP, int W, int MODE>
+__global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, WalkArgs w, int vecs) {
   constexpr int N = Io<IO>::kN, NO = Io<IO>::kOutTerms, kThreads = 64 * W, kRing = N == 1 ? 5 : 2;
-  constexpr int kTiles = KP / 16, kSteps = KP / 32, kVecs = STATES ? kVecFloatsBwd : kVecFloats;
+  constexpr int kTiles = KP / 16, kSteps = KP / 32;
+  constexpr bool OUT = MODE == kOut;
   typedef Tile<KP> TileK;
-  typedef WalkLds<IO, KP, !STATES, NO, kVecFloats> Lds;
+  typedef WalkLds<IO, KP, OUT, NO, kVecFloats> Lds;
   __shared__ __attribute__((aligned(256))) char lds[Lds::kSets * Lds::kSet];
   __shared__ __attribute__((aligned(16))) char lds_v[W * ColumnsAhead<IO>::kLds];
 
   const int tid = int(threadIdx.x), lane = tid & 63, wave = wave_id(), i = lane & 15, qd = lane >> 4;
-  const int64_t bh = int64_t(blockIdx.x) / nvb, b = bh / a.hv;
+  const int blocks = w.nvb + (MODE == kEnds ? (KP + 16 * W - 1) / (16 * W) : 0);
+  const int vb = int(blockIdx.x % unsigned(blocks)), seg = int(blockIdx.x / unsigned(blocks) % unsigned(w.nseg));
+  const int64_t bh = blockIdx.x / unsigned(blocks) / unsigned(w.nseg), b = bh / a.hv, at_seg = bh * w.nseg + seg;
+  const bool ident = MODE == kEnds && vb >= w.nvb;
+  if (MODE == kEnds && (seg == w.nseg - 1 || (ident && seg == 0))) return;  // nobody reads these
   const int h = int(bh % a.hv), hq = h / (a.hv / a.hk);
-  const int col = int(int64_t(blockIdx.x) % nvb) * (16 * W) + 16 * wave + i;
+  const int col = (ident ? vb - w.nvb : vb) * (16 * W) + 16 * wave + i;
   const int L = int(a.len), Lb = row_len(a.lengths, b, a.len);
-  const int live_chunks = (Lb + kC - 1) / kC;
+  const int first = seg * w.seg_chunks, live_chunks = (Lb + kC - 1) / kC;
+  const int past = live_chunks < first + w.seg_chunks ? live_chunks : first + w.seg_chunks;  // chunks first .. past - 1
   const IO* kp = static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h;
   const IO* qp = static_cast<const IO*>(a.q) + b * a.sq.b + hq * a.sq.h;
   const IO* vp = static_cast<const IO*>(a.v) + b * a.sv.b + h * a.sv.h;
   IO* op = static_cast<IO*>(a.out) + (b * a.len * a.hv + h) * a.dv;
   const int64_t out_t = int64_t(a.hv) * a.dv;
-  const bool wide_qk = wide & 1, wide_v = wide & 2, live_col = col < a.dv;
+  const bool wide_qk = w.wide & 1, wide_v = w.wide & 2, live_col = !ident && col < a.dv;
   // byte offset of this lane's first token (8 qd) and column in a chunk's output rows; its
   // other tokens are 32 (m >> 1) + 4 (m & 1) + r rows on
   const int o_lane = live_col ? (8 * qd * int(out_t) + col) * int(sizeof(IO)) : kOutside;
@@ -169,11 +188,20 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
   }
 
   const int s_lane = live_col ? (8 * qd * a.dv + col) * 4 : kOutside;
-  const int w_lane = STATES && col < dvp ? (8 * qd * dvp + col) * 4 : kOutside;
+  const int w_lane = !ident && col < w.dvp ? (8 * qd * w.dvp + col) * 4 : kOutside;
   const uint32_t state_bytes = uint32_t(a.dk * a.dv * 4);
 
   f32x4 S[kTiles] = {};
-  if (a.h0) load_state(buffer_of(a.h0 + bh * a.dk * a.dv, state_bytes), s_lane, a.dv, S);
+  if (ident) {
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[m][r] = chained(m, 4 * qd + r) == col ? 1.0f : 0.0f;
+  } else if (seg == 0) {
+    if (a.h0) load_state(buffer_of(a.h0 + bh * a.dk * a.dv, state_bytes), s_lane, a.dv, S);
+  } else if (MODE != kEnds) {
+    load_state(buffer_of(w.ends + (at_seg - 1) * KP * w.dvp, KP * w.dvp * 4), w_lane, w.dvp, S);
+  }
 
   RowsAhead<IO, KP, kThreads> next_k, next_q;
   BytesAhead<Lds::kBytesT, kThreads> next_t;
@@ -183,36 +211,36 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
   const auto load_rows = [&](int c) {
     const int t0 = c * kC;
     next_k.load(kp, a.sk.t, t0, Lb, a.dk, wide_qk);
-    if constexpr (!STATES) next_q.load(qp, a.sq.t, t0, Lb, a.dk, wide_qk);
-    next_v.load(rows_of(vp + t0 * a.sv.t, Lb - t0 < kC ? Lb - t0 : kC, a.sv.t, a.dv), a.sv.t, col - i, a.dv, wide_v);
+    if constexpr (OUT) next_q.load(qp, a.sq.t, t0, Lb, a.dk, wide_qk);
+    next_v.load(rows_of(vp + t0 * a.sv.t, Lb - t0 < kC ? Lb - t0 : kC, a.sv.t, a.dv), a.sv.t, ident ? a.dv : col - i, a.dv, wide_v);
   };
   const auto load_frags = [&](int c) {
-    const int64_t idx = bh * nchunk + c;
-    next_t.load(frag_t + idx * Lds::kBytesT);
-    if constexpr (!STATES) next_p.load(frag_p + idx * Lds::kBytesP);
-    if (tid < kVecFloats / 4) next_vec = reinterpret_cast<const f32x4*>(vec + idx * kVecs)[tid];
+    const int64_t idx = bh * w.nchunk + c;
+    next_t.load(w.frag_t + idx * Lds::kBytesT);
+    if constexpr (OUT) next_p.load(w.frag_p + idx * Lds::kBytesP);
+    if (tid < kVecFloats / 4) next_vec = reinterpret_cast<const f32x4*>(w.vec + idx * vecs)[tid];
   };
   const auto store_rows = [&](char* set) {
     next_k.store(reinterpret_cast<bf16*>(set));
-    if constexpr (!STATES) next_q.store(reinterpret_cast<bf16*>(set + Lds::kQ));
+    if constexpr (OUT) next_q.store(reinterpret_cast<bf16*>(set + Lds::kQ));
   };
   const auto store_frags = [&](char* set) {
     next_t.store(set + Lds::kT);
-    if constexpr (!STATES) next_p.store(set + Lds::kP);
+    if constexpr (OUT) next_p.store(set + Lds::kP);
     if (tid < kVecFloats / 4) reinterpret_cast<f32x4*>(set + Lds::kVec)[tid] = next_vec;
   };
-  if (live_chunks > 0) {
-    load_rows(0);
-    load_frags(0);
+  if (first < past) {
+    load_rows(first);
+    load_frags(first);
     if (Lds::kSets == 2) {
-      store_rows(lds);
-      store_frags(lds);
+      store_rows(lds + (first & 1) * Lds::kSet);
+      store_frags(lds + (first & 1) * Lds::kSet);
     }
   }
 
-  for (int c = 0; c < live_chunks; ++c) {
+  for (int c = first; c < past; ++c) {
     const int t0 = c * kC;
-    const int64_t idx = bh * nchunk + c;
+    const int64_t idx = bh * w.nchunk + c;
     const char* set = lds + (Lds::kSets == 2 ? (c & 1) * Lds::kSet : 0);
     char* other = lds + (Lds::kSets == 2 ? (~c & 1) * Lds::kSet : 0);
     f32x4 x[4];
@@ -223,12 +251,13 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
       store_frags(lds);
       __syncthreads();
     }
-    const bool more = c + 1 < live_chunks;
+    const bool more = c + 1 < past;
     if (more) {
       load_rows(c + 1);
       if (Lds::kSets == 1) load_frags(c + 1);
     }
-    if constexpr (STATES) store_state(buffer_of(states + idx * KP * dvp, KP * dvp * 4), w_lane, dvp, S);
+    if constexpr (MODE == kStates)
+      store_state(buffer_of(w.states + idx * KP * w.dvp, KP * w.dvp * 4), w_lane, w.dvp, S);
     const bf16 *sk = reinterpret_cast<const bf16*>(set), *sq = reinterpret_cast<const bf16*>(set + Lds::kQ);
     const char *st = set + Lds::kT + lane * 16, *sp = set + Lds::kP + lane * 16;
     const float* svec = reinterpret_cast<const float*>(set + Lds::kVec);
@@ -242,7 +271,7 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         f.k.t[n] = row_frag(sk + n * TileK::kElems + at);
-        if constexpr (!STATES) f.q.t[n] = row_frag(sq + n * TileK::kElems + at);
+        if constexpr (OUT) f.q.t[n] = row_frag(sq + n * TileK::kElems + at);
       }
     };
     constexpr int kRingT = 4;
@@ -271,10 +300,10 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
     ring_run<4 * kSteps>(rows_ring, read_rows, [&](int j, const Rows& f) {
       const int m = j / kSteps, s = j % kSteps, tok = chained(m, 4 * qd);
       ks = mul(f.k, sf[s], s == 0 ? f32x4{} : ks);
-      if constexpr (!STATES) o[m] = mul<NO>(f.q, sf[s], o[m]);
+      if constexpr (OUT) o[m] = mul<NO>(f.q, sf[s], o[m]);
       if (s == kSteps - 1) {
         x[m] -= *reinterpret_cast<const f32x4*>(&svec[tok]) * ks;
-        if constexpr (!STATES) o[m] *= *reinterpret_cast<const f32x4*>(&svec[2 * kC + tok]);
+        if constexpr (OUT) o[m] *= *reinterpret_cast<const f32x4*>(&svec[2 * kC + tok]);
       }
     });
     Frag<3> t_ring[kRingT];
@@ -289,7 +318,7 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
     ring_run<kFrags>(t_ring, read_t,
                      [&](int j, const Frag<3>& f) { u[lower_m(j)] = mul(f, xf[lower_s(j)], u[lower_m(j)]); });
     // o += P u
-    if constexpr (!STATES) {
+    if constexpr (OUT) {
       Frag<NO> p_ring[kRingT];
       ring_start<kFrags>(p_ring, read_p);
       const Frag<3> uf[2] = {split(u[0], u[1]), split(u[2], u[3])};
@@ -302,8 +331,8 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
       for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r) store1(rows, at + (32 * (m >> 1) + 4 * (m & 1) + r) * o_row, IO(o[m][r]));
-    } else {
-      store_state(buffer_of(values + idx * kC * dvp, kC * dvp * 4), w_lane, dvp, u);
+    } else if constexpr (MODE == kStates) {
+      store_state(buffer_of(w.values + idx * kC * w.dvp, kC * w.dvp * 4), w_lane, w.dvp, u);
     }
     // S = last S + K^T (d u)
     Frag<N> c_ring[kRing];
@@ -317,11 +346,77 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, int nc
     ring_run<2 * kTiles>(c_ring, read_cols, [&](int j, const Frag<N>& f) { S[j >> 1] = mul(f, df[j & 1], S[j >> 1]); });
     if (Lds::kSets == 2 && more) store_frags(other);
   }
-  if constexpr (STATES) return;
-  // tokens past the row's length: zeros (those of its last chunk were written above)
-  if (live_col)
-    for (int t = live_chunks * kC + qd; t < L; t += 4) op[t * out_t + col] = IO(0.0f);
-  store_state(buffer_of(a.h_last + bh * a.dk * a.dv, state_bytes), s_lane, a.dv, S);
+  if constexpr (MODE == kEnds) {
+    if (ident)
+      store_state(buffer_of(w.moves + at_seg * KP * KP, KP * KP * 4), col < KP ? (8 * qd * KP + col) * 4 : kOutside, KP, S);
+    else
+      store_state(buffer_of(w.ends + at_seg * KP * w.dvp, KP * w.dvp * 4), w_lane, w.dvp, S);
+  }
+  if constexpr (OUT) {
+    // tokens past the row's length: zeros (those of its last chunk were written above)
+    const int from = (first < live_chunks ? past : first) * kC, to = (first + w.seg_chunks) * kC;
+    if (live_col)
+      for (int t = from + qd; t < L && t < to; t += 4) op[t * out_t + col] = IO(0.0f);
+    if (seg == w.nseg - 1) store_state(buffer_of(a.h_last + bh * a.dk * a.dv, state_bytes), s_lane, a.dv, S);
+  }
+}
+
+// The chain over segments: X_j += M_j X_(j-1) for j = 1 .. nseg - 2 (REV: X_j += M_j^T
+// X_(j+1) downwards), X the state columns left by the segments.  A block is W waves of
+// sixteen columns; M's terms go through LDS, the next segment's loaded meanwhile.  Four
+// waves: with eight a CU's LDS reads (96 KB a wave and step at 128 x 128) make a step
+// twice as long, 6.8 us.
+template <int KP, int W, bool REV>
+__global__ __launch_bounds__(64 * W) void delta_carry_kernel(const float* moves, float* x, int nseg, int dvp, int nvb) {
+  constexpr int kThreads = 64 * W, kTiles = KP / 16, kSteps = KP / 32, kUnits = KP * KP / 8 / kThreads;
+  typedef Tile<KP> TileK;  // KP rows of it here
+  __shared__ __attribute__((aligned(16))) bf16 sm[3][KP * KP];
+  const int tid = int(threadIdx.x), lane = tid & 63, i = lane & 15, qd = lane >> 4;
+  const int64_t bh = blockIdx.x / unsigned(nvb);
+  const int col = int(blockIdx.x % unsigned(nvb)) * (16 * W) + 16 * wave_id() + i;
+  const int at = col < dvp ? (8 * qd * dvp + col) * 4 : kOutside;
+  const auto x_of = [&](int j) { return buffer_of(x + (bh * nseg + j) * KP * dvp, KP * dvp * 4); };
+  const int start = REV ? nseg - 2 : 1, step = REV ? -1 : 1;
+  f32x8 next[kUnits];
+  f32x4 S[kTiles], add[kTiles];
+  const auto load = [&](int j) {
+    const Buffer m = buffer_of(moves + (bh * nseg + j) * KP * KP, KP * KP * 4);
+#pragma unroll
+    for (int n = 0; n < kUnits; ++n) load_wide(m, (tid + kThreads * n) * 32, &next[n]);
+    load_state(x_of(j), at, dvp, add);
+  };
+  load_state(x_of(start - step), at, dvp, S);
+  load(start);
+  for (int k = 0; k < nseg - 2; ++k) {
+    const int j = start + k * step;
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kUnits; ++n) {
+      const int u = tid + kThreads * n;
+      const Frag<3> f = split(next[n]);
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+        *reinterpret_cast<bf16x8*>(&sm[t][TileK::unit_at(u / (KP / 8), u % (KP / 8))]) = f.t[t];
+    }
+    Frag<3> sf[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) sf[s] = split(S[2 * s], S[2 * s + 1]);
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m) S[m] = add[m];
+    __syncthreads();
+    if (k + 1 < nseg - 2) load(j + step);
+    const auto read = [&](int k, Frag<3>& f) {
+      const int m = k / kSteps, s = k % kSteps;
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+        f.t[t] = REV ? col_frag<KP>(sm[t], 32 * s + 8 * qd, chained(m, 4 * (i & 3)))
+                     : row_frag(&sm[t][TileK::unit_at(chained(m, i), 4 * s + qd)]);
+    };
+    Frag<3> ring[3];
+    ring_start<kTiles * kSteps>(ring, read);
+    ring_run<kTiles * kSteps>(ring, read, [&](int k, const Frag<3>& f) { S[k / kSteps] = mul(f, sf[k % kSteps], S[k / kSteps]); });
+    store_state(x_of(j), at, dvp, S);
+  }
 }
 
 }  // namespace delta

@@ -97,6 +97,20 @@ def test_resets_and_strong_decays(L):
     close(last, ref_last, "h_last")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dk,dv", [(64, 48), (128, 130)])
+def test_long_rows_walked_in_segments(dk, dv, dtype):
+    """Few rows, many chunks: entry states come from the segments' transitions; rows end
+    inside the first, a middle and the last segment, on a segment's edge, and not at all."""
+    ins = inputs(5, 1300, 1, 1, dk, dv, dtype, seed=21, g_scale=0.02)
+    h0 = state(5, 1, dk, dv)
+    n = torch.tensor([1300, 7, 640, 1290, 0], dtype=torch.int32)
+    out, last = run(ins, h0, n)
+    ref, ref_last = delta_ref.delta(*ins, h0, n)
+    close(out, ref, "out")
+    close(last, ref_last, "h_last")
+
+
 def test_correlated_keys():
     """Keys that nearly repeat make the chunk's triangular system as ill behaved as it gets."""
     gen = torch.Generator().manual_seed(2)

@@ -73,6 +73,14 @@ def test_gradients_lengths(dtype):
             assert not r[name][i, int(m):].any(), name
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dk,dv", [(64, 48), (128, 130)])
+def test_gradients_of_long_rows_walked_in_segments(dk, dv, dtype):
+    n = torch.tensor([1200, 640, 3], dtype=torch.int32)
+    check(inputs(3, 1200, 1, 1, dk, dv, dtype, seed=21, g_scale=0.02), state(3, 1, dk, dv),
+          state(3, 1, dk, dv, seed=8), n)
+
+
 def test_gradients_resets_zero_beta_and_zero_keys():
     ins = list(inputs(1, 140, 1, 2, 64, 64, torch.float32, seed=4, unit=False))
     ins[4][0, 10:20] = 0.0
