@@ -524,8 +524,8 @@ SSCAN_API int sscan_bwd_plan(int64_t batch, int64_t dim, int64_t len, int64_t ds
  * v_heads, dv] io_dtype and the states [batch, v_heads, dk, dv] float32 are contiguous.
  * lengths (optional, device int32 [batch]): tokens of each row, clamped to 0..len; later
  * tokens are not read, their outputs and gradients are 0 and they leave the state alone.
- * dk in 1..128, dv in 1..256, len <= 2^30; token strides of q, k, v and v_heads * dv below
- * 2^23 elements.  States and accumulators are float32; bf16
+ * dk in 1..128, dv in 1..256, len <= 2^30; token strides of q, k, v, v_heads * dv and
+ * qk_heads * dk below 2^23 elements.  States and accumulators are float32; bf16
  * outputs round to nearest even.  Sequences are walked in chunks of 64 tokens by matrix
  * products: a non-finite q, k, v or beta makes the outputs of its whole chunk (and the
  * state after it) non-finite. */

@@ -231,43 +231,75 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_
 
 // ---- the gradients of a chunk --------------------------------------------------------
 
+// Sum over the sixteen lanes of a row, in every one of them.
 __device__ __forceinline__ float row16_sum(float x) {
-#pragma unroll
-  for (int m = 1; m < 16; m *= 2) x += __shfl_xor(x, m);
+  const auto ror = [](float y, auto n) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, y), 0x120 + decltype(n)::value, 0xf, 0xf, true));
+  };
+  x += ror(x, std::integral_constant<int, 8>());
+  x += ror(x, std::integral_constant<int, 4>());
+  x += ror(x, std::integral_constant<int, 2>());
+  x += ror(x, std::integral_constant<int, 1>());
   return x;
 }
 
-// One block per (batch row, key head, chunk); the value heads that share the key head
-// are walked in order and their dq, dk summed in registers.  Wave w owns the key
-// dimensions of tiles w, w + 4 for all 64 tokens.
-template <typename IO, int KP>
-__global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs b_, int nchunk, const float* vec,
+// LDS tile of 64 tokens by VS value columns, in units of eight permuted by the row so
+// that sixteen consecutive rows read at one unit touch every bank once.
+template <int VS>
+struct Slab {
+  static constexpr int kUnits = VS / 8, kRows = 16 / kUnits, kElems = kC * VS;
+  __device__ static __forceinline__ int at(int row, int unit) {
+    return row * VS + ((unit ^ (row / kRows % kUnits)) << 3);
+  }
+};
+
+template <typename IO, int KP, int VS>
+struct GradLds {
+  static constexpr int N = Io<IO>::kN, kLdG = 72, kG = kC * kLdG;  // a term of a 64 x 64 factor
+  // bf16: the three factors dO U^T, X~ U^T and beta X~ U^T side by side; float32: in turn
+  static constexpr int kFactors = N == 1 ? 3 : 1;
+  static constexpr int kSlabs = (N + 6) * Slab<VS>::kElems;        // dO, U, X~
+  static constexpr int kShared = kSlabs > kFactors * 3 * kG ? kSlabs : kFactors * 3 * kG;
+};
+
+// One block of eight waves per (batch row, key head, chunk); the value heads that share
+// the key head are walked in order and their dq, dk summed in registers.  A wave owns one
+// tile of sixteen key dimensions for all tokens (KP = 64: for half of them).  The value
+// axis comes in slabs of VS columns: U, X~ (cut into terms once) and dO through LDS, the
+// rows of S0 and E that a wave needs straight to its lanes.
+template <typename IO, int KP, int VS>
+__global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nchunk, const float* vec,
                                                          const float* states, const float* adjoints,
                                                          const float* values, const float* xgrad, int dvp, int wide) {
-  constexpr int N = Io<IO>::kN, NT = KP / 64, kLdG = 72;
+  typedef GradLds<IO, KP, VS> Lds;
   typedef Tile<KP> TileK;
+  typedef Slab<VS> SlabV;
   typedef typename Io<IO>::V8 V8;
-  __shared__ __attribute__((aligned(16))) bf16 sk[N][TileK::kElems];
-  __shared__ __attribute__((aligned(16))) bf16 sq[N][TileK::kElems];
-  __shared__ __attribute__((aligned(16))) bf16 sg[3][kC * kLdG];
+  constexpr int N = Lds::N, kLdG = Lds::kLdG, kG = Lds::kG, kTilesK = KP / 16, MT = kTilesK / 2;
+  __shared__ __attribute__((aligned(256))) bf16 sk[N * TileK::kElems];
+  __shared__ __attribute__((aligned(256))) bf16 sq[N * TileK::kElems];
+  __shared__ __attribute__((aligned(256))) bf16 shared[Lds::kShared];
   __shared__ __attribute__((aligned(16))) float svec[kVecFloatsBwd];
   __shared__ double gsum[kC];
-  __shared__ float sdot[4][4][kC], sxv[kC], sse[4];
+  __shared__ float sdot[8][4][kC], sxv[kC], sse[8];
+  bf16 *sd = shared, *su = shared + N * SlabV::kElems, *sx = su + 3 * SlabV::kElems;
 
   const DeltaArgs& a = b_.f;
   const int tid = int(threadIdx.x), lane = tid & 63, wave = wave_id(), i = lane & 15, qd = lane >> 4;
+  const int kt = wave % kTilesK, m0 = wave / kTilesK * MT;  // key tile, first token tile
   const int c = int(blockIdx.x % unsigned(nchunk));
   const int64_t bhk = blockIdx.x / unsigned(nchunk), b = bhk / a.hk;
   const int hq = int(bhk % a.hk), share = a.hv / a.hk;
   const int L = int(a.len), Lb = row_len(a.lengths, b, a.len), t0 = c * kC;
   const int64_t qk_t = int64_t(a.hk) * a.dk, v_t = int64_t(a.hv) * a.dv;
   const bool wide_qk = wide & 1, wide_v = wide & 2, wide_d = wide & 4, wide_gv = wide & 16;
+  const int out_rows = L - t0 < kC ? L - t0 : kC, rows = Lb - t0 < kC ? Lb - t0 : kC;
   IO* dq_out = static_cast<IO*>(b_.dq) + (b * a.len * a.hk + hq) * a.dk;
   IO* dk_out = static_cast<IO*>(b_.dk) + (b * a.len * a.hk + hq) * a.dk;
 
   if (t0 >= Lb) {  // past the row's length: zeros
-    const int rows = L - t0 < kC ? L - t0 : kC;
-    for (int u = tid; u < rows * a.dk; u += 256) {
+    for (int u = tid; u < out_rows * a.dk; u += 512) {
       const int64_t at = (t0 + u / a.dk) * qk_t + u % a.dk;
       dq_out[at] = IO(0.0f);
       dk_out[at] = IO(0.0f);
@@ -275,8 +307,8 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs b_, int nc
     for (int hh = 0; hh < share; ++hh) {
       const int64_t h = hq * share + hh;
       IO* dv_out = static_cast<IO*>(b_.dv) + (b * a.len * a.hv + h) * a.dv;
-      for (int u = tid; u < rows * a.dv; u += 256) dv_out[(t0 + u / a.dv) * v_t + u % a.dv] = IO(0.0f);
-      if (tid < rows) {
+      for (int u = tid; u < out_rows * a.dv; u += 512) dv_out[(t0 + u / a.dv) * v_t + u % a.dv] = IO(0.0f);
+      if (tid < out_rows) {
         b_.dg[(b * a.len + t0 + tid) * a.hv + h] = 0.0f;
         b_.dbeta[(b * a.len + t0 + tid) * a.hv + h] = 0.0f;
       }
@@ -284,243 +316,258 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs b_, int nc
     return;
   }
 
-  const IO* kp = static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h;
-  const IO* qp = static_cast<const IO*>(a.q) + b * a.sq.b + hq * a.sq.h;
-  for (int u = tid; u < kC * KP / 8; u += 256) {
-    const int row = u / (KP / 8), d8 = (u % (KP / 8)) * 8;
-    const bool in = t0 + row < Lb;
-    const auto fk = as_frag(load8(kp + (t0 + row) * a.sk.t + d8, in ? a.dk - d8 : 0, wide_qk));
-    const auto fq = as_frag(load8(qp + (t0 + row) * a.sq.t + d8, in ? a.dk - d8 : 0, wide_qk));
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      *reinterpret_cast<bf16x8*>(&sk[n][TileK::unit_at(row, d8 / 8)]) = fk.t[n];
-      *reinterpret_cast<bf16x8*>(&sq[n][TileK::unit_at(row, d8 / 8)]) = fq.t[n];
-    }
+  {
+    RowsAhead<IO, KP, 512> k, q;
+    k.load(static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h, a.sk.t, t0, Lb, a.dk, wide_qk);
+    q.load(static_cast<const IO*>(a.q) + b * a.sq.b + hq * a.sq.h, a.sq.t, t0, Lb, a.dk, wide_qk);
+    k.store(sk);
+    q.store(sq);
   }
-  const auto at_tile = [](const bf16 (&s)[N][TileK::kElems], int row, int dim) {
+  const auto at_tile = [](const bf16* s, int row, int dim) {
     float x = 0.0f;
 #pragma unroll
-    for (int n = N - 1; n >= 0; --n) x += float(s[n][TileK::at(row, dim)]);
+    for (int n = N - 1; n >= 0; --n) x += float(s[n * TileK::kElems + TileK::at(row, dim)]);
     return x;
   };
 
-  f32x4 dq[4][NT] = {}, dk[4][NT] = {};
+  f32x4 dq[MT] = {}, dk[MT] = {};
   for (int hh = 0; hh < share; ++hh) {
     const int h = hq * share + hh;
     const int64_t idx = (b * a.hv + h) * nchunk + c;
-    const float* up = values + idx * kC * dvp;
-    const float* xp = xgrad + idx * kC * dvp;
-    const float* sp = states + idx * KP * dvp;
-    const float* ep = adjoints + idx * KP * dvp;
-    const IO* dp = static_cast<const IO*>(b_.dout) + (b * a.len * a.hv + h) * a.dv;
-    __syncthreads();
-    for (int u = tid; u < kVecFloatsBwd; u += 256) svec[u] = vec[idx * kVecFloatsBwd + u];
-    if (wave == 0) {
+    const Buffer ub = buffer_of(values + idx * kC * dvp, kC * dvp * 4);
+    const Buffer xb = buffer_of(xgrad + idx * kC * dvp, kC * dvp * 4);
+    const Buffer sb = buffer_of(states + idx * KP * dvp, KP * dvp * 4);
+    const Buffer eb = buffer_of(adjoints + idx * KP * dvp, KP * dvp * 4);
+    const Buffer db = rows_of(static_cast<const IO*>(b_.dout) + (b * a.len * a.hv + h) * a.dv + t0 * v_t, rows, v_t, a.dv);
+    const Buffer vb = rows_of(static_cast<const IO*>(a.v) + b * a.sv.b + h * a.sv.h + t0 * a.sv.t, rows, a.sv.t, a.dv);
+    const Buffer gb = rows_of(static_cast<const IO*>(b_.dv) + (b * a.len * a.hv + h) * a.dv + t0 * v_t, out_rows, v_t, a.dv);
+    __syncthreads();  // the last head's readers are done
+    if (tid < kVecFloatsBwd) svec[tid] = vec[idx * kVecFloatsBwd + tid];
+    if (tid < kC) sxv[tid] = 0.0f;
+    if (wave == 7) {
       const int t = t0 + lane;
       const float g = t < Lb ? clamp_decay(a.g[b * a.sg.b + t * a.sg.t + h * a.sg.h]) : 0.0f;
       gsum[lane] = wave_running_sum(double(g));
     }
-    __syncthreads();
 
-    // dv = beta x~, and x~ . v per token (four threads a token)
-    {
-      const int row = tid >> 2, t = t0 + row;
-      const float beta = svec[4 * kC + row];
-      const IO* vp = static_cast<const IO*>(a.v) + b * a.sv.b + t * a.sv.t + h * a.sv.h;
-      IO* dst = static_cast<IO*>(b_.dv) + ((b * a.len + t) * a.hv + h) * a.dv;
-      float dot = 0.0f;
-      if (t < L)
-        for (int c8 = (tid & 3) * 8; c8 < a.dv; c8 += 32) {
-          const f32x8 x = load8(xp + row * dvp + c8, 8, true);
-          const V8 v = load8(vp + c8, t < Lb ? a.dv - c8 : 0, wide_v);
+    f32x4 h1[MT] = {}, h2[MT] = {}, h3[MT] = {}, gacc[3] = {};
+    float se = 0.0f;
+    for (int v0 = 0; v0 < dvp; v0 += VS) {
+      __syncthreads();
+      // the slab of U, X~ and dO; dV = beta X~ and X~ . v on the way
+#pragma unroll
+      for (int n = 0; n < (kC * VS / 8 + 511) / 512; ++n) {
+        const int u = tid + 512 * n, row = u / SlabV::kUnits, unit = u % SlabV::kUnits, c8 = v0 + 8 * unit;
+        if (u < kC * SlabV::kUnits) {
+          const int at = c8 < dvp ? (row * dvp + c8) * 4 : kOutside;
+          f32x8 uv, xv;
+          V8 dv, vv;
+          load_wide(ub, at, &uv);
+          load_wide(xb, at, &xv);
+          load8<IO>(db, (row * int(v_t) + c8) * int(sizeof(IO)), a.dv - c8, wide_d, &dv);
+          load8<IO>(vb, (row * int(a.sv.t) + c8) * int(sizeof(IO)), a.dv - c8, wide_v, &vv);
+          const Frag<3> fu = split(uv), fx = split(xv);
+          const auto fd = as_frag(dv);
+          const int lds_at = SlabV::at(row, unit);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            *reinterpret_cast<bf16x8*>(su + k * SlabV::kElems + lds_at) = fu.t[k];
+            *reinterpret_cast<bf16x8*>(sx + k * SlabV::kElems + lds_at) = fx.t[k];
+          }
+#pragma unroll
+          for (int k = 0; k < N; ++k) *reinterpret_cast<bf16x8*>(sd + k * SlabV::kElems + lds_at) = fd.t[k];
+          const float beta = svec[4 * kC + row];
+          float dot = 0.0f;
           V8 y;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            dot += x[j] * float(v[j]);
-            y[j] = IO(beta * x[j]);
+            dot += xv[j] * float(vv[j]);
+            y[j] = IO(beta * xv[j]);
           }
-          if (wide_gv) {
-            *reinterpret_cast<V8*>(dst + c8) = y;
+          store8<IO>(gb, (row * int(v_t) + c8) * int(sizeof(IO)), a.dv - c8, wide_gv, y);
+#pragma unroll
+          for (int k = 1; k < SlabV::kUnits; k *= 2) dot += __shfl_xor(dot, k);
+          if (unit == 0) sxv[row] += dot;  // the same thread for every slab
+        }
+      }
+      __syncthreads();
+      // products with the states: dO S0^T, X~ S0^T, U E^T
+#pragma unroll
+      for (int s = 0; s < VS / 32; ++s) {
+        if (v0 + 32 * s >= dvp) break;
+        const int at = ((16 * kt + i) * dvp + v0 + 32 * s + 8 * qd) * 4;
+        f32x8 s8, e8;
+        load_wide(sb, at, &s8);
+        load_wide(eb, at, &e8);
+        const Frag<3> fs = split(s8), fe = split(e8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) se += s8[j] * e8[j];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int lds_at = SlabV::at(16 * (m0 + m) + i, 4 * s + qd);
+          Frag<N> fd;
+          Frag<3> fx, fu;
+#pragma unroll
+          for (int k = 0; k < N; ++k) fd.t[k] = row_frag(sd + k * SlabV::kElems + lds_at);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            fx.t[k] = row_frag(sx + k * SlabV::kElems + lds_at);
+            fu.t[k] = row_frag(su + k * SlabV::kElems + lds_at);
+          }
+          h1[m] = mul(fd, fs, h1[m]);
+          h2[m] = mul(fx, fs, h2[m]);
+          h3[m] = mul(fu, fe, h3[m]);
+        }
+        // dO U^T and X~ U^T, ten lower tiles each, two or three a wave
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+          const int item = wave + 8 * n;
+          if (item >= 20) break;
+          const int tile = item < 10 ? item : item - 10;
+          const int rt = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, ct = tile - rt * (rt + 1) / 2;
+          const int row_at = SlabV::at(16 * rt + i, 4 * s + qd), col_at = SlabV::at(16 * ct + i, 4 * s + qd);
+          Frag<3> fu;
+#pragma unroll
+          for (int k = 0; k < 3; ++k) fu.t[k] = row_frag(su + k * SlabV::kElems + col_at);
+          if (item < 10) {
+            Frag<N> fd;
+#pragma unroll
+            for (int k = 0; k < N; ++k) fd.t[k] = row_frag(sd + k * SlabV::kElems + row_at);
+            gacc[n] = mul(fd, fu, gacc[n]);
           } else {
+            Frag<3> fx;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (c8 + j < a.dv) dst[c8 + j] = y[j];
+            for (int k = 0; k < 3; ++k) fx.t[k] = row_frag(sx + k * SlabV::kElems + row_at);
+            gacc[n] = mul(fx, fu, gacc[n]);
           }
-        }
-      dot += __shfl_xor(dot, 1);
-      dot += __shfl_xor(dot, 2);
-      if ((tid & 3) == 0) sxv[row] = dot;
-    }
-
-    // dO U^T and X~ U^T: wave w takes tokens 16 w .. + 15 against all earlier ones
-    f32x4 g1[4] = {}, g2[4] = {};
-    {
-      const int t = t0 + 16 * wave + i;
-      for (int v0 = 0; v0 < dvp; v0 += 32) {
-        const int v8 = v0 + 8 * qd;
-        const auto fd = as_frag(load8(dp + t * v_t + v8, t < Lb ? a.dv - v8 : 0, wide_d));
-        const Frag<3> fx = split(load8(xp + (16 * wave + i) * dvp + v8, 8, true));
-#pragma unroll
-        for (int ct = 0; ct < 4; ++ct)
-          if (ct <= wave) {
-            const Frag<3> fu = split(load8(up + (16 * ct + i) * dvp + v8, 8, true));
-            g1[ct] = mul(fd, fu, g1[ct]);
-            g2[ct] = mul(fx, fu, g2[ct]);
-          }
-      }
-#pragma unroll
-      for (int ct = 0; ct < 4; ++ct)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int ti = 16 * wave + 4 * qd + r, tj = 16 * ct + i;
-          const float decay = tj <= ti ? expf(float(gsum[ti] - gsum[tj])) * svec[5 * kC + tj] : 0.0f;
-          g1[ct][r] = tj <= ti ? g1[ct][r] * decay * a.scale * svec[6 * kC + ti] : 0.0f;
-          g2[ct][r] = tj < ti ? g2[ct][r] * decay * svec[5 * kC + ti] : 0.0f;
-        }
-    }
-    const auto put = [&](const f32x4 (&g)[4], bool with_beta) {
-#pragma unroll
-      for (int ct = 0; ct < 4; ++ct)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int ti = 16 * wave + 4 * qd + r;
-          float x = with_beta ? g[ct][r] * svec[4 * kC + ti] : g[ct][r];
-#pragma unroll
-          for (int n = 0; n < 3; ++n) {
-            const bf16 t = bf16(x);
-            sg[n][ti * kLdG + 16 * ct + i] = t;
-            x -= float(t);
-          }
-        }
-    };
-    put(g1, false);
-
-    // products with the states: dO S0^T, X~ S0^T, U E^T
-    f32x4 h1[4][NT] = {}, h2[4][NT] = {}, h3[4][NT] = {};
-    float se = 0.0f;
-    for (int v0 = 0; v0 < dvp; v0 += 32) {
-      const int v8 = v0 + 8 * qd;
-      Frag<3> fs[NT], fe[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int dim = 16 * (wave + 4 * n) + i;
-        const f32x8 s = load8(sp + dim * dvp + v8, 8, true), e = load8(ep + dim * dvp + v8, 8, true);
-        fs[n] = split(s);
-        fe[n] = split(e);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) se += s[j] * e[j];
-      }
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int row = 16 * m + i, t = t0 + row;
-        const auto fd = as_frag(load8(dp + t * v_t + v8, t < Lb ? a.dv - v8 : 0, wide_d));
-        const Frag<3> fx = split(load8(xp + row * dvp + v8, 8, true));
-        const Frag<3> fu = split(load8(up + row * dvp + v8, 8, true));
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          h1[m][n] = mul(fd, fs[n], h1[m][n]);
-          h2[m][n] = mul(fx, fs[n], h2[m][n]);
-          h3[m][n] = mul(fu, fe[n], h3[m][n]);
         }
       }
     }
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) se += __shfl_xor(se, m);
-    if (lane == 0) sse[wave] = se;
+    if (lane == 0) sse[wave] = m0 == 0 ? se : 0.0f;  // waves of the same key tile hold the same sum
     // h1: dq, h2: -R, h3: U E^T's part of W (all times the inverse norms)
-    float kh3[4][4];
+    float kh3[MT][4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int tok = 16 * m + 4 * qd;
+    for (int m = 0; m < MT; ++m) {
+      const int tok = 16 * (m0 + m) + 4 * qd;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        kh3[m][r] = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          h1[m][n][r] *= svec[2 * kC + tok + r];
-          h2[m][n][r] *= svec[tok + r];
-          h3[m][n][r] *= svec[kC + tok + r];
-          kh3[m][r] += at_tile(sk, tok + r, 16 * (wave + 4 * n) + i) * h3[m][n][r];
-        }
+        h1[m][r] *= svec[2 * kC + tok + r];
+        h2[m][r] *= svec[tok + r];
+        h3[m][r] *= svec[kC + tok + r];
+        kh3[m][r] = at_tile(sk, tok + r, 16 * kt + i) * h3[m][r];
       }
     }
-    f32x4 w[4][NT] = {};
-    // lower: acc += G B over tokens j <= i; upper: acc += G^T B over i >= j
-    const auto by_rows = [&](f32x4 (&acc)[4][NT], const bf16 (&tile)[N][TileK::kElems]) {
+    // the factors take the slabs' place: masked, decayed, times the inverse norms; which
+    // 0: dO U^T, 1: X~ U^T, 2: beta X~ U^T (two tiles right of the diagonal are read too)
+    const auto put = [&](int which, bf16* dst) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
+      for (int n = 0; n < 3; ++n) {
+        const int item = wave + 8 * n;
+        if (item >= 20) break;
+        if ((item < 10) != (which == 0)) continue;
+        const int tile = item < 10 ? item : item - 10;
+        const int rt = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, ct = tile - rt * (rt + 1) / 2;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (lower_frag(m, s) < 0) continue;
-          Frag<3> fg;
+        for (int r = 0; r < 4; ++r) {
+          const int ti = 16 * rt + 4 * qd + r, tj = 16 * ct + i;
+          const bool in = which == 0 ? tj <= ti : tj < ti;
+          float x = 0.0f;
+          if (in) {
+            x = gacc[n][r] * expf(float(gsum[ti] - gsum[tj])) * svec[5 * kC + tj];
+            x *= which == 0 ? a.scale * svec[6 * kC + ti] : svec[5 * kC + ti];
+            if (which == 2) x *= svec[4 * kC + ti];
+          }
 #pragma unroll
-          for (int n = 0; n < 3; ++n) fg.t[n] = row_frag(&sg[n][(16 * m + i) * kLdG + 32 * s + 8 * qd]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            Frag<N> fb;
-#pragma unroll
-            for (int t = 0; t < N; ++t)
-              fb.t[t] = col_frag<KP>(tile[t], 32 * s + 8 * qd, 16 * (wave + 4 * n) + 4 * (i & 3));
-            acc[m][n] = mul(fg, fb, acc[m][n]);
+          for (int k = 0; k < 3; ++k) {
+            const bf16 t = bf16(x);
+            dst[k * kG + ti * kLdG + tj] = t;
+            x -= float(t);
           }
         }
-    };
-    const auto by_cols = [&](f32x4 (&acc)[4][NT], const bf16 (&tile)[N][TileK::kElems], bool minus) {
+      }
+      if (wave >= 6)  // tiles (0, 1) and (2, 3): above the diagonal, but in the fragments read
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            dst[k * kG + ((wave - 6) * 32 + 4 * qd + r) * kLdG + (wave - 6) * 32 + 16 + i] = bf16(0.0f);
+    };
+    f32x4 w[MT] = {};
+    // acc += G B over tokens j <= i, and acc += G^T B over i >= j
+    const auto by_rows = [&](f32x4 (&acc)[MT], const bf16* g, const bf16* tile) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (upper_frag(m, s) < 0) continue;
+          if (m0 + m < 2 && s == 1) continue;
+          Frag<3> fg;
+#pragma unroll
+          for (int n = 0; n < 3; ++n) fg.t[n] = row_frag(g + n * kG + (16 * (m0 + m) + i) * kLdG + 32 * s + 8 * qd);
+          Frag<N> fb;
+#pragma unroll
+          for (int t = 0; t < N; ++t) fb.t[t] = col_frag<KP>(tile + t * TileK::kElems, 32 * s + 8 * qd, 16 * kt + 4 * (i & 3));
+          acc[m] = mul(fg, fb, acc[m]);
+        }
+    };
+    const auto by_cols = [&](f32x4 (&acc)[MT], const bf16* g, const bf16* tile, bool minus) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (m0 + m >= 2 && s == 0) continue;
           Frag<3> fg;
 #pragma unroll
           for (int n = 0; n < 3; ++n) {
-            fg.t[n] = col_frag(&sg[n][(32 * s + 8 * qd + (i >> 2)) * kLdG + 16 * m + 4 * (i & 3)], kLdG);
+            fg.t[n] = col_frag(g + n * kG + (32 * s + 8 * qd + (i >> 2)) * kLdG + 16 * (m0 + m) + 4 * (i & 3), kLdG);
             if (minus) fg.t[n] = -fg.t[n];
           }
+          Frag<N> fb;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            Frag<N> fb;
-#pragma unroll
-            for (int t = 0; t < N; ++t)
-              fb.t[t] = col_frag<KP>(tile[t], 32 * s + 8 * qd, 16 * (wave + 4 * n) + 4 * (i & 3));
-            acc[m][n] = mul(fg, fb, acc[m][n]);
-          }
+          for (int t = 0; t < N; ++t) fb.t[t] = col_frag<KP>(tile + t * TileK::kElems, 32 * s + 8 * qd, 16 * kt + 4 * (i & 3));
+          acc[m] = mul(fg, fb, acc[m]);
         }
     };
     __syncthreads();
-    by_rows(h1, sk);
-    by_cols(w, sq, false);
-    __syncthreads();
-    put(g2, false);
-    __syncthreads();
-    by_rows(h2, sk);
-    __syncthreads();
-    put(g2, true);
-    __syncthreads();
-    by_cols(w, sk, true);
+    if constexpr (Lds::kFactors == 3) {
+      put(0, shared);
+      put(1, shared + 3 * kG);
+      put(2, shared + 6 * kG);
+      __syncthreads();
+      by_rows(h1, shared, sk);
+      by_rows(h2, shared + 3 * kG, sk);
+      by_cols(w, shared, sq, false);
+      by_cols(w, shared + 6 * kG, sk, true);
+    } else {
+      put(0, shared);
+      __syncthreads();
+      by_rows(h1, shared, sk);
+      by_cols(w, shared, sq, false);
+      __syncthreads();
+      put(1, shared);
+      __syncthreads();
+      by_rows(h2, shared, sk);
+      __syncthreads();
+      put(2, shared);
+      __syncthreads();
+      by_cols(w, shared, sk, true);
+    }
 
     // per token: q . dq, k . R, k . (W without U E^T), k . U E^T
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int tok = 16 * m + 4 * qd + r;
-        const float beta = svec[4 * kC + tok];
-        float d[4] = {0.0f, 0.0f, 0.0f, kh3[m][r]};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int dim = 16 * (wave + 4 * n) + i;
-          const float k = at_tile(sk, tok, dim), q = at_tile(sq, tok, dim);
-          d[0] += q * h1[m][n][r];
-          d[1] -= k * h2[m][n][r];
-          d[2] += k * w[m][n][r];
-          dq[m][n][r] += h1[m][n][r];
-          dk[m][n][r] += w[m][n][r] + h3[m][n][r] - beta * h2[m][n][r];
-        }
+        const int tok = 16 * (m0 + m) + 4 * qd + r, dim = 16 * kt + i;
+        const float beta = svec[4 * kC + tok], k = at_tile(sk, tok, dim), q = at_tile(sq, tok, dim);
+        const float d[4] = {q * h1[m][r], -k * h2[m][r], k * w[m][r], kh3[m][r]};
+        dq[m][r] += h1[m][r];
+        dk[m][r] += w[m][r] + h3[m][r] - beta * h2[m][r];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          d[x] = row16_sum(d[x]);
-          if (i == 0) sdot[wave][x][tok] = d[x];
+          const float sum = row16_sum(d[x]);
+          if (i == 0) sdot[kt][x][tok] = sum;
         }
       }
     __syncthreads();
@@ -528,13 +575,19 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs b_, int nc
       const int t = t0 + lane;
       float d[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) d[x] = (sdot[0][x][lane] + sdot[1][x][lane]) + (sdot[2][x][lane] + sdot[3][x][lane]);
+      for (int x = 0; x < 4; ++x) {
+        d[x] = sdot[0][x][lane];
+#pragma unroll
+        for (int k = 1; k < kTilesK; ++k) d[x] += sdot[k][x][lane];
+      }
       const float beta = svec[4 * kC + lane];
       const double own = double(d[0]) + double(beta) * d[1] - d[2];
       // sum over i >= t of own, over j < t of k . U E^T, and exp(G_C) <E, S0>
       const double upto = wave_running_sum(own), wrote = wave_running_sum(double(d[3]));
-      const double all = __shfl(upto, 63);
-      const double s0e = double(sse[0]) + sse[1] + sse[2] + sse[3];
+      const double all = lane_of(upto, 63);
+      double s0e = 0.0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s0e += sse[k];
       if (t < L) {
         const int64_t at = (b * a.len + t) * a.hv + h;
         b_.dg[at] = t < Lb ? float((all - upto + own) + (wrote - d[3]) + svec[3 * kC] * s0e) : 0.0f;
@@ -547,45 +600,53 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs b_, int nc
   __syncthreads();
   if (a.qk_norm) {
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int tok = 16 * m + 4 * qd + r;
-        float d[2] = {};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int dim = 16 * (wave + 4 * n) + i;
-          d[0] += at_tile(sq, tok, dim) * dq[m][n][r];
-          d[1] += at_tile(sk, tok, dim) * dk[m][n][r];
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          d[x] = row16_sum(d[x]);
-          if (i == 0) sdot[wave][x][tok] = d[x];
+        const int tok = 16 * (m0 + m) + 4 * qd + r, dim = 16 * kt + i;
+        const float sums[2] = {row16_sum(at_tile(sq, tok, dim) * dq[m][r]), row16_sum(at_tile(sk, tok, dim) * dk[m][r])};
+        if (i == 0) {
+          sdot[kt][0][tok] = sums[0];
+          sdot[kt][1][tok] = sums[1];
         }
       }
     __syncthreads();
   }
+  const int dim = 16 * kt + i;
+  const Buffer dqb = rows_of(dq_out + t0 * qk_t, out_rows, qk_t, a.dk), dkb = rows_of(dk_out + t0 * qk_t, out_rows, qk_t, a.dk);
 #pragma unroll
-  for (int m = 0; m < 4; ++m)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int tok = 16 * m + 4 * qd + r, t = t0 + tok;
+      const int tok = 16 * (m0 + m) + 4 * qd + r;
       float fq = 0.0f, fk = 0.0f;
       if (a.qk_norm) {
         const float rk = svec[5 * kC + tok], rq = svec[6 * kC + tok];
-        fq = rq * rq * ((sdot[0][0][tok] + sdot[1][0][tok]) + (sdot[2][0][tok] + sdot[3][0][tok]));
-        fk = rk * rk * ((sdot[0][1][tok] + sdot[1][1][tok]) + (sdot[2][1][tok] + sdot[3][1][tok]));
-      }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int dim = 16 * (wave + 4 * n) + i;
-        if (t < L && dim < a.dk) {
-          dq_out[t * qk_t + dim] = IO(dq[m][n][r] - fq * at_tile(sq, tok, dim));
-          dk_out[t * qk_t + dim] = IO(dk[m][n][r] - fk * at_tile(sk, tok, dim));
+        for (int k = 0; k < kTilesK; ++k) {
+          fq += sdot[k][0][tok];
+          fk += sdot[k][1][tok];
         }
+        fq *= rq * rq;
+        fk *= rk * rk;
       }
+      const int at = dim < a.dk ? (tok * int(qk_t) + dim) * int(sizeof(IO)) : kOutside;
+      store1(dqb, at, IO(dq[m][r] - fq * at_tile(sq, tok, dim)));
+      store1(dkb, at, IO(dk[m][r] - fk * at_tile(sk, tok, dim)));
     }
+}
+
+// Value columns of a slab: what LDS holds beside K and Q.
+template <typename IO, int KP>
+void launch_grad(const DeltaBwdArgs& b, int n, const float* vec, const float* s, const float* e, const float* u,
+                 const float* x, int dvp, int wide, hipStream_t stream) {
+  constexpr bool kBf16 = std::is_same<IO, bf16>::value;
+  constexpr int kMost = kBf16 ? 128 : KP == 64 ? 64 : 32, kLeast = kMost < 64 ? kMost : 64;
+  const dim3 grid{unsigned(b.f.batch * b.f.hk * n)};
+  if (dvp > 64)
+    delta_grad_kernel<IO, KP, kMost><<<grid, 512, 0, stream>>>(b, n, vec, s, e, u, x, dvp, wide);
+  else
+    delta_grad_kernel<IO, KP, kLeast><<<grid, 512, 0, stream>>>(b, n, vec, s, e, u, x, dvp, wide);
 }
 
 template <typename IO, int KP, int W>
@@ -620,7 +681,7 @@ hipError_t launch_bwd(const DeltaBwdArgs& b, const DeltaBwdPlan& p, char* ws, hi
   }
   delta_chunk_bwd_kernel<IO, KP, W, false><<<walk, 64 * W, 0, stream>>>(b, wb);
   if (n > 0)
-    delta_grad_kernel<IO, KP><<<dim3(unsigned(a.batch * a.hk * n)), 256, 0, stream>>>(b, n, vec, s, e, u, x, f.dvp, wide);
+    launch_grad<IO, KP>(b, n, vec, s, e, u, x, f.dvp, wide, stream);
   return hipGetLastError();
 }
 

@@ -103,7 +103,8 @@ int view_delta(const sscan_delta_params* p, DeltaView* w) {
     return SSCAN_ERR_ALIGN;
   // a chunk's rows are addressed by 32-bit byte offsets
   if (p->q_stride[1] >= sscan::kDeltaMaxStride || p->k_stride[1] >= sscan::kDeltaMaxStride ||
-      p->v_stride[1] >= sscan::kDeltaMaxStride || p->v_heads * p->dv >= sscan::kDeltaMaxStride)
+      p->v_stride[1] >= sscan::kDeltaMaxStride || p->v_heads * p->dv >= sscan::kDeltaMaxStride ||
+      p->qk_heads * p->dk >= sscan::kDeltaMaxStride)
     return SSCAN_ERR_UNSUPPORTED;
   const int64_t qd[3] = {p->batch, p->len, p->qk_heads}, vd[3] = {p->batch, p->len, p->v_heads};
   const int64_t eq = extent(qd, p->q_stride, 3, p->dk), ek = extent(qd, p->k_stride, 3, p->dk),

@@ -205,6 +205,21 @@ __device__ __forceinline__ void load8(Buffer b, int off, int left, bool wide, V8
   }
 }
 
+template <typename T, typename V8>
+__device__ __forceinline__ void store8(Buffer b, int off, int left, bool wide, V8 x) {
+  if (wide) {
+    typedef unsigned W __attribute__((ext_vector_type(sizeof(V8) / 4)));
+    const W w = __builtin_bit_cast(W, x);
+    off = left > 0 ? off : kOutside;
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[0], w[1], w[2], w[3]}, b, off, 0, 0);
+    if constexpr (sizeof(V8) == 32)
+      __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[4], w[5], w[6], w[7]}, b, off + 16, 0, 0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) store1(b, j < left ? off + j * int(sizeof(T)) : kOutside, T(x[j]));
+  }
+}
+
 // A state's columns in the accumulator layout, from or to rows of `ld` floats: lane_at
 // is the byte offset of the lane's row 8 qd and column, or kOutside.
 template <int kTiles>
