@@ -333,6 +333,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
   f32x4 dq[MT] = {}, dk[MT] = {};
   for (int hh = 0; hh < share; ++hh) {
     const int h = hq * share + hh;
+    const int i = here(lane & 15), qd = here(lane >> 4);  // LDS addresses are not kept across heads
     const int64_t idx = (b * a.hv + h) * nchunk + c;
     const Buffer ub = buffer_of(values + idx * kC * dvp, kC * dvp * 4);
     const Buffer xb = buffer_of(xgrad + idx * kC * dvp, kC * dvp * 4);
@@ -353,6 +354,14 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
     f32x4 h1[MT] = {}, h2[MT] = {}, h3[MT] = {}, gacc[3] = {};
     float se = 0.0f;
     for (int v0 = 0; v0 < dvp; v0 += VS) {
+      // this wave's rows of S0 and E, on their way while the slab is staged
+      f32x8 s8[VS / 32], e8[VS / 32];
+#pragma unroll
+      for (int s = 0; s < VS / 32; ++s) {
+        const int at = v0 + 32 * s < dvp ? ((16 * kt + i) * dvp + v0 + 32 * s + 8 * qd) * 4 : kOutside;
+        load_wide(sb, at, &s8[s]);
+        load_wide(eb, at, &e8[s]);
+      }
       __syncthreads();
       // the slab of U, X~ and dO; dV = beta X~ and X~ . v on the way
 #pragma unroll
@@ -395,13 +404,9 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
 #pragma unroll
       for (int s = 0; s < VS / 32; ++s) {
         if (v0 + 32 * s >= dvp) break;
-        const int at = ((16 * kt + i) * dvp + v0 + 32 * s + 8 * qd) * 4;
-        f32x8 s8, e8;
-        load_wide(sb, at, &s8);
-        load_wide(eb, at, &e8);
-        const Frag<3> fs = split(s8), fe = split(e8);
+        const Frag<3> fs = split(s8[s]), fe = split(e8[s]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) se += s8[j] * e8[j];
+        for (int j = 0; j < 8; ++j) se += s8[s][j] * e8[s][j];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const int lds_at = SlabV::at(16 * (m0 + m) + i, 4 * s + qd);
