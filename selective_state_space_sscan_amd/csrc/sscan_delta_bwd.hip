@@ -330,17 +330,55 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
     return x;
   };
 
+  // What a slab needs, loaded while the one before it (or the last head's factors) is
+  // computed: a unit or two of U, X~, dO and V a thread, and this wave's rows of S0 and E.
+  constexpr int kAhead = (kC * VS / 8 + 511) / 512;
+  f32x8 next_u[kAhead], next_x[kAhead], s8[VS / 32], e8[VS / 32];
+  V8 next_d[kAhead], next_v[kAhead];
+  const auto unit_of = [&](int n, int* row, int* unit) {
+    const int u = here(tid) + 512 * n;
+    *row = u / SlabV::kUnits;
+    *unit = u % SlabV::kUnits;
+    return u < kC * SlabV::kUnits;
+  };
+  const auto load_slab = [&](int hh, int v0) {
+    const int h = hq * share + hh;
+    const int64_t idx = (b * a.hv + h) * nchunk + c;
+    const Buffer ub = buffer_of(values + idx * kC * dvp, kC * dvp * 4);
+    const Buffer xb = buffer_of(xgrad + idx * kC * dvp, kC * dvp * 4);
+    const Buffer db = rows_of(static_cast<const IO*>(b_.dout) + (b * a.len * a.hv + h) * a.dv + t0 * v_t, rows, v_t, a.dv);
+    const Buffer vb = rows_of(static_cast<const IO*>(a.v) + b * a.sv.b + h * a.sv.h + t0 * a.sv.t, rows, a.sv.t, a.dv);
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      int row, unit;
+      const bool live = unit_of(n, &row, &unit);
+      const int c8 = v0 + 8 * unit, at = live && c8 < dvp ? (row * dvp + c8) * 4 : kOutside, left = live ? a.dv - c8 : 0;
+      load_wide(ub, at, &next_u[n]);
+      load_wide(xb, at, &next_x[n]);
+      load8<IO>(db, (row * int(v_t) + c8) * int(sizeof(IO)), left, wide_d, &next_d[n]);
+      load8<IO>(vb, (row * int(a.sv.t) + c8) * int(sizeof(IO)), left, wide_v, &next_v[n]);
+    }
+  };
+  const auto load_states = [&](int hh, int v0) {
+    const int64_t idx = (b * a.hv + hq * share + hh) * nchunk + c;
+    const Buffer sb = buffer_of(states + idx * KP * dvp, KP * dvp * 4);
+    const Buffer eb = buffer_of(adjoints + idx * KP * dvp, KP * dvp * 4);
+    const int l = here(lane), row = 16 * kt + (l & 15);
+#pragma unroll
+    for (int s = 0; s < VS / 32; ++s) {
+      const int at = v0 + 32 * s < dvp ? (row * dvp + v0 + 32 * s + 8 * (l >> 4)) * 4 : kOutside;
+      load_wide(sb, at, &s8[s]);
+      load_wide(eb, at, &e8[s]);
+    }
+  };
+  load_slab(0, 0);
+  load_states(0, 0);
+
   f32x4 dq[MT] = {}, dk[MT] = {};
   for (int hh = 0; hh < share; ++hh) {
     const int h = hq * share + hh;
     const int i = here(lane & 15), qd = here(lane >> 4);  // LDS addresses are not kept across heads
     const int64_t idx = (b * a.hv + h) * nchunk + c;
-    const Buffer ub = buffer_of(values + idx * kC * dvp, kC * dvp * 4);
-    const Buffer xb = buffer_of(xgrad + idx * kC * dvp, kC * dvp * 4);
-    const Buffer sb = buffer_of(states + idx * KP * dvp, KP * dvp * 4);
-    const Buffer eb = buffer_of(adjoints + idx * KP * dvp, KP * dvp * 4);
-    const Buffer db = rows_of(static_cast<const IO*>(b_.dout) + (b * a.len * a.hv + h) * a.dv + t0 * v_t, rows, v_t, a.dv);
-    const Buffer vb = rows_of(static_cast<const IO*>(a.v) + b * a.sv.b + h * a.sv.h + t0 * a.sv.t, rows, a.sv.t, a.dv);
     const Buffer gb = rows_of(static_cast<const IO*>(b_.dv) + (b * a.len * a.hv + h) * a.dv + t0 * v_t, out_rows, v_t, a.dv);
     __syncthreads();  // the last head's readers are done
     if (tid < kVecFloatsBwd) svec[tid] = vec[idx * kVecFloatsBwd + tid];
@@ -354,51 +392,38 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
     f32x4 h1[MT] = {}, h2[MT] = {}, h3[MT] = {}, gacc[3] = {};
     float se = 0.0f;
     for (int v0 = 0; v0 < dvp; v0 += VS) {
-      // this wave's rows of S0 and E, on their way while the slab is staged
-      f32x8 s8[VS / 32], e8[VS / 32];
-#pragma unroll
-      for (int s = 0; s < VS / 32; ++s) {
-        const int at = v0 + 32 * s < dvp ? ((16 * kt + i) * dvp + v0 + 32 * s + 8 * qd) * 4 : kOutside;
-        load_wide(sb, at, &s8[s]);
-        load_wide(eb, at, &e8[s]);
-      }
+      const bool more = v0 + VS < dvp, any = more || hh + 1 < share;
+      const int next_hh = more ? hh : hh + 1, next_v0 = more ? v0 + VS : 0;
       __syncthreads();
       // the slab of U, X~ and dO; dV = beta X~ and X~ . v on the way
 #pragma unroll
-      for (int n = 0; n < (kC * VS / 8 + 511) / 512; ++n) {
-        const int u = tid + 512 * n, row = u / SlabV::kUnits, unit = u % SlabV::kUnits, c8 = v0 + 8 * unit;
-        if (u < kC * SlabV::kUnits) {
-          const int at = c8 < dvp ? (row * dvp + c8) * 4 : kOutside;
-          f32x8 uv, xv;
-          V8 dv, vv;
-          load_wide(ub, at, &uv);
-          load_wide(xb, at, &xv);
-          load8<IO>(db, (row * int(v_t) + c8) * int(sizeof(IO)), a.dv - c8, wide_d, &dv);
-          load8<IO>(vb, (row * int(a.sv.t) + c8) * int(sizeof(IO)), a.dv - c8, wide_v, &vv);
-          const Frag<3> fu = split(uv), fx = split(xv);
-          const auto fd = as_frag(dv);
-          const int lds_at = SlabV::at(row, unit);
+      for (int n = 0; n < kAhead; ++n) {
+        int row, unit;
+        if (!unit_of(n, &row, &unit)) continue;
+        const int c8 = v0 + 8 * unit, lds_at = SlabV::at(row, unit);
+        const Frag<3> fu = split(next_u[n]), fx = split(next_x[n]);
+        const auto fd = as_frag(next_d[n]);
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            *reinterpret_cast<bf16x8*>(su + k * SlabV::kElems + lds_at) = fu.t[k];
-            *reinterpret_cast<bf16x8*>(sx + k * SlabV::kElems + lds_at) = fx.t[k];
-          }
-#pragma unroll
-          for (int k = 0; k < N; ++k) *reinterpret_cast<bf16x8*>(sd + k * SlabV::kElems + lds_at) = fd.t[k];
-          const float beta = svec[4 * kC + row];
-          float dot = 0.0f;
-          V8 y;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            dot += xv[j] * float(vv[j]);
-            y[j] = IO(beta * xv[j]);
-          }
-          store8<IO>(gb, (row * int(v_t) + c8) * int(sizeof(IO)), a.dv - c8, wide_gv, y);
-#pragma unroll
-          for (int k = 1; k < SlabV::kUnits; k *= 2) dot += __shfl_xor(dot, k);
-          if (unit == 0) sxv[row] += dot;  // the same thread for every slab
+        for (int k = 0; k < 3; ++k) {
+          *reinterpret_cast<bf16x8*>(su + k * SlabV::kElems + lds_at) = fu.t[k];
+          *reinterpret_cast<bf16x8*>(sx + k * SlabV::kElems + lds_at) = fx.t[k];
         }
+#pragma unroll
+        for (int k = 0; k < N; ++k) *reinterpret_cast<bf16x8*>(sd + k * SlabV::kElems + lds_at) = fd.t[k];
+        const float beta = svec[4 * kC + row];
+        float dot = 0.0f;
+        V8 y;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          dot += next_x[n][j] * float(next_v[n][j]);
+          y[j] = IO(beta * next_x[n][j]);
+        }
+        store8<IO>(gb, (row * int(v_t) + c8) * int(sizeof(IO)), a.dv - c8, wide_gv, y);
+#pragma unroll
+        for (int k = 1; k < SlabV::kUnits; k *= 2) dot += __shfl_xor(dot, k);
+        if (unit == 0) sxv[row] += dot;  // the same thread for every slab
       }
+      if (any) load_slab(next_hh, next_v0);
       __syncthreads();
       // products with the states: dO S0^T, X~ S0^T, U E^T
 #pragma unroll
@@ -447,6 +472,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
           }
         }
       }
+      if (any) load_states(next_hh, next_v0);
     }
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) se += __shfl_xor(se, m);
@@ -646,12 +672,9 @@ template <typename IO, int KP>
 void launch_grad(const DeltaBwdArgs& b, int n, const float* vec, const float* s, const float* e, const float* u,
                  const float* x, int dvp, int wide, hipStream_t stream) {
   constexpr bool kBf16 = std::is_same<IO, bf16>::value;
-  constexpr int kMost = kBf16 ? 128 : KP == 64 ? 64 : 32, kLeast = kMost < 64 ? kMost : 64;
+  constexpr int kMost = kBf16 || KP == 64 ? 64 : 32;
   const dim3 grid{unsigned(b.f.batch * b.f.hk * n)};
-  if (dvp > 64)
-    delta_grad_kernel<IO, KP, kMost><<<grid, 512, 0, stream>>>(b, n, vec, s, e, u, x, dvp, wide);
-  else
-    delta_grad_kernel<IO, KP, kLeast><<<grid, 512, 0, stream>>>(b, n, vec, s, e, u, x, dvp, wide);
+  delta_grad_kernel<IO, KP, kMost><<<grid, 512, 0, stream>>>(b, n, vec, s, e, u, x, dvp, wide);
 }
 
 template <typename IO, int KP, int W>
