@@ -131,9 +131,11 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int nchunk
   __shared__ float srk[kC], srq[kC], from[3][kC], to_end[kC];
 
   const int tid = int(threadIdx.x), lane = tid & 63, wave = wave_id(), i = lane & 15, qd = lane >> 4;
-  const int c = int(blockIdx.x % unsigned(nchunk));
-  const int64_t idx = blockIdx.x, bh = blockIdx.x / unsigned(nchunk), b = bh / a.hv;
-  const int h = int(bh % a.hv), hq = h / (a.hv / a.hk);
+  // fewer than 2^24 blocks: 32-bit divisions
+  const unsigned bh = blockIdx.x / unsigned(nchunk), row_b = bh / unsigned(a.hv);
+  const int c = int(blockIdx.x - bh * unsigned(nchunk)), h = int(bh - row_b * unsigned(a.hv));
+  const int hq = int(unsigned(h) / (unsigned(a.hv) / unsigned(a.hk)));
+  const int64_t idx = blockIdx.x, b = row_b;
   const int Lb = row_len(a.lengths, b, a.len), t0 = c * kC;
   if (t0 >= Lb) return;
   const bool wide_qk = wide & 1;
@@ -180,7 +182,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int nchunk
     }
     ssq += __shfl_xor(ssq, 16);
     ssq += __shfl_xor(ssq, 32);
-    if (qd == 0) srq[16 * wave + i] = a.qk_norm ? 1.0f / sqrtf(ssq + 1e-6f) : 1.0f;
+    // the keys' squares are the diagonal of K K^T: lane (qd, i) with i / 4 == qd holds key i's
+    float diag = 0.0f;
 #pragma unroll
     for (int ct = 0; ct < 4; ++ct) {
       kk[ct] = qk[ct] = f32x4{};
@@ -197,11 +200,19 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int nchunk
         kk[ct] = mul(fk[s], fb, kk[ct]);
         qk[ct] = mul(fq[s], fb, qk[ct]);
       }
-      if (ct == wave) {  // the diagonal holds the keys' squares
+      if (ct == wave) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (4 * qd + r == i) srk[16 * wave + i] = a.qk_norm ? 1.0f / sqrtf(kk[ct][r] + 1e-6f) : 1.0f;
+        for (int r = 0; r < 4; ++r) diag = (i & 3) == r ? kk[ct][r] : diag;
       }
+    }
+    float rq = 1.0f, rk = 1.0f;
+    if (a.qk_norm) {
+      rq = 1.0f / sqrtf(ssq + 1e-6f);
+      rk = 1.0f / sqrtf(diag + 1e-6f);
+    }
+    if ((i >> 2) == qd) {
+      srq[16 * wave + i] = rq;
+      srk[16 * wave + i] = rk;
     }
   }
   __syncthreads();
@@ -218,18 +229,30 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int nchunk
       v[6 * kC + lane] = srq[lane];
     }
   }
-#pragma unroll
-  for (int ct = 0; ct < 4; ++ct) {
-    const int tj = 16 * ct + i;
+  {
+    const int row = 16 * wave + 4 * qd;
+    float fk[4], fq[4];  // beta rk, scale rq of this lane's four rows
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int ti = 16 * wave + 4 * qd + r;
-      float decay = 0.0f;
-      if (ct < wave) decay = from[ct < 3 ? ct : 0][ti] * to_end[tj];
-      if (ct == wave && tj <= ti) decay = expf(float(gsum[ti] - gsum[tj]));
-      decay *= srk[tj];
-      tmat[ti * kLdM + tj] = tj < ti ? sbeta[ti] * decay * srk[ti] * kk[ct][r] : 0.0f;
-      pmat[ti * kLdM + tj] = tj <= ti ? a.scale * decay * srq[ti] * qk[ct][r] : 0.0f;
+      fk[r] = sbeta[row + r] * srk[row + r];
+      fq[r] = a.scale * srq[row + r];
+    }
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) {
+      if (ct > (wave | 1)) continue;  // only the tile that shares a fragment with the diagonal is read beyond it
+      const int tj = 16 * ct + i;
+      const float rk = srk[tj], end = to_end[tj];
+      const double sum_j = gsum[tj];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float decay = 0.0f;
+        if (ct < wave) decay = from[ct < 3 ? ct : 0][row + r] * end;
+        if (ct == wave) decay = expf(float(gsum[row + r] - sum_j));
+        decay *= rk;
+        const float t = fk[r] * decay * kk[ct][r], p = fq[r] * decay * qk[ct][r];
+        tmat[(row + r) * kLdM + tj] = ct < wave || tj < row + r ? t : 0.0f;
+        pmat[(row + r) * kLdM + tj] = ct < wave || tj <= row + r ? p : 0.0f;
+      }
     }
   }
   __syncthreads();
