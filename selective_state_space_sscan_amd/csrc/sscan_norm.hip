@@ -2,8 +2,8 @@
 // mixer's heads normed with their silu gate, and the residual scale and sum with the
 // next block's norm.  All of them are bound by HBM: a group of TPR threads holds one
 // normed vector in registers (eight elements a thread), so every input is read once
-// and every output written once, and blocks walk over rows so that the weights are
-// loaded once per block.  Sums and norms are float32.  The gradients of
+// and every output written once; blocks walk over rows, so that the weights are loaded
+// once per block and the next row's values while a row is reduced.  Sums and norms are float32.  The gradients of
 // the weights are summed per thread over a block's rows, across the block in LDS and
 // over the blocks by a second kernel, always in the same order.
 #include "sscan_delta.h"
@@ -18,8 +18,11 @@ using delta::bf16x8;
 using delta::f32x4;
 using delta::f32x8;
 
-constexpr int kMaxBlocks = 2048;     // forward: blocks that walk over the rows
-constexpr int kMaxBackBlocks = 512;  // backward: each leaves one row of partial sums
+// Blocks that walk over the rows.  Forward, 16384 x 16 x 128 bf16: 8192 blocks 34.9 us, 4096
+// 36.5.  Backward each block leaves a row of partial sums: gated norm, 8192 x 1536 bf16,
+// 1024 blocks 30.9 us, 512 38.7; residual norm with a post norm (three rows of sums and
+// 157 registers a thread: 512 blocks are most of what fits) 512 blocks 87 us, 1024 100.
+constexpr int kMaxBlocks = 8192, kMaxGatedBackBlocks = 1024, kMaxAddBackBlocks = 512;
 
 template <int TPR>
 constexpr int threads() {
@@ -69,22 +72,30 @@ __device__ __forceinline__ void load_or(const float* p, int size, int t, bool wi
   }
 }
 
-// Sum over the TPR threads of a group; every thread of the block takes part.
-template <int TPR>
-__device__ __forceinline__ float group_sum(float x, float* lds) {
+// Sums over the TPR threads of a group, n of them at once; every thread of the block
+// takes part.  Consecutive calls of a block alternate `turn`, so that one barrier a call
+// is enough: a buffer is written again only after the barrier of the call between.
+template <int TPR, int n>
+__device__ __forceinline__ void group_sum(float (&x)[n], float (*lds)[3][16], int turn) {
 #pragma unroll
-  for (int m = 1; m < (TPR < 64 ? TPR : 64); m *= 2) x += __shfl_xor(x, m);
+  for (int k = 0; k < n; ++k)
+#pragma unroll
+    for (int m = 1; m < (TPR < 64 ? TPR : 64); m *= 2) x[k] += __shfl_xor(x[k], m);
   if constexpr (TPR > 64) {
     constexpr int kWaves = TPR / 64;
     const int wave = int(threadIdx.x) >> 6;
-    __syncthreads();  // the last sum's readers are done
-    if ((threadIdx.x & 63) == 0) lds[wave] = x;
-    __syncthreads();
-    x = lds[wave / kWaves * kWaves];
+    if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) x += lds[wave / kWaves * kWaves + w];
+      for (int k = 0; k < n; ++k) lds[turn][k][wave] = x[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      x[k] = lds[turn][k][wave / kWaves * kWaves];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) x[k] += lds[turn][k][wave / kWaves * kWaves + w];
+    }
   }
-  return x;
 }
 
 // Adds the groups' sums of one block in order and writes them as the block's partial.
@@ -112,79 +123,137 @@ constexpr int partial_lds() {
   return TPR >= 256 ? 16 : 256 * 8;
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+// By the hardware's exp2 and reciprocal (one unit in the last place each): the error is
+// (|z| + 2) 2^-24 of the value, and the gradients' kernel would otherwise spend as long on
+// expf and the division as on its memory traffic.
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
+}
+
+// A group's walk over the units (row, head) first, first + step, ...: divided once, then
+// advanced by the step's quotient and remainder.
+struct UnitWalk {
+  int64_t u, row, h, units, heads, step, step_rows, step_heads;
+
+  __device__ __forceinline__ UnitWalk(int64_t first, int64_t step_, int64_t units_, int64_t heads_)
+      : u(first), units(units_), heads(heads_), step(step_) {
+    row = heads == 1 ? u : u / heads;
+    h = heads == 1 ? 0 : u % heads;
+    step_rows = heads == 1 ? step : step / heads;
+    step_heads = heads == 1 ? 0 : step % heads;
+  }
+  __device__ __forceinline__ bool live() const { return u < units; }
+  __device__ __forceinline__ void next() {
+    u += step;
+    row += step_rows;
+    h += step_heads;
+    if (h >= heads) {
+      h -= heads;
+      ++row;
+    }
+  }
+};
 
 // ---- norm and gate of a mixer's heads -------------------------------------------------
 //   y = x r w silu(z), r = 1 / rms(x)           (gate after the norm)
 //   y = m r w, m = x silu(z), r = 1 / rms(m)    (gate_first)
-template <typename IO, int TPR>
-__global__ __launch_bounds__(threads<TPR>()) void gated_norm_kernel(GatedNormArgs a, bool wide) {
-  __shared__ float lds[16];
+template <typename IO, int TPR, bool wide>
+__global__ __launch_bounds__(threads<TPR>()) void gated_norm_kernel(GatedNormArgs a) {
+  __shared__ float lds[2][3][16];
   constexpr int kGroups = threads<TPR>() / TPR;
   const int t = int(threadIdx.x) % TPR, grp = int(threadIdx.x) / TPR;
   const int64_t units = a.rows * a.heads, step = int64_t(gridDim.x) * kGroups;
-  float w[8];
-  if (!a.per_head) load_or<TPR>(a.weight, a.size, t, wide, 1.0f, w);
+  UnitWalk at(int64_t(blockIdx.x) * kGroups + grp, step, units, a.heads);
+  float w[8], next_x[8], next_z[8], next_w[8];
+  const auto load_next = [&] {
+    const int size = at.live() ? int(a.size) : 0;
+    load<IO, TPR>(static_cast<const IO*>(a.x) + at.row * a.xr + at.h * a.xh, size, t, wide, next_x);
+    load<IO, TPR>(static_cast<const IO*>(a.z) + at.row * a.zr + at.h * a.zh, size, t, wide, next_z);
+    if (a.per_head) load<float, TPR>(a.weight + at.h * a.size, size, t, wide, next_w);
+  };
+  if (!a.per_head) load_or<TPR>(a.weight, int(a.size), t, wide, 1.0f, w);
+  load_next();
+  const float inv = 1.0f / float(a.size);
+  int turn = 0;
   for (int64_t u0 = int64_t(blockIdx.x) * kGroups; u0 < units; u0 += step) {
-    const int64_t u = u0 + grp;
-    const bool live = u < units;
-    const int64_t row = live ? u / a.heads : 0, h = live ? u % a.heads : 0;
-    const int size = live ? int(a.size) : 0;
-    float x[8], z[8];
-    load<IO, TPR>(static_cast<const IO*>(a.x) + row * a.xr + h * a.xh, size, t, wide, x);
-    load<IO, TPR>(static_cast<const IO*>(a.z) + row * a.zr + h * a.zh, size, t, wide, z);
-    if (a.per_head) load<float, TPR>(a.weight + h * a.size, size, t, wide, w);
-    float ss = 0.0f;
+    float x[8], z[8], ss[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = next_x[j];
+      z[j] = next_z[j];
+      if (a.per_head) w[j] = next_w[j];
+    }
+    const int size = at.live() ? int(a.size) : 0;
+    IO* out = static_cast<IO*>(a.out) + at.u * a.size;
+    at.next();
+    load_next();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       z[j] *= sigmoid(z[j]);
       if (a.gate_first) x[j] *= z[j];
-      ss += x[j] * x[j];
+      ss[0] += x[j] * x[j];
     }
-    const float r = 1.0f / sqrtf(group_sum<TPR>(ss, lds) / float(a.size) + a.eps);
+    group_sum<TPR>(ss, lds, turn);
+    turn ^= 1;
+    const float r = 1.0f / sqrtf(ss[0] * inv + a.eps);
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] *= a.gate_first ? r * w[j] : r * w[j] * z[j];
-    store<IO, TPR>(static_cast<IO*>(a.out) + u * a.size, size, t, wide, x);
+    store<IO, TPR>(out, size, t, wide, x);
   }
 }
 
 // With n = m r the gradient at m is r (dn - m r^2 mean(dn m)).  Per block: all units
 // (shared weight), or the units of head blockIdx % heads (per_head).
-template <typename IO, int TPR>
-__global__ __launch_bounds__(threads<TPR>()) void gated_norm_bwd_kernel(GatedNormArgs a, float* partial, bool wide) {
-  __shared__ float lds[partial_lds<TPR>()];
+template <typename IO, int TPR, bool wide>
+__global__ __launch_bounds__(threads<TPR>()) void gated_norm_bwd_kernel(GatedNormArgs a, float* partial) {
+  __shared__ float lds[2][3][16];
+  __shared__ float sums[partial_lds<TPR>()];
   constexpr int kGroups = threads<TPR>() / TPR;
   const int t = int(threadIdx.x) % TPR, grp = int(threadIdx.x) / TPR;
-  const int64_t heads = a.per_head ? a.heads : 1;  // heads told apart
-  const int64_t head = int64_t(blockIdx.x) % heads;
-  const int64_t units = a.per_head ? a.rows : a.rows * a.heads;
-  const int64_t step = int64_t(gridDim.x) / heads * kGroups;
-  float w[8], dw[8] = {};
-  load_or<TPR>(a.weight ? a.weight + head * a.size : nullptr, a.size, t, wide, 1.0f, w);
-  for (int64_t u0 = int64_t(blockIdx.x) / heads * kGroups; u0 < units; u0 += step) {
-    const int64_t u = u0 + grp;
-    const bool live = u < units;
-    const int64_t row = !live ? 0 : a.per_head ? u : u / a.heads, h = !live ? 0 : a.per_head ? head : u % a.heads;
-    const int size = live ? int(a.size) : 0;
-    const int64_t flat = (row * a.heads + h) * a.size;
-    float x[8], z[8], d[8];
-    load<IO, TPR>(static_cast<const IO*>(a.x) + row * a.xr + h * a.xh, size, t, wide, x);
-    load<IO, TPR>(static_cast<const IO*>(a.z) + row * a.zr + h * a.zh, size, t, wide, z);
-    load<IO, TPR>(static_cast<const IO*>(a.dout) + flat, size, t, wide, d);
-    float ss = 0.0f, dot = 0.0f;
+  const int64_t sets = a.per_head ? a.heads : 1;  // heads told apart
+  const int64_t set = int64_t(blockIdx.x) % sets, first = int64_t(blockIdx.x) / sets * kGroups;
+  const int64_t units = a.per_head ? a.rows : a.rows * a.heads, step = int64_t(gridDim.x) / sets * kGroups;
+  UnitWalk at(first + grp, step, units, a.per_head ? 1 : a.heads);
+  float w[8], dw[8] = {}, next_x[8], next_z[8], next_d[8];
+  const auto load_next = [&] {
+    const int size = at.live() ? int(a.size) : 0;
+    const int64_t h = a.per_head ? set : at.h;
+    load<IO, TPR>(static_cast<const IO*>(a.x) + at.row * a.xr + h * a.xh, size, t, wide, next_x);
+    load<IO, TPR>(static_cast<const IO*>(a.z) + at.row * a.zr + h * a.zh, size, t, wide, next_z);
+    load<IO, TPR>(static_cast<const IO*>(a.dout) + (at.row * a.heads + h) * a.size, size, t, wide, next_d);
+  };
+  load_or<TPR>(a.weight ? a.weight + set * a.size : nullptr, int(a.size), t, wide, 1.0f, w);
+  load_next();
+  const float inv = 1.0f / float(a.size);
+  int turn = 0;
+  for (int64_t u0 = first; u0 < units; u0 += step) {
+    float x[8], z[8], d[8], sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float sig = sigmoid(z[j]), gate = z[j] * sig;
+      x[j] = next_x[j];
+      z[j] = next_z[j];
+      d[j] = next_d[j];
+    }
+    const int size = at.live() ? int(a.size) : 0;
+    const int64_t flat = (at.row * a.heads + (a.per_head ? set : at.h)) * a.size;
+    at.next();
+    load_next();
+    float sig[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      sig[j] = sigmoid(z[j]);
+      const float gate = z[j] * sig[j];
       const float m = a.gate_first ? x[j] * gate : x[j];
       const float dn = a.gate_first ? d[j] * w[j] : d[j] * w[j] * gate;
-      ss += m * m;
-      dot += dn * m;
+      sum[0] += m * m;
+      sum[1] += dn * m;
     }
-    const float r = 1.0f / sqrtf(group_sum<TPR>(ss, lds) / float(a.size) + a.eps);
-    const float mean = group_sum<TPR>(dot, lds) / float(a.size);
+    group_sum<TPR>(sum, lds, turn);
+    turn ^= 1;
+    const float r = 1.0f / sqrtf(sum[0] * inv + a.eps), mean = sum[1] * inv;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float sig = sigmoid(z[j]), gate = z[j] * sig, slope = sig * (1.0f + z[j] * (1.0f - sig));
+      const float gate = z[j] * sig[j], slope = sig[j] * (1.0f + z[j] * (1.0f - sig[j]));
       if (a.gate_first) {
         const float m = x[j] * gate, dm = r * (d[j] * w[j] - m * (r * r) * mean);
         dw[j] += d[j] * m * r;
@@ -200,45 +269,62 @@ __global__ __launch_bounds__(threads<TPR>()) void gated_norm_bwd_kernel(GatedNor
     store<IO, TPR>(static_cast<IO*>(a.dx) + flat, size, t, wide, x);
     store<IO, TPR>(static_cast<IO*>(a.dz) + flat, size, t, wide, z);
   }
-  if (a.dweight) write_partial<TPR>(partial + int64_t(blockIdx.x) * a.size, a.size, t, wide, dw, lds);
+  if (a.dweight) write_partial<TPR>(partial + int64_t(blockIdx.x) * a.size, int(a.size), t, wide, dw, sums);
 }
 
 // ---- residual scale and sum with the next norm ----------------------------------------
 //   total = residual + scale a, a = x or x / rms(x) * post_weight; out = total / rms(total) * weight
 // The norm is taken of the total as it is stored, so that the backward pass (which
 // reads the stored total) differentiates what was computed.
-template <typename IO, typename RES, int TPR>
-__global__ __launch_bounds__(threads<TPR>()) void add_norm_kernel(AddNormArgs a, bool wide) {
-  __shared__ float lds[16];
+template <typename IO, typename RES, int TPR, bool wide>
+__global__ __launch_bounds__(threads<TPR>()) void add_norm_kernel(AddNormArgs a) {
+  __shared__ float lds[2][3][16];
   constexpr int kGroups = threads<TPR>() / TPR;
   const int t = int(threadIdx.x) % TPR, grp = int(threadIdx.x) / TPR;
-  float w[8], sc[8], pw[8];
-  load_or<TPR>(a.weight, a.size, t, wide, 1.0f, w);
-  load_or<TPR>(a.scale, a.size, t, wide, 1.0f, sc);
-  load_or<TPR>(a.post_weight, a.size, t, wide, 1.0f, pw);
-  for (int64_t u0 = int64_t(blockIdx.x) * kGroups; u0 < a.rows; u0 += int64_t(gridDim.x) * kGroups) {
-    const bool live = u0 + grp < a.rows;
-    const int64_t flat = (live ? u0 + grp : 0) * a.size;
-    const int size = live ? int(a.size) : 0;
+  const int64_t step = int64_t(gridDim.x) * kGroups;
+  float w[8], sc[8], pw[8], next_x[8], next_y[8];
+  const auto load_next = [&](int64_t u) {
+    const int size = u < a.rows ? int(a.size) : 0;
+    const int64_t flat = size ? u * a.size : 0;
+    load<IO, TPR>(static_cast<const IO*>(a.x) + flat, size, t, wide, next_x);
+    load<RES, TPR>(static_cast<const RES*>(a.residual) + flat, a.residual ? size : 0, t, wide, next_y);
+  };
+  load_next(int64_t(blockIdx.x) * kGroups + grp);
+  load_or<TPR>(a.weight, int(a.size), t, wide, 1.0f, w);
+  load_or<TPR>(a.scale, int(a.size), t, wide, 1.0f, sc);
+  load_or<TPR>(a.post_weight, int(a.size), t, wide, 1.0f, pw);
+  const float inv = 1.0f / float(a.size);
+  int turn = 0;
+  for (int64_t u0 = int64_t(blockIdx.x) * kGroups; u0 < a.rows; u0 += step) {
+    const int64_t u = u0 + grp, flat = u * a.size;
+    const int size = u < a.rows ? int(a.size) : 0;
     float x[8], y[8];
-    load<IO, TPR>(static_cast<const IO*>(a.x) + flat, size, t, wide, x);
-    load<RES, TPR>(static_cast<const RES*>(a.residual) + flat, a.residual ? size : 0, t, wide, y);
-    if (a.post_weight) {
-      float ss = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
-      const float r = 1.0f / sqrtf(group_sum<TPR>(ss, lds) / float(a.size) + a.eps);
+    for (int j = 0; j < 8; ++j) {
+      x[j] = next_x[j];
+      y[j] = next_y[j];
+    }
+    load_next(u + step);
+    if (a.post_weight) {
+      float ss[1] = {0.0f};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss[0] += x[j] * x[j];
+      group_sum<TPR>(ss, lds, turn);
+      turn ^= 1;
+      const float r = 1.0f / sqrtf(ss[0] * inv + a.eps);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] *= r * pw[j];
     }
-    float ss = 0.0f;
+    float ss[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       y[j] = float(RES(y[j] + x[j] * sc[j]));
-      ss += y[j] * y[j];
+      ss[0] += y[j] * y[j];
     }
     store<RES, TPR>(static_cast<RES*>(a.residual_out) + flat, size, t, wide, y);
-    const float r = 1.0f / sqrtf(group_sum<TPR>(ss, lds) / float(a.size) + a.eps);
+    group_sum<TPR>(ss, lds, turn);
+    turn ^= 1;
+    const float r = 1.0f / sqrtf(ss[0] * inv + a.eps);
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] *= r * w[j];
     store<IO, TPR>(static_cast<IO*>(a.out) + flat, size, t, wide, y);
@@ -246,36 +332,64 @@ __global__ __launch_bounds__(threads<TPR>()) void add_norm_kernel(AddNormArgs a,
 }
 
 // POST: with a norm of x itself.  Sums left by a block: dweight, dscale, dpost_weight.
-template <typename IO, typename RES, int TPR, bool POST>
-__global__ __launch_bounds__(threads<TPR>()) void add_norm_bwd_kernel(AddNormArgs a, float* partial, bool wide) {
-  __shared__ float lds[partial_lds<TPR>()];
+// Blocks of 1024 threads have 128 registers a thread: they read the vectors per row.
+template <typename IO, typename RES, int TPR, bool wide, bool POST>
+__global__ __launch_bounds__(threads<TPR>()) void add_norm_bwd_kernel(AddNormArgs a, float* partial) {
+  __shared__ float lds[2][3][16];
+  __shared__ float sums[partial_lds<TPR>()];
   constexpr int kGroups = threads<TPR>() / TPR;
+  constexpr bool kHold = TPR < 1024;
   const int t = int(threadIdx.x) % TPR, grp = int(threadIdx.x) / TPR;
+  const int64_t step = int64_t(gridDim.x) * kGroups;
   float w[8], sc[8], pw[8], dw[8] = {}, ds[8] = {}, dp[8] = {};
-  load_or<TPR>(a.weight, a.size, t, wide, 1.0f, w);
-  load_or<TPR>(a.scale, a.size, t, wide, 1.0f, sc);
-  if (POST) load_or<TPR>(a.post_weight, a.size, t, wide, 1.0f, pw);
+  float next_x[8], next_y[8], next_d[8], next_e[8];
+  const auto load_next = [&](int64_t u) {
+    const int size = u < a.rows ? int(a.size) : 0;
+    const int64_t flat = size ? u * a.size : 0;
+    load<IO, TPR>(static_cast<const IO*>(a.x) + flat, size, t, wide, next_x);
+    load<RES, TPR>(static_cast<const RES*>(a.residual) + flat, size, t, wide, next_y);
+    load<IO, TPR>(static_cast<const IO*>(a.dout) + flat, size, t, wide, next_d);
+    load<RES, TPR>(static_cast<const RES*>(a.dresidual_out) + flat, a.dresidual_out ? size : 0, t, wide, next_e);
+  };
+  const auto load_vectors = [&] {
+    load_or<TPR>(a.weight, int(a.size), t, wide, 1.0f, w);
+    load_or<TPR>(a.scale, int(a.size), t, wide, 1.0f, sc);
+    if (POST) load_or<TPR>(a.post_weight, int(a.size), t, wide, 1.0f, pw);
+  };
+  if (kHold) {
+    load_next(int64_t(blockIdx.x) * kGroups + grp);
+    load_vectors();
+  }
   const float inv = 1.0f / float(a.size);
-  for (int64_t u0 = int64_t(blockIdx.x) * kGroups; u0 < a.rows; u0 += int64_t(gridDim.x) * kGroups) {
-    const bool live = u0 + grp < a.rows;
-    const int64_t flat = (live ? u0 + grp : 0) * a.size;
-    const int size = live ? int(a.size) : 0;
+  int turn = 0;
+  for (int64_t u0 = int64_t(blockIdx.x) * kGroups; u0 < a.rows; u0 += step) {
+    const int64_t u = u0 + grp, flat = u * a.size;
+    const int size = u < a.rows ? int(a.size) : 0;
+    if (!kHold) {
+      load_next(u);
+      load_vectors();
+    }
     float x[8], y[8], d[8], e[8];
-    load<IO, TPR>(static_cast<const IO*>(a.x) + flat, size, t, wide, x);
-    load<RES, TPR>(static_cast<const RES*>(a.residual) + flat, size, t, wide, y);
-    load<IO, TPR>(static_cast<const IO*>(a.dout) + flat, size, t, wide, d);
-    load<RES, TPR>(static_cast<const RES*>(a.dresidual_out) + flat, a.dresidual_out ? size : 0, t, wide, e);
-    float ss = 0.0f, dot = 0.0f, xx = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      ss += y[j] * y[j];
-      dot += d[j] * w[j] * y[j];
-      if (POST) xx += x[j] * x[j];
+      x[j] = next_x[j];
+      y[j] = next_y[j];
+      d[j] = next_d[j];
+      e[j] = next_e[j];
     }
-    const float r = 1.0f / sqrtf(group_sum<TPR>(ss, lds) * inv + a.eps);
-    const float mean = group_sum<TPR>(dot, lds) * inv;
-    const float rx = POST ? 1.0f / sqrtf(group_sum<TPR>(xx, lds) * inv + a.eps) : 1.0f;
-    float dot2 = 0.0f;
+    if (kHold) load_next(u + step);
+    float sum[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      sum[0] += y[j] * y[j];
+      sum[1] += d[j] * w[j] * y[j];
+      if (POST) sum[2] += x[j] * x[j];
+    }
+    group_sum<TPR>(sum, lds, turn);
+    turn ^= 1;
+    const float r = 1.0f / sqrtf(sum[0] * inv + a.eps), mean = sum[1] * inv;
+    const float rx = POST ? 1.0f / sqrtf(sum[2] * inv + a.eps) : 1.0f;
+    float dot[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       dw[j] += d[j] * y[j] * r;
@@ -285,7 +399,7 @@ __global__ __launch_bounds__(threads<TPR>()) void add_norm_bwd_kernel(AddNormArg
         ds[j] += e[j] * n * pw[j];
         dp[j] += scaled * n;
         d[j] = scaled * pw[j];
-        dot2 += d[j] * x[j];
+        dot[0] += d[j] * x[j];
       } else {
         ds[j] += e[j] * x[j];
         d[j] = scaled;
@@ -293,45 +407,51 @@ __global__ __launch_bounds__(threads<TPR>()) void add_norm_bwd_kernel(AddNormArg
     }
     store<RES, TPR>(static_cast<RES*>(a.dresidual) + flat, size, t, wide, e);
     if (POST) {
-      const float m2 = group_sum<TPR>(dot2, lds) * inv;
+      group_sum<TPR>(dot, lds, turn);
+      turn ^= 1;
+      const float m2 = dot[0] * inv;
 #pragma unroll
       for (int j = 0; j < 8; ++j) d[j] = rx * (d[j] - x[j] * (rx * rx) * m2);
     }
     store<IO, TPR>(static_cast<IO*>(a.dx) + flat, size, t, wide, d);
   }
   float* dst = partial + int64_t(blockIdx.x) * 3 * a.size;
-  if (a.dweight) write_partial<TPR>(dst, a.size, t, wide, dw, lds);
-  if (a.dscale) write_partial<TPR>(dst + a.size, a.size, t, wide, ds, lds);
-  if (POST && a.dpost_weight) write_partial<TPR>(dst + 2 * a.size, a.size, t, wide, dp, lds);
+  if (a.dweight) write_partial<TPR>(dst, int(a.size), t, wide, dw, sums);
+  if (a.dscale) write_partial<TPR>(dst + a.size, int(a.size), t, wide, ds, sums);
+  if (POST && a.dpost_weight) write_partial<TPR>(dst + 2 * a.size, int(a.size), t, wide, dp, sums);
 }
 
 // out[set][e] = sum over the blocks of set `set` of partial[block][part][e], in order:
-// blocks set, set + sets, ... of nblocks; 16 slices of the blocks per element.
+// blocks set, set + sets, ... of nblocks; 64 slices of the blocks per element.
 struct SumArgs {
   const float* partial;
   float* out[3];
   int64_t size, pitch, nblocks, sets;
 };
 
+constexpr int kSumCols = 16, kSumSlices = 64;
+
 __global__ __launch_bounds__(1024) void partial_sum_kernel(SumArgs s) {
-  __shared__ float lds[16][64];
-  const int lane = int(threadIdx.x) & 63, slice = int(threadIdx.x) >> 6;
-  const int64_t nb = (s.size + 63) / 64;
-  const int64_t set = int64_t(blockIdx.x) / nb, e = int64_t(blockIdx.x) % nb * 64 + lane;
+  __shared__ float lds[kSumSlices][kSumCols];
+  const int lane = int(threadIdx.x) % kSumCols, slice = int(threadIdx.x) / kSumCols;
+  const int64_t nb = (s.size + kSumCols - 1) / kSumCols;
+  const int64_t set = int64_t(blockIdx.x) / nb, e = int64_t(blockIdx.x) % nb * kSumCols + lane;
   const int part = int(blockIdx.y);
   if (!s.out[part]) return;
   const int64_t per_set = s.nblocks / s.sets;
   float x = 0.0f;
   if (e < s.size)
-    for (int64_t k = slice; k < per_set; k += 16)
+#pragma unroll 8
+    for (int64_t k = slice; k < per_set; k += kSumSlices)
       x += s.partial[(set + k * s.sets) * s.pitch + part * s.size + e];
   lds[slice][lane] = x;
   __syncthreads();
-  if (slice == 0 && e < s.size) {
 #pragma unroll
-    for (int k = 1; k < 16; ++k) x += lds[k][lane];
-    s.out[part][set * s.size + e] = x;
+  for (int half = kSumSlices / 2; half > 0; half /= 2) {
+    if (slice < half) lds[slice][lane] += lds[slice + half][lane];
+    __syncthreads();
   }
+  if (slice == 0 && e < s.size) s.out[part][set * s.size + e] = lds[0][lane];
 }
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -344,26 +464,35 @@ int threads_of(int64_t size) {
   return t;
 }
 
-int64_t back_blocks(int64_t units, int64_t size, int64_t heads) {
+int64_t back_blocks(int64_t units, int64_t size, int64_t heads, int64_t limit) {
   const int64_t groups = threads_of(size) < 256 ? 256 / threads_of(size) : 1;
   if (heads == 0) return 0;
-  const int64_t most = kMaxBackBlocks > heads ? kMaxBackBlocks / heads : 1;
+  const int64_t most = limit > heads ? limit / heads : 1;
   const int64_t want = div_up(units, groups);
   return (want < most ? want : most) * heads;
 }
 
 bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+template <int TPR, typename F>
+void by_width(bool wide, F f) {
+  if (wide)
+    f(std::integral_constant<int, TPR>(), std::true_type());
+  else
+    f(std::integral_constant<int, TPR>(), std::false_type());
+}
+
+// f(threads a vector, wide accesses), both as constants.
 template <typename F>
-hipError_t by_threads(int64_t size, F f) {
+hipError_t by_shape(int64_t size, bool wide, F f) {
   switch (threads_of(size)) {
-    case 16: f(std::integral_constant<int, 16>()); break;
-    case 32: f(std::integral_constant<int, 32>()); break;
-    case 64: f(std::integral_constant<int, 64>()); break;
-    case 128: f(std::integral_constant<int, 128>()); break;
-    case 256: f(std::integral_constant<int, 256>()); break;
-    case 512: f(std::integral_constant<int, 512>()); break;
-    default: f(std::integral_constant<int, 1024>()); break;  // size <= kNormMaxSize
+    case 16: by_width<16>(wide, f); break;
+    case 32: by_width<32>(wide, f); break;
+    case 64: by_width<64>(wide, f); break;
+    case 128: by_width<128>(wide, f); break;
+    case 256: by_width<256>(wide, f); break;
+    case 512: by_width<512>(wide, f); break;
+    default: by_width<1024>(wide, f); break;  // size <= kNormMaxSize
   }
   return hipGetLastError();
 }
@@ -389,73 +518,86 @@ using norm::bf16;
 
 size_t gated_norm_bwd_workspace(int64_t rows, int64_t heads, int64_t size) {
   // whichever of the shared and the per-head weight needs more blocks
-  const int64_t a = norm::back_blocks(rows * heads, size, 1), b = norm::back_blocks(rows, size, heads);
+  const int64_t a = norm::back_blocks(rows * heads, size, 1, norm::kMaxGatedBackBlocks),
+                b = norm::back_blocks(rows, size, heads, norm::kMaxGatedBackBlocks);
   return size_t(a > b ? a : b) * size_t(size) * 4;
 }
 
 size_t add_norm_bwd_workspace(int64_t rows, int64_t size) {
-  return size_t(norm::back_blocks(rows, size, 1)) * 3 * size_t(size) * 4;
+  return size_t(norm::back_blocks(rows, size, 1, norm::kMaxAddBackBlocks)) * 3 * size_t(size) * 4;
 }
 
 template <typename IO>
 static hipError_t gated_fwd(const GatedNormArgs& a, hipStream_t stream) {
-  return norm::by_threads(a.size, [&](auto tpr) {
+  return norm::by_shape(a.size, norm::gated_wide<IO>(a), [&](auto tpr, auto wide) {
     constexpr int T = decltype(tpr)::value, B = norm::threads<T>();
     int64_t n = norm::div_up(a.rows * a.heads, B / T);
     if (n > norm::kMaxBlocks) n = norm::kMaxBlocks;
-    norm::gated_norm_kernel<IO, T><<<dim3(unsigned(n)), B, 0, stream>>>(a, norm::gated_wide<IO>(a));
+    norm::gated_norm_kernel<IO, T, decltype(wide)::value><<<dim3(unsigned(n)), B, 0, stream>>>(a);
   });
 }
 
 template <typename IO>
 static hipError_t gated_bwd(const GatedNormArgs& a, float* ws, hipStream_t stream) {
   const int64_t sets = a.per_head ? a.heads : 1;
-  const int64_t n = norm::back_blocks(a.per_head ? a.rows : a.rows * a.heads, a.size, sets);
+  const int64_t n = norm::back_blocks(a.per_head ? a.rows : a.rows * a.heads, a.size, sets, norm::kMaxGatedBackBlocks);
   if (sets == 0) return hipSuccess;  // per-head weights of no heads
   // without rows there are no blocks, and the sums over none are zeros
-  const hipError_t e = n == 0 ? hipSuccess : norm::by_threads(a.size, [&](auto tpr) {
+  const hipError_t e = n == 0 ? hipSuccess : norm::by_shape(a.size, norm::gated_wide<IO>(a), [&](auto tpr, auto wide) {
     constexpr int T = decltype(tpr)::value, B = norm::threads<T>();
-    norm::gated_norm_bwd_kernel<IO, T>
-        <<<dim3(unsigned(n)), B, 0, stream>>>(a, ws, norm::gated_wide<IO>(a));
+    norm::gated_norm_bwd_kernel<IO, T, decltype(wide)::value><<<dim3(unsigned(n)), B, 0, stream>>>(a, ws);
   });
   if (e != hipSuccess || !a.dweight) return e;
   const norm::SumArgs s{ws, {a.dweight, nullptr, nullptr}, a.size, a.size, n, sets};
-  norm::partial_sum_kernel<<<dim3(unsigned(sets * norm::div_up(a.size, 64))), 1024, 0, stream>>>(s);
+  norm::partial_sum_kernel<<<dim3(unsigned(sets * norm::div_up(a.size, norm::kSumCols))), 1024, 0, stream>>>(s);
   return hipGetLastError();
 }
 
 template <typename IO, typename RES>
 static hipError_t add_fwd(const AddNormArgs& a, hipStream_t stream) {
-  return norm::by_threads(a.size, [&](auto tpr) {
+  return norm::by_shape(a.size, norm::add_wide(a), [&](auto tpr, auto wide) {
     constexpr int T = decltype(tpr)::value, B = norm::threads<T>();
     int64_t n = norm::div_up(a.rows, B / T);
     if (n > norm::kMaxBlocks) n = norm::kMaxBlocks;
-    norm::add_norm_kernel<IO, RES, T><<<dim3(unsigned(n)), B, 0, stream>>>(a, norm::add_wide(a));
+    norm::add_norm_kernel<IO, RES, T, decltype(wide)::value><<<dim3(unsigned(n)), B, 0, stream>>>(a);
   });
 }
 
 template <typename IO, typename RES>
 static hipError_t add_bwd(const AddNormArgs& a, float* ws, hipStream_t stream) {
-  const int64_t n = norm::back_blocks(a.rows, a.size, 1);
-  const hipError_t e = n == 0 ? hipSuccess : norm::by_threads(a.size, [&](auto tpr) {
+  const int64_t n = norm::back_blocks(a.rows, a.size, 1, norm::kMaxAddBackBlocks);
+  const hipError_t e = n == 0 ? hipSuccess : norm::by_shape(a.size, norm::add_wide(a), [&](auto tpr, auto wide) {
     constexpr int T = decltype(tpr)::value, B = norm::threads<T>();
     const dim3 grid{unsigned(n)};
     if (a.post_weight)
-      norm::add_norm_bwd_kernel<IO, RES, T, true><<<grid, B, 0, stream>>>(a, ws, norm::add_wide(a));
+      norm::add_norm_bwd_kernel<IO, RES, T, decltype(wide)::value, true><<<grid, B, 0, stream>>>(a, ws);
     else
-      norm::add_norm_bwd_kernel<IO, RES, T, false><<<grid, B, 0, stream>>>(a, ws, norm::add_wide(a));
+      norm::add_norm_bwd_kernel<IO, RES, T, decltype(wide)::value, false><<<grid, B, 0, stream>>>(a, ws);
   });
   if (e != hipSuccess || !(a.dweight || a.dscale || a.dpost_weight)) return e;
   const norm::SumArgs s{ws, {a.dweight, a.dscale, a.dpost_weight}, a.size, 3 * a.size, n, 1};
-  norm::partial_sum_kernel<<<dim3(unsigned(norm::div_up(a.size, 64)), 3), 1024, 0, stream>>>(s);
+  norm::partial_sum_kernel<<<dim3(unsigned(norm::div_up(a.size, norm::kSumCols)), 3), 1024, 0, stream>>>(s);
   return hipGetLastError();
 }
 
-hipError_t launch_gated_norm(const GatedNormArgs& a, hipStream_t stream) {
+// Heads that continue each other in memory are rows, where their weight is shared.
+static GatedNormArgs collapsed(GatedNormArgs a) {
+  if (!a.per_head && a.heads > 1 && a.xr == a.heads * a.xh && a.zr == a.heads * a.zh) {
+    a.rows *= a.heads;
+    a.heads = 1;
+    a.xr = a.xh;
+    a.zr = a.zh;
+  }
+  return a;
+}
+
+hipError_t launch_gated_norm(const GatedNormArgs& args, hipStream_t stream) {
+  const GatedNormArgs a = collapsed(args);
   return a.io_bf16 ? gated_fwd<bf16>(a, stream) : gated_fwd<float>(a, stream);
 }
 
-hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, float* ws, hipStream_t stream) {
+hipError_t launch_gated_norm_bwd(const GatedNormArgs& args, float* ws, hipStream_t stream) {
+  const GatedNormArgs a = collapsed(args);
   return a.io_bf16 ? gated_bwd<bf16>(a, ws, stream) : gated_bwd<float>(a, ws, stream);
 }
 
