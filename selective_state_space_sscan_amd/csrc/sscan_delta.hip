@@ -14,60 +14,86 @@ namespace delta {
 //
 // A wave owns 32 columns of S: lane (rg, cg) holds rows rg NR .. + NR - 1 of columns
 // 4 cg .. + 3.  One pass over S gives S'^T k and S'^T q together (o = S'^T q + (k.q) u),
-// so a decode step reads and writes the state once.
-template <typename IO, int NR>
-__global__ __launch_bounds__(256) void delta_recurrent_kernel(DeltaArgs a, int ncol, int64_t waves, int wide) {
+// so a decode step reads and writes the state once and is bound by that traffic (128
+// sequences of 32 heads of 128 x 128: 537 MB).  wide: 16-byte accesses to the state, q
+// and k; otherwise every element is loaded by itself.
+
+// Sum over the eight row groups (lane bits 3 to 5), in every lane.
+__device__ __forceinline__ float group_rows_sum(float x) {
+  x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x128, 0xf, 0xf, true));
+  const unsigned u = __builtin_bit_cast(unsigned, x);
+  const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  x = __builtin_bit_cast(float, unsigned(p[0])) + __builtin_bit_cast(float, unsigned(p[1]));
+  const unsigned v = __builtin_bit_cast(unsigned, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return __builtin_bit_cast(float, unsigned(r[0])) + __builtin_bit_cast(float, unsigned(r[1]));
+}
+
+template <typename IO, int NR, bool WIDE>
+__global__ __launch_bounds__(256) void delta_recurrent_kernel(DeltaArgs a, unsigned ncol, unsigned waves) {
   const int lane = lane_id(), rg = lane >> 3, cg = lane & 7;
-  const int64_t w = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const unsigned w = __builtin_amdgcn_readfirstlane(blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6));
   if (w >= waves) return;
-  const int64_t bh = w / ncol, b = bh / a.hv;
-  const int h = int(bh % a.hv), hq = h / (a.hv / a.hk);
-  const int col = int(w % ncol) * 32 + 4 * cg, row0 = rg * NR;
+  const unsigned bh = w / ncol, row_b = bh / unsigned(a.hv);
+  const int64_t b = row_b;
+  const int h = int(bh - row_b * unsigned(a.hv)), hq = int(unsigned(h) / (unsigned(a.hv) / unsigned(a.hk)));
+  const int col = int(w - bh * ncol) * 32 + 4 * cg, row0 = rg * NR;
   const int L = int(a.len), Lb = row_len(a.lengths, b, a.len);
-  const bool wide_qk = wide & 1, wide_s = wide & 8;
-  const IO* kp = static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h + row0;
-  const IO* qp = static_cast<const IO*>(a.q) + b * a.sq.b + hq * a.sq.h + row0;
-  const IO* vp = static_cast<const IO*>(a.v) + b * a.sv.b + h * a.sv.h + col;
+  const IO* kp = static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h;
+  const IO* qp = static_cast<const IO*>(a.q) + b * a.sq.b + hq * a.sq.h;
+  const IO* vp = static_cast<const IO*>(a.v) + b * a.sv.b + h * a.sv.h;
   const float* gp = a.g + b * a.sg.b + h * a.sg.h;
   const float* bp = a.beta + b * a.sb.b + h * a.sb.h;
-  IO* op = static_cast<IO*>(a.out) + (b * a.len * a.hv + h) * a.dv + col;
   const int64_t out_t = int64_t(a.hv) * a.dv;
-  const int64_t state = (bh * a.dk + row0) * a.dv + col;
-  const int cols = a.dv - col, rows = a.dk - row0;
+  IO* op = static_cast<IO*>(a.out) + (b * a.len * a.hv + h) * a.dv;
+  const uint32_t state_bytes = uint32_t(a.dk * a.dv * 4);
+  // a lane's columns in a state row (kOutside: none)
+  const int at = col < a.dv ? (row0 * a.dv + col) * 4 : kOutside;
 
-  f32x4 S[NR];
+  const auto state_io = [&](const float* p, auto body) {
+    const Buffer s = buffer_of(p + int64_t(bh) * a.dk * a.dv, state_bytes);
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    S[r] = f32x4{};
-    if (a.h0 && r < rows) {
-      const float* p = a.h0 + state + int64_t(r) * a.dv;
-      if (wide_s) {
-        if (cols > 0) S[r] = *reinterpret_cast<const f32x4*>(p);
+    for (int r = 0; r < NR; ++r) body(s, at + r * a.dv * 4, r);
+  };
+  f32x4 S[NR];
+  if (a.h0) {
+    state_io(a.h0, [&](Buffer s, int off, int r) {
+      if constexpr (WIDE) {
+        S[r] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(s, off, 0, 0));
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < cols) S[r][j] = p[j];
+        for (int j = 0; j < 4; ++j) {
+          float x;
+          load1(s, col + j < a.dv ? off + 4 * j : kOutside, &x);
+          S[r][j] = x;
+        }
       }
-    }
+    });
+  } else {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) S[r] = f32x4{};
   }
   for (int t = 0; t < Lb; ++t) {
+    const Buffer kb = buffer_of(kp + t * a.sk.t, uint32_t(a.dk * sizeof(IO)));
+    const Buffer qb = buffer_of(qp + t * a.sq.t, uint32_t(a.dk * sizeof(IO)));
+    const Buffer vb = buffer_of(vp + t * a.sv.t, uint32_t(a.dv * sizeof(IO)));
+    typename Io<IO>::V8 k8[NR / 8], q8[NR / 8];
+#pragma unroll
+    for (int n = 0; n < NR / 8; ++n) {
+      load8<IO>(kb, (row0 + 8 * n) * int(sizeof(IO)), a.dk - row0 - 8 * n, WIDE, &k8[n]);
+      load8<IO>(qb, (row0 + 8 * n) * int(sizeof(IO)), a.dk - row0 - 8 * n, WIDE, &q8[n]);
+    }
+    IO v4[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load1(vb, (col + j) * int(sizeof(IO)), &v4[j]);
+    const float decay = expf(clamp_decay(gp[t * a.sg.t])), beta = bp[t * a.sb.t];
     float k[NR], q[NR];
 #pragma unroll
-    for (int r8 = 0; r8 < NR; r8 += 8) {
-      const auto k8 = load8(kp + t * a.sk.t + r8, rows - r8, wide_qk);
-      const auto q8 = load8(qp + t * a.sq.t + r8, rows - r8, wide_qk);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        k[r8 + j] = to_f32(k8[j]);
-        q[r8 + j] = to_f32(q8[j]);
-      }
+    for (int r = 0; r < NR; ++r) {
+      k[r] = to_f32(k8[r / 8][r % 8]);
+      q[r] = to_f32(q8[r / 8][r % 8]);
     }
-    f32x4 v = {};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < cols) v[j] = to_f32(vp[t * a.sv.t + j]);
-    const float decay = expf(clamp_decay(gp[t * a.sg.t])), beta = bp[t * a.sb.t];
-    f32x4 ks = {}, qs = {};
+    f32x4 ks = {}, qs = {}, v;
     float kk = 0, qq = 0, kq = 0;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -78,44 +104,53 @@ __global__ __launch_bounds__(256) void delta_recurrent_kernel(DeltaArgs a, int n
       kq += k[r] * q[r];
     }
 #pragma unroll
-    for (int m = 8; m < 64; m *= 2) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        ks[j] += __shfl_xor(ks[j], m);
-        qs[j] += __shfl_xor(qs[j], m);
-      }
-      kk += __shfl_xor(kk, m);
-      qq += __shfl_xor(qq, m);
-      kq += __shfl_xor(kq, m);
+    for (int j = 0; j < 4; ++j) {
+      ks[j] = group_rows_sum(ks[j]);
+      qs[j] = group_rows_sum(qs[j]);
+      v[j] = to_f32(v4[j]);
     }
+    kk = group_rows_sum(kk);
+    qq = group_rows_sum(qq);
+    kq = group_rows_sum(kq);
     const float rk = a.qk_norm ? 1.0f / sqrtf(kk + 1e-6f) : 1.0f, rq = a.qk_norm ? 1.0f / sqrtf(qq + 1e-6f) : 1.0f;
     const f32x4 u = beta * (v - (decay * rk) * ks), ku = rk * u;
     const f32x4 o = (a.scale * rq) * (decay * qs + kq * ku);
 #pragma unroll
     for (int r = 0; r < NR; ++r) S[r] = decay * S[r] + k[r] * ku;
     if (rg == 0) {
+      const Buffer ob = buffer_of(op + t * out_t, uint32_t(a.dv * sizeof(IO)));
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < cols) op[t * out_t + j] = IO(o[j]);
+      for (int j = 0; j < 4; ++j) store1(ob, (col + j) * int(sizeof(IO)), IO(o[j]));
     }
   }
   if (rg == 0)
-    for (int t = Lb; t < L; ++t)
+    for (int t = Lb; t < L; ++t) {
+      const Buffer ob = buffer_of(op + t * out_t, uint32_t(a.dv * sizeof(IO)));
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < cols) op[t * out_t + j] = IO(0.0f);
-#pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    if (r >= rows) continue;
-    float* p = a.h_last + state + int64_t(r) * a.dv;
-    if (wide_s) {
-      if (cols > 0) *reinterpret_cast<f32x4*>(p) = S[r];
+      for (int j = 0; j < 4; ++j) store1(ob, (col + j) * int(sizeof(IO)), IO(0.0f));
+    }
+  state_io(a.h_last, [&](Buffer s, int off, int r) {
+    if constexpr (WIDE) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[r]), s, off, 0, 0);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < cols) p[j] = S[r][j];
+      for (int j = 0; j < 4; ++j) store1(s, col + j < a.dv ? off + 4 * j : kOutside, S[r][j]);
     }
-  }
+  });
+}
+
+template <typename IO, int NR>
+hipError_t launch_recurrent(const DeltaArgs& a, hipStream_t stream) {
+  const int wide = wide_flags<IO>(a), ncol = (a.dv + 31) / 32;
+  const unsigned waves = unsigned(a.batch * a.hv * ncol);
+  // blocks of one wave while there are fewer than four a CU: a small batch then uses as
+  // many CUs as it has waves
+  const unsigned per_block = waves <= 1024 ? 1 : 4, blocks = (waves + per_block - 1) / per_block;
+  if ((wide & 9) == 9)
+    delta_recurrent_kernel<IO, NR, true><<<dim3(blocks), 64 * per_block, 0, stream>>>(a, unsigned(ncol), waves);
+  else
+    delta_recurrent_kernel<IO, NR, false><<<dim3(blocks), 64 * per_block, 0, stream>>>(a, unsigned(ncol), waves);
+  return hipGetLastError();
 }
 
 template <typename IO, int KP, int W>
@@ -142,17 +177,7 @@ hipError_t launch_walk(const DeltaArgs& a, const DeltaPlan& p, char* ws, hipStre
 
 template <typename IO>
 hipError_t launch_fwd(const DeltaArgs& a, const DeltaPlan& p, char* ws, hipStream_t stream) {
-  const int wide = wide_flags<IO>(a);
-  if (p.recurrent) {
-    const int ncol = (a.dv + 31) / 32;
-    const int64_t waves = a.batch * a.hv * ncol;
-    const dim3 grid{unsigned((waves + 3) / 4)};
-    if (a.dk <= 64)
-      delta_recurrent_kernel<IO, 8><<<grid, 256, 0, stream>>>(a, ncol, waves, wide);
-    else
-      delta_recurrent_kernel<IO, 16><<<grid, 256, 0, stream>>>(a, ncol, waves, wide);
-    return hipGetLastError();
-  }
+  if (p.recurrent) return a.dk <= 64 ? launch_recurrent<IO, 8>(a, stream) : launch_recurrent<IO, 16>(a, stream);
   if (p.kp == 64)
     return p.waves == 8 ? launch_walk<IO, 64, 8>(a, p, ws, stream) : launch_walk<IO, 64, 4>(a, p, ws, stream);
   return p.waves == 8 ? launch_walk<IO, 128, 8>(a, p, ws, stream) : launch_walk<IO, 128, 4>(a, p, ws, stream);
