@@ -187,20 +187,32 @@ hipError_t launch_fwd(const DeltaArgs& a, const DeltaPlan& p, char* ws, hipStrea
 
 static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Segments a row is walked in.  One CU holds one block of a walk, so a walk takes
-// ceil(blocks / CUs) times its chunks; in units of the time of one chunk of the output
-// walk, a chunk of the transitions' walk takes 3/4 and a step of the chain between
-// segments 1/2.
-static int choose_segments(int64_t heads, int64_t nchunk, int nvb, int nkb) {
-  constexpr int64_t kCus = 256;
-  const auto rounds = [](int64_t blocks) { return double((blocks + kCus - 1) / kCus); };
+// Segments a row is walked in, by a model of the walks' times in units of one chunk of
+// one output walk alone on its CU (4.4 us at 128 x 128): a CU holds one block; chunks
+// take up to 1.4 times as long when every CU is busy; a walk has 2 units of its own for
+// its first loads; a chunk of the transitions' walk takes 3/4, and its blocks end at
+// different times, so its rounds count fractionally; a step of the chain between segments
+// takes 1 (1/4 for keys of 64).  Measured against forced counts, bf16, 128 x 128: 64 heads
+// of 32 chunks 178 us in 4 segments (the model's choice), 201 in 3, 207 in 8, 203 whole;
+// 16 heads of 512 chunks 690 us in 16 (its choice), 793 in 8, 764 in 12, 794 in 32,
+// 2900 whole; 256 heads of 16 chunks 191 us whole (its choice), 325 in 2.
+static int choose_segments(int64_t heads, int64_t nchunk, int nvb, int nkb, int kp) {
+  const auto walk = [](int64_t blocks, double rounds, double chunks) {
+    const double busy = blocks < 256 ? double(blocks) / 256.0 : 1.0;
+    return rounds * chunks * (1.0 + 0.4 * busy) + 2.0;
+  };
+  const auto output = [&](int n) {
+    const int64_t blocks = heads * nvb * n;
+    return walk(blocks, double((blocks + 255) / 256), double((nchunk + n - 1) / n));
+  };
   int best = 1;
-  double least = rounds(heads * nvb) * double(nchunk);
-  for (int n = 2; n <= 64 && nchunk / n >= 4; ++n) {
+  double least = 0.97 * output(1);
+  for (int n = 2; n <= 64 && nchunk / n >= 2; ++n) {
     const double chunks = double((nchunk + n - 1) / n);
-    const double cost = rounds(heads * nvb * n) * chunks +
-                        0.75 * rounds(heads * (nvb * (n - 1) + nkb * (n - 2))) * chunks + 0.5 * (n - 2) + 2.0;
-    if (cost < 0.9 * least) {
+    const int64_t blocks = heads * (int64_t(nvb) * (n - 1) + int64_t(nkb) * (n - 2));
+    const double rounds = blocks < 256 ? 1.0 : double(blocks) / 256.0;
+    const double cost = output(n) + walk(blocks, rounds, 0.75 * chunks) + (n - 2) * (kp == 64 ? 0.25 : 1.0) + 1.0;
+    if (cost < least) {
       least = cost;
       best = n;
     }
@@ -219,7 +231,7 @@ DeltaPlan make_delta_plan(int64_t batch, int64_t len, int hk, int hv, int dk, in
   if (p.recurrent) return p;
   const int cols = 16 * p.waves;
   const int64_t heads = batch * hv;
-  p.nseg = choose_segments(heads, p.nchunk, (dv + cols - 1) / cols, (p.kp + cols - 1) / cols);
+  p.nseg = choose_segments(heads, p.nchunk, (dv + cols - 1) / cols, (p.kp + cols - 1) / cols, p.kp);
   p.seg_chunks = int((p.nchunk + p.nseg - 1) / p.nseg);
   p.nseg = int((p.nchunk + p.seg_chunks - 1) / p.seg_chunks);
   const size_t n = size_t(heads) * size_t(p.nchunk);
