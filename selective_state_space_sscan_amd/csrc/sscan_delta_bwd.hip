@@ -231,17 +231,30 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_
 
 // ---- the gradients of a chunk --------------------------------------------------------
 
-// Sum over the sixteen lanes of a row, in every one of them.
-__device__ __forceinline__ float row16_sum(float x) {
-  const auto ror = [](float y, auto n) {
-    return __builtin_bit_cast(
-        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, y), 0x120 + decltype(n)::value, 0xf, 0xf, true));
-  };
-  x += ror(x, std::integral_constant<int, 8>());
-  x += ror(x, std::integral_constant<int, 4>());
-  x += ror(x, std::integral_constant<int, 2>());
-  x += ror(x, std::integral_constant<int, 1>());
-  return x;
+template <int kCtrl>
+__device__ __forceinline__ float dpp_f32(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), kCtrl, 0xf, 0xf, true));
+}
+
+// Sums over the sixteen lanes of a row of n values (8 or 16): lane i receives the sum of
+// value i (mod n).  Each step exchanges half of what a lane still holds with the lane
+// across bit 3, 2, 1, 0 (by the DPP controls that flip it: rotation by 8, half mirror,
+// quad permutations), 45 instructions for sixteen sums.
+template <int n>
+__device__ __forceinline__ float lane_sums(float (&v)[n]) {
+  const int i = lane_id();
+  if constexpr (n == 16) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = (i & 8 ? v[k + 8] : v[k]) + dpp_f32<0x128>(i & 8 ? v[k] : v[k + 8]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += dpp_f32<0x128>(v[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = (i & 4 ? v[k + 4] : v[k]) + dpp_f32<0x141>(i & 4 ? v[k] : v[k + 4]);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) v[k] = (i & 2 ? v[k + 2] : v[k]) + dpp_f32<0x4e>(i & 2 ? v[k] : v[k + 2]);
+  return (i & 1 ? v[1] : v[0]) + dpp_f32<0xb1>(i & 1 ? v[0] : v[1]);
 }
 
 // LDS tile of 64 tokens by VS value columns, in units of eight permuted by the row so
@@ -478,7 +491,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
     for (int m = 1; m < 64; m *= 2) se += __shfl_xor(se, m);
     if (lane == 0) sse[wave] = m0 == 0 ? se : 0.0f;  // waves of the same key tile hold the same sum
     // h1: dq, h2: -R, h3: U E^T's part of W (all times the inverse norms)
-    float kh3[MT][4];
+    float kh3[4 * MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int tok = 16 * (m0 + m) + 4 * qd;
@@ -487,43 +500,51 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
         h1[m][r] *= svec[2 * kC + tok + r];
         h2[m][r] *= svec[tok + r];
         h3[m][r] *= svec[kC + tok + r];
-        kh3[m][r] = at_tile(sk, tok + r, 16 * kt + i) * h3[m][r];
+        kh3[4 * m + r] = at_tile(sk, tok + r, 16 * kt + i) * h3[m][r];
       }
     }
-    // the factors take the slabs' place: masked, decayed, times the inverse norms; which
-    // 0: dO U^T, 1: X~ U^T, 2: beta X~ U^T (two tiles right of the diagonal are read too)
-    const auto put = [&](int which, bf16* dst) {
+    // the factors take the slabs' place: masked, decayed, times the inverse norms.  dO U^T
+    // to g0, X~ U^T to g1, -beta X~ U^T to g2, where given
+    const auto put = [&](bf16* g0, bf16* g1, bf16* g2) {
+      const auto write = [&](bf16* dst, int at, float x) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const bf16 t = bf16(x);
+          dst[k * kG + at] = t;
+          x -= float(t);
+        }
+      };
 #pragma unroll
       for (int n = 0; n < 3; ++n) {
         const int item = wave + 8 * n;
-        if (item >= 20) break;
-        if ((item < 10) != (which == 0)) continue;
+        if (item >= 20 || (item < 10 ? !g0 : !g1 && !g2)) continue;
         const int tile = item < 10 ? item : item - 10;
         const int rt = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, ct = tile - rt * (rt + 1) / 2;
+        const int tj = 16 * ct + i, row = 16 * rt + 4 * qd;
+        const double sum_j = gsum[tj];
+        const float rk_j = svec[5 * kC + tj];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int ti = 16 * rt + 4 * qd + r, tj = 16 * ct + i;
-          const bool in = which == 0 ? tj <= ti : tj < ti;
-          float x = 0.0f;
-          if (in) {
-            x = gacc[n][r] * expf(float(gsum[ti] - gsum[tj])) * svec[5 * kC + tj];
-            x *= which == 0 ? a.scale * svec[6 * kC + ti] : svec[5 * kC + ti];
-            if (which == 2) x *= svec[4 * kC + ti];
-          }
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const bf16 t = bf16(x);
-            dst[k * kG + ti * kLdG + tj] = t;
-            x -= float(t);
+          const int ti = row + r, at = ti * kLdG + tj;
+          const float x = gacc[n][r] * expf(float(gsum[ti] - sum_j)) * rk_j;
+          if (item < 10) {
+            write(g0, at, tj <= ti ? x * (a.scale * svec[6 * kC + ti]) : 0.0f);
+          } else {
+            const float y = tj < ti ? x * svec[5 * kC + ti] : 0.0f;
+            if (g1) write(g1, at, y);
+            if (g2) write(g2, at, -y * svec[4 * kC + ti]);
           }
         }
       }
-      if (wave >= 6)  // tiles (0, 1) and (2, 3): above the diagonal, but in the fragments read
+      if (wave >= 6) {  // tiles (0, 1) and (2, 3): above the diagonal, but in the fragments read
+        const int at = ((wave - 6) * 32 + 4 * qd) * kLdG + (wave - 6) * 32 + 16 + i;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int k = 0; k < 3; ++k)
-            dst[k * kG + ((wave - 6) * 32 + 4 * qd + r) * kLdG + (wave - 6) * 32 + 16 + i] = bf16(0.0f);
+        for (int r = 0; r < 4; ++r) {
+          if (g0) write(g0, at + r * kLdG, 0.0f);
+          if (g1) write(g1, at + r * kLdG, 0.0f);
+          if (g2) write(g2, at + r * kLdG, 0.0f);
+        }
+      }
     };
     f32x4 w[MT] = {};
     // acc += G B over tokens j <= i, and acc += G^T B over i >= j
@@ -542,7 +563,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
           acc[m] = mul(fg, fb, acc[m]);
         }
     };
-    const auto by_cols = [&](f32x4 (&acc)[MT], const bf16* g, const bf16* tile, bool minus) {
+    const auto by_cols = [&](f32x4 (&acc)[MT], const bf16* g, const bf16* tile) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -550,10 +571,8 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
           if (m0 + m >= 2 && s == 0) continue;
           Frag<3> fg;
 #pragma unroll
-          for (int n = 0; n < 3; ++n) {
+          for (int n = 0; n < 3; ++n)
             fg.t[n] = col_frag(g + n * kG + (32 * s + 8 * qd + (i >> 2)) * kLdG + 16 * (m0 + m) + 4 * (i & 3), kLdG);
-            if (minus) fg.t[n] = -fg.t[n];
-          }
           Frag<N> fb;
 #pragma unroll
           for (int t = 0; t < N; ++t) fb.t[t] = col_frag<KP>(tile + t * TileK::kElems, 32 * s + 8 * qd, 16 * kt + 4 * (i & 3));
@@ -562,45 +581,46 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
     };
     __syncthreads();
     if constexpr (Lds::kFactors == 3) {
-      put(0, shared);
-      put(1, shared + 3 * kG);
-      put(2, shared + 6 * kG);
+      put(shared, shared + 3 * kG, shared + 6 * kG);
       __syncthreads();
       by_rows(h1, shared, sk);
       by_rows(h2, shared + 3 * kG, sk);
-      by_cols(w, shared, sq, false);
-      by_cols(w, shared + 6 * kG, sk, true);
+      by_cols(w, shared, sq);
+      by_cols(w, shared + 6 * kG, sk);
     } else {
-      put(0, shared);
+      put(shared, nullptr, nullptr);
       __syncthreads();
       by_rows(h1, shared, sk);
-      by_cols(w, shared, sq, false);
+      by_cols(w, shared, sq);
       __syncthreads();
-      put(1, shared);
+      put(nullptr, shared, nullptr);
       __syncthreads();
       by_rows(h2, shared, sk);
       __syncthreads();
-      put(2, shared);
+      put(nullptr, nullptr, shared);
       __syncthreads();
-      by_cols(w, shared, sk, true);
+      by_cols(w, shared, sk);
     }
 
     // per token: q . dq, k . R, k . (W without U E^T), k . U E^T
+    float d0[4 * MT], d1[4 * MT], d2[4 * MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int tok = 16 * (m0 + m) + 4 * qd + r, dim = 16 * kt + i;
-        const float beta = svec[4 * kC + tok], k = at_tile(sk, tok, dim), q = at_tile(sq, tok, dim);
-        const float d[4] = {q * h1[m][r], -k * h2[m][r], k * w[m][r], kh3[m][r]};
+        const float k = at_tile(sk, tok, dim), q = at_tile(sq, tok, dim);
+        d0[4 * m + r] = q * h1[m][r];
+        d1[4 * m + r] = -k * h2[m][r];
+        d2[4 * m + r] = k * w[m][r];
         dq[m][r] += h1[m][r];
-        dk[m][r] += w[m][r] + h3[m][r] - beta * h2[m][r];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float sum = row16_sum(d[x]);
-          if (i == 0) sdot[kt][x][tok] = sum;
-        }
+        dk[m][r] += w[m][r] + h3[m][r] - svec[4 * kC + tok] * h2[m][r];
       }
+    const int sum_tok = 16 * m0 + 16 * ((i >> 2) % MT) + 4 * qd + (i & 3);  // value i of the sums
+    sdot[kt][0][sum_tok] = lane_sums(d0);
+    sdot[kt][1][sum_tok] = lane_sums(d1);
+    sdot[kt][2][sum_tok] = lane_sums(d2);
+    sdot[kt][3][sum_tok] = lane_sums(kh3);
     __syncthreads();
     if (wave == 0) {
       const int t = t0 + lane;
@@ -630,17 +650,18 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
   // through the norms: d raw = d - raw r^2 (raw . d), d already times r
   __syncthreads();
   if (a.qk_norm) {
+    float dots_q[4 * MT], dots_k[4 * MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int tok = 16 * (m0 + m) + 4 * qd + r, dim = 16 * kt + i;
-        const float sums[2] = {row16_sum(at_tile(sq, tok, dim) * dq[m][r]), row16_sum(at_tile(sk, tok, dim) * dk[m][r])};
-        if (i == 0) {
-          sdot[kt][0][tok] = sums[0];
-          sdot[kt][1][tok] = sums[1];
-        }
+        dots_q[4 * m + r] = at_tile(sq, tok, dim) * dq[m][r];
+        dots_k[4 * m + r] = at_tile(sk, tok, dim) * dk[m][r];
       }
+    const int sum_tok = 16 * m0 + 16 * ((i >> 2) % MT) + 4 * qd + (i & 3);
+    sdot[kt][0][sum_tok] = lane_sums(dots_q);
+    sdot[kt][1][sum_tok] = lane_sums(dots_k);
     __syncthreads();
   }
   const int dim = 16 * kt + i;
