@@ -491,17 +491,12 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
     for (int m = 1; m < 64; m *= 2) se += __shfl_xor(se, m);
     if (lane == 0) sse[wave] = m0 == 0 ? se : 0.0f;  // waves of the same key tile hold the same sum
     // h1: dq, h2: -R, h3: U E^T's part of W (all times the inverse norms)
-    float kh3[4 * MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int tok = 16 * (m0 + m) + 4 * qd;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        h1[m][r] *= svec[2 * kC + tok + r];
-        h2[m][r] *= svec[tok + r];
-        h3[m][r] *= svec[kC + tok + r];
-        kh3[4 * m + r] = at_tile(sk, tok + r, 16 * kt + i) * h3[m][r];
-      }
+      h1[m] *= *reinterpret_cast<const f32x4*>(&svec[2 * kC + tok]);
+      h2[m] *= *reinterpret_cast<const f32x4*>(&svec[tok]);
+      h3[m] *= *reinterpret_cast<const f32x4*>(&svec[kC + tok]);
     }
     // the factors take the slabs' place: masked, decayed, times the inverse norms.  dO U^T
     // to g0, X~ U^T to g1, -beta X~ U^T to g2, where given
@@ -603,24 +598,26 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
     }
 
     // per token: q . dq, k . R, k . (W without U E^T), k . U E^T
-    float d0[4 * MT], d1[4 * MT], d2[4 * MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int tok = 16 * (m0 + m) + 4 * qd + r, dim = 16 * kt + i;
-        const float k = at_tile(sk, tok, dim), q = at_tile(sq, tok, dim);
-        d0[4 * m + r] = q * h1[m][r];
-        d1[4 * m + r] = -k * h2[m][r];
-        d2[4 * m + r] = k * w[m][r];
-        dq[m][r] += h1[m][r];
-        dk[m][r] += w[m][r] + h3[m][r] - svec[4 * kC + tok] * h2[m][r];
-      }
     const int sum_tok = 16 * m0 + 16 * ((i >> 2) % MT) + 4 * qd + (i & 3);  // value i of the sums
-    sdot[kt][0][sum_tok] = lane_sums(d0);
-    sdot[kt][1][sum_tok] = lane_sums(d1);
-    sdot[kt][2][sum_tok] = lane_sums(d2);
-    sdot[kt][3][sum_tok] = lane_sums(kh3);
+    const auto dots = [&](int which, auto value) {
+      float v[4 * MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[4 * m + r] = value(m, r, 16 * (m0 + m) + 4 * qd + r);
+      sdot[kt][which][sum_tok] = lane_sums(v);
+      __builtin_amdgcn_sched_barrier(0);  // one set of sums in registers at a time
+    };
+    const int dim = 16 * kt + i;
+    dots(0, [&](int m, int r, int tok) { return at_tile(sq, tok, dim) * h1[m][r]; });
+    dots(1, [&](int m, int r, int tok) { return -at_tile(sk, tok, dim) * h2[m][r]; });
+    dots(2, [&](int m, int r, int tok) { return at_tile(sk, tok, dim) * w[m][r]; });
+    dots(3, [&](int m, int r, int tok) { return at_tile(sk, tok, dim) * h3[m][r]; });
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      dq[m] += h1[m];
+      dk[m] += w[m] + h3[m] - *reinterpret_cast<const f32x4*>(&svec[4 * kC + 16 * (m0 + m) + 4 * qd]) * h2[m];
+    }
     __syncthreads();
     if (wave == 0) {
       const int t = t0 + lane;
