@@ -169,8 +169,8 @@ hipError_t launch_walk(const DeltaArgs& a, const DeltaPlan& p, char* ws, hipStre
         <<<dim3(unsigned(bh * p.nseg * (nvb + kIdent))), 64 * W, 0, stream>>>(a, w, kVecFloats);
   }
   if (p.nseg > 2)
-    delta_carry_kernel<KP, 4, false>
-        <<<dim3(unsigned(bh * ((p.dvp + 63) / 64))), 256, 0, stream>>>(w.moves, w.ends, p.nseg, p.dvp, (p.dvp + 63) / 64);
+    delta_carry_kernel<KP, false>
+        <<<dim3(unsigned(bh * (p.dvp / 16))), 2 * KP, 0, stream>>>(w.moves, w.ends, p.nseg, p.dvp);
   delta_chunk_kernel<IO, KP, W, kOut><<<dim3(unsigned(bh * p.nseg * nvb)), 64 * W, 0, stream>>>(a, w, kVecFloats);
   return hipGetLastError();
 }

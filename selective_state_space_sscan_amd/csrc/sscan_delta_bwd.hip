@@ -710,7 +710,7 @@ hipError_t launch_bwd(const DeltaBwdArgs& b, const DeltaBwdPlan& p, char* ws, hi
   const WalkArgs w{n, nvb, f.nseg, f.seg_chunks, f.dvp, wide, ft, nullptr, vec, s, u, ends, moves};
   const WalkBackArgs wb{n, nvb, f.nseg, f.seg_chunks, f.dvp, wide, ftt, fpt, vec, e, x, back};
   const int64_t bh = a.batch * a.hv;
-  const dim3 walk{unsigned(bh * f.nseg * nvb)}, chain{unsigned(bh * ((f.dvp + 63) / 64))};
+  const dim3 walk{unsigned(bh * f.nseg * nvb)}, chain{unsigned(bh * (f.dvp / 16))};
   if (n > 0) {
     delta_prep_kernel<IO, KP, true><<<dim3(unsigned(bh * n)), 256, 0, stream>>>(a, n, ft, fpt, ftt, vec, wide);
     if (f.nseg > 1) {
@@ -720,8 +720,8 @@ hipError_t launch_bwd(const DeltaBwdArgs& b, const DeltaBwdPlan& p, char* ws, hi
       delta_chunk_bwd_kernel<IO, KP, W, true><<<walk, 64 * W, 0, stream>>>(b, wb);
     }
     if (f.nseg > 2) {
-      delta_carry_kernel<KP, 4, false><<<chain, 256, 0, stream>>>(moves, ends, f.nseg, f.dvp, (f.dvp + 63) / 64);
-      delta_carry_kernel<KP, 4, true><<<chain, 256, 0, stream>>>(moves, back, f.nseg, f.dvp, (f.dvp + 63) / 64);
+      delta_carry_kernel<KP, false><<<chain, 2 * KP, 0, stream>>>(moves, ends, f.nseg, f.dvp);
+      delta_carry_kernel<KP, true><<<chain, 2 * KP, 0, stream>>>(moves, back, f.nseg, f.dvp);
     }
     delta_chunk_kernel<IO, KP, W, kStates><<<walk, 64 * W, 0, stream>>>(a, w, kVecFloatsBwd);
   }

@@ -362,60 +362,75 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, WalkAr
 }
 
 // The chain over segments: X_j += M_j X_(j-1) for j = 1 .. nseg - 2 (REV: X_j += M_j^T
-// X_(j+1) downwards), X the state columns left by the segments.  A block is W waves of
-// sixteen columns; M's terms go through LDS, the next segment's loaded meanwhile.  Four
-// waves: with eight a CU's LDS reads (96 KB a wave and step at 128 x 128) make a step
-// twice as long, 6.8 us.
-template <int KP, int W, bool REV>
-__global__ __launch_bounds__(64 * W) void delta_carry_kernel(const float* moves, float* x, int nseg, int dvp, int nvb) {
-  constexpr int kThreads = 64 * W, kTiles = KP / 16, kSteps = KP / 32, kUnits = KP * KP / 8 / kThreads;
-  typedef Tile<KP> TileK;  // KP rows of it here
-  __shared__ __attribute__((aligned(16))) bf16 sm[3][KP * KP];
-  const int tid = int(threadIdx.x), lane = tid & 63, i = lane & 15, qd = lane >> 4;
-  const int64_t bh = blockIdx.x / unsigned(nvb);
-  const int col = int(blockIdx.x % unsigned(nvb)) * (16 * W) + 16 * wave_id() + i;
-  const int at = col < dvp ? (8 * qd * dvp + col) * 4 : kOutside;
-  const auto x_of = [&](int j) { return buffer_of(x + (bh * nseg + j) * KP * dvp, KP * dvp * 4); };
+// X_(j+1) downwards), X the state columns left by the segments.  A step waits for the
+// one before it, so as little as possible lies on that path: a block has sixteen columns,
+// each of its KP / 32 waves computes 32 rows of them, and takes its rows of M straight to
+// its lanes, cut into terms before the step that needs them; only the columns' terms
+// (3 KB a wave) go round through LDS, one barrier a step.
+template <int KP, bool REV>
+__global__ __launch_bounds__(2 * KP) void delta_carry_kernel(const float* moves, float* x, int nseg, int dvp) {
+  constexpr int kSteps = KP / 32;
+  __shared__ __attribute__((aligned(16))) bf16 terms[2][kSteps][3][64 * 8];
+  const int lane = lane_id(), wave = wave_id(), i = lane & 15, qd = lane >> 4;
+  // the blocks of a head, which all read its M, are neighbours
+  const unsigned ncol = unsigned(dvp) / 16, blk = xcd_block(), head = blk / ncol;
+  const int64_t bh = head;
+  const int col = int(blk - head * ncol) * 16 + i, steps = nseg - 2;
   const int start = REV ? nseg - 2 : 1, step = REV ? -1 : 1;
-  f32x8 next[kUnits];
-  f32x4 S[kTiles], add[kTiles];
+  const int x_at = ((32 * wave + 8 * qd) * dvp + col) * 4;  // rows 8 qd .. + 7 of this wave's 32
+  const auto x_of = [&](int j) { return buffer_of(x + (bh * nseg + j) * KP * dvp, KP * dvp * 4); };
+  f32x8 raw[2][kSteps];
+  f32x4 S[2], add[2];
+  Frag<3> m[2][kSteps];
   const auto load = [&](int j) {
-    const Buffer m = buffer_of(moves + (bh * nseg + j) * KP * KP, KP * KP * 4);
+    const Buffer b = buffer_of(moves + (bh * nseg + j) * KP * KP, KP * KP * 4);
+    const int l = here(lane);
 #pragma unroll
-    for (int n = 0; n < kUnits; ++n) load_wide(m, (tid + kThreads * n) * 32, &next[n]);
-    load_state(x_of(j), at, dvp, add);
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const int row = chained(2 * wave + p, l & 15), k0 = 32 * k + 8 * (l >> 4);
+        if constexpr (REV) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float y;
+            load1(b, ((k0 + e) * KP + row) * 4, &y);
+            raw[p][k][e] = y;
+          }
+        } else {
+          load_wide(b, (row * KP + k0) * 4, &raw[p][k]);
+        }
+      }
+    load_state(x_of(j), x_at, dvp, add);
   };
-  load_state(x_of(start - step), at, dvp, S);
+  const auto cut = [&] {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) m[p][k] = split(raw[p][k]);
+  };
+  load_state(x_of(start - step), x_at, dvp, S);
   load(start);
-  for (int k = 0; k < nseg - 2; ++k) {
-    const int j = start + k * step;
+  cut();
+  for (int n = 0; n < steps; ++n) {
+    const int j = start + n * step;
+    const Frag<3> own = split(S[0], S[1]);
+#pragma unroll
+    for (int t = 0; t < 3; ++t) *reinterpret_cast<bf16x8*>(&terms[n & 1][wave][t][8 * lane]) = own.t[t];
+    S[0] = add[0];
+    S[1] = add[1];
+    if (n + 1 < steps) load(j + step);
     __syncthreads();
 #pragma unroll
-    for (int n = 0; n < kUnits; ++n) {
-      const int u = tid + kThreads * n;
-      const Frag<3> f = split(next[n]);
+    for (int k = 0; k < kSteps; ++k) {
+      Frag<3> f;
 #pragma unroll
-      for (int t = 0; t < 3; ++t)
-        *reinterpret_cast<bf16x8*>(&sm[t][TileK::unit_at(u / (KP / 8), u % (KP / 8))]) = f.t[t];
+      for (int t = 0; t < 3; ++t) f.t[t] = row_frag(&terms[n & 1][k][t][8 * lane]);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) S[p] = mul(m[p][k], f, S[p]);
     }
-    Frag<3> sf[kSteps];
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) sf[s] = split(S[2 * s], S[2 * s + 1]);
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m) S[m] = add[m];
-    __syncthreads();
-    if (k + 1 < nseg - 2) load(j + step);
-    const auto read = [&](int k, Frag<3>& f) {
-      const int m = k / kSteps, s = k % kSteps;
-#pragma unroll
-      for (int t = 0; t < 3; ++t)
-        f.t[t] = REV ? col_frag<KP>(sm[t], 32 * s + 8 * qd, chained(m, 4 * (i & 3)))
-                     : row_frag(&sm[t][TileK::unit_at(chained(m, i), 4 * s + qd)]);
-    };
-    Frag<3> ring[3];
-    ring_start<kTiles * kSteps>(ring, read);
-    ring_run<kTiles * kSteps>(ring, read, [&](int k, const Frag<3>& f) { S[k / kSteps] = mul(f, sf[k % kSteps], S[k / kSteps]); });
-    store_state(x_of(j), at, dvp, S);
+    store_state(x_of(j), x_at, dvp, S);
+    if (n + 1 < steps) cut();
   }
 }
 

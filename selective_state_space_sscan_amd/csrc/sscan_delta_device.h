@@ -101,6 +101,13 @@ __device__ __forceinline__ int lane_id() { return int(threadIdx.x) & 63; }
 // In a scalar register, so that what depends on it branches without masks.
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6); }
 
+// This block's place in an order whose neighbours run on one XCD and share its L2 (blocks
+// go to the eight XCDs in turn): each XCD takes a contiguous part of the grid.
+__device__ __forceinline__ unsigned xcd_block() {
+  const unsigned q = gridDim.x >> 3, r = gridDim.x & 7, x = blockIdx.x & 7;
+  return x * q + (x < r ? x : r) + (blockIdx.x >> 3);
+}
+
 template <typename T>
 __device__ __forceinline__ float to_f32(T x) {
   return float(x);
