@@ -369,7 +369,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
       load_wide(ub, at, &next_u[n]);
       load_wide(xb, at, &next_x[n]);
       load8<IO>(db, (row * int(v_t) + c8) * int(sizeof(IO)), left, wide_d, &next_d[n]);
-      load8<IO>(vb, (row * int(a.sv.t) + c8) * int(sizeof(IO)), left, wide_v, &next_v[n]);
+      load8<IO>(vb, (row * int(a.sv.t) + c8) * int(sizeof(IO)), row < rows ? left : 0, wide_v, &next_v[n]);
     }
   };
   const auto load_states = [&](int hh, int v0) {

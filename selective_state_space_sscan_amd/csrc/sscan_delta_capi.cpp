@@ -101,10 +101,12 @@ int view_delta(const sscan_delta_params* p, DeltaView* w) {
   if (!aligned(p->q, w->esz) || !aligned(p->k, w->esz) || !aligned(p->v, w->esz) || !aligned(p->g, 4) ||
       !aligned(p->beta, 4) || !aligned(p->lengths, 4) || !aligned(p->h0, 16))
     return SSCAN_ERR_ALIGN;
-  // a chunk's rows are addressed by 32-bit byte offsets
-  if (p->q_stride[1] >= sscan::kDeltaMaxStride || p->k_stride[1] >= sscan::kDeltaMaxStride ||
-      p->v_stride[1] >= sscan::kDeltaMaxStride || p->v_heads * p->dv >= sscan::kDeltaMaxStride ||
-      p->qk_heads * p->dk >= sscan::kDeltaMaxStride)
+  // a chunk's rows are addressed by 32-bit byte offsets; a single token's stride is never
+  // used
+  if (p->v_heads * p->dv >= sscan::kDeltaMaxStride || p->qk_heads * p->dk >= sscan::kDeltaMaxStride)
+    return SSCAN_ERR_UNSUPPORTED;
+  if (p->len > 1 && (p->q_stride[1] >= sscan::kDeltaMaxStride || p->k_stride[1] >= sscan::kDeltaMaxStride ||
+                     p->v_stride[1] >= sscan::kDeltaMaxStride))
     return SSCAN_ERR_UNSUPPORTED;
   const int64_t qd[3] = {p->batch, p->len, p->qk_heads}, vd[3] = {p->batch, p->len, p->v_heads};
   const int64_t eq = extent(qd, p->q_stride, 3, p->dk), ek = extent(qd, p->k_stride, 3, p->dk),
@@ -123,6 +125,10 @@ int view_delta(const sscan_delta_params* p, DeltaView* w) {
                           stride_of(p->v_stride), stride_of(p->g_stride), stride_of(p->beta_stride), p->lengths,
                           p->h0, nullptr, nullptr, p->batch, p->len, int(p->qk_heads), int(p->v_heads), int(p->dk),
                           int(p->dv), p->scale, p->qk_norm, p->io_dtype == SSCAN_BF16};
+  if (p->len <= 1) {
+    w->a.sq.t = w->a.sk.t = p->dk;
+    w->a.sv.t = p->dv;
+  }
   return SSCAN_OK;
 }
 

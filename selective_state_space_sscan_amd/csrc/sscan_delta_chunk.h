@@ -16,11 +16,14 @@ struct RowsAhead {
   typename Io<IO>::V8 x[kUnits];
 
   __device__ __forceinline__ void load(const IO* p, int64_t stride, int t0, int len, int dk, bool wide) {
-    const Buffer rows = rows_of(p + t0 * stride, len - t0 < kC ? len - t0 : kC, stride, dk);
+    const int live = len - t0 < kC ? len - t0 : kC;
+    const Buffer rows = rows_of(p + t0 * stride, live, stride, dk);
 #pragma unroll
     for (int n = 0; n < kUnits; ++n) {
       const int u = int(threadIdx.x) + kThreads * n, row = u / (KP / 8), unit = u % (KP / 8);
-      load8<IO>(rows, (row * int(stride) + 8 * unit) * int(sizeof(IO)), dk - 8 * unit, wide, &x[n]);
+      // rows past the end are told apart by their number: overlapping ones (a token stride
+      // below the row's size, 0 for a broadcast) lie inside the buffer
+      load8<IO>(rows, (row * int(stride) + 8 * unit) * int(sizeof(IO)), row < live ? dk - 8 * unit : 0, wide, &x[n]);
     }
   }
 
@@ -69,14 +72,18 @@ struct ColumnsAhead {
   static constexpr int kLds = 16;
   IO x[4][4];
 
-  __device__ __forceinline__ void load(Buffer rows, int64_t stride, int col0, int dv, bool) {
-    const int i = lane_id() & 15, qd = lane_id() >> 4;
-    const int at = here(col0 + i < dv ? (8 * qd * int(stride) + col0 + i) * int(sizeof(IO)) : kOutside);
+  // p: the chunk's first row, of which `live` are read (the others are zeros)
+  __device__ __forceinline__ void load(const IO* p, int live, int64_t stride, int col0, int dv, bool) {
+    const Buffer rows = rows_of(p, live, stride, dv);
+    const int i = lane_id() & 15, first = 8 * (lane_id() >> 4);
+    const int at = here(col0 + i < dv ? (first * int(stride) + col0 + i) * int(sizeof(IO)) : kOutside);
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        load1(rows, at + (32 * (m >> 1) + 4 * (m & 1) + r) * int(stride) * int(sizeof(IO)), &x[m][r]);
+      for (int r = 0; r < 4; ++r) {
+        const int row = 32 * (m >> 1) + 4 * (m & 1) + r;
+        load1(rows, first + row < live ? at + row * int(stride) * int(sizeof(IO)) : kOutside, &x[m][r]);
+      }
   }
 
   __device__ __forceinline__ void get(char*, f32x4 (&v)[4]) const {
@@ -92,10 +99,11 @@ struct ColumnsAhead<bf16> {
   static constexpr int kLds = kC * 16 * 2;  // bytes a wave
   bf16x8 x[2];
 
-  __device__ __forceinline__ void load(Buffer rows, int64_t stride, int col0, int dv, bool wide) {
+  __device__ __forceinline__ void load(const bf16* p, int live, int64_t stride, int col0, int dv, bool wide) {
+    const Buffer rows = rows_of(p, live, stride, dv);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
-      load8<bf16>(rows, (lane_id() * int(stride) + col0 + 8 * n) * 2, dv - col0 - 8 * n, wide, &x[n]);
+      load8<bf16>(rows, (lane_id() * int(stride) + col0 + 8 * n) * 2, lane_id() < live ? dv - col0 - 8 * n : 0, wide, &x[n]);
   }
 
   __device__ __forceinline__ void get(char* own, f32x4 (&v)[4]) const {
@@ -212,7 +220,7 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, WalkAr
     const int t0 = c * kC;
     next_k.load(kp, a.sk.t, t0, Lb, a.dk, wide_qk);
     if constexpr (OUT) next_q.load(qp, a.sq.t, t0, Lb, a.dk, wide_qk);
-    next_v.load(rows_of(vp + t0 * a.sv.t, Lb - t0 < kC ? Lb - t0 : kC, a.sv.t, a.dv), a.sv.t, ident ? a.dv : col - i, a.dv, wide_v);
+    next_v.load(vp + t0 * a.sv.t, Lb - t0 < kC ? Lb - t0 : kC, a.sv.t, ident ? a.dv : col - i, a.dv, wide_v);
   };
   const auto load_frags = [&](int c) {
     const int64_t idx = bh * w.nchunk + c;

@@ -144,7 +144,8 @@ __device__ __forceinline__ f32x8 load8(const float* p, int left, bool wide) {
 }
 
 // Chunk rows are read and written through buffer descriptors whose size ends with the
-// last row: an access past it reads 0 or is dropped, so tails cost no branches.  Offsets
+// last row: an access past it (or at kOutside) reads 0 or is dropped, so tails cost no
+// branches.  Offsets
 // are bytes from the chunk's first row, in 32 bits (the callers' token strides are
 // limited to kDeltaMaxStride elements).
 typedef __amdgpu_buffer_rsrc_t Buffer;

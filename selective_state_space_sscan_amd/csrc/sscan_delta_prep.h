@@ -147,8 +147,9 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int nchunk
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     const int d8 = 32 * s + 8 * qd, row = 16 * wave + i;
-    load8<IO>(kb, (row * int(a.sk.t) + d8) * int(sizeof(IO)), a.dk - d8, wide_qk, &xk[s]);
-    load8<IO>(qb, (row * int(a.sq.t) + d8) * int(sizeof(IO)), a.dk - d8, wide_qk, &xq[s]);
+    const int left = row < rows ? a.dk - d8 : 0;
+    load8<IO>(kb, (row * int(a.sk.t) + d8) * int(sizeof(IO)), left, wide_qk, &xk[s]);
+    load8<IO>(qb, (row * int(a.sq.t) + d8) * int(sizeof(IO)), left, wide_qk, &xq[s]);
   }
   // every wave has all tokens' running sums of g, and computes one of the tables
   const int t = t0 + lane;
@@ -194,7 +195,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int nchunk
         if (ct != wave) {
           const int d8 = 32 * s + 8 * qd;
           typename Io<IO>::V8 x;
-          load8<IO>(kb, ((16 * ct + i) * int(a.sk.t) + d8) * int(sizeof(IO)), a.dk - d8, wide_qk, &x);
+          load8<IO>(kb, ((16 * ct + i) * int(a.sk.t) + d8) * int(sizeof(IO)), 16 * ct + i < rows ? a.dk - d8 : 0, wide_qk, &x);
           fb = as_frag(x);
         }
         kk[ct] = mul(fk[s], fb, kk[ct]);

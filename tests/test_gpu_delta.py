@@ -172,6 +172,39 @@ def test_shared_inputs_by_broadcast():
     close(last, ref_last.expand(3, -1, -1, -1), "h_last")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("L", [5, 70, 1300])
+def test_rows_that_overlap(L, dtype):
+    """One key and value for all tokens (token stride 0) and windows sliding by less than a
+    row: the tokens past the end of the last chunk are not taken for live ones."""
+    q, k, v, g, beta = inputs(1, L, 1, 1, 64, 64, dtype, seed=9)
+    q_line = torch.randn(L * 16 + 64, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV) / 8
+    q_win = q_line.as_strided((1, L, 1, 64), (0, 16, 64, 1))
+    k0, v0 = k[:, :1].to(DEV), v[:, :1].to(DEV)
+    out, last = sscan.delta_fwd(q_win, k0.expand(1, L, 1, 64), v0.expand(1, L, 1, 64), g.to(DEV), beta.to(DEV))
+    full = [q_win.cpu().clone(), k[:, :1].expand(1, L, 1, 64), v[:, :1].expand(1, L, 1, 64), g, beta]
+    ref, ref_last = delta_ref.delta(*full)
+    close(out, ref, "out")
+    close(last, ref_last, "h_last")
+    dout = torch.randn(1, L, 1, 64, generator=torch.Generator().manual_seed(2)).to(dtype).to(DEV)
+    r = sscan.delta_bwd(q_win, k0.expand(1, L, 1, 64), v0.expand(1, L, 1, 64), g.to(DEV), beta.to(DEV), dout)
+    r2 = sscan.delta_bwd(*[x.contiguous().to(DEV) for x in full], dout)
+    for name in r:
+        assert torch.equal(r[name], r2[name]), name
+
+
+def test_one_token_of_a_huge_stride():
+    x = [t.to(DEV) for t in inputs(1, 1, 1, 1, 64, 64, torch.float32, seed=3)]
+    odd = [t.as_strided(t.shape, (t.stride(0), 1 << 40, *t.stride()[2:])) for t in x]
+    out, last = sscan.delta_fwd(*odd)
+    want, want_last = sscan.delta_fwd(*x)
+    assert torch.equal(out, want) and torch.equal(last, want_last)
+    dout = torch.ones(1, 1, 1, 64, device=DEV)
+    a, b = sscan.delta_bwd(*odd, dout), sscan.delta_bwd(*x, dout)
+    for name in a:
+        assert torch.equal(a[name], b[name]), name
+
+
 def test_empty_calls():
     ins = inputs(2, 0, 1, 1, 64, 64, torch.float32)
     h0 = state(2, 1, 64, 64)
