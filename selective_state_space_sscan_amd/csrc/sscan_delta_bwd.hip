@@ -47,8 +47,9 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_
 
   const DeltaArgs& a = b_.f;
   const int tid = int(threadIdx.x), lane = tid & 63, wave = wave_id(), i = lane & 15, qd = lane >> 4;
-  const int vb = int(blockIdx.x % unsigned(w.nvb)), seg = int(blockIdx.x / unsigned(w.nvb) % unsigned(w.nseg));
-  const int64_t bh = blockIdx.x / unsigned(w.nvb) / unsigned(w.nseg), b = bh / a.hv, at_seg = bh * w.nseg + seg;
+  const unsigned blk = xcd_block();
+  const int vb = int(blk % unsigned(w.nvb)), seg = int(blk / unsigned(w.nvb) % unsigned(w.nseg));
+  const int64_t bh = blk / unsigned(w.nvb) / unsigned(w.nseg), b = bh / a.hv, at_seg = bh * w.nseg + seg;
   if (ENDS && seg == 0) return;  // nobody reads it
   const int h = int(bh % a.hv), hq = h / (a.hv / a.hk);
   const int col = vb * (16 * W) + 16 * wave + i, dvp = w.dvp;

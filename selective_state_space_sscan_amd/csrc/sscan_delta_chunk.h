@@ -168,8 +168,10 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, WalkAr
 
   const int tid = int(threadIdx.x), lane = tid & 63, wave = wave_id(), i = lane & 15, qd = lane >> 4;
   const int blocks = w.nvb + (MODE == kEnds ? (KP + 16 * W - 1) / (16 * W) : 0);
-  const int vb = int(blockIdx.x % unsigned(blocks)), seg = int(blockIdx.x / unsigned(blocks) % unsigned(w.nseg));
-  const int64_t bh = blockIdx.x / unsigned(blocks) / unsigned(w.nseg), b = bh / a.hv, at_seg = bh * w.nseg + seg;
+  // blocks of a segment, which read the same keys and factors, are neighbours
+  const unsigned blk = xcd_block();
+  const int vb = int(blk % unsigned(blocks)), seg = int(blk / unsigned(blocks) % unsigned(w.nseg));
+  const int64_t bh = blk / unsigned(blocks) / unsigned(w.nseg), b = bh / a.hv, at_seg = bh * w.nseg + seg;
   const bool ident = MODE == kEnds && vb >= w.nvb;
   if (MODE == kEnds && (seg == w.nseg - 1 || (ident && seg == 0))) return;  // nobody reads these
   const int h = int(bh % a.hv), hq = h / (a.hv / a.hk);
