@@ -178,9 +178,9 @@ hipError_t launch_walk(const DeltaArgs& a, const DeltaPlan& p, char* ws, hipStre
 template <typename IO>
 hipError_t launch_fwd(const DeltaArgs& a, const DeltaPlan& p, char* ws, hipStream_t stream) {
   if (p.recurrent) return a.dk <= 64 ? launch_recurrent<IO, 8>(a, stream) : launch_recurrent<IO, 16>(a, stream);
-  if (p.kp == 64)
-    return p.waves == 8 ? launch_walk<IO, 64, 8>(a, p, ws, stream) : launch_walk<IO, 64, 4>(a, p, ws, stream);
-  return p.waves == 8 ? launch_walk<IO, 128, 8>(a, p, ws, stream) : launch_walk<IO, 128, 4>(a, p, ws, stream);
+  if constexpr (std::is_same<IO, bf16>::value)  // float32 walks have four waves
+    if (p.waves == 8) return p.kp == 64 ? launch_walk<IO, 64, 8>(a, p, ws, stream) : launch_walk<IO, 128, 8>(a, p, ws, stream);
+  return p.kp == 64 ? launch_walk<IO, 64, 4>(a, p, ws, stream) : launch_walk<IO, 128, 4>(a, p, ws, stream);
 }
 
 }  // namespace delta
@@ -227,7 +227,12 @@ DeltaPlan make_delta_plan(int64_t batch, int64_t len, int hk, int hv, int dk, in
   p.recurrent = len <= kDeltaRecurrentMax;
   p.kp = dk <= 64 ? 64 : 128;
   p.dvp = (dv + 31) / 32 * 32;
-  p.waves = dv > 64 ? 8 : 4;
+  // Waves of a walk's block.  Eight share a chunk's tiles between 128 columns, four take a
+  // CU for themselves and end a chunk sooner (4.5 us against 5.4): four for float32 (whose
+  // registers eight waves spill: 2 x 2048 tokens of 8 heads 125 us against 136, one row of
+  // 500 72 against 108) and where there are few chunks for the GPU (bf16, 4 heads of 500 tokens 47 us
+  // against 55; 64 heads of 2048 the same, 178; 256 heads of 1024 229 against 184).
+  p.waves = dv > 64 && io_bf16 && batch * hv * p.nchunk >= 1024 ? 8 : 4;
   if (p.recurrent) return p;
   const int cols = 16 * p.waves;
   const int64_t heads = batch * hv;

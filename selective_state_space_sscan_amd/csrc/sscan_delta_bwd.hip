@@ -734,9 +734,10 @@ hipError_t launch_bwd(const DeltaBwdArgs& b, const DeltaBwdPlan& p, char* ws, hi
 
 template <typename IO>
 hipError_t launch_bwd(const DeltaBwdArgs& b, const DeltaBwdPlan& p, char* ws, hipStream_t stream) {
-  if (p.f.kp == 64)
-    return p.f.waves == 8 ? launch_bwd<IO, 64, 8>(b, p, ws, stream) : launch_bwd<IO, 64, 4>(b, p, ws, stream);
-  return p.f.waves == 8 ? launch_bwd<IO, 128, 8>(b, p, ws, stream) : launch_bwd<IO, 128, 4>(b, p, ws, stream);
+  if constexpr (std::is_same<IO, bf16>::value)  // float32 walks have four waves
+    if (p.f.waves == 8)
+      return p.f.kp == 64 ? launch_bwd<IO, 64, 8>(b, p, ws, stream) : launch_bwd<IO, 128, 8>(b, p, ws, stream);
+  return p.f.kp == 64 ? launch_bwd<IO, 64, 4>(b, p, ws, stream) : launch_bwd<IO, 128, 4>(b, p, ws, stream);
 }
 
 }  // namespace delta
