@@ -3,9 +3,11 @@
 // next block's norm.  All of them are bound by HBM: a group of TPR threads holds one
 // normed vector in registers (eight elements a thread), so every input is read once
 // and every output written once; blocks walk over rows, so that the weights are loaded
-// once per block and the next row's values while a row is reduced.  Sums and norms are float32.  The gradients of
-// the weights are summed per thread over a block's rows, across the block in LDS and
-// over the blocks by a second kernel, always in the same order.
+// once per block and the next row's values while a row is reduced.  Sums and norms are
+// float32.  The gradients of the weights are summed per thread over a block's rows, across
+// the block in LDS and over the blocks by a second kernel, always in the same order.
+// Measured, of what a large copy moves (4.7 TB/s): norm and gate of 16384 x 16 x 128 bf16
+// 5.9 TB/s, its gradients at 8192 x 1536 3.7, residual norm gradients of 16384 x 1536 4.9.
 #include "sscan_delta.h"
 
 #include "sscan_delta_device.h"
@@ -29,43 +31,82 @@ constexpr int threads() {
   return TPR < 256 ? 256 : TPR;
 }
 
-// Element j of thread t: eight neighbours where 16-byte accesses are possible,
-// otherwise neighbours across threads.
-template <int TPR>
-__device__ __forceinline__ int elem(int j, int t, bool wide) {
-  return wide ? 8 * t + j : j * TPR + t;
+// Thread t holds elements 8 t .. 8 t + 7 of a vector, moved by 16-byte accesses at
+// whatever alignment the rows have, which global memory takes (one element at a time,
+// residual norm gradients of 8000 x 2001 took 166 us).  Where a size is no multiple of
+// eight (not `whole`) the thread at its end reads the last eight elements instead, and
+// takes for zeros the `dup` of them that its neighbour holds: loads of single elements
+// would have to be waited for where they are put together, before the row ahead is
+// reduced (99 us, so 78; 8000 x 2000 55).  In place, its neighbour may have stored them
+// already: whatever it reads there is dropped.  Only its stores, and vectors of less than
+// eight, go one element at a time.
+struct Place {
+  int off, dup;
+};
+
+template <bool whole>
+__device__ __forceinline__ Place place(int size, int t) {
+  if (whole || 8 * t + 8 <= size || size < 8) return {8 * t, 0};
+  return {size - 8, 8 * t + 8 - size};
 }
 
-template <typename T, int TPR>
-__device__ __forceinline__ void load(const T* p, int size, int t, bool wide, float (&x)[8]) {
-  if (wide) {
-    const auto y = delta::load8(p + 8 * t, 8 * t < size ? 8 : 0, true);
+typedef bf16x8 bf16x8_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+__device__ __forceinline__ bf16x8 load_eight(const bf16* p) {
+  return *reinterpret_cast<const bf16x8_any*>(p);
+}
+
+__device__ __forceinline__ f32x8 load_eight(const float* p) {
+  const f32x4 a = *reinterpret_cast<const f32x4_any*>(p), b = *reinterpret_cast<const f32x4_any*>(p + 4);
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+__device__ __forceinline__ void store_eight(bf16* p, bf16x8 x) { *reinterpret_cast<bf16x8_any*>(p) = x; }
+
+__device__ __forceinline__ void store_eight(float* p, f32x8 x) {
+  *reinterpret_cast<f32x4_any*>(p) = f32x4{x[0], x[1], x[2], x[3]};
+  *reinterpret_cast<f32x4_any*>(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+}
+
+// The vector's elements that thread t holds, zeros beyond its size.  Converted after the
+// branches: inside them each would end with a wait for its load, and a row's loads would
+// not be under way while the row before is reduced (residual norm gradients 119 us, so 92).
+template <bool whole, typename T>
+__device__ __forceinline__ void load(const T* p, int size, int t, float (&x)[8]) {
+  const Place at = place<whole>(size, t);
+  typename delta::Io<T>::V8 y = {};
+  if (whole || size >= 8) {
+    if (8 * t < size) y = load_eight(p + at.off);
+  } else if (t == 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = float(y[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = j * TPR + t < size ? float(p[j * TPR + t]) : 0.0f;
+    for (int j = 0; j < 7; ++j)
+      if (j < size) y[j] = p[j];
   }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = j < at.dup ? 0.0f : float(y[j]);
 }
 
-template <typename T, int TPR>
-__device__ __forceinline__ void store(T* p, int size, int t, bool wide, const float (&x)[8]) {
-  if (wide) {
-    typename delta::Io<T>::V8 y;
+template <bool whole, typename T>
+__device__ __forceinline__ void store(T* p, int size, int t, const float (&x)[8]) {
+  const Place at = place<whole>(size, t);
+  const int left = size - 8 * t;
+  typename delta::Io<T>::V8 y;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = T(x[j]);
-    if (8 * t < size) *reinterpret_cast<typename delta::Io<T>::V8*>(p + 8 * t) = y;
-  } else {
+  for (int j = 0; j < 8; ++j) y[j] = T(x[j]);
+  if (whole ? left > 0 : left >= 8) {
+    store_eight(p + 8 * t, y);
+  } else if (!whole && left > 0) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j * TPR + t < size) p[j * TPR + t] = T(x[j]);
+      if (j >= at.dup && at.off + j < size) p[at.off + j] = y[j];
   }
 }
 
-template <int TPR>
-__device__ __forceinline__ void load_or(const float* p, int size, int t, bool wide, float missing, float (&x)[8]) {
+template <bool whole>
+__device__ __forceinline__ void load_or(const float* p, int size, int t, float missing, float (&x)[8]) {
   if (p) {
-    load<float, TPR>(p, size, t, wide, x);
+    load<whole>(p, size, t, x);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = missing;
@@ -99,16 +140,18 @@ __device__ __forceinline__ void group_sum(float (&x)[n], float (*lds)[3][16], in
 }
 
 // Adds the groups' sums of one block in order and writes them as the block's partial.
-template <int TPR>
-__device__ __forceinline__ void write_partial(float* dst, int size, int t, bool wide, const float (&x)[8], float* lds) {
+template <int TPR, bool whole>
+__device__ __forceinline__ void write_partial(float* dst, int size, int t, const float (&x)[8], float* lds) {
   if constexpr (TPR >= 256) {
-    store<float, TPR>(dst, size, t, wide, x);
+    store<whole>(dst, size, t, x);
   } else {
     constexpr int kGroups = 256 / TPR, kCap = TPR * 8;
     const int grp = int(threadIdx.x) / TPR;
+    const Place at = place<whole>(size, t);
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) lds[grp * kCap + elem<TPR>(j, t, wide)] = x[j];
+    for (int j = 0; j < 8; ++j)
+      if (j >= at.dup) lds[grp * kCap + at.off + j] = x[j];
     __syncthreads();
     for (int e = int(threadIdx.x); e < kCap; e += 256) {
       float s = 0.0f;
@@ -157,7 +200,7 @@ struct UnitWalk {
 // ---- norm and gate of a mixer's heads -------------------------------------------------
 //   y = x r w silu(z), r = 1 / rms(x)           (gate after the norm)
 //   y = m r w, m = x silu(z), r = 1 / rms(m)    (gate_first)
-template <typename IO, int TPR, bool wide>
+template <typename IO, int TPR, bool whole>
 __global__ __launch_bounds__(threads<TPR>()) void gated_norm_kernel(GatedNormArgs a) {
   __shared__ float lds[2][3][16];
   constexpr int kGroups = threads<TPR>() / TPR;
@@ -167,11 +210,11 @@ __global__ __launch_bounds__(threads<TPR>()) void gated_norm_kernel(GatedNormArg
   float w[8], next_x[8], next_z[8], next_w[8];
   const auto load_next = [&] {
     const int size = at.live() ? int(a.size) : 0;
-    load<IO, TPR>(static_cast<const IO*>(a.x) + at.row * a.xr + at.h * a.xh, size, t, wide, next_x);
-    load<IO, TPR>(static_cast<const IO*>(a.z) + at.row * a.zr + at.h * a.zh, size, t, wide, next_z);
-    if (a.per_head) load<float, TPR>(a.weight + at.h * a.size, size, t, wide, next_w);
+    load<whole>(static_cast<const IO*>(a.x) + at.row * a.xr + at.h * a.xh, size, t, next_x);
+    load<whole>(static_cast<const IO*>(a.z) + at.row * a.zr + at.h * a.zh, size, t, next_z);
+    if (a.per_head) load<whole>(a.weight + at.h * a.size, size, t, next_w);
   };
-  if (!a.per_head) load_or<TPR>(a.weight, int(a.size), t, wide, 1.0f, w);
+  if (!a.per_head) load_or<whole>(a.weight, int(a.size), t, 1.0f, w);
   load_next();
   const float inv = 1.0f / float(a.size);
   int turn = 0;
@@ -198,13 +241,13 @@ __global__ __launch_bounds__(threads<TPR>()) void gated_norm_kernel(GatedNormArg
     const float r = 1.0f / sqrtf(ss[0] * inv + a.eps);
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] *= a.gate_first ? r * w[j] : r * w[j] * z[j];
-    store<IO, TPR>(out, size, t, wide, x);
+    store<whole>(out, size, t, x);
   }
 }
 
 // With n = m r the gradient at m is r (dn - m r^2 mean(dn m)).  Per block: all units
 // (shared weight), or the units of head blockIdx % heads (per_head).
-template <typename IO, int TPR, bool wide>
+template <typename IO, int TPR, bool whole>
 __global__ __launch_bounds__(threads<TPR>()) void gated_norm_bwd_kernel(GatedNormArgs a, float* partial) {
   __shared__ float lds[2][3][16];
   __shared__ float sums[partial_lds<TPR>()];
@@ -218,11 +261,11 @@ __global__ __launch_bounds__(threads<TPR>()) void gated_norm_bwd_kernel(GatedNor
   const auto load_next = [&] {
     const int size = at.live() ? int(a.size) : 0;
     const int64_t h = a.per_head ? set : at.h;
-    load<IO, TPR>(static_cast<const IO*>(a.x) + at.row * a.xr + h * a.xh, size, t, wide, next_x);
-    load<IO, TPR>(static_cast<const IO*>(a.z) + at.row * a.zr + h * a.zh, size, t, wide, next_z);
-    load<IO, TPR>(static_cast<const IO*>(a.dout) + (at.row * a.heads + h) * a.size, size, t, wide, next_d);
+    load<whole>(static_cast<const IO*>(a.x) + at.row * a.xr + h * a.xh, size, t, next_x);
+    load<whole>(static_cast<const IO*>(a.z) + at.row * a.zr + h * a.zh, size, t, next_z);
+    load<whole>(static_cast<const IO*>(a.dout) + (at.row * a.heads + h) * a.size, size, t, next_d);
   };
-  load_or<TPR>(a.weight ? a.weight + set * a.size : nullptr, int(a.size), t, wide, 1.0f, w);
+  load_or<whole>(a.weight ? a.weight + set * a.size : nullptr, int(a.size), t, 1.0f, w);
   load_next();
   const float inv = 1.0f / float(a.size);
   int turn = 0;
@@ -266,17 +309,17 @@ __global__ __launch_bounds__(threads<TPR>()) void gated_norm_bwd_kernel(GatedNor
         x[j] = r * (d[j] * w[j] * gate - x[j] * (r * r) * mean);
       }
     }
-    store<IO, TPR>(static_cast<IO*>(a.dx) + flat, size, t, wide, x);
-    store<IO, TPR>(static_cast<IO*>(a.dz) + flat, size, t, wide, z);
+    store<whole>(static_cast<IO*>(a.dx) + flat, size, t, x);
+    store<whole>(static_cast<IO*>(a.dz) + flat, size, t, z);
   }
-  if (a.dweight) write_partial<TPR>(partial + int64_t(blockIdx.x) * a.size, int(a.size), t, wide, dw, sums);
+  if (a.dweight) write_partial<TPR, whole>(partial + int64_t(blockIdx.x) * a.size, int(a.size), t, dw, sums);
 }
 
 // ---- residual scale and sum with the next norm ----------------------------------------
 //   total = residual + scale a, a = x or x / rms(x) * post_weight; out = total / rms(total) * weight
 // The norm is taken of the total as it is stored, so that the backward pass (which
 // reads the stored total) differentiates what was computed.
-template <typename IO, typename RES, int TPR, bool wide>
+template <typename IO, typename RES, int TPR, bool whole>
 __global__ __launch_bounds__(threads<TPR>()) void add_norm_kernel(AddNormArgs a) {
   __shared__ float lds[2][3][16];
   constexpr int kGroups = threads<TPR>() / TPR;
@@ -286,13 +329,13 @@ __global__ __launch_bounds__(threads<TPR>()) void add_norm_kernel(AddNormArgs a)
   const auto load_next = [&](int64_t u) {
     const int size = u < a.rows ? int(a.size) : 0;
     const int64_t flat = size ? u * a.size : 0;
-    load<IO, TPR>(static_cast<const IO*>(a.x) + flat, size, t, wide, next_x);
-    load<RES, TPR>(static_cast<const RES*>(a.residual) + flat, a.residual ? size : 0, t, wide, next_y);
+    load<whole>(static_cast<const IO*>(a.x) + flat, size, t, next_x);
+    load<whole>(static_cast<const RES*>(a.residual) + flat, a.residual ? size : 0, t, next_y);
   };
   load_next(int64_t(blockIdx.x) * kGroups + grp);
-  load_or<TPR>(a.weight, int(a.size), t, wide, 1.0f, w);
-  load_or<TPR>(a.scale, int(a.size), t, wide, 1.0f, sc);
-  load_or<TPR>(a.post_weight, int(a.size), t, wide, 1.0f, pw);
+  load_or<whole>(a.weight, int(a.size), t, 1.0f, w);
+  load_or<whole>(a.scale, int(a.size), t, 1.0f, sc);
+  load_or<whole>(a.post_weight, int(a.size), t, 1.0f, pw);
   const float inv = 1.0f / float(a.size);
   int turn = 0;
   for (int64_t u0 = int64_t(blockIdx.x) * kGroups; u0 < a.rows; u0 += step) {
@@ -321,19 +364,19 @@ __global__ __launch_bounds__(threads<TPR>()) void add_norm_kernel(AddNormArgs a)
       y[j] = float(RES(y[j] + x[j] * sc[j]));
       ss[0] += y[j] * y[j];
     }
-    store<RES, TPR>(static_cast<RES*>(a.residual_out) + flat, size, t, wide, y);
+    store<whole>(static_cast<RES*>(a.residual_out) + flat, size, t, y);
     group_sum<TPR>(ss, lds, turn);
     turn ^= 1;
     const float r = 1.0f / sqrtf(ss[0] * inv + a.eps);
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] *= r * w[j];
-    store<IO, TPR>(static_cast<IO*>(a.out) + flat, size, t, wide, y);
+    store<whole>(static_cast<IO*>(a.out) + flat, size, t, y);
   }
 }
 
 // POST: with a norm of x itself.  Sums left by a block: dweight, dscale, dpost_weight.
 // Blocks of 1024 threads have 128 registers a thread: they read the vectors per row.
-template <typename IO, typename RES, int TPR, bool wide, bool POST>
+template <typename IO, typename RES, int TPR, bool whole, bool POST>
 __global__ __launch_bounds__(threads<TPR>()) void add_norm_bwd_kernel(AddNormArgs a, float* partial) {
   __shared__ float lds[2][3][16];
   __shared__ float sums[partial_lds<TPR>()];
@@ -346,15 +389,15 @@ __global__ __launch_bounds__(threads<TPR>()) void add_norm_bwd_kernel(AddNormArg
   const auto load_next = [&](int64_t u) {
     const int size = u < a.rows ? int(a.size) : 0;
     const int64_t flat = size ? u * a.size : 0;
-    load<IO, TPR>(static_cast<const IO*>(a.x) + flat, size, t, wide, next_x);
-    load<RES, TPR>(static_cast<const RES*>(a.residual) + flat, size, t, wide, next_y);
-    load<IO, TPR>(static_cast<const IO*>(a.dout) + flat, size, t, wide, next_d);
-    load<RES, TPR>(static_cast<const RES*>(a.dresidual_out) + flat, a.dresidual_out ? size : 0, t, wide, next_e);
+    load<whole>(static_cast<const IO*>(a.x) + flat, size, t, next_x);
+    load<whole>(static_cast<const RES*>(a.residual) + flat, size, t, next_y);
+    load<whole>(static_cast<const IO*>(a.dout) + flat, size, t, next_d);
+    load<whole>(static_cast<const RES*>(a.dresidual_out) + flat, a.dresidual_out ? size : 0, t, next_e);
   };
   const auto load_vectors = [&] {
-    load_or<TPR>(a.weight, int(a.size), t, wide, 1.0f, w);
-    load_or<TPR>(a.scale, int(a.size), t, wide, 1.0f, sc);
-    if (POST) load_or<TPR>(a.post_weight, int(a.size), t, wide, 1.0f, pw);
+    load_or<whole>(a.weight, int(a.size), t, 1.0f, w);
+    load_or<whole>(a.scale, int(a.size), t, 1.0f, sc);
+    if (POST) load_or<whole>(a.post_weight, int(a.size), t, 1.0f, pw);
   };
   if (kHold) {
     load_next(int64_t(blockIdx.x) * kGroups + grp);
@@ -405,7 +448,7 @@ __global__ __launch_bounds__(threads<TPR>()) void add_norm_bwd_kernel(AddNormArg
         d[j] = scaled;
       }
     }
-    store<RES, TPR>(static_cast<RES*>(a.dresidual) + flat, size, t, wide, e);
+    store<whole>(static_cast<RES*>(a.dresidual) + flat, size, t, e);
     if (POST) {
       group_sum<TPR>(dot, lds, turn);
       turn ^= 1;
@@ -413,12 +456,12 @@ __global__ __launch_bounds__(threads<TPR>()) void add_norm_bwd_kernel(AddNormArg
 #pragma unroll
       for (int j = 0; j < 8; ++j) d[j] = rx * (d[j] - x[j] * (rx * rx) * m2);
     }
-    store<IO, TPR>(static_cast<IO*>(a.dx) + flat, size, t, wide, d);
+    store<whole>(static_cast<IO*>(a.dx) + flat, size, t, d);
   }
   float* dst = partial + int64_t(blockIdx.x) * 3 * a.size;
-  if (a.dweight) write_partial<TPR>(dst, int(a.size), t, wide, dw, sums);
-  if (a.dscale) write_partial<TPR>(dst + a.size, int(a.size), t, wide, ds, sums);
-  if (POST && a.dpost_weight) write_partial<TPR>(dst + 2 * a.size, int(a.size), t, wide, dp, sums);
+  if (a.dweight) write_partial<TPR, whole>(dst, int(a.size), t, dw, sums);
+  if (a.dscale) write_partial<TPR, whole>(dst + a.size, int(a.size), t, ds, sums);
+  if (POST && a.dpost_weight) write_partial<TPR, whole>(dst + 2 * a.size, int(a.size), t, dp, sums);
 }
 
 // out[set][e] = sum over the blocks of set `set` of partial[block][part][e], in order:
@@ -472,44 +515,27 @@ int64_t back_blocks(int64_t units, int64_t size, int64_t heads, int64_t limit) {
   return (want < most ? want : most) * heads;
 }
 
-bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
 template <int TPR, typename F>
-void by_width(bool wide, F f) {
-  if (wide)
+void by_end(int64_t size, F f) {
+  if (size % 8 == 0)
     f(std::integral_constant<int, TPR>(), std::true_type());
   else
     f(std::integral_constant<int, TPR>(), std::false_type());
 }
 
-// f(threads a vector, wide accesses), both as constants.
+// f(threads a vector, whole), as constants.
 template <typename F>
-hipError_t by_shape(int64_t size, bool wide, F f) {
+hipError_t by_shape(int64_t size, F f) {
   switch (threads_of(size)) {
-    case 16: by_width<16>(wide, f); break;
-    case 32: by_width<32>(wide, f); break;
-    case 64: by_width<64>(wide, f); break;
-    case 128: by_width<128>(wide, f); break;
-    case 256: by_width<256>(wide, f); break;
-    case 512: by_width<512>(wide, f); break;
-    default: by_width<1024>(wide, f); break;  // size <= kNormMaxSize
+    case 16: by_end<16>(size, f); break;
+    case 32: by_end<32>(size, f); break;
+    case 64: by_end<64>(size, f); break;
+    case 128: by_end<128>(size, f); break;
+    case 256: by_end<256>(size, f); break;
+    case 512: by_end<512>(size, f); break;
+    default: by_end<1024>(size, f); break;  // size <= kNormMaxSize
   }
   return hipGetLastError();
-}
-
-// Whether a call's tensors allow 16-byte accesses throughout (one choice per call: the
-// weights and the data share the threads' element order).
-template <typename IO>
-bool gated_wide(const GatedNormArgs& a) {
-  const int64_t n = 16 / int64_t(sizeof(IO));
-  return a.size % 8 == 0 && al16(a.x) && al16(a.z) && al16(a.out) && al16(a.dout) && al16(a.dx) && al16(a.dz) &&
-         al16(a.weight) && a.xr % n == 0 && a.xh % n == 0 && a.zr % n == 0 && a.zh % n == 0;
-}
-
-bool add_wide(const AddNormArgs& a) {
-  return a.size % 8 == 0 && al16(a.x) && al16(a.residual) && al16(a.out) && al16(a.residual_out) && al16(a.dout) &&
-         al16(a.dresidual_out) && al16(a.dx) && al16(a.dresidual) && al16(a.weight) && al16(a.scale) &&
-         al16(a.post_weight);
 }
 
 }  // namespace norm
@@ -529,11 +555,11 @@ size_t add_norm_bwd_workspace(int64_t rows, int64_t size) {
 
 template <typename IO>
 static hipError_t gated_fwd(const GatedNormArgs& a, hipStream_t stream) {
-  return norm::by_shape(a.size, norm::gated_wide<IO>(a), [&](auto tpr, auto wide) {
+  return norm::by_shape(a.size, [&](auto tpr, auto whole) {
     constexpr int T = decltype(tpr)::value, B = norm::threads<T>();
     int64_t n = norm::div_up(a.rows * a.heads, B / T);
     if (n > norm::kMaxBlocks) n = norm::kMaxBlocks;
-    norm::gated_norm_kernel<IO, T, decltype(wide)::value><<<dim3(unsigned(n)), B, 0, stream>>>(a);
+    norm::gated_norm_kernel<IO, T, decltype(whole)::value><<<dim3(unsigned(n)), B, 0, stream>>>(a);
   });
 }
 
@@ -543,9 +569,9 @@ static hipError_t gated_bwd(const GatedNormArgs& a, float* ws, hipStream_t strea
   const int64_t n = norm::back_blocks(a.per_head ? a.rows : a.rows * a.heads, a.size, sets, norm::kMaxGatedBackBlocks);
   if (sets == 0) return hipSuccess;  // per-head weights of no heads
   // without rows there are no blocks, and the sums over none are zeros
-  const hipError_t e = n == 0 ? hipSuccess : norm::by_shape(a.size, norm::gated_wide<IO>(a), [&](auto tpr, auto wide) {
+  const hipError_t e = n == 0 ? hipSuccess : norm::by_shape(a.size, [&](auto tpr, auto whole) {
     constexpr int T = decltype(tpr)::value, B = norm::threads<T>();
-    norm::gated_norm_bwd_kernel<IO, T, decltype(wide)::value><<<dim3(unsigned(n)), B, 0, stream>>>(a, ws);
+    norm::gated_norm_bwd_kernel<IO, T, decltype(whole)::value><<<dim3(unsigned(n)), B, 0, stream>>>(a, ws);
   });
   if (e != hipSuccess || !a.dweight) return e;
   const norm::SumArgs s{ws, {a.dweight, nullptr, nullptr}, a.size, a.size, n, sets};
@@ -555,24 +581,24 @@ static hipError_t gated_bwd(const GatedNormArgs& a, float* ws, hipStream_t strea
 
 template <typename IO, typename RES>
 static hipError_t add_fwd(const AddNormArgs& a, hipStream_t stream) {
-  return norm::by_shape(a.size, norm::add_wide(a), [&](auto tpr, auto wide) {
+  return norm::by_shape(a.size, [&](auto tpr, auto whole) {
     constexpr int T = decltype(tpr)::value, B = norm::threads<T>();
     int64_t n = norm::div_up(a.rows, B / T);
     if (n > norm::kMaxBlocks) n = norm::kMaxBlocks;
-    norm::add_norm_kernel<IO, RES, T, decltype(wide)::value><<<dim3(unsigned(n)), B, 0, stream>>>(a);
+    norm::add_norm_kernel<IO, RES, T, decltype(whole)::value><<<dim3(unsigned(n)), B, 0, stream>>>(a);
   });
 }
 
 template <typename IO, typename RES>
 static hipError_t add_bwd(const AddNormArgs& a, float* ws, hipStream_t stream) {
   const int64_t n = norm::back_blocks(a.rows, a.size, 1, norm::kMaxAddBackBlocks);
-  const hipError_t e = n == 0 ? hipSuccess : norm::by_shape(a.size, norm::add_wide(a), [&](auto tpr, auto wide) {
+  const hipError_t e = n == 0 ? hipSuccess : norm::by_shape(a.size, [&](auto tpr, auto whole) {
     constexpr int T = decltype(tpr)::value, B = norm::threads<T>();
     const dim3 grid{unsigned(n)};
     if (a.post_weight)
-      norm::add_norm_bwd_kernel<IO, RES, T, decltype(wide)::value, true><<<grid, B, 0, stream>>>(a, ws);
+      norm::add_norm_bwd_kernel<IO, RES, T, decltype(whole)::value, true><<<grid, B, 0, stream>>>(a, ws);
     else
-      norm::add_norm_bwd_kernel<IO, RES, T, decltype(wide)::value, false><<<grid, B, 0, stream>>>(a, ws);
+      norm::add_norm_bwd_kernel<IO, RES, T, decltype(whole)::value, false><<<grid, B, 0, stream>>>(a, ws);
   });
   if (e != hipSuccess || !(a.dweight || a.dscale || a.dpost_weight)) return e;
   const norm::SumArgs s{ws, {a.dweight, a.dscale, a.dpost_weight}, a.size, 3 * a.size, n, 1};

@@ -137,6 +137,23 @@ def test_add_norm_in_place_and_unaligned():
     close(y2, y.cpu().double(), "y")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [5, 7, 9, 15, 129, 1031, 2047, 4097, 8185])
+def test_sizes_with_a_rest(size, dtype):
+    test_gated_norm(9, 1, size, "shared", False, dtype)
+    test_gated_norm(3, 4, size, "per_head", True, dtype)
+    test_add_norm(11, size, "all", dtype, torch.float32)
+
+
+@pytest.mark.parametrize("size", [9, 513, 2001])
+def test_in_place_with_a_rest(size):
+    x, res, w = on(rand(700, size, seed=1), rand(700, size, seed=2), 1 + rand(size, seed=3))
+    y, total = sscan.add_norm(x, res, w)
+    kept = res.clone()
+    y2, _ = sscan.add_norm(x, kept, w, residual_out=kept)
+    assert torch.equal(total, kept) and torch.equal(y, y2)
+
+
 def test_reduced_over_no_rows_is_zero():
     r = sscan.gated_norm_bwd(*on(torch.zeros(0, 2, 64), torch.zeros(0, 2, 64), torch.zeros(0, 2, 64), torch.ones(64)))
     assert r["dx"].shape == (0, 2, 64) and not r["dweight"].any()
