@@ -15,8 +15,11 @@ namespace delta {
 // A wave owns 32 columns of S: lane (rg, cg) holds rows rg NR .. + NR - 1 of columns
 // 4 cg .. + 3.  One pass over S gives S'^T k and S'^T q together (o = S'^T q + (k.q) u),
 // so a decode step reads and writes the state once and is bound by that traffic (128
-// sequences of 32 heads of 128 x 128: 537 MB).  wide: 16-byte accesses to the state, q
-// and k; otherwise every element is loaded by itself.
+// sequences of 32 heads of 128 x 128: 537 MB).  WIDE: 16-byte accesses to the state, whose
+// rows allow it for dv a multiple of four; QK to q and k, where their size, strides and
+// alignment allow it.  Otherwise every element is loaded by itself (q and k: one row of 16
+// heads 4.1 us a token against 3.7, of 8 tokens 15.3 against 12.2; the state: 128 sequences
+// 145 against 86).
 
 // Sum over the eight row groups (lane bits 3 to 5), in every lane.
 __device__ __forceinline__ float group_rows_sum(float x) {
@@ -29,7 +32,7 @@ __device__ __forceinline__ float group_rows_sum(float x) {
   return __builtin_bit_cast(float, unsigned(r[0])) + __builtin_bit_cast(float, unsigned(r[1]));
 }
 
-template <typename IO, int NR, bool WIDE>
+template <typename IO, int NR, bool WIDE, bool QK>
 __global__ __launch_bounds__(256) void delta_recurrent_kernel(DeltaArgs a, unsigned ncol, unsigned waves) {
   const int lane = lane_id(), rg = lane >> 3, cg = lane & 7;
   const unsigned w = __builtin_amdgcn_readfirstlane(blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6));
@@ -80,8 +83,8 @@ __global__ __launch_bounds__(256) void delta_recurrent_kernel(DeltaArgs a, unsig
     typename Io<IO>::V8 k8[NR / 8], q8[NR / 8];
 #pragma unroll
     for (int n = 0; n < NR / 8; ++n) {
-      load8<IO>(kb, (row0 + 8 * n) * int(sizeof(IO)), a.dk - row0 - 8 * n, WIDE, &k8[n]);
-      load8<IO>(qb, (row0 + 8 * n) * int(sizeof(IO)), a.dk - row0 - 8 * n, WIDE, &q8[n]);
+      load8<IO>(kb, (row0 + 8 * n) * int(sizeof(IO)), a.dk - row0 - 8 * n, QK, &k8[n]);
+      load8<IO>(qb, (row0 + 8 * n) * int(sizeof(IO)), a.dk - row0 - 8 * n, QK, &q8[n]);
     }
     IO v4[4];
 #pragma unroll
@@ -143,13 +146,20 @@ template <typename IO, int NR>
 hipError_t launch_recurrent(const DeltaArgs& a, hipStream_t stream) {
   const int wide = wide_flags<IO>(a), ncol = (a.dv + 31) / 32;
   const unsigned waves = unsigned(a.batch * a.hv * ncol);
-  // blocks of one wave while there are fewer than four a CU: a small batch then uses as
-  // many CUs as it has waves
-  const unsigned per_block = waves <= 1024 ? 1 : 4, blocks = (waves + per_block - 1) / per_block;
+  // Blocks of one wave while there are at most two a CU: a small batch then uses as many CUs
+  // as it has waves.  One token of 16 heads of 128 x 128, one wave a block and four (us):
+  // 64 waves 3.7 and 4.3, 512 waves 5.2 and 5.6, 1024 waves 7.1 and 7.0, 2048 10.5 and 10.1.
+  const unsigned per_block = waves <= 512 ? 1 : 4, blocks = (waves + per_block - 1) / per_block;
+  const auto run = [&](auto states, auto qk) {
+    delta_recurrent_kernel<IO, NR, decltype(states)::value, decltype(qk)::value>
+        <<<dim3(blocks), 64 * per_block, 0, stream>>>(a, unsigned(ncol), waves);
+  };
   if ((wide & 9) == 9)
-    delta_recurrent_kernel<IO, NR, true><<<dim3(blocks), 64 * per_block, 0, stream>>>(a, unsigned(ncol), waves);
+    run(std::true_type(), std::true_type());
+  else if (wide & 8)
+    run(std::true_type(), std::false_type());
   else
-    delta_recurrent_kernel<IO, NR, false><<<dim3(blocks), 64 * per_block, 0, stream>>>(a, unsigned(ncol), waves);
+    run(std::false_type(), std::false_type());
   return hipGetLastError();
 }
 
