@@ -146,6 +146,13 @@ struct WalkLds {
 // segments' transitions S -> M S + N, walked before those two where nseg > 1: the state
 // columns from zero (segment 0: from h0) give N, and the columns of the identity without
 // values give M.  Blocks nvb .. of a segment hold the identity's columns.
+//
+// Bound by the matrix instructions: with float32 factors in three bf16 terms a chunk and
+// 128 columns cost 26 MFLOP of them for the output walk (19 without Q and P), 8.4 as
+// written down.  A document of 32768 tokens of 16 heads of 128 x 128: 0.21 TFLOP in 230 us
+// (0.93 PFLOP/s; a large bf16 product reaches 1.18), its transitions, twice the columns,
+// 0.31 TFLOP in 290 us (1.07; matrix units busy 41% of the cycles).  Of that document's bytes (0.4 GB, 86 us at a large copy's
+// rate) HBM is not the bound.  4 x 2048 tokens of 16 heads: 58 and 72 us.
 enum WalkMode { kOut, kStates, kEnds };
 
 struct WalkArgs {
@@ -376,7 +383,8 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, WalkAr
 // one before it, so as little as possible lies on that path: a block has sixteen columns,
 // each of its KP / 32 waves computes 32 rows of them, and takes its rows of M straight to
 // its lanes, cut into terms before the step that needs them; only the columns' terms
-// (3 KB a wave) go round through LDS, one barrier a step.
+// (3 KB a wave) go round through LDS, one barrier a step.  Bound by that chain: 64 heads of 4
+// segments 14 us, 16 heads of 16 segments 50 us (3.5 us a step, of 14).
 template <int KP, bool REV>
 __global__ __launch_bounds__(2 * KP) void delta_carry_kernel(const float* moves, float* x, int nseg, int dvp) {
   constexpr int kSteps = KP / 32;
