@@ -147,12 +147,14 @@ struct WalkLds {
 // columns from zero (segment 0: from h0) give N, and the columns of the identity without
 // values give M.  Blocks nvb .. of a segment hold the identity's columns.
 //
-// Bound by the matrix instructions: with float32 factors in three bf16 terms a chunk and
-// 128 columns cost 26 MFLOP of them for the output walk (19 without Q and P), 8.4 as
-// written down.  A document of 32768 tokens of 16 heads of 128 x 128: 0.21 TFLOP in 230 us
-// (0.93 PFLOP/s; a large bf16 product reaches 1.18), its transitions, twice the columns,
-// 0.31 TFLOP in 290 us (1.07; matrix units busy 41% of the cycles).  Of that document's bytes (0.4 GB, 86 us at a large copy's
-// rate) HBM is not the bound.  4 x 2048 tokens of 16 heads: 58 and 72 us.
+// Bound by the issue of matrix instructions and of the vector ones that cut float32
+// factors into terms.  With three terms a chunk and 128 columns cost 26 MFLOP of products
+// for the output walk (19 without Q and P), 8.4 as written down.  A document of 32768
+// tokens of 16 heads of 128 x 128: 0.21 TFLOP in 230 us (0.93 PFLOP/s; a large bf16 product
+// reaches 1.18), its transitions, twice the columns, 0.31 TFLOP in 290 us (1.07): matrix
+// units busy 41% of the cycles, vector units some 47%.  LDS is not the bound (32 columns a
+// wave, which halves its reads, take as long), nor HBM (0.4 GB, 86 us at a large copy's
+// rate).  4 x 2048 tokens of 16 heads: 58 and 72 us.
 enum WalkMode { kOut, kStates, kEnds };
 
 struct WalkArgs {
