@@ -252,7 +252,7 @@ DeltaPlan make_delta_plan(int64_t batch, int64_t len, int hk, int hv, int dk, in
   const size_t n = size_t(heads) * size_t(p.nchunk);
   p.off_t = 0;
   p.off_p = p.off_t + round256(n * delta::kFrags * 3 * delta::kFragBytes);
-  p.off_vec = p.off_p + round256(n * delta::kFrags * (io_bf16 ? 2 : 3) * delta::kFragBytes);
+  p.off_vec = p.off_p + round256(n * delta::kFrags * 3 * delta::kFragBytes);
   p.off_ends = p.off_vec + round256(n * delta::kVecFloats * 4);
   const size_t segs = p.nseg > 1 ? size_t(heads) * size_t(p.nseg) * size_t(p.kp) * 4 : 0;
   p.off_moves = p.off_ends + round256(segs * size_t(p.dvp));

@@ -43,7 +43,7 @@ template <typename IO, int KP, int W, bool ENDS>
 __global__ __launch_bounds__(64 * W) void delta_chunk_bwd_kernel(DeltaBwdArgs b_, WalkBackArgs w) {
   constexpr int N = Io<IO>::kN, kTiles = KP / 16, kSteps = KP / 32, kThreads = 64 * W, kVecs = 5 * kC;
   typedef Tile<KP> TileK;
-  typedef WalkLds<IO, KP, true, 3, kVecs> Lds;
+  typedef WalkLds<IO, KP, true, kVecs> Lds;
   __shared__ __attribute__((aligned(256))) char lds[Lds::kSets * Lds::kSet];
 
   const DeltaArgs& a = b_.f;

@@ -124,10 +124,10 @@ struct ColumnsAhead<bf16> {
 // LDS of a walk: per chunk the K tile, the Q tile, the fragments of two triangular
 // matrices and the per-token factors.  bf16: two sets, the next chunk's being filled
 // while one is read (one barrier a chunk); float32 has room for one (two barriers).
-template <typename IO, int KP, bool kWithQ, int kTermsP, int kVecs>
+template <typename IO, int KP, bool kWithQ, int kVecs>
 struct WalkLds {
   static constexpr int kTileBytes = Io<IO>::kN * Tile<KP>::kElems * 2;
-  static constexpr int kBytesT = kFrags * 3 * kFragBytes, kBytesP = kWithQ ? kFrags * kTermsP * kFragBytes : 0;
+  static constexpr int kBytesT = kFrags * kTerms * kFragBytes, kBytesP = kWithQ ? kBytesT : 0;
   static constexpr int kQ = kTileBytes, kT = kQ + (kWithQ ? kTileBytes : 0), kP = kT + kBytesT, kVec = kP + kBytesP;
   static constexpr int kSet = kVec + kVecs * 4, kSets = std::is_same<IO, bf16>::value ? 2 : 1;
 };
@@ -147,14 +147,18 @@ struct WalkLds {
 // columns from zero (segment 0: from h0) give N, and the columns of the identity without
 // values give M.  Blocks nvb .. of a segment hold the identity's columns.
 //
+// Outputs are computed from float32 factors as the states are, and rounded once: with two
+// terms (16 bits) in their products the output walk of 4 x 2048 tokens of 16 heads took 57 us
+// and not 62, a document of 32768 650 in all and not 685, and outputs whose parts cancel lost
+// up to 2^-16 of the parts.
+//
 // Bound by the issue of matrix instructions and of the vector ones that cut float32
-// factors into terms.  With three terms a chunk and 128 columns cost 26 MFLOP of products
-// for the output walk (19 without Q and P), 8.4 as written down.  A document of 32768
-// tokens of 16 heads of 128 x 128: 0.21 TFLOP in 230 us (0.93 PFLOP/s; a large bf16 product
-// reaches 1.18), its transitions, twice the columns, 0.31 TFLOP in 290 us (1.07): matrix
-// units busy 41% of the cycles, vector units some 47%.  LDS is not the bound (32 columns a
-// wave, which halves its reads, take as long), nor HBM (0.4 GB, 86 us at a large copy's
-// rate).  4 x 2048 tokens of 16 heads: 58 and 72 us.
+// factors into terms.  A chunk and 128 columns cost 28.3 MFLOP of products for the output
+// walk (17.3 without Q and P), 8.4 as written down.  A document of 32768 tokens of 16 heads
+// of 128 x 128: 0.23 TFLOP in 241 to 266 us (0.87 to 0.96 PFLOP/s; a large bf16 product
+// reaches 1.18), its transitions, 29 blocks of 32 chunks a head, 0.26 TFLOP in 280 to 312 us
+// (0.82 to 0.92).  LDS is not the bound (32 columns a wave, which halves its reads, take as
+// long), nor HBM (0.4 GB, 86 us at a large copy's rate).
 enum WalkMode { kOut, kStates, kEnds };
 
 struct WalkArgs {
@@ -167,11 +171,11 @@ struct WalkArgs {
 
 template <typename IO, int KP, int W, int MODE>
 __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, WalkArgs w, int vecs) {
-  constexpr int N = Io<IO>::kN, NO = Io<IO>::kOutTerms, kThreads = 64 * W, kRing = N == 1 ? 5 : 2;
+  constexpr int N = Io<IO>::kN, kThreads = 64 * W, kRing = N == 1 ? 5 : 2;
   constexpr int kTiles = KP / 16, kSteps = KP / 32;
   constexpr bool OUT = MODE == kOut;
   typedef Tile<KP> TileK;
-  typedef WalkLds<IO, KP, OUT, NO, kVecFloats> Lds;
+  typedef WalkLds<IO, KP, OUT, kVecFloats> Lds;
   __shared__ __attribute__((aligned(256))) char lds[Lds::kSets * Lds::kSet];
   __shared__ __attribute__((aligned(16))) char lds_v[W * ColumnsAhead<IO>::kLds];
 
@@ -298,9 +302,9 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, WalkAr
 #pragma unroll
       for (int n = 0; n < 3; ++n) f.t[n] = *reinterpret_cast<const bf16x8*>(st + (j * 3 + n) * kFragBytes);
     };
-    const auto read_p = [&](int j, Frag<NO>& f) {
+    const auto read_p = [&](int j, Frag<3>& f) {
 #pragma unroll
-      for (int n = 0; n < NO; ++n) f.t[n] = *reinterpret_cast<const bf16x8*>(sp + (j * NO + n) * kFragBytes);
+      for (int n = 0; n < 3; ++n) f.t[n] = *reinterpret_cast<const bf16x8*>(sp + (j * 3 + n) * kFragBytes);
     };
     const auto read_cols = [&](int j, Frag<N>& f) {
       const int m = j >> 1, s = j & 1;
@@ -319,7 +323,7 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, WalkAr
     ring_run<4 * kSteps>(rows_ring, read_rows, [&](int j, const Rows& f) {
       const int m = j / kSteps, s = j % kSteps, tok = chained(m, 4 * qd);
       ks = mul(f.k, sf[s], s == 0 ? f32x4{} : ks);
-      if constexpr (OUT) o[m] = mul<NO>(f.q, sf[s], o[m]);
+      if constexpr (OUT) o[m] = mul(f.q, sf[s], o[m]);
       if (s == kSteps - 1) {
         x[m] -= *reinterpret_cast<const f32x4*>(&svec[tok]) * ks;
         if constexpr (OUT) o[m] *= *reinterpret_cast<const f32x4*>(&svec[2 * kC + tok]);
@@ -338,12 +342,11 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, WalkAr
                      [&](int j, const Frag<3>& f) { u[lower_m(j)] = mul(f, xf[lower_s(j)], u[lower_m(j)]); });
     // o += P u
     if constexpr (OUT) {
-      Frag<NO> p_ring[kRingT];
+      Frag<3> p_ring[kRingT];
       ring_start<kFrags>(p_ring, read_p);
       const Frag<3> uf[2] = {split(u[0], u[1]), split(u[2], u[3])};
-      ring_run<kFrags>(p_ring, read_p, [&](int j, const Frag<NO>& f) {
-        o[lower_m(j)] = mul<NO>(f, uf[lower_s(j)], o[lower_m(j)]);
-      });
+      ring_run<kFrags>(p_ring, read_p,
+                       [&](int j, const Frag<3>& f) { o[lower_m(j)] = mul(f, uf[lower_s(j)], o[lower_m(j)]); });
       const Buffer rows = rows_of(op + t0 * out_t, L - t0 < kC ? L - t0 : kC, out_t, a.dv);
       const int at = here(o_lane);
 #pragma unroll

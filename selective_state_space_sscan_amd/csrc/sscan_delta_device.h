@@ -79,11 +79,11 @@ __device__ __forceinline__ Frag<3> split(f32x4 lo, f32x4 hi) {
 }
 
 // c + a b, dropping the products below 2^-24 of the leading one; the small products
-// are added first.  kUse caps the terms used (2 where the result is rounded to bf16).
-template <int kUse = 3, int NA, int NB>
+// are added first.
+template <int NA, int NB>
 __device__ __forceinline__ f32x4 mul(const Frag<NA>& a, const Frag<NB>& b, f32x4 c) {
 #pragma unroll
-  for (int sum = kUse - 1; sum >= 0; --sum)
+  for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
     for (int i = 0; i < NA; ++i)
       if (sum - i >= 0 && sum - i < NB) c = mfma(a.t[i], b.t[sum - i], c);
@@ -259,14 +259,12 @@ template <typename T>
 struct Io;
 template <>
 struct Io<bf16> {
-  static constexpr int kN = 1;       // bf16 terms of an input
-  static constexpr int kOutTerms = 2;  // terms used where only the rounded output depends on them
+  static constexpr int kN = 1;  // bf16 terms of an input
   typedef bf16x8 V8;
 };
 template <>
 struct Io<float> {
   static constexpr int kN = 3;
-  static constexpr int kOutTerms = 3;
   typedef f32x8 V8;
 };
 

@@ -128,7 +128,7 @@ __device__ __forceinline__ double lane_of(double x, int lane) {
 template <typename IO, int KP, bool BWD>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int nchunk, char* frag_t, char* frag_p,
                                                          char* frag_tt, float* vec, int wide) {
-  constexpr int N = Io<IO>::kN, NP = BWD ? 3 : Io<IO>::kOutTerms, kSteps = KP / 32;
+  constexpr int N = Io<IO>::kN, kSteps = KP / 32;
   __shared__ __attribute__((aligned(16))) float pmat[kC * kLdM];
   __shared__ __attribute__((aligned(16))) float tmat[kC * kLdM];
   __shared__ double gsum[kC];
@@ -283,11 +283,9 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int nchunk
     }
     if (kind == 0) x *= read8(&sbeta[k0]);
     const Frag<3> fr = split(x);
-    const int terms = kind == 1 ? NP : 3;
-    char* dst = (kind == 0 ? frag_t : kind == 1 ? frag_p : frag_tt) + (idx * kFrags + f) * terms * kFragBytes;
+    char* dst = (kind == 0 ? frag_t : kind == 1 ? frag_p : frag_tt) + (idx * kFrags + f) * kTerms * kFragBytes;
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
-      if (k < terms) *reinterpret_cast<bf16x8*>(dst + (k * 64 + lane) * 16) = fr.t[k];
+    for (int k = 0; k < kTerms; ++k) *reinterpret_cast<bf16x8*>(dst + (k * 64 + lane) * 16) = fr.t[k];
   }
 }
 
