@@ -583,6 +583,14 @@ SSCAN_API size_t sscan_delta_workspace_bytes(int64_t batch, int64_t len, int64_t
 SSCAN_API size_t sscan_delta_bwd_workspace_bytes(int64_t batch, int64_t len, int64_t qk_heads, int64_t v_heads,
                                        int64_t dk, int64_t dv, int io_dtype);
 
+/* How sscan_delta_fwd walks rows of these sizes, for tools and tests: out[0] chunks per
+ * row (0: token by token), out[1] segments of a row that are walked at once, out[2] chunks
+ * per segment, out[3] waves per block (of sixteen value columns each).  sscan_delta_bwd
+ * walks alike, but always by chunks.  out is HOST memory (4 entries).  Returns what the
+ * call itself would of these sizes. */
+SSCAN_API int sscan_delta_plan(int64_t batch, int64_t len, int64_t qk_heads, int64_t v_heads, int64_t dk, int64_t dv,
+                     int io_dtype, int64_t* out);
+
 /* The checks of the three calls above, without touching the GPU. */
 SSCAN_API int sscan_validate_delta_fwd(const sscan_delta_params* p, const void* out, const float* h_last,
                              const void* workspace, size_t workspace_bytes);

@@ -200,9 +200,9 @@ int check_delta_bwd(const sscan_delta_params* p, const void* dout, const float* 
   return SSCAN_OK;
 }
 
-// The sizes a workspace query is asked for, as the call itself checks them.
-bool delta_sizes_ok(int64_t batch, int64_t len, int64_t hk, int64_t hv, int64_t dk, int64_t dv, int io_dtype,
-                    sscan_delta_params* p) {
+// The sizes a workspace or plan query is asked for, as the call itself checks them.
+int check_delta_sizes(int64_t batch, int64_t len, int64_t hk, int64_t hv, int64_t dk, int64_t dv, int io_dtype,
+                      sscan_delta_params* p, bool* no_rows) {
   *p = sscan_delta_params{};
   p->batch = batch;
   p->len = len;
@@ -213,7 +213,14 @@ bool delta_sizes_ok(int64_t batch, int64_t len, int64_t hk, int64_t hv, int64_t 
   p->io_dtype = io_dtype;
   DeltaView w{};
   const int st = view_delta(p, &w);
-  return (st == SSCAN_OK || st == SSCAN_ERR_NULL) && !w.no_rows;
+  *no_rows = w.no_rows;
+  return st == SSCAN_ERR_NULL ? SSCAN_OK : st;  // there are no pointers to check
+}
+
+bool delta_sizes_ok(int64_t batch, int64_t len, int64_t hk, int64_t hv, int64_t dk, int64_t dv, int io_dtype,
+                    sscan_delta_params* p) {
+  bool no_rows = false;
+  return check_delta_sizes(batch, len, hk, hv, dk, dv, io_dtype, p, &no_rows) == SSCAN_OK && !no_rows;
 }
 
 struct GatedView {
@@ -421,6 +428,21 @@ size_t sscan_delta_bwd_workspace_bytes(int64_t batch, int64_t len, int64_t qk_he
                                        int64_t dv, int io_dtype) {
   sscan_delta_params p;
   return delta_sizes_ok(batch, len, qk_heads, v_heads, dk, dv, io_dtype, &p) ? bwd_plan_of(&p).workspace_bytes : 0;
+}
+
+int sscan_delta_plan(int64_t batch, int64_t len, int64_t qk_heads, int64_t v_heads, int64_t dk, int64_t dv,
+                     int io_dtype, int64_t* out) {
+  if (!out) return SSCAN_ERR_NULL;
+  sscan_delta_params p;
+  bool no_rows = false;
+  const int st = check_delta_sizes(batch, len, qk_heads, v_heads, dk, dv, io_dtype, &p, &no_rows);
+  if (st != SSCAN_OK) return st;
+  const sscan::DeltaPlan plan = no_rows ? sscan::DeltaPlan{} : plan_of(&p);
+  out[0] = plan.recurrent ? 0 : plan.nchunk;
+  out[1] = plan.nseg;
+  out[2] = plan.seg_chunks;
+  out[3] = plan.waves;
+  return SSCAN_OK;
 }
 
 int sscan_validate_gated_norm(const sscan_gated_norm_params* p, const void* out) {

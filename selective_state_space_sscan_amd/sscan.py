@@ -216,6 +216,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     for name in ("sscan_delta_workspace_bytes", "sscan_delta_bwd_workspace_bytes"):
         getattr(lib, name).argtypes = [I64] * 6 + [I]
         getattr(lib, name).restype = SZ
+    lib.sscan_delta_plan.argtypes = [I64] * 6 + [I, ctypes.POINTER(ctypes.c_int64)]
+    lib.sscan_delta_plan.restype = I
     lib.sscan_gated_norm_bwd_workspace_bytes.argtypes = [I64, I64, I64]
     lib.sscan_gated_norm_bwd_workspace_bytes.restype = SZ
     lib.sscan_add_norm_bwd_workspace_bytes.argtypes = [I64, I64]
@@ -1166,6 +1168,17 @@ def delta_workspace_bytes(batch: int, length: int, qk_heads: int, v_heads: int, 
     lib = load_library()
     f = lib.sscan_delta_bwd_workspace_bytes if backward else lib.sscan_delta_workspace_bytes
     return int(f(batch, length, qk_heads, v_heads, dk, dv, _DT_CODE[io_dtype]))
+
+
+def delta_plan(batch: int, length: int, qk_heads: int, v_heads: int, dk: int, dv: int,
+               io_dtype=torch.bfloat16) -> dict:
+    """How rows of these sizes are walked (``sscan_delta_plan``): chunks per row (0: token
+    by token), segments walked at once, chunks per segment, waves per block."""
+    out = (ctypes.c_int64 * 4)()
+    st = load_library().sscan_delta_plan(batch, length, qk_heads, v_heads, dk, dv, _DT_CODE[io_dtype], out)
+    if st != 0:
+        raise SScanError(st, "sscan_delta_plan")
+    return dict(nchunk=out[0], nseg=out[1], seg_chunks=out[2], waves=out[3])
 
 
 def delta_fwd(q, k, v, g, beta, h0: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
