@@ -166,7 +166,9 @@ struct WalkArgs {
   const char *frag_t, *frag_p;
   const float* vec;
   float *states, *values;   // kStates
-  float *ends, *moves;      // N [row, head][nseg][KP][dvp] (as carried: entry states), M [..][KP][KP]
+  // N [row, head][nseg][KP][dvp] (as carried: entry states; the last: a copy of h0 where
+  // h_last replaces it), M [..][KP][KP]
+  float *ends, *moves;
 };
 
 template <typename IO, int KP, int W, int MODE>
@@ -186,12 +188,17 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, WalkAr
   const int vb = int(blk % unsigned(blocks)), seg = int(blk / unsigned(blocks) % unsigned(w.nseg));
   const int64_t bh = blk / unsigned(blocks) / unsigned(w.nseg), b = bh / a.hv, at_seg = bh * w.nseg + seg;
   const bool ident = MODE == kEnds && vb >= w.nvb;
-  if (MODE == kEnds && (seg == w.nseg - 1 || (ident && seg == 0))) return;  // nobody reads these
+  // The last state may replace the entry state, which the output walk's blocks of the first
+  // segment read while those of the last one write it.  Walked in segments, they read a copy
+  // that the transitions' launch leaves in the last segment's place, which has no end state.
+  const bool in_place = w.nseg > 1 && a.h0 && a.h0 == a.h_last, copies = MODE == kEnds && seg == w.nseg - 1;
+  if (MODE == kEnds && ((copies && (ident || !in_place)) || (ident && seg == 0))) return;  // nobody reads these
   const int h = int(bh % a.hv), hq = h / (a.hv / a.hk);
   const int col = (ident ? vb - w.nvb : vb) * (16 * W) + 16 * wave + i;
   const int L = int(a.len), Lb = row_len(a.lengths, b, a.len);
   const int first = seg * w.seg_chunks, live_chunks = (Lb + kC - 1) / kC;
-  const int past = live_chunks < first + w.seg_chunks ? live_chunks : first + w.seg_chunks;  // chunks first .. past - 1
+  // chunks first .. past - 1
+  const int past = copies ? first : live_chunks < first + w.seg_chunks ? live_chunks : first + w.seg_chunks;
   const IO* kp = static_cast<const IO*>(a.k) + b * a.sk.b + hq * a.sk.h;
   const IO* qp = static_cast<const IO*>(a.q) + b * a.sq.b + hq * a.sq.h;
   const IO* vp = static_cast<const IO*>(a.v) + b * a.sv.b + h * a.sv.h;
@@ -220,10 +227,11 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, WalkAr
     for (int m = 0; m < kTiles; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[m][r] = chained(m, 4 * qd + r) == col ? 1.0f : 0.0f;
-  } else if (seg == 0) {
+  } else if (copies || (seg == 0 && !(OUT && in_place))) {
     if (a.h0) load_state(buffer_of(a.h0 + bh * a.dk * a.dv, state_bytes), s_lane, a.dv, S);
   } else if (MODE != kEnds) {
-    load_state(buffer_of(w.ends + (at_seg - 1) * KP * w.dvp, KP * w.dvp * 4), w_lane, w.dvp, S);
+    const int64_t from = seg == 0 ? at_seg + w.nseg - 1 : at_seg - 1;
+    load_state(buffer_of(w.ends + from * KP * w.dvp, KP * w.dvp * 4), w_lane, w.dvp, S);
   }
 
   RowsAhead<IO, KP, kThreads> next_k, next_q;
