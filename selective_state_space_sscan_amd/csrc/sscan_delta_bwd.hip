@@ -435,7 +435,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           dot += next_x[n][j] * float(next_v[n][j]);
-          y[j] = IO(beta * next_x[n][j]);
+          y[j] = IO(row < rows ? beta * next_x[n][j] : 0.0f);  // past the row's end whatever X~ holds
         }
         store8<IO>(gb, (row * int(v_t) + c8) * int(sizeof(IO)), a.dv - c8, wide_gv, y);
 #pragma unroll
@@ -686,8 +686,8 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nc
         fk *= rk * rk;
       }
       const int at = dim < a.dk ? (tok * int(qk_t) + dim) * int(sizeof(IO)) : kOutside;
-      store1(dqb, at, IO(dq[m][r] - fq * at_tile(sq, tok, dim)));
-      store1(dkb, at, IO(dk[m][r] - fk * at_tile(sk, tok, dim)));
+      store1(dqb, at, IO(tok < rows ? dq[m][r] - fq * at_tile(sq, tok, dim) : 0.0f));
+      store1(dkb, at, IO(tok < rows ? dk[m][r] - fk * at_tile(sk, tok, dim) : 0.0f));
     }
 }
 

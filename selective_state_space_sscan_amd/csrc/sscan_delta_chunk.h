@@ -355,6 +355,12 @@ __global__ __launch_bounds__(64 * W) void delta_chunk_kernel(DeltaArgs a, WalkAr
       const Frag<3> uf[2] = {split(u[0], u[1]), split(u[2], u[3])};
       ring_run<kFrags>(p_ring, read_p,
                        [&](int j, const Frag<3>& f) { o[lower_m(j)] = mul(f, uf[lower_s(j)], o[lower_m(j)]); });
+      // a state that is not finite times the zero queries past the row's end is none of theirs
+      if (Lb - t0 < kC)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[m][r] = chained(m, 4 * qd + r) < Lb - t0 ? o[m][r] : 0.0f;
       const Buffer rows = rows_of(op + t0 * out_t, L - t0 < kC ? L - t0 : kC, out_t, a.dv);
       const int at = here(o_lane);
 #pragma unroll
