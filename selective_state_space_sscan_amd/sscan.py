@@ -1094,6 +1094,17 @@ def selective_scan_bidir(u, z, fwd_params: dict, rev_params: dict, softplus: boo
 
 # ---- the gated delta rule ---------------------------------------------------------
 
+_bump = torch.autograd.graph.increment_version
+
+
+def _written(*tensors) -> None:
+    """Tells autograd that the kernels wrote to the caller's tensors (None: not given): a
+    backward pass that saved one of them before raises instead of using what it holds now."""
+    for t in tensors:
+        if t is not None:
+            _bump(t)
+
+
 def _strided(t, name: str, device, dtype, shape, unit: bool = True):
     """A tensor the kernels read through its own strides: only the last dimension has
     to be contiguous (``unit``; the gates have none)."""
@@ -1191,6 +1202,7 @@ def delta_fwd(q, k, v, g, beta, h0: Optional[torch.Tensor] = None, lengths: Opti
     defaults to dk ** -0.5.  Returns (out, h_last); h_last may be given as h0."""
     lib = load_library()
     p, dev, (b, L, hk, hv, dk, dv), code = _delta_pack("delta_fwd", q, k, v, g, beta, h0, lengths, scale, qk_norm)
+    given = out, h_last
     if out is None:
         out = torch.empty((b, L, hv, dv), dtype=q.dtype, device=dev)
     else:
@@ -1205,6 +1217,7 @@ def delta_fwd(q, k, v, g, beta, h0: Optional[torch.Tensor] = None, lengths: Opti
     st = lib.sscan_delta_fwd(p, out.data_ptr(), h_last.data_ptr(), _stream(dev), _ptr(ws), ws_bytes)
     if st != 0:
         raise SScanError(st, "sscan_delta_fwd")
+    _written(*given)
     return out, h_last
 
 
@@ -1220,6 +1233,7 @@ def delta_step(state, q, k, v, g, beta, lengths: Optional[torch.Tensor] = None, 
     if state is None:
         raise ValueError("state is required")
     _check(state, "state", dev, torch.float32, (b, hv, dk, dv))
+    given = out
     if out is None:
         out = torch.empty((b, hv, dv), dtype=q.dtype, device=dev)
     else:
@@ -1229,6 +1243,7 @@ def delta_step(state, q, k, v, g, beta, lengths: Optional[torch.Tensor] = None, 
     st = lib.sscan_delta_step(p, state.data_ptr(), out.data_ptr(), _stream(dev))
     if st != 0:
         raise SScanError(st, "sscan_delta_step")
+    _written(state, given)
     return out
 
 
@@ -1336,6 +1351,7 @@ def gated_norm(x, z, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, g
     strided); weight: [size] or [heads, size] f32.  Returns a contiguous tensor."""
     lib = load_library()
     p, dev, _ = _gated_params("gated_norm", x, z, weight, eps, gate_first)
+    given = out
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=dev)
     else:
@@ -1343,6 +1359,7 @@ def gated_norm(x, z, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, g
     st = lib.sscan_gated_norm(p, out.data_ptr(), _stream(dev))
     if st != 0:
         raise SScanError(st, "sscan_gated_norm")
+    _written(given)
     return out
 
 
@@ -1399,6 +1416,7 @@ def add_norm(x, residual: Optional[torch.Tensor] = None, weight: Optional[torch.
     if residual_dtype is None:
         residual_dtype = x.dtype if residual is None else residual.dtype
     p, dev, _ = _add_params("add_norm", x, residual, residual_dtype, weight, scale, post_weight, eps)
+    given = out, residual_out
     if out is None:
         out = torch.empty_like(x)
     else:
@@ -1410,6 +1428,7 @@ def add_norm(x, residual: Optional[torch.Tensor] = None, weight: Optional[torch.
     st = lib.sscan_add_norm(p, out.data_ptr(), residual_out.data_ptr(), _stream(dev))
     if st != 0:
         raise SScanError(st, "sscan_add_norm")
+    _written(*given)
     return out, residual_out
 
 
