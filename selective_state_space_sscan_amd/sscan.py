@@ -8,6 +8,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 from typing import Optional
@@ -1105,6 +1106,38 @@ def _written(*tensors) -> None:
             _bump(t)
 
 
+class _NoSecond(torch.autograd.Function):
+    """Gradients as they are, whose own backward pass raises."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the gated delta rule and the norms around a mixer have no second derivatives")
+
+
+def _first_order(backward):
+    """A backward pass whose gradients cannot be differentiated again: where a graph of them
+    is made (``create_graph``) they say so when it is used, instead of counting as constants
+    (torch's once_differentiable leaves them constants where only the saved inputs require
+    gradients, as those of a sum of the outputs do)."""
+
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        with torch.no_grad():
+            r = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return r
+        at = [i for i, t in enumerate(r) if t is not None]
+        on = [t for t in (*ctx.saved_tensors, *grads) if t is not None and t.requires_grad]
+        marked = dict(zip(at, _NoSecond.apply(len(at), *(r[i] for i in at), *on)))
+        return tuple(marked.get(i) for i in range(len(r)))
+
+    return run
+
+
 def _strided(t, name: str, device, dtype, shape, unit: bool = True):
     """A tensor the kernels read through its own strides: only the last dimension has
     to be contiguous (``unit``; the gates have none)."""
@@ -1284,6 +1317,7 @@ class _DeltaFn(torch.autograd.Function):
         return delta_fwd(q, k, v, g, beta, h0, lengths, scale, qk_norm)
 
     @staticmethod
+    @_first_order
     def backward(ctx, dout, dh_last):
         q, k, v, g, beta, h0, lengths = ctx.saved_tensors
         if dout is None:
@@ -1461,6 +1495,7 @@ class _GatedNormFn(torch.autograd.Function):
         return gated_norm(x, z, weight, eps, gate_first)
 
     @staticmethod
+    @_first_order
     def backward(ctx, dout):
         x, z, weight = ctx.saved_tensors
         r = gated_norm_bwd(x, z, dout.contiguous(), weight, ctx.eps, ctx.gate_first)
@@ -1482,6 +1517,7 @@ class _AddNormFn(torch.autograd.Function):
         return out, total
 
     @staticmethod
+    @_first_order
     def backward(ctx, dout, dtotal):
         x, total, weight, scale, post_weight = ctx.saved_tensors
         dout = torch.zeros_like(x) if dout is None else dout.contiguous()

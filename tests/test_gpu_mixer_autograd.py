@@ -1,4 +1,5 @@
-"""What autograd has to know of the mixer's operators: which tensors are written in place."""
+"""What autograd has to know of the mixer's operators: which tensors are written in place, and
+that the gradients have none of their own."""
 import pytest
 import torch
 
@@ -57,3 +58,17 @@ def test_states_of_inference_mode():
     t = s.clone()
     one = [x[:, 0].contiguous() for x in some()]
     assert torch.equal(sscan.delta_step(s, *one), sscan.delta_step(t, *one)) and torch.equal(s, t)
+
+
+def test_second_derivatives_are_refused():
+    ins = [x.requires_grad_(True) for x in some()]
+    x, z = (torch.randn(5, 64, device=DEV, requires_grad=True) for _ in range(2))
+    w = torch.ones(64, device=DEV, requires_grad=True)
+    for f, at in ((lambda: sscan.gated_delta(*ins)[0], ins[0]), (lambda: sscan.gated_rms_norm(x, z, w), x),
+                  (lambda: sscan.add_rms_norm(x, z, w)[0], x)):
+        for loss in (lambda: f().square().sum(), lambda: f().sum()):
+            (want,) = torch.autograd.grad(loss(), [at])
+            (g,) = torch.autograd.grad(loss(), [at], create_graph=True)
+            assert torch.equal(g, want)
+            with pytest.raises(RuntimeError, match="no second derivatives"):
+                torch.autograd.grad(g.sum() + at.square().sum(), [at])
