@@ -566,8 +566,8 @@ typedef struct sscan_delta_grads {
 SSCAN_API int sscan_delta_fwd(const sscan_delta_params* p, void* out, float* h_last, void* stream, void* workspace,
                     size_t workspace_bytes);
 
-/* One token from a stored state, updated in place (p->len must be 1 and p->h0 NULL; a
- * row of lengths 0 keeps its state and answers 0).  No workspace. */
+/* One token from a stored state (16-byte aligned), updated in place (p->len must be 1 and
+ * p->h0 NULL; a row of lengths 0 keeps its state and answers 0).  No workspace. */
 SSCAN_API int sscan_delta_step(const sscan_delta_params* p, float* state, void* out, void* stream);
 
 /* Gradients of sum(dout * out) + sum(dh_last * h_last) (dout [batch, len, v_heads, dv]

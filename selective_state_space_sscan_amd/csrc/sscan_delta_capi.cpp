@@ -182,7 +182,7 @@ int check_delta_bwd(const sscan_delta_params* p, const void* dout, const float* 
   const sscan_delta_grads& g = *grads;
   if (!w->no_tokens && (!dout || !g.dq || !g.dk || !g.dv || !g.dg || !g.dbeta)) return SSCAN_ERR_NULL;
   if (!aligned(dout, w->esz) || !aligned(g.dq, w->esz) || !aligned(g.dk, w->esz) || !aligned(g.dv, w->esz) ||
-      !aligned(g.dg, 4) || !aligned(g.dbeta, 4) || !aligned(g.dh0, 16) || !aligned(dh_last, 16))
+      !aligned(g.dg, 4) || !aligned(g.dbeta, 4) || !aligned(g.dh0, 4) || !aligned(dh_last, 4))
     return SSCAN_ERR_ALIGN;
   *plan = bwd_plan_of(p);
   st = check_workspace(workspace, workspace_bytes, plan->workspace_bytes, 256);

@@ -1106,6 +1106,20 @@ def _written(*tensors) -> None:
             _bump(t)
 
 
+def _aligned(t):
+    """A state at a 16-byte boundary, as the kernels take them: a copy of a slice of a pool
+    whose states' sizes are no multiple of four."""
+    return t.clone() if isinstance(t, torch.Tensor) and t.data_ptr() % 16 else t
+
+
+def _apart(state, out) -> None:
+    """Refuses an output over a state that is written through a copy, of which the C checks
+    do not know."""
+    a, b = state.data_ptr(), out.data_ptr()
+    if a < b + out.numel() * out.element_size() and b < a + state.numel() * 4:
+        raise ValueError("out and the state overlap")
+
+
 class _NoSecond(torch.autograd.Function):
     """Gradients as they are, whose own backward pass raises."""
 
@@ -1234,6 +1248,7 @@ def delta_fwd(q, k, v, g, beta, h0: Optional[torch.Tensor] = None, lengths: Opti
     contiguous.  h0: [batch, v_heads, dk, dv] f32; lengths: int32 [batch].  scale
     defaults to dk ** -0.5.  Returns (out, h_last); h_last may be given as h0."""
     lib = load_library()
+    h0 = _aligned(h0)
     p, dev, (b, L, hk, hv, dk, dv), code = _delta_pack("delta_fwd", q, k, v, g, beta, h0, lengths, scale, qk_norm)
     given = out, h_last
     if out is None:
@@ -1246,10 +1261,16 @@ def delta_fwd(q, k, v, g, beta, h0: Optional[torch.Tensor] = None, lengths: Opti
         _check(h_last, "h_last", dev, torch.float32, (b, hv, dk, dv))
     if b * hv == 0:
         return out, h_last
+    last = h_last
+    if h_last.data_ptr() % 16:
+        _apart(h_last, out)
+        last = torch.empty_like(h_last)
     ws, ws_bytes = _workspace(lib.sscan_delta_workspace_bytes(b, L, hk, hv, dk, dv, code), dev, workspace)
-    st = lib.sscan_delta_fwd(p, out.data_ptr(), h_last.data_ptr(), _stream(dev), _ptr(ws), ws_bytes)
+    st = lib.sscan_delta_fwd(p, out.data_ptr(), last.data_ptr(), _stream(dev), _ptr(ws), ws_bytes)
     if st != 0:
         raise SScanError(st, "sscan_delta_fwd")
+    if last is not h_last:
+        h_last.copy_(last)
     _written(*given)
     return out, h_last
 
@@ -1273,9 +1294,15 @@ def delta_step(state, q, k, v, g, beta, lengths: Optional[torch.Tensor] = None, 
         _check(out, "out", dev, q.dtype, (b, hv, dv))
     if b * hv == 0:
         return out
-    st = lib.sscan_delta_step(p, state.data_ptr(), out.data_ptr(), _stream(dev))
+    s = state
+    if state.data_ptr() % 16:
+        _apart(state, out)
+        s = state.clone()
+    st = lib.sscan_delta_step(p, s.data_ptr(), out.data_ptr(), _stream(dev))
     if st != 0:
         raise SScanError(st, "sscan_delta_step")
+    if s is not state:
+        state.copy_(s)
     _written(state, given)
     return out
 
@@ -1287,6 +1314,7 @@ def delta_bwd(q, k, v, g, beta, dout, h0: Optional[torch.Tensor] = None, dh_last
     sum(dout * out) + sum(dh_last * h_last) as {"dq", "dk", "dv" (q's dtype), "dg",
     "dbeta", "dh0" (f32)}, contiguous; the states are recomputed."""
     lib = load_library()
+    h0 = _aligned(h0)
     p, dev, (b, L, hk, hv, dk, dv), code = _delta_pack("delta_bwd", q, k, v, g, beta, h0, lengths, scale, qk_norm)
     _check(dout, "dout", dev, q.dtype, (b, L, hv, dv))
     _check(dh_last, "dh_last", dev, torch.float32, (b, hv, dk, dv))
