@@ -469,16 +469,18 @@ __global__ __launch_bounds__(threads<TPR>()) void add_norm_bwd_kernel(AddNormArg
 struct SumArgs {
   const float* partial;
   float* out[3];
-  int64_t size, pitch, nblocks, sets;
+  int64_t size, pitch, nblocks, sets, first;  // first: sets before this launch's
 };
 
-constexpr int kSumCols = 16, kSumSlices = 64;
+// Most blocks of a launch in x: per-head weights of 65536 heads of 1024 need 2^22, whose 2^32
+// threads no launch takes.
+constexpr int kSumCols = 16, kSumSlices = 64, kMaxSumBlocks = 1 << 20;
 
 __global__ __launch_bounds__(1024) void partial_sum_kernel(SumArgs s) {
   __shared__ float lds[kSumSlices][kSumCols];
   const int lane = int(threadIdx.x) % kSumCols, slice = int(threadIdx.x) / kSumCols;
   const int64_t nb = (s.size + kSumCols - 1) / kSumCols;
-  const int64_t set = int64_t(blockIdx.x) / nb, e = int64_t(blockIdx.x) % nb * kSumCols + lane;
+  const int64_t set = s.first + int64_t(blockIdx.x) / nb, e = int64_t(blockIdx.x) % nb * kSumCols + lane;
   const int part = int(blockIdx.y);
   if (!s.out[part]) return;
   const int64_t per_set = s.nblocks / s.sets;
@@ -513,6 +515,15 @@ int64_t back_blocks(int64_t units, int64_t size, int64_t heads, int64_t limit) {
   const int64_t most = limit > heads ? limit / heads : 1;
   const int64_t want = div_up(units, groups);
   return (want < most ? want : most) * heads;
+}
+
+hipError_t launch_sums(SumArgs s, int parts, hipStream_t stream) {
+  const int64_t nb = div_up(s.size, kSumCols), most = kMaxSumBlocks / nb;  // nb <= 512
+  for (s.first = 0; s.first < s.sets; s.first += most) {
+    const int64_t sets = s.sets - s.first < most ? s.sets - s.first : most;
+    partial_sum_kernel<<<dim3(unsigned(sets * nb), unsigned(parts)), 1024, 0, stream>>>(s);
+  }
+  return hipGetLastError();
 }
 
 template <int TPR, typename F>
@@ -574,9 +585,7 @@ static hipError_t gated_bwd(const GatedNormArgs& a, float* ws, hipStream_t strea
     norm::gated_norm_bwd_kernel<IO, T, decltype(whole)::value><<<dim3(unsigned(n)), B, 0, stream>>>(a, ws);
   });
   if (e != hipSuccess || !a.dweight) return e;
-  const norm::SumArgs s{ws, {a.dweight, nullptr, nullptr}, a.size, a.size, n, sets};
-  norm::partial_sum_kernel<<<dim3(unsigned(sets * norm::div_up(a.size, norm::kSumCols))), 1024, 0, stream>>>(s);
-  return hipGetLastError();
+  return norm::launch_sums({ws, {a.dweight, nullptr, nullptr}, a.size, a.size, n, sets, 0}, 1, stream);
 }
 
 template <typename IO, typename RES>
@@ -601,9 +610,7 @@ static hipError_t add_bwd(const AddNormArgs& a, float* ws, hipStream_t stream) {
       norm::add_norm_bwd_kernel<IO, RES, T, decltype(whole)::value, false><<<grid, B, 0, stream>>>(a, ws);
   });
   if (e != hipSuccess || !(a.dweight || a.dscale || a.dpost_weight)) return e;
-  const norm::SumArgs s{ws, {a.dweight, a.dscale, a.dpost_weight}, a.size, 3 * a.size, n, 1};
-  norm::partial_sum_kernel<<<dim3(unsigned(norm::div_up(a.size, norm::kSumCols)), 3), 1024, 0, stream>>>(s);
-  return hipGetLastError();
+  return norm::launch_sums({ws, {a.dweight, a.dscale, a.dpost_weight}, a.size, 3 * a.size, n, 1, 0}, 3, stream);
 }
 
 // Heads that continue each other in memory are rows, where their weight is shared.
