@@ -605,7 +605,7 @@ SSCAN_API int sscan_validate_delta_bwd(const sscan_delta_params* p, const void* 
  *   out = m / rms(m) * weight, m = x * silu(z)        (gate_first != 0)
  * x, z [rows, heads, size] io_dtype with strides between rows and heads (elements,
  * >= 0); out contiguous; weight float32 [size], or [heads, size] with per_head != 0
- * (optional unless per_head: NULL = 1).  size in 1..8192. */
+ * (optional unless per_head: NULL = 1).  size in 1..8192; with per_head at most 2^20 heads. */
 typedef struct sscan_gated_norm_params {
   const void* x;
   const void* z;

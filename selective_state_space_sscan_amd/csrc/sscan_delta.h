@@ -87,6 +87,7 @@ hipError_t launch_delta_bwd(const DeltaBwdArgs& a, const DeltaBwdPlan& p, char* 
 
 // RMS norms fused with what stands beside them in a block.
 constexpr int kNormMaxSize = 8192;   // eight elements for each of 1024 threads
+constexpr int64_t kNormMaxHeads = 1 << 20;  // with a weight each
 
 struct GatedNormArgs {
   const void *x, *z;                 // [rows, heads, size] io dtype by these strides, size contiguous

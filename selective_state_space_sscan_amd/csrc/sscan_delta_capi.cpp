@@ -237,7 +237,8 @@ int view_gated(const sscan_gated_norm_params* p, GatedView* w) {
       (p->gate_first != 0 && p->gate_first != 1) || (p->per_head != 0 && p->per_head != 1) ||
       !std::isfinite(p->eps) || p->eps < 0)
     return SSCAN_ERR_UNSUPPORTED;
-  if (p->heads > (1 << 20)) return SSCAN_ERR_SHAPE;
+  // a block or more for each head whose weight's gradient is summed
+  if (p->per_head && p->heads > sscan::kNormMaxHeads) return SSCAN_ERR_SHAPE;
   w->empty = p->rows == 0 || p->heads == 0;
   const int64_t n = product({p->rows, p->heads, p->size}), nw = p->size * (p->per_head ? p->heads : 1);
   if (n < 0) return SSCAN_ERR_SHAPE;
@@ -478,9 +479,7 @@ int sscan_gated_norm_bwd(const sscan_gated_norm_params* p, const void* dout, voi
 }
 
 size_t sscan_gated_norm_bwd_workspace_bytes(int64_t rows, int64_t heads, int64_t size) {
-  if (rows <= 0 || heads <= 0 || heads > (1 << 20) || size < 1 || size > sscan::kNormMaxSize ||
-      product({rows, heads, size}) < 0)
-    return 0;
+  if (rows <= 0 || heads <= 0 || size < 1 || size > sscan::kNormMaxSize || product({rows, heads, size}) < 0) return 0;
   return sscan::gated_norm_bwd_workspace(rows, heads, size);
 }
 

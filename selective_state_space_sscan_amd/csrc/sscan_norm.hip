@@ -556,7 +556,7 @@ using norm::bf16;
 size_t gated_norm_bwd_workspace(int64_t rows, int64_t heads, int64_t size) {
   // whichever of the shared and the per-head weight needs more blocks
   const int64_t a = norm::back_blocks(rows * heads, size, 1, norm::kMaxGatedBackBlocks),
-                b = norm::back_blocks(rows, size, heads, norm::kMaxGatedBackBlocks);
+                b = heads > kNormMaxHeads ? 0 : norm::back_blocks(rows, size, heads, norm::kMaxGatedBackBlocks);
   return size_t(a > b ? a : b) * size_t(size) * 4;
 }
 

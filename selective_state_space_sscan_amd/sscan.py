@@ -1364,6 +1364,27 @@ def gated_delta(q, k, v, g, beta, h0: Optional[torch.Tensor] = None, lengths: Op
 
 # ---- RMS norms around a mixer -----------------------------------------------------
 
+# More "heads" than this are the tokens of [batch, len, size]: rows, where their strides and
+# a shared weight allow it.  (The workspace of the gradients is sized for a weight each.)
+_ROW_HEADS = 1024
+
+
+def _row_stride(shape, stride, keep: int):
+    """The one stride between the rows that the first ``keep`` dimensions collapse to, or None."""
+    if keep == 1:
+        return stride[0] if shape[0] > 1 else 0
+    row = reach = None
+    for i in range(keep - 1, -1, -1):  # innermost first: each must continue the one inside
+        if shape[i] <= 1:
+            continue
+        if row is None:
+            row = stride[i]
+        elif stride[i] != reach:
+            return None
+        reach = stride[i] * shape[i]
+    return row or 0
+
+
 def _gated_params(what, x, z, weight, eps, gate_first):
     """(packed params, device, (rows, heads, size)): x and z are [..., size] or [..., heads, size]; all
     leading dimensions but the last one (the heads, where there are two or more)
@@ -1379,25 +1400,21 @@ def _gated_params(what, x, z, weight, eps, gate_first):
     _strided(x, "x", dev, dt, xs)
     _strided(z, "z", dev, dt, xs)
     heads = xs[-2] if len(xs) >= 3 else 1
+    keep = len(xs) - 2 if len(xs) >= 3 else len(xs) - 1  # dimensions that collapse to rows
     per_head = weight is not None and weight.dim() == 2
     if weight is not None:
         _check(weight, "weight", dev, torch.float32, (heads, size) if per_head else (size,))
     n = x.numel()
+    if heads > _ROW_HEADS and not per_head and None not in (_row_stride(xs, x.stride(), keep + 1),
+                                                            _row_stride(xs, z.stride(), keep + 1)):
+        heads, keep = 1, keep + 1
     rows = n // (heads * size) if n else 0
 
     def strides(t, name):
-        st = t.stride()
-        keep = len(xs) - 2 if len(xs) >= 3 else len(xs) - 1
-        row = reach = None
-        for i in range(keep - 1, -1, -1):  # innermost first: each must continue the one inside
-            if xs[i] <= 1:
-                continue
-            if row is None:
-                row = st[i]
-            elif st[i] != reach:
-                raise ValueError(f"the leading dimensions of {name} must collapse to rows of one stride")
-            reach = st[i] * xs[i]
-        return row or 0, st[-2] if len(xs) >= 3 else 0
+        row = _row_stride(xs, t.stride(), keep)
+        if row is None:
+            raise ValueError(f"the leading dimensions of {name} must collapse to rows of one stride")
+        return row, t.stride(-2) if heads > 1 else 0
 
     p = _GATED.pack(x.data_ptr(), z.data_ptr(), 0 if weight is None else weight.data_ptr(), *strides(x, "x"),
                     *strides(z, "z"), rows, heads, size, eps, 1 if gate_first else 0, 1 if per_head else 0,

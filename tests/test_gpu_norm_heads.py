@@ -32,3 +32,23 @@ def test_gradients_of_weights_per_head(rows, heads, size):
         xs, zs, ds = (t[:, h:h + step].float() for t in (x, z, dout))
         t = ds * xs * torch.rsqrt(xs.square().mean(-1, keepdim=True) + 1e-6) * zs * torch.sigmoid(zs)
         assert bool(((r["dweight"][h:h + step] - t.sum(0)).abs() <= 2e-5 * t.abs().sum(0) + 1e-12).all()), h
+
+
+@pytest.mark.parametrize("shape", [(1, (1 << 20) + 7, 24), (2, 3000, 40), (3, 1025, 1, 40)])
+def test_tokens_are_no_heads(shape):
+    """[batch, len, size] of any length, and gradients whose workspace does not grow with it."""
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    x, dout = (torch.randn(*shape, device=DEV, generator=gen).bfloat16() for _ in range(2))
+    z = torch.randn(*shape[:-1], shape[-1] + 8, device=DEV, generator=gen).bfloat16()[..., 8:]
+    w = 1 + 0.2 * torch.randn(shape[-1], device=DEV, generator=gen)
+    flat = [t.reshape(-1, shape[-1]) for t in (x, z, dout)]
+    y, want = sscan.gated_norm(x, z, w), sscan.gated_norm(*flat[:2], w)
+    assert torch.equal(y.view_as(want), want)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    r = sscan.gated_norm_bwd(x, z, dout, w)
+    assert torch.cuda.max_memory_allocated() - before <= 2 * x.numel() * 2 + (1 << 21)
+    want = sscan.gated_norm_bwd(*flat, w)
+    for name in ("dx", "dz", "dweight"):
+        assert torch.equal(r[name].view_as(want[name]), want[name]), name
