@@ -1095,12 +1095,13 @@ def selective_scan_bidir(u, z, fwd_params: dict, rev_params: dict, softplus: boo
 
 # ---- the gated delta rule ---------------------------------------------------------
 
+# Tells autograd that kernels wrote to a tensor: a backward pass that saved it before raises
+# instead of using what it holds now.
 _bump = torch.autograd.graph.increment_version
 
 
 def _written(*tensors) -> None:
-    """Tells autograd that the kernels wrote to the caller's tensors (None: not given): a
-    backward pass that saved one of them before raises instead of using what it holds now."""
+    """``_bump`` of the caller's tensors that the kernels wrote to (None: not given)."""
     for t in tensors:
         if t is not None:
             _bump(t)
@@ -1294,16 +1295,17 @@ def delta_step(state, q, k, v, g, beta, lengths: Optional[torch.Tensor] = None, 
         _check(out, "out", dev, q.dtype, (b, hv, dv))
     if b * hv == 0:
         return out
-    s = state
-    if state.data_ptr() % 16:
+    s, at = state, state.data_ptr()
+    if at % 16:
         _apart(state, out)
         s = state.clone()
-    st = lib.sscan_delta_step(p, s.data_ptr(), out.data_ptr(), _stream(dev))
+        at = s.data_ptr()
+    st = lib.sscan_delta_step(p, at, out.data_ptr(), _stream(dev))
     if st != 0:
         raise SScanError(st, "sscan_delta_step")
     if s is not state:
         state.copy_(s)
-    _written(state, given)
+    _bump(state if given is None else [state, given])
     return out
 
 
