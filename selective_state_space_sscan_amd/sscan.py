@@ -1194,8 +1194,12 @@ def _delta_check(what, q, k, v, g, beta, lengths, tokens: bool):
 
 def _delta_pack(what, q, k, v, g, beta, h0, lengths, scale, qk_norm, tokens: bool = True):
     """Checks the inputs of a delta call; (packed params, device, sizes (b, L, hk, hv, dk, dv), dtype code)."""
-    qs, vs, dt, di = q.shape, v.shape, q.dtype, q.get_device()
-    qt, kt, vt, gt, bt = q.stride(), k.stride(), v.stride(), g.stride(), beta.stride()
+    try:
+        qs, vs, dt, di = q.shape, v.shape, q.dtype, q.get_device()
+        qt, kt, vt, gt, bt = q.stride(), k.stride(), v.stride(), g.stride(), beta.stride()
+    except AttributeError:
+        _delta_check(what, q, k, v, g, beta, lengths, tokens)  # says which of them is no tensor
+        raise
     code = _DT_CODE.get(dt)
     # one test of everything that is wrong only in a wrong call; _delta_check says what
     if not (code is not None and di >= 0 and len(qs) == 3 + tokens and k.shape == qs and len(vs) == len(qs)
@@ -1391,6 +1395,8 @@ def _gated_params(what, x, z, weight, eps, gate_first):
     """(packed params, device, (rows, heads, size)): x and z are [..., size] or [..., heads, size]; all
     leading dimensions but the last one (the heads, where there are two or more)
     collapse to rows."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
     dev, xs, dt = x.device, x.shape, x.dtype
     if dev.type != "cuda":
         raise ValueError(f"sscan.{what} needs CUDA (HIP) tensors")
@@ -1403,7 +1409,7 @@ def _gated_params(what, x, z, weight, eps, gate_first):
     _strided(z, "z", dev, dt, xs)
     heads = xs[-2] if len(xs) >= 3 else 1
     keep = len(xs) - 2 if len(xs) >= 3 else len(xs) - 1  # dimensions that collapse to rows
-    per_head = weight is not None and weight.dim() == 2
+    per_head = isinstance(weight, torch.Tensor) and weight.dim() == 2
     if weight is not None:
         _check(weight, "weight", dev, torch.float32, (heads, size) if per_head else (size,))
     n = x.numel()
@@ -1462,6 +1468,18 @@ def gated_norm_bwd(x, z, dout, weight: Optional[torch.Tensor] = None, eps: float
 
 
 def _add_params(what, x, residual, residual_dtype, weight, scale, post_weight, eps):
+    try:
+        return _add_pack(what, x, residual, residual_dtype, weight, scale, post_weight, eps)
+    except AttributeError:
+        for name, t in (("x", x), ("residual", residual), ("weight", weight), ("scale", scale),
+                        ("post_weight", post_weight)):
+            if not isinstance(t, torch.Tensor) and (t is not None or name == "x"):
+                raise TypeError(f"{name} must be a torch.Tensor") from None
+        raise
+
+
+def _add_pack(what, x, residual, residual_dtype, weight, scale, post_weight, eps):
+    """(packed params, device, (rows, size))"""
     dev = x.device
     if dev.type != "cuda":
         raise ValueError(f"sscan.{what} needs CUDA (HIP) tensors")
@@ -1495,7 +1513,7 @@ def add_norm(x, residual: Optional[torch.Tensor] = None, weight: Optional[torch.
     ``residual_out`` may be ``residual`` itself."""
     lib = load_library()
     if residual_dtype is None:
-        residual_dtype = x.dtype if residual is None else residual.dtype
+        residual_dtype = getattr(x if residual is None else residual, "dtype", None)
     p, dev, _ = _add_params("add_norm", x, residual, residual_dtype, weight, scale, post_weight, eps)
     given = out, residual_out
     if out is None:
@@ -1521,7 +1539,8 @@ def add_norm_bwd(x, residual_out, dout, weight: Optional[torch.Tensor] = None,
     {"dx", "dresidual", "dweight", "dscale", "dpost_weight"} (the last three f32, None
     for a vector that was not given)."""
     lib = load_library()
-    p, dev, sizes = _add_params("add_norm_bwd", x, residual_out, residual_out.dtype, weight, scale, post_weight, eps)
+    p, dev, sizes = _add_params("add_norm_bwd", x, residual_out, getattr(residual_out, "dtype", None), weight, scale,
+                                post_weight, eps)
     _check(dout, "dout", dev, x.dtype, x.shape)
     _check(dresidual_out, "dresidual_out", dev, residual_out.dtype, x.shape)
     dx, dres = torch.empty_like(x), torch.empty_like(residual_out)
