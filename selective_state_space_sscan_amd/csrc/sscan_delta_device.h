@@ -93,8 +93,7 @@ __device__ __forceinline__ f32x4 mul(const Frag<NA>& a, const Frag<NB>& b, f32x4
 // Token (or state row) of tile m, tile row i, in the chained order above.
 __device__ __forceinline__ int chained(int m, int i) { return 32 * (m >> 1) + 8 * (i >> 2) + 4 * (m & 1) + (i & 3); }
 
-// Index of the fragment (tile m, contraction step s) of a triangular matrix, or -1.
-__device__ constexpr int lower_frag(int m, int s) { return m < 2 ? (s == 0 ? m : -1) : 2 * m - 2 + s; }
+// Index of the fragment (tile m, contraction step s) of an upper triangular matrix, or -1.
 __device__ constexpr int upper_frag(int m, int s) { return m < 2 ? 2 * m + s : (s == 1 ? m + 2 : -1); }
 
 __device__ __forceinline__ int lane_id() { return int(threadIdx.x) & 63; }
@@ -111,36 +110,6 @@ __device__ __forceinline__ unsigned xcd_block() {
 template <typename T>
 __device__ __forceinline__ float to_f32(T x) {
   return float(x);
-}
-
-// Eight consecutive elements from p, of which those at `left` and beyond read as 0.
-// wide: p is aligned to 8 elements' natural width (16 bytes bf16, 32 bytes as two
-// 16-byte loads float32) and left is 0 or at least 8.
-__device__ __forceinline__ bf16x8 load8(const bf16* p, int left, bool wide) {
-  bf16x8 x = {};
-  if (wide) {
-    if (left > 0) x = *reinterpret_cast<const bf16x8*>(p);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < left) x[j] = p[j];
-  }
-  return x;
-}
-
-__device__ __forceinline__ f32x8 load8(const float* p, int left, bool wide) {
-  f32x8 x = {};
-  if (wide) {
-    if (left > 0) {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
-      x = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < left) x[j] = p[j];
-  }
-  return x;
 }
 
 // Chunk rows are read and written through buffer descriptors whose size ends with the
