@@ -166,9 +166,11 @@ constexpr int partial_lds() {
   return TPR >= 256 ? 16 : 256 * 8;
 }
 
-// By the hardware's exp2 and reciprocal (one unit in the last place each): the error is
-// (|z| + 2) 2^-24 of the value, and the gradients' kernel would otherwise spend as long on
-// expf and the division as on its memory traffic.
+// By the hardware's exp2 and reciprocal, a unit in the last place (2^-23) each: the gradients'
+// kernel would otherwise spend as long on expf and the division as on its memory traffic.
+// The error is at most (1.25 |z| + 5) 2^-24 of the value: 1.25 |z| from the exponent z log2 e
+// (the constant and the product rounded, times ln 2), 2 each from exp2 and the reciprocal, 1
+// from the sum.  Float32 calls have it too.
 __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
 }
