@@ -526,9 +526,10 @@ SSCAN_API int sscan_bwd_plan(int64_t batch, int64_t dim, int64_t len, int64_t ds
  * tokens are not read, their outputs and gradients are 0 and they leave the state alone.
  * dk in 1..128, dv in 1..256, len <= 2^30; token strides of q, k, v, v_heads * dv and
  * qk_heads * dk below 2^23 elements.  States and accumulators are float32; bf16
- * outputs round to nearest even.  Sequences are walked in chunks of 64 tokens by matrix
- * products: a non-finite q, k, v or beta makes the outputs of its whole chunk (and the
- * state after it) non-finite. */
+ * outputs round to nearest even, once.  Sequences are walked in chunks of 64 tokens by
+ * matrix products: a non-finite q, k, v or beta, or a g that is NaN or +inf, may make the
+ * outputs of its whole chunk (and the state after it) non-finite, but none past the row's
+ * length. */
 typedef struct sscan_delta_params {
   const void* q;
   const void* k;
@@ -574,7 +575,9 @@ SSCAN_API int sscan_delta_step(const sscan_delta_params* p, float* state, void* 
  * io_dtype, contiguous; dh_last optional).  The forward states are recomputed; nothing
  * from the forward call is needed.  No atomics: results are bitwise reproducible.
  * Gradients of heads that are shared are summed in float32 and rounded once.  Outputs must not
- * overlap each other, any input or the workspace (sscan_delta_bwd_workspace_bytes). */
+ * overlap each other, any input or the workspace (sscan_delta_bwd_workspace_bytes), which
+ * keeps the states and adjoints of every chunk in float32: some 250 KB for each 64 tokens of
+ * a head of 128 x 128. */
 SSCAN_API int sscan_delta_bwd(const sscan_delta_params* p, const void* dout, const float* dh_last,
                     const sscan_delta_grads* grads, void* stream, void* workspace, size_t workspace_bytes);
 

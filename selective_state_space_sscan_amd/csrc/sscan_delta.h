@@ -25,10 +25,10 @@ constexpr int kDeltaMaxK = 128;      // key size (a state's rows, held in regist
 constexpr int kDeltaMaxV = 256;      // value size
 constexpr int64_t kDeltaMaxStride = 1 << 23;  // elements between tokens: a chunk's rows stay within 2^31 bytes
 // Sequences of at most this many tokens take the token-by-token kernel, whose time grows
-// with them.  At heads of 128 x 128, by tokens and by chunks (us): one row of 8 heads, bf16,
-// 12.2 and 15.6 for 8 tokens, 17.2 and 15.7 for 12; 8 rows of 16 heads 14 and 19 for 8, 19
-// and 19 for 12, 24 and 19 for 16; 128 rows of 16 heads 61 and 104, 84 and 104, 107 and 103;
-// float32 gains up to 16.
+// with them.  At heads of 128 x 128, by tokens and by chunks (us a call): one row of 8 heads,
+// bf16, 13.5 and 18.9 for 8 tokens, 18.1 and 18.9 for 12, 23 and 19 for 16; 8 rows of 16 heads
+// 15.3 and 21.5, 20.0 and 21.1, 25 and 21; 128 rows of 16 heads 63 and 114, 81 and 109, 106
+// and 108; float32 gains up to 16 and more (22 and 23, 24 and 27, 103 and 210).
 constexpr int kDeltaRecurrentMax = 10;
 
 struct DeltaStride {

@@ -198,14 +198,16 @@ hipError_t launch_fwd(const DeltaArgs& a, const DeltaPlan& p, char* ws, hipStrea
 static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Segments a row is walked in, by a model of the walks' times in units of one chunk of
-// one output walk alone on its CU (4.4 us at 128 x 128): a CU holds one block; chunks
-// take up to 1.4 times as long when every CU is busy; a walk has 2 units of its own for
-// its first loads; a chunk of the transitions' walk takes 3/4, and its blocks end at
+// one output walk alone on its CU (4.5 us at 128 x 128 by four waves, 5.6 by eight): a CU
+// holds one block (so it does of the output walks and of eight waves; of the transitions and
+// states of four waves with keys of 64 it holds two, and the model counts their rounds twice);
+// chunks take up to 1.4 times as long when every CU is busy; a walk has 2 units of its own
+// for its first loads; a chunk of the transitions' walk takes 3/4, and its blocks end at
 // different times, so its rounds count fractionally; a step of the chain between segments
-// takes 1 (1/4 for keys of 64).  Measured against forced counts, bf16, 128 x 128: 64 heads
-// of 32 chunks 178 us in 4 segments (the model's choice), 201 in 3, 207 in 8, 203 whole;
-// 16 heads of 512 chunks 690 us in 16 (its choice), 793 in 8, 764 in 12, 794 in 32,
-// 2900 whole; 256 heads of 16 chunks 191 us whole (its choice), 325 in 2.
+// takes 1 (1/4 for keys of 64).  Measured against forced counts, all of them bf16, 128 x 128
+// (us a call): 64 heads of 32 chunks 175 in 4 segments (the model's choice), 167 in 3, 207 in
+// 8, 223 whole; 16 heads of 512 chunks 706 in 16 (its choice), 823 in 8, 781 in 12, 755 in
+// 32, 3200 whole; 256 heads of 16 chunks 200 whole (its choice), 331 in 2.
 static int choose_segments(int64_t heads, int64_t nchunk, int nvb, int nkb, int kp) {
   const auto walk = [](int64_t blocks, double rounds, double chunks) {
     const double busy = blocks < 256 ? double(blocks) / 256.0 : 1.0;
@@ -238,10 +240,11 @@ DeltaPlan make_delta_plan(int64_t batch, int64_t len, int hk, int hv, int dk, in
   p.kp = dk <= 64 ? 64 : 128;
   p.dvp = (dv + 31) / 32 * 32;
   // Waves of a walk's block.  Eight share a chunk's tiles between 128 columns, four take a
-  // CU for themselves and end a chunk sooner (4.5 us against 5.4): four for float32 (whose
+  // CU for themselves and end a chunk sooner (4.5 us against 5.6): four for float32 (whose
   // registers eight waves spill: 2 x 2048 tokens of 8 heads 125 us against 136, one row of
-  // 500 72 against 108) and where there are few chunks for the GPU (bf16, 4 heads of 500 tokens 47 us
-  // against 55; 64 heads of 2048 the same, 178; 256 heads of 1024 229 against 184).
+  // 500 72 against 108) and where there are few chunks for the GPU (bf16, 4 heads of 500
+  // tokens 50 us against 60; 64 heads of 2048 195 against 181; 256 heads of 1024 248 against
+  // 212).
   p.waves = dv > 64 && io_bf16 && batch * hv * p.nchunk >= 1024 ? 8 : 4;
   if (p.recurrent) return p;
   const int cols = 16 * p.waves;

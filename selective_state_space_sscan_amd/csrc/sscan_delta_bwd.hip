@@ -284,9 +284,11 @@ struct GradLds {
 // axis comes in slabs of VS columns: U, X~ (cut into terms once) and dO through LDS, the
 // rows of S0 and E that a wave needs straight to its lanes.  2 x 4096 tokens of 16 heads
 // (8 key heads) of 128 x 128, 2048 chunks and heads: 252 us, where the bytes (0.32 GB
-// counted) take 67 us at a large copy's rate and the products, 0.1 TFLOP with the float32
-// factors' terms, 90 us (matrix units busy 17% of the cycles): a block's slabs pass through
-// LDS in phases that nothing else fills (one block of 142 KB a CU).
+// counted) take 62 us at a large copy's 5.1 TB/s and the products, 0.096 TFLOP with the
+// float32 factors' terms, 81 us (matrix units busy 17% of the cycles): a block's slabs pass
+// through LDS in phases that nothing else fills.  A CU holds one block, by its registers (256
+// a thread, about 108 of them sums) and its LDS (124 KB; float32 143 KB, which leaves eight
+// registers to scratch).
 template <typename IO, int KP, int VS>
 __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaBwdArgs b_, int nchunk, const float* vec,
                                                          const float* states, const float* adjoints,

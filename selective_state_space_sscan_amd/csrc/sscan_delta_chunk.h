@@ -158,7 +158,7 @@ struct WalkLds {
 // of 128 x 128: 0.23 TFLOP in 241 to 266 us (0.87 to 0.96 PFLOP/s; a large bf16 product
 // reaches 1.18), its transitions, 29 blocks of 32 chunks a head, 0.26 TFLOP in 280 to 312 us
 // (0.82 to 0.92).  LDS is not the bound (32 columns a wave, which halves its reads, take as
-// long), nor HBM (0.4 GB, 86 us at a large copy's rate).
+// long), nor HBM (0.43 GB, 85 us at a large copy's 5.1 TB/s).
 enum WalkMode { kOut, kStates, kEnds };
 
 struct WalkArgs {

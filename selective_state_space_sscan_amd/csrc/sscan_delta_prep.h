@@ -291,8 +291,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int nchunk
 
 // Which loads may be 16 bytes wide (per-call, from alignment and sizes): bit 0 q and
 // k, bit 1 v, bit 2 out, bit 3 the states.  All of them single, rows of 2-byte alignment:
-// 4 x 2048 tokens of 8 heads 226 us against 122, a document of 32768 of 16 heads 1465
-// against 720, gradients of 4 x 2048 513 against 372.
+// 4 x 2048 tokens of 8 heads 225 us against 123, a document of 32768 of 16 heads 1495
+// against 722, gradients of 4 x 2048 509 against 371.
 template <typename IO>
 int wide_flags(const DeltaArgs& a) {
   const auto ok = [](const void* p, const DeltaStride& s) {

@@ -1364,7 +1364,7 @@ class _DeltaFn(torch.autograd.Function):
 def gated_delta(q, k, v, g, beta, h0: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
                 scale: Optional[float] = None, qk_norm: bool = False):
     """``delta_fwd`` with gradients in q, k, v, g, beta and h0 (``sscan_delta_bwd`` in
-    the backward pass).  Returns (out, h_last)."""
+    the backward pass; no second derivatives).  Returns (out, h_last)."""
     return _DeltaFn.apply(q, k, v, g, beta, h0, lengths, scale, qk_norm)
 
 
@@ -1569,7 +1569,7 @@ class _GatedNormFn(torch.autograd.Function):
 
 
 def gated_rms_norm(x, z, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, gate_first: bool = False):
-    """``gated_norm`` with gradients in x, z and weight."""
+    """``gated_norm`` with gradients in x, z and weight (no second derivatives)."""
     return _GatedNormFn.apply(x, z, weight, eps, gate_first)
 
 
@@ -1596,6 +1596,6 @@ class _AddNormFn(torch.autograd.Function):
 def add_rms_norm(x, residual: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
                  scale: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
                  residual_dtype=None):
-    """``add_norm`` with gradients in x, residual, weight, scale and post_weight.
-    Returns (out, total)."""
+    """``add_norm`` with gradients in x, residual, weight, scale and post_weight (no second
+    derivatives).  Returns (out, total)."""
     return _AddNormFn.apply(x, residual, weight, scale, post_weight, eps, residual_dtype)
