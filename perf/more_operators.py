@@ -1,0 +1,546 @@
+"""Cases of the gated recurrence, of activations kept in 8 bits and of the layer norm.
+
+Operators (``sscan`` names): ``rec_fwd``, ``rec_bwd`` and ``rec_step`` (a gated linear
+recurrence over whole sequences, its gradients, and one token from a stored state),
+``gated_recurrence`` with ``checkpoint=True`` (a training pass whose backward reads
+activations kept in 8 bits), ``pack8`` / ``unpack8`` (those 8 bits by themselves) and
+``layer_norm`` / ``layer_norm_bwd`` (residual sum and layer norm).  ``run`` calls them
+where ``own`` is true and otherwise computes the same in plain float32 torch operations.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+C = 8.0            # decay exponent of the gated form
+BLOCK = 64         # elements that share a scale in 8 bits
+TINY = 2.0 ** -100  # a block below this is kept as zeros
+LN_EPS = 1e-5
+
+
+def rec_case(op, b, l, d, dtype, gated=True, igate=True, z=True, state=False, ragged=False, reverse=False, name=None):
+    c = dict(op=op, b=b, l=l, d=d, dtype=dtype, gated=gated, igate=igate, z=z, state=state, ragged=ragged,
+             reverse=reverse)
+    return c if name is None else dict(c, name=name)
+
+
+def pack_case(n, d, dtype, name=None):
+    c = dict(op="pack8", n=n, d=d, dtype=dtype)
+    return c if name is None else dict(c, name=name)
+
+
+def norm_case(op, n, d, dtype, res=None, bias=True, name=None):
+    c = dict(op=op, n=n, d=d, dtype=dtype, res=res, bias=bias)
+    return c if name is None else dict(c, name=name)
+
+
+def listed():
+    return [
+        # one sequence being answered: the latency of one layer's step
+        rec_case("rec_step", 1, 1, 2560, "bf16", name="step, one sequence"),
+        # a full serving batch
+        rec_case("rec_step", 256, 1, 4096, "bf16", name="step, 256 sequences"),
+        # short prompts of their own lengths, continued from states
+        rec_case("rec_fwd", 3, 77, 384, "bf16", state=True, ragged=True, name="prompts of 77"),
+        # an ordinary training or prefill forward
+        rec_case("rec_fwd", 4, 2048, 2560, "bf16", name="forward, 4 x 2048"),
+        # one very long document: few channels, a long axis
+        rec_case("rec_fwd", 1, 262144, 1536, "bf16", state=True, name="document of 262144"),
+        # float32 with decays as they are, scanned from the end, an odd size, resets inside rows
+        rec_case("rec_fwd", 3, 1000, 333, "f32", gated=False, igate=False, z=False, ragged=True, reverse=True,
+                 name="decays, f32, reverse"),
+        # gradients of an ordinary training step's layer
+        rec_case("rec_bwd", 2, 4096, 2560, "bf16", name="gradients, 2 x 4096"),
+        # gradients in float32 with a learned entry state, odd length
+        rec_case("rec_bwd", 2, 333, 768, "f32", state=True, ragged=True, name="gradients, f32, 333"),
+        # a training pass that keeps its activations in 8 bits
+        rec_case("rec_train", 4, 4096, 2048, "bf16", name="training pass, 8 bits kept"),
+        # a layer's activations kept in 8 bits and read back
+        pack_case(16384, 1536, "bf16", name="8 bits, 16384 x 1536"),
+        # a few sequences being answered: latency of the residual sum and norm
+        norm_case("layer_norm", 4, 768, "bf16", res="f32", name="layer norm, 4 tokens"),
+        # a training batch's residual sum and norm, gradients
+        norm_case("layer_norm_bwd", 16384, 1536, "bf16", res="f32", name="layer norm gradients"),
+    ]
+
+
+def draw(rng):
+    def size(lo, hi):
+        return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+    op = rng.choice(["rec_step", "rec_fwd", "rec_fwd", "rec_bwd", "rec_train", "pack8", "layer_norm", "layer_norm_bwd"])
+    dtype = rng.choice(["bf16", "bf16", "bf16", "f32"])
+    if op.startswith("rec"):
+        d = rng.choice([size(1, 4096), 64 * size(1, 64), 128 * size(1, 32)])
+        if op == "rec_step":
+            b, l = size(1, 256), 1
+        else:
+            most = (1 << 26 if op == "rec_fwd" else 1 << 24) // d  # tokens in the batch
+            l = size(1, min(most, 262144 if op == "rec_fwd" else 16384))
+            b = size(1, max(1, min(32, most // l)))
+        gated = rng.random() < 0.7
+        return rec_case(op, b, l, d, dtype, gated=gated, igate=rng.random() < 0.7, z=rng.random() < 0.6,
+                        state=rng.random() < 0.5, ragged=op != "rec_step" and rng.random() < 0.3,
+                        reverse=op != "rec_step" and rng.random() < 0.3)
+    d = size(8, 8192)
+    n = size(1, max(2, (1 << 24) // d))
+    if op == "pack8":
+        return pack_case(n, d, dtype)
+    return norm_case(op, n, d, dtype, res=rng.choice([None, "f32", "f32", dtype]), bias=rng.random() < 0.7)
+
+
+# ---- inputs -----------------------------------------------------------------------
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(int(seed))
+    dt = DTYPES[case["dtype"]]
+
+    def randn(*shape):
+        return torch.randn(shape, device="cuda", generator=gen)
+
+    def rand(*shape):
+        return torch.rand(shape, device="cuda", generator=gen)
+
+    s = dict(case=case)
+    if case["op"] == "pack8":
+        # activations with a few channels far larger than the others
+        s["x"] = (randn(case["n"], case["d"]) * torch.exp(0.7 * randn(case["d"]))).to(dt)
+        return s
+    if case["op"].startswith("layer"):
+        n, d = case["n"], case["d"]
+        res = None if case["res"] is None else DTYPES[case["res"]]
+        s.update(x=randn(n, d).to(dt), weight=1 + 0.1 * randn(d), bias=0.1 * randn(d) if case["bias"] else None,
+                 residual=None if res is None else (3 * randn(n, d) + 0.5).to(res))
+        if case["op"].endswith("bwd"):  # "total": the sum that the forward stored (x without a residual)
+            total = s["x"] if res is None else s["residual"]
+            s.update(total=total, dout=randn(n, d).to(dt), dtotal=None if res is None else randn(n, d).to(res))
+        return s
+    b, l, d = case["b"], case["l"], case["d"]
+    lead = (b,) if case["op"] == "rec_step" else (b, l)
+    s["x"] = randn(*lead, d).to(dt)
+    if case["gated"]:
+        s["g"] = randn(*lead, d).to(dt)
+        # exp(-C softplus(lam)) between 0.9 and 0.999: a channel's decay where its gate is open
+        s["lam"] = torch.log(torch.expm1(-torch.log(0.9 + 0.099 * rand(d)) / C))
+    else:
+        # log decays of 1e-3 to 1 a token, and now and then a reset of the whole row
+        g = -torch.exp(math.log(1e-3) * rand(*lead, d))
+        g = torch.where(rand(*lead, 1) < 0.002, torch.full_like(g, -math.inf), g)
+        s.update(g=g.to(dt), lam=None)
+    s["i"] = randn(*lead, d).to(dt) if case["igate"] else None
+    s["z"] = randn(*lead, d).to(dt) if case["z"] else None
+    s["h0"] = randn(b, d) if case["state"] or case["op"] == "rec_step" else None
+    s["lengths"] = (rand(b) * (l + 1)).to(torch.int32).clamp_(0, l) if case["ragged"] else None
+    if case["op"] in ("rec_bwd", "rec_train"):
+        s["dout"] = randn(b, l, d).to(dt)
+        s["dh_last"] = randn(b, d) if case["state"] and case["op"] == "rec_bwd" else None
+    if case["op"] == "rec_train":
+        for k in ("x", "g", "i", "lam", "z", "h0"):
+            if s[k] is not None:
+                s[k].requires_grad_(True)
+    return s
+
+
+# ---- one pass ---------------------------------------------------------------------
+
+def run(state):
+    return _run_own(state) if own else PLAIN[state["case"]["op"]](state)
+
+
+def _run_own(s):
+    from selective_state_space_sscan_amd import sscan
+
+    c = s["case"]
+    if c["op"] == "rec_step":
+        out = sscan.rec_step(s["h0"], s["x"], s["g"], s["i"], s["lam"], s["z"], c=C)
+        return {"out": out, "state": s["h0"]}
+    if c["op"] == "rec_fwd":
+        out, h_last = sscan.rec_fwd(s["x"], s["g"], s["i"], s["lam"], s["z"], h0=s["h0"], lengths=s["lengths"], c=C,
+                                    reverse=c["reverse"])
+        return {"out": out, "h_last": h_last}
+    if c["op"] == "rec_bwd":
+        r = sscan.rec_bwd(s["x"], s["g"], s["dout"], s["i"], s["lam"], s["z"], h0=s["h0"], dh_last=s["dh_last"],
+                          lengths=s["lengths"], c=C, reverse=c["reverse"])
+        return {k: v for k, v in r.items() if v is not None and (k != "dh0" or c["state"])}
+    if c["op"] == "rec_train":
+        names = [n for n in ("x", "g", "i", "lam", "z", "h0") if s[n] is not None]
+        out, _ = sscan.gated_recurrence(s["x"], s["g"], s["i"], s["lam"], s["z"], h0=s["h0"], lengths=s["lengths"],
+                                        c=C, reverse=c["reverse"], checkpoint=True)
+        grads = torch.autograd.grad(out, [s[n] for n in names], s["dout"])
+        return dict({"d" + n: t for n, t in zip(names, grads)}, out=out.detach())
+    if c["op"] == "pack8":
+        return sscan.unpack8(sscan.pack8(s["x"]), s["x"].dtype)
+    if c["op"] == "layer_norm":
+        out, total = sscan.layer_norm(s["x"], s["weight"], s["bias"], residual=s["residual"], eps=LN_EPS)
+        return {"out": out} if s["residual"] is None else {"out": out, "total": total}
+    r = sscan.layer_norm_bwd(s["total"], s["dout"], s["weight"], s["bias"], dtotal=s["dtotal"], eps=LN_EPS)
+    if s["residual"] is None:
+        del r["dresidual"]
+    return {k: v for k, v in r.items() if v is not None}
+
+
+# ---- plain forms ------------------------------------------------------------------
+
+def _scan(a, b):
+    """h_t = a_t h_{t-1} + b_t along dim 1 from 0, and the running products of a: doubling
+    steps within 64 tokens, then over the ends of the groups of 64."""
+    l = a.shape[1]
+    if l > 64:
+        n = -(-l // 64)
+        pad = (0, 0, 0, n * 64 - l)
+        a = torch.nn.functional.pad(a, pad, value=1.0).reshape(-1, 64, a.shape[2])
+        b = torch.nn.functional.pad(b, pad).reshape(-1, 64, b.shape[2])
+        p, h = _scan(a, b)
+        p, h = p.view(-1, n, 64, p.shape[2]), h.view(-1, n, 64, h.shape[2])
+        pe, he = _scan(p[:, :, -1], h[:, :, -1])
+        p, h = p.clone(), h.clone()
+        h[:, 1:] += p[:, 1:] * he[:, :-1, None]
+        p[:, 1:] *= pe[:, :-1, None]
+        return p.flatten(1, 2)[:, :l], h.flatten(1, 2)[:, :l]
+    step = 1
+    while step < l:
+        b = torch.cat([b[:, :step], b[:, step:] + a[:, step:] * b[:, :-step]], 1)
+        a = torch.cat([a[:, :step], a[:, step:] * a[:, :-step]], 1)
+        step *= 2
+    return a, b
+
+
+def _sig(x):
+    return 1 / (1 + torch.exp(-x))
+
+
+def _softplus(x):
+    return x.clamp(min=0) + torch.log1p(torch.exp(-x.abs()))
+
+
+def _gates(c, x, g, i, lam):
+    """(a, input multiplier's parts r, s, beta) of the tokens."""
+    s = _sig(i) if i is not None else None
+    if not c["gated"]:
+        return torch.exp(g), None, s, None
+    r = _sig(g)
+    m = C * _softplus(lam) * r
+    return torch.exp(-m), r, s, torch.sqrt(-torch.expm1(-2 * m))
+
+
+def _along(c, s, x):
+    """x [b, l, ...] in the order of the scan, zeros past a row's end (in front, backwards)."""
+    if s["lengths"] is not None:
+        x = torch.where(_inside(c, s)[..., None], x, x.new_zeros(()))
+    return x.flip(1) if c["reverse"] else x
+
+
+def _inside(c, s):
+    return torch.arange(c["l"], device="cuda")[None, :] < s["lengths"][:, None]
+
+
+def _forward(c, s, t):
+    """States of every token in the order of the scan: (a, h, state before each token)."""
+    a, r, sg, beta = _gates(c, t["x"], t["g"], t["i"], t["lam"])
+    u = t["x"]
+    u = u if sg is None else u * sg
+    u = u if beta is None else u * beta
+    if s["lengths"] is not None:  # a token past the end leaves the state as it is
+        a = torch.where(_inside(c, s)[..., None], a, a.new_ones(()))
+    a, u = a.flip(1) if c["reverse"] else a, _along(c, s, u)
+    p, h = _scan(a, u)
+    h0 = t["h0"] if t["h0"] is not None else torch.zeros_like(h[:, 0])
+    h = h + p * h0[:, None]
+    return a, h, torch.cat([h0[:, None], h[:, :-1]], 1), (r, sg, beta)
+
+
+def _floats(s):
+    return {k: s[k].detach().float() if s.get(k) is not None else None for k in ("x", "g", "i", "lam", "z", "h0", "dout")}
+
+
+def _answer(c, s, t, h):
+    h = h.flip(1) if c["reverse"] else h
+    out = h if t["z"] is None else h * t["z"] * _sig(t["z"])
+    if s["lengths"] is not None:
+        out = torch.where(_inside(c, s)[..., None], out, out.new_zeros(()))
+    return out.to(DTYPES[c["dtype"]])
+
+
+def _plain_rec_fwd(s):
+    c, t = s["case"], _floats(s)
+    _, h, _, _ = _forward(c, s, t)
+    return {"out": _answer(c, s, t, h).contiguous(), "h_last": h[:, -1].contiguous()}
+
+
+def _plain_rec_step(s):
+    c, t = s["case"], _floats(s)
+    a, r, sg, beta = _gates(c, t["x"], t["g"], t["i"], t["lam"])
+    u = t["x"]
+    u = u if sg is None else u * sg
+    u = u if beta is None else u * beta
+    h = s["h0"].mul_(a).add_(u)
+    out = h if t["z"] is None else h * t["z"] * _sig(t["z"])
+    return {"out": out.to(DTYPES[c["dtype"]]), "state": h}
+
+
+def _gradients(c, s, t, dh_last):
+    a, h, before, (r, sg, beta) = _forward(c, s, t)
+    dout = _along(c, s, t["dout"])
+    z = None if t["z"] is None else _along(c, s, t["z"])
+    e, out = dout, {}
+    if z is not None:
+        sz = _sig(z)
+        e = dout * z * sz
+        out["dz"] = dout * h * sz * (1 + z * (1 - sz))
+    # adjoints run against the scan: D_t = e_t + a_{t+1} D_{t+1}
+    nxt = torch.cat([a[:, 1:], torch.ones_like(a[:, :1])], 1).flip(1)
+    p, adj = _scan(nxt, e.flip(1))
+    if dh_last is not None:
+        adj = adj + p * dh_last[:, None]
+    adj = adj.flip(1)
+    dlog = adj * a * before
+    w = None
+    x = _along(c, s, t["x"])
+    if sg is not None:
+        sg = _along(c, s, sg)
+    if c["gated"]:
+        r, beta = _along(c, s, r), _along(c, s, beta)
+        w = beta
+        inv = torch.where(beta > 0, 1 / torch.where(beta > 0, beta, torch.ones_like(beta)), torch.zeros_like(beta))
+        dlog = dlog - adj * (x if sg is None else x * sg) * a * a * inv
+        sp = _softplus(t["lam"])
+        out["dg"] = -dlog * C * sp * r * (1 - r)
+        out["dlam"] = (-dlog * C * r).sum((0, 1)) * _sig(t["lam"])
+    else:
+        out["dg"] = dlog
+    dx = adj if w is None else adj * w
+    if sg is not None:
+        out["di"] = dx * x * sg * (1 - sg)
+        dx = dx * sg
+    out["dx"] = dx
+    dt = DTYPES[c["dtype"]]
+    for k in ("dx", "dg", "di", "dz"):
+        if k in out:
+            v = out[k].flip(1) if c["reverse"] else out[k]
+            if s["lengths"] is not None:
+                v = torch.where(_inside(c, s)[..., None], v, v.new_zeros(()))
+            out[k] = v.to(dt).contiguous()
+    if t["h0"] is not None:
+        out["dh0"] = (a[:, 0] * adj[:, 0]).contiguous()
+    return out
+
+
+def _plain_rec_bwd(s):
+    c = s["case"]
+    return _gradients(c, s, _floats(s), s["dh_last"])
+
+
+def _eight(x):
+    """float32 x as its 8 bits give it back: whole steps of a block's largest value / 127."""
+    d = x.shape[-1]
+    n = -(-d // BLOCK)
+    y = torch.nn.functional.pad(x, (0, n * BLOCK - d)).unflatten(-1, (n, BLOCK))
+    top = y.abs().amax(-1, keepdim=True)
+    keep = top >= TINY
+    inv = 127 / torch.where(keep, top, torch.ones_like(top))
+    q = torch.where(keep, torch.round(y * inv), torch.zeros_like(y))
+    y = q * (torch.where(keep, top, torch.zeros_like(top)) / 127)
+    # a block with an infinity or a NaN is NaN throughout
+    y = torch.where(torch.isfinite(top), y, torch.full_like(y, math.nan))
+    return y.flatten(-2)[..., :d]
+
+
+def _plain_rec_train(s):
+    c, t = s["case"], _floats(s)
+    _, h, _, _ = _forward(c, s, t)
+    out = _answer(c, s, t, h).contiguous()
+    kept = dict(t, **{k: _eight(t[k]) for k in ("x", "g", "i", "z") if t[k] is not None})
+    return dict(_gradients(c, s, kept, None), out=out)
+
+
+def _plain_pack8(s):
+    return _eight(s["x"].float()).to(s["x"].dtype)
+
+
+def _plain_layer_norm(s):
+    x = s["x"].float()
+    total = s["x"]
+    if s["residual"] is not None:
+        total = (s["residual"].float() + x).to(s["residual"].dtype)
+        x = total.float()
+    x = x - x.mean(-1, keepdim=True)
+    y = x * torch.rsqrt(x.square().mean(-1, keepdim=True) + LN_EPS) * s["weight"]
+    y = (y if s["bias"] is None else y + s["bias"]).to(s["x"].dtype)
+    return {"out": y} if s["residual"] is None else {"out": y, "total": total}
+
+
+def _plain_layer_norm_bwd(s):
+    x, dout = s["total"].float(), s["dout"].float()
+    x = x - x.mean(-1, keepdim=True)
+    r = torch.rsqrt(x.square().mean(-1, keepdim=True) + LN_EPS)
+    n, dn = x * r, dout * s["weight"]
+    dx = r * (dn - dn.mean(-1, keepdim=True) - n * (dn * n).mean(-1, keepdim=True))
+    if s["dtotal"] is not None:
+        dx = dx + s["dtotal"].float()
+    out = {"dx": dx.to(s["x"].dtype), "dweight": (dout * n).sum(0)}
+    if s["residual"] is not None:
+        out["dresidual"] = dx.to(s["total"].dtype)
+    if s["bias"] is not None:
+        out["dbias"] = dout.sum(0)
+    return out
+
+
+PLAIN = {"rec_step": _plain_rec_step, "rec_fwd": _plain_rec_fwd, "rec_bwd": _plain_rec_bwd,
+         "rec_train": _plain_rec_train, "pack8": _plain_pack8, "layer_norm": _plain_layer_norm,
+         "layer_norm_bwd": _plain_layer_norm_bwd}
+
+
+# ---- what a pass cannot do without ------------------------------------------------
+
+def work(case):
+    esz = 2 if case["dtype"] == "bf16" else 4
+    op = case["op"]
+    if op == "pack8":
+        e = case["n"] * case["d"]
+        kept = e + 4 * case["n"] * -(-case["d"] // BLOCK)
+        return {"bytes": 2 * e * esz + 2 * kept, "flops": 5.0 * e}
+    if op.startswith("layer"):
+        e = case["n"] * case["d"]
+        rsz = 0 if case["res"] is None else 2 if case["res"] == "bf16" else 4
+        vecs = 4 * case["d"] * (1 + case["bias"])
+        if op.endswith("bwd"):
+            # total, dout and dtotal read, dx written, in the residual's type too where that is another
+            moved = 3 * esz if not rsz else 2 * esz + 2 * rsz + (rsz if rsz != esz else 0)
+            return {"bytes": e * moved + 2 * vecs, "flops": 16.0 * e}
+        return {"bytes": e * (2 * esz + 2 * rsz) + vecs, "flops": 8.0 * e}
+    e, row = case["b"] * case["l"] * case["d"], case["b"] * case["d"] * 4
+    ins = 2 + case["igate"] + case["z"]
+    fwd = 6.0 + 10.0 * case["gated"] + 5.0 * case["igate"] + 6.0 * case["z"]
+    reads_state = case["state"] or op == "rec_step"
+    if op in ("rec_step", "rec_fwd"):
+        return {"bytes": e * esz * (ins + 1) + row * (2 if reads_state else 1), "flops": fwd * e}
+    if op == "rec_bwd":
+        return {"bytes": e * esz * (2 * ins + 1) + row * (3 if case["state"] else 0), "flops": 3 * fwd * e}
+    kept = ins * (e + 4 * case["b"] * case["l"] * -(-case["d"] // BLOCK))
+    return {"bytes": e * esz * (2 * ins + 2) + 2 * kept + row * (2 if case["state"] else 0), "flops": 4 * fwd * e}
+
+
+# ---- the definition in 64 bits ----------------------------------------------------
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "pack8":
+        return _exact_eight(s["x"])
+    d = {k: v.detach().double() if isinstance(v, torch.Tensor) and v.is_floating_point() else v for k, v in s.items()}
+    if case["op"].startswith("layer"):
+        return _exact_layer_norm(case, s, d)
+    if case["op"] == "rec_train":
+        kept = dict(d, **{k: _exact_eight(s[k].detach()) for k in ("x", "g", "i", "z") if s[k] is not None})
+        out = _exact_rec(case, d, False)["out"]
+        return dict(_exact_rec(case, kept, True), out=out)
+    return _exact_rec(case, d, case["op"] == "rec_bwd")
+
+
+def _exact_eight(x):
+    """Block by block: steps of float32(top / 127), values rounded to the nearest step (ties to even)."""
+    x = x.float()
+    parts = []
+    for part in x.split(BLOCK, -1):
+        top = part.abs().max(-1, keepdim=True).values
+        safe = torch.where(top < TINY, torch.ones_like(top), top)
+        q = (part * (127 / safe)).round()
+        val = q.double() * (top / 127).double()
+        val = torch.where(top < TINY, torch.zeros_like(val), val)
+        parts.append(torch.where(torch.isfinite(top), val, torch.full_like(val, math.nan)))
+    return torch.cat(parts, -1)
+
+
+def _exact_rec(c, d, back):
+    """Token by token: h <- a h + u, out = h silu(z); adjoints token by token against it."""
+    step = c["op"] == "rec_step"
+    x, g, i, z = (d[n][:, None] if step and d[n] is not None else d[n] for n in ("x", "g", "i", "z"))
+    b, l, dim = x.shape
+    lam = d["lam"]
+    s = torch.ones_like(x) if i is None else torch.sigmoid(i)
+    if lam is None:
+        loga, mult = g, s
+    else:
+        sp = torch.log1p(torch.exp(-lam.abs())) + lam.clamp(min=0)
+        r = torch.sigmoid(g)
+        loga = -C * sp * r
+        beta = torch.sqrt(-torch.expm1(2 * loga))
+        mult = beta * s
+    a, u = torch.exp(loga), mult * x
+    order = range(l - 1, -1, -1) if c["reverse"] else range(l)
+    n = d["lengths"]
+    if n is not None:
+        live = (torch.arange(l, device="cuda")[None, :] < n[:, None])[..., None]
+        a, u = torch.where(live, a, torch.ones_like(a)), torch.where(live, u, torch.zeros_like(u))
+    hs = torch.empty(l, b, dim, dtype=torch.float64, device="cuda")
+    at, ut = a.transpose(0, 1), u.transpose(0, 1)
+    h = first = torch.zeros(b, dim, dtype=torch.float64, device="cuda") if d["h0"] is None else d["h0"]
+    for t in order:
+        h = torch.addcmul(ut[t], at[t], h, out=hs[t])
+    h_last = h.clone()
+    hs = hs.transpose(0, 1)
+    gate = torch.ones_like(x) if z is None else z * torch.sigmoid(z)
+    if not back:
+        out = hs * gate
+        if n is not None:
+            out = torch.where(live, out, torch.zeros_like(out))
+        return {"out": out[:, 0], "state": h_last} if step else {"out": out, "h_last": h_last}
+    dout = d["dout"] if n is None else torch.where(live, d["dout"], torch.zeros_like(d["dout"]))
+    e = (dout * gate).transpose(0, 1)
+    adj = torch.empty(l, b, dim, dtype=torch.float64, device="cuda")
+    carry = torch.zeros(b, dim, dtype=torch.float64, device="cuda") if d.get("dh_last") is None else d["dh_last"]
+    for t in reversed(order):
+        torch.add(e[t], carry, out=adj[t])
+        carry = at[t] * adj[t]
+    adj = adj.transpose(0, 1)
+    before = torch.cat([hs[:, 1:], first[:, None]], 1) if c["reverse"] else torch.cat([first[:, None], hs[:, :-1]], 1)
+    got = {"dx": adj * mult}
+    if z is not None:
+        sz = torch.sigmoid(z)
+        got["dz"] = dout * hs * (sz + z * sz * (1 - sz))
+    if i is not None:
+        got["di"] = adj * x * mult * (1 - s)
+    dlog = adj * before * a
+    if lam is None:
+        got["dg"] = dlog
+    else:
+        # u = beta s x with beta^2 = 1 - a^2: d beta / d log a = -a^2 / beta
+        dlog = dlog - adj * s * x * a * a / beta
+        if n is not None:
+            dlog = torch.where(live, dlog, torch.zeros_like(dlog))
+        got["dg"] = -dlog * C * sp * r * (1 - r)
+        got["dlam"] = (-dlog * C * r).sum((0, 1)) * torch.sigmoid(lam)
+    if n is not None:
+        got = {k: torch.where(live, v, torch.zeros_like(v)) if v.dim() == 3 else v for k, v in got.items()}
+    if d["h0"] is not None:
+        got["dh0"] = carry
+    return got
+
+
+def _exact_layer_norm(c, s, d):
+    """From the definition, gradients by differentiation in 64 bits."""
+    def norm(x, w, bias):
+        m = x.sum(-1, keepdim=True) / x.shape[-1]
+        v = (x - m).pow(2).sum(-1, keepdim=True) / x.shape[-1]
+        y = (x - m) / (v + LN_EPS).sqrt() * w
+        return y if bias is None else y + bias
+
+    if c["op"] == "layer_norm":
+        if s["residual"] is None:
+            return {"out": norm(d["x"], d["weight"], d["bias"])}
+        total = d["residual"] + d["x"]
+        # a sum stored in fewer bits is normed as it was stored, and that is rounded from 32 bits
+        y = norm(total, d["weight"], d["bias"]) if s["residual"].dtype is torch.float32 else None
+        return {"out": y, "total": total}
+    ins = [d[k].detach().requires_grad_(True) for k in ("total", "weight", "bias") if d[k] is not None]
+    y = norm(*ins, *([None] if s["bias"] is None else []))
+    got = torch.autograd.grad(y, ins, d["dout"])
+    dx = got[0] if d["dtotal"] is None else got[0] + d["dtotal"]
+    out = {"dx": dx, "dweight": got[1]}
+    if s["bias"] is not None:
+        out["dbias"] = got[2]
+    if s["residual"] is not None:
+        out["dresidual"] = dx
+    return out
