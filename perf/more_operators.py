@@ -340,9 +340,10 @@ def _eight(x):
     y = torch.nn.functional.pad(x, (0, n * BLOCK - d)).unflatten(-1, (n, BLOCK))
     top = y.abs().amax(-1, keepdim=True)
     keep = top >= TINY
-    inv = 127 / torch.where(keep, top, torch.ones_like(top))
+    full = torch.full_like(top, 127.0)  # quotients of tensors: with a number torch multiplies by a reciprocal
+    inv = full / torch.where(keep, top, torch.ones_like(top))
     q = torch.where(keep, torch.round(y * inv), torch.zeros_like(y))
-    y = q * (torch.where(keep, top, torch.zeros_like(top)) / 127)
+    y = q * (torch.where(keep, top, torch.zeros_like(top)) / full)
     # a block with an infinity or a NaN is NaN throughout
     y = torch.where(torch.isfinite(top), y, torch.full_like(y, math.nan))
     return y.flatten(-2)[..., :d]
@@ -446,8 +447,9 @@ def _exact_eight(x):
     for part in x.split(BLOCK, -1):
         top = part.abs().max(-1, keepdim=True).values
         safe = torch.where(top < TINY, torch.ones_like(top), top)
-        q = (part * (127 / safe)).round()
-        val = q.double() * (top / 127).double()
+        full = torch.full_like(top, 127.0)
+        q = (part * (full / safe)).round()
+        val = q.double() * (top / full).double()
         val = torch.where(top < TINY, torch.zeros_like(val), val)
         parts.append(torch.where(torch.isfinite(top), val, torch.full_like(val, math.nan)))
     return torch.cat(parts, -1)
