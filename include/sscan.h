@@ -664,6 +664,150 @@ SSCAN_API int sscan_validate_add_norm_bwd(const sscan_add_norm_params* p, const 
                                 const void* dx, const void* dresidual, const float* dweight, const float* dscale,
                                 const float* dpost_weight, const void* workspace, size_t workspace_bytes);
 
+/* ---- The gated recurrence -------------------------------------------------------------
+ * A linear recurrence with one state per channel.  Per batch row and channel, with a
+ * float32 state h (0 before the first scanned token, or h0):
+ *   a_t = exp(-c softplus(lam) r_t), r_t = sigmoid(g_t), w_t = sqrt(1 - a_t^2)   (lam given)
+ *   a_t = exp(g_t), w_t = 1                          (lam NULL: g is the log decay, normally
+ *                                                     <= 0; -inf resets the state)
+ *   h <- a_t h + w_t sigmoid(i_t) x_t                (i NULL: no input gate)
+ *   out_t = h silu(z_t)                              (z NULL: out_t = h)
+ *
+ * x, g, i, z [batch, len, dim] io_dtype, each with its own element strides between batch
+ * rows and tokens (>= 0); dim is contiguous.  out [batch, len, dim] io_dtype and the states
+ * [batch, dim] float32 are contiguous; lam float32 [dim].  lengths (optional, device int32
+ * [batch]): tokens of each row, clamped to 0..len; later tokens are not read, their outputs
+ * and gradients are 0 and they leave the state alone.  With reverse != 0 a row is scanned
+ * from its last token to its first.  States and sums are float32; bf16 outputs round to
+ * nearest even, once.  len <= 2^30, dim <= 2^24, batch * ceil(dim / 64) * (len / 64 + 1) at
+ * most 2^24, c finite and >= 0. */
+typedef struct sscan_rec_params {
+  const void* x;
+  const void* g;
+  const void* i;            /* optional */
+  const void* z;            /* optional */
+  const float* lam;         /* optional */
+  const int32_t* lengths;   /* optional */
+  const float* h0;          /* optional; not used by sscan_rec_step */
+  int64_t x_stride[2];      /* elements between batch rows, tokens */
+  int64_t g_stride[2];
+  int64_t i_stride[2];
+  int64_t z_stride[2];
+  int64_t batch, len, dim;
+  float c;
+  int reverse;              /* 0 or 1 */
+  int io_dtype;             /* of x, g, i, z, out and their gradients */
+} sscan_rec_params;
+
+/* The inputs in 8 bits (sscan_pack8 of each token's channels; contiguous [batch, len, dim]
+ * and [batch, len, ceil(dim / 64)]): what a backward pass needs of them in half the memory.
+ * i and z with their scales where the call has them. */
+typedef struct sscan_rec_kept {
+  int8_t* x;
+  int8_t* g;
+  int8_t* i;
+  int8_t* z;
+  float* x_scale;
+  float* g_scale;
+  float* i_scale;
+  float* z_scale;
+} sscan_rec_kept;
+
+/* Gradients (device pointers, contiguous).  dx and dg are required when they have
+ * elements, di and dz with i and z; dlam (only with lam) and dh0 are optional. */
+typedef struct sscan_rec_grads {
+  void* dx;                 /* [batch, len, dim] io_dtype */
+  void* dg;
+  void* di;
+  void* dz;
+  float* dlam;              /* [dim] */
+  float* dh0;               /* [batch, dim] */
+} sscan_rec_grads;
+
+/* Whole sequences.  h_last (required) receives the state after each row's last scanned
+ * token; it may be h0 itself.  kept (optional) receives the inputs in 8 bits; tokens past a
+ * row's length are not written there.  Outputs must not overlap each other, any other input
+ * or the workspace (sscan_rec_workspace_bytes(...) bytes, 256-byte aligned).  len == 0
+ * copies the entry state (or zeros) to h_last. */
+SSCAN_API int sscan_rec_fwd(const sscan_rec_params* p, void* out, float* h_last, const sscan_rec_kept* kept,
+                  void* stream, void* workspace, size_t workspace_bytes);
+
+/* One token from a stored state, updated in place (p->len must be 1, p->h0 NULL and
+ * p->reverse 0; a row of lengths 0 keeps its state and answers 0).  No workspace. */
+SSCAN_API int sscan_rec_step(const sscan_rec_params* p, float* state, void* out, void* stream);
+
+/* Gradients of sum(dout * out) + sum(dh_last * h_last) (dout [batch, len, dim] io_dtype,
+ * contiguous; dh_last optional).  The forward states are recomputed; no atomics on sums:
+ * results are bitwise reproducible.  With kept the inputs are read from there (x, g, i and z
+ * of p must be NULL) and the gradients are those at the values that the 8 bits stand for.
+ * Where a decay rounds to 1 (w_t = 0) the slope of w_t is taken as 0.  Outputs must not
+ * overlap each other, any input or the workspace (sscan_rec_bwd_workspace_bytes). */
+SSCAN_API int sscan_rec_bwd(const sscan_rec_params* p, const sscan_rec_kept* kept, const void* dout,
+                  const float* dh_last, const sscan_rec_grads* grads, void* stream, void* workspace,
+                  size_t workspace_bytes);
+
+SSCAN_API size_t sscan_rec_workspace_bytes(int64_t batch, int64_t len, int64_t dim, int io_dtype);
+SSCAN_API size_t sscan_rec_bwd_workspace_bytes(int64_t batch, int64_t len, int64_t dim, int io_dtype);
+
+/* The checks of the three calls above, without touching the GPU. */
+SSCAN_API int sscan_validate_rec_fwd(const sscan_rec_params* p, const void* out, const float* h_last,
+                           const sscan_rec_kept* kept, const void* workspace, size_t workspace_bytes);
+SSCAN_API int sscan_validate_rec_step(const sscan_rec_params* p, const float* state, const void* out);
+SSCAN_API int sscan_validate_rec_bwd(const sscan_rec_params* p, const sscan_rec_kept* kept, const void* dout,
+                           const float* dh_last, const sscan_rec_grads* grads, const void* workspace,
+                           size_t workspace_bytes);
+
+/* ---- Activations in 8 bits --------------------------------------------------------------
+ * Rows of `size` elements, in blocks of 64 (the last one may be shorter), each with a scale:
+ *   scale = m / 127, q = x * (127 / m) rounded to the nearest integer (ties to even),
+ * m the block's largest |x|, all in float32.  A block whose m is below 2^-100 is kept as
+ * zeros (scale 0); one that holds an infinity or a NaN has scale NaN and is read back as
+ * NaN.  x [rows, size] io_dtype with a stride between rows (elements, >= 0); q [rows, size]
+ * and scale [rows, ceil(size / 64)] contiguous.  An element is read back as q * scale, off
+ * by at most half a scale (and the rounding to io_dtype). */
+SSCAN_API int sscan_pack8(const void* x, int64_t x_stride, int64_t rows, int64_t size, int io_dtype, int8_t* q,
+                float* scale, void* stream);
+SSCAN_API int sscan_unpack8(const int8_t* q, const float* scale, int64_t rows, int64_t size, int io_dtype, void* out,
+                  void* stream);
+SSCAN_API int sscan_validate_pack8(const void* x, int64_t x_stride, int64_t rows, int64_t size, int io_dtype,
+                         const int8_t* q, const float* scale);
+SSCAN_API int sscan_validate_unpack8(const int8_t* q, const float* scale, int64_t rows, int64_t size, int io_dtype,
+                           const void* out);
+
+/* ---- Layer norm -------------------------------------------------------------------------
+ * The residual sum and the layer norm of it (mean and variance over `size` elements):
+ *   total = residual + x,  out = (total - mean) / sqrt(var + eps) * weight + bias
+ * x [rows, size] io_dtype with a stride between rows (elements, >= 0); residual and total
+ * [rows, size] residual_dtype, contiguous; out contiguous; weight, bias float32 [size]
+ * (optional: 1 and 0).  The norm is that of the total as stored.  Without a residual total
+ * may be NULL: x itself is normed (and residual_dtype not used); otherwise it is required
+ * and may be residual itself.  size in 1..8192. */
+typedef struct sscan_layer_norm_params {
+  const void* x;            /* backward: the total (or x), residual_dtype */
+  const void* residual;     /* optional; not used backward */
+  const float* weight;
+  const float* bias;
+  int64_t x_stride;
+  int64_t rows, size;
+  float eps;
+  int io_dtype, residual_dtype;
+} sscan_layer_norm_params;
+
+SSCAN_API int sscan_layer_norm(const sscan_layer_norm_params* p, void* out, void* total, void* stream);
+/* From dout (io_dtype) and dtotal (residual_dtype, optional, contiguous), with p->x the
+ * total that the forward stored (or x, where residual_dtype is io_dtype): dx (io_dtype) and
+ * the same gradient in residual_dtype as dresidual (optional; may be dtotal itself), and
+ * the optional float32 dweight and dbias [size].  Sums run in a fixed order.  Workspace:
+ * sscan_layer_norm_bwd_workspace_bytes, 16-byte aligned. */
+SSCAN_API int sscan_layer_norm_bwd(const sscan_layer_norm_params* p, const void* dout, const void* dtotal, void* dx,
+                         void* dresidual, float* dweight, float* dbias, void* stream, void* workspace,
+                         size_t workspace_bytes);
+SSCAN_API size_t sscan_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t size);
+SSCAN_API int sscan_validate_layer_norm(const sscan_layer_norm_params* p, const void* out, const void* total);
+SSCAN_API int sscan_validate_layer_norm_bwd(const sscan_layer_norm_params* p, const void* dout, const void* dtotal,
+                                  const void* dx, const void* dresidual, const float* dweight, const float* dbias,
+                                  const void* workspace, size_t workspace_bytes);
+
 /* Static description of a status code; never NULL. */
 SSCAN_API const char* sscan_strerror(int status);
 

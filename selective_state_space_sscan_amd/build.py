@@ -15,8 +15,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsscan.so")
 
-SOURCES = ["sscan_kernels.hip", "sscan_short.hip", "sscan_bwd.hip", "sscan_conv_bwd.hip", "sscan_multi.hip", "sscan_noalloc.hip", "sscan_delta.hip", "sscan_delta_bwd.hip", "sscan_norm.hip", "sscan_capi.cpp",
-           "sscan_delta_capi.cpp"]
+SOURCES = ["sscan_kernels.hip", "sscan_short.hip", "sscan_bwd.hip", "sscan_conv_bwd.hip", "sscan_multi.hip", "sscan_noalloc.hip", "sscan_delta.hip", "sscan_delta_bwd.hip", "sscan_norm.hip", "sscan_rec.hip", "sscan_rec_bwd.hip",
+           "sscan_pack8.hip", "sscan_layer_norm.hip", "sscan_capi.cpp",
+           "sscan_delta_capi.cpp", "sscan_rec_capi.cpp"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

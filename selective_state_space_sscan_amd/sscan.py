@@ -11,7 +11,7 @@ import ctypes
 import functools
 import os
 import struct
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -79,11 +79,38 @@ class AddNormParams(ctypes.Structure):
                 ("residual_dtype", ctypes.c_int)]
 
 
+class RecParams(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("g", ctypes.c_void_p), ("i", ctypes.c_void_p), ("z", ctypes.c_void_p),
+                ("lam", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("h0", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64 * 2), ("g_stride", ctypes.c_int64 * 2), ("i_stride", ctypes.c_int64 * 2),
+                ("z_stride", ctypes.c_int64 * 2), ("batch", ctypes.c_int64), ("len", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("c", ctypes.c_float), ("reverse", ctypes.c_int), ("io_dtype", ctypes.c_int)]
+
+
+class RecKept(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "g", "i", "z", "x_scale", "g_scale", "i_scale", "z_scale")]
+
+
+class RecGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "dg", "di", "dz", "dlam", "dh0")]
+
+
+class LayerNormParams(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("size", ctypes.c_int64), ("eps", ctypes.c_float), ("io_dtype", ctypes.c_int),
+                ("residual_dtype", ctypes.c_int)]
+
+
 # The parameter structs packed in one go: small calls are bound by the host, and a
 # ctypes.Structure of thirty fields takes several microseconds to fill.
 _DELTA = struct.Struct("7P21qfii4x")
 _GATED = struct.Struct("3P7qfiii")
 _ADD = struct.Struct("5P2qfii4x")
+_REC = struct.Struct("7P11qfii4x")
+_KEPT = struct.Struct("8P")
+_REC_GRADS = struct.Struct("6P")
+_LAYER = struct.Struct("4P3qfii4x")
 
 
 _lib = None
@@ -223,6 +250,28 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.sscan_gated_norm_bwd_workspace_bytes.restype = SZ
     lib.sscan_add_norm_bwd_workspace_bytes.argtypes = [I64, I64]
     lib.sscan_add_norm_bwd_workspace_bytes.restype = SZ
+    lib.sscan_rec_fwd.argtypes = [V, V, V, V, V, V, SZ]
+    lib.sscan_rec_step.argtypes = [V, V, V, V]
+    lib.sscan_rec_bwd.argtypes = [V, V, V, V, V, V, V, SZ]
+    lib.sscan_validate_rec_fwd.argtypes = [V, V, V, V, V, SZ]
+    lib.sscan_validate_rec_step.argtypes = [V, V, V]
+    lib.sscan_validate_rec_bwd.argtypes = [V, V, V, V, V, V, SZ]
+    lib.sscan_pack8.argtypes = [V, I64, I64, I64, I, V, V, V]
+    lib.sscan_unpack8.argtypes = [V, V, I64, I64, I, V, V]
+    lib.sscan_validate_pack8.argtypes = [V, I64, I64, I64, I, V, V]
+    lib.sscan_validate_unpack8.argtypes = [V, V, I64, I64, I, V]
+    lib.sscan_layer_norm.argtypes = [V, V, V, V]
+    lib.sscan_layer_norm_bwd.argtypes = [V, V, V, V, V, V, V, V, V, SZ]
+    lib.sscan_validate_layer_norm.argtypes = [V, V, V]
+    lib.sscan_validate_layer_norm_bwd.argtypes = [V, V, V, V, V, V, V, V, SZ]
+    for name in ("rec_fwd", "rec_step", "rec_bwd", "pack8", "unpack8", "layer_norm", "layer_norm_bwd"):
+        getattr(lib, "sscan_" + name).restype = I
+        getattr(lib, "sscan_validate_" + name).restype = I
+    for name in ("sscan_rec_workspace_bytes", "sscan_rec_bwd_workspace_bytes"):
+        getattr(lib, name).argtypes = [I64, I64, I64, I]
+        getattr(lib, name).restype = SZ
+    lib.sscan_layer_norm_bwd_workspace_bytes.argtypes = [I64, I64]
+    lib.sscan_layer_norm_bwd_workspace_bytes.restype = SZ
     lib.sscan_strerror.argtypes = [I]
     lib.sscan_strerror.restype = ctypes.c_char_p
     lib.sscan_version.argtypes = []
@@ -1121,6 +1170,9 @@ def _apart(state, out) -> None:
         raise ValueError("out and the state overlap")
 
 
+_NO_SECOND = "the gated delta rule, the gated recurrence and the norms around a mixer have no second derivatives"
+
+
 class _NoSecond(torch.autograd.Function):
     """Gradients as they are, whose own backward pass raises."""
 
@@ -1130,7 +1182,7 @@ class _NoSecond(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *grads):
-        raise RuntimeError("the gated delta rule and the norms around a mixer have no second derivatives")
+        raise RuntimeError(_NO_SECOND)
 
 
 def _first_order(backward):
@@ -1141,6 +1193,9 @@ def _first_order(backward):
 
     @functools.wraps(backward)
     def run(ctx, *grads):
+        if torch.is_grad_enabled() and getattr(ctx, "checkpoint", False):
+            # the inputs themselves are not kept, and a graph of the gradients could not reach them
+            raise RuntimeError(_NO_SECOND)
         with torch.no_grad():
             r = backward(ctx, *grads)
         if not torch.is_grad_enabled():
@@ -1599,3 +1654,432 @@ def add_rms_norm(x, residual: Optional[torch.Tensor] = None, weight: Optional[to
     """``add_norm`` with gradients in x, residual, weight, scale and post_weight (no second
     derivatives).  Returns (out, total)."""
     return _AddNormFn.apply(x, residual, weight, scale, post_weight, eps, residual_dtype)
+
+
+# ---- activations in 8 bits --------------------------------------------------------
+
+PACK_BLOCK = 64  # elements that share a scale
+
+
+class Packed8(NamedTuple):
+    """A tensor in 8 bits: q [..., size] int8 and scale [..., ceil(size / 64)] f32."""
+    q: torch.Tensor
+    scale: torch.Tensor
+
+
+def _pack_blocks(size: int) -> int:
+    return -(-size // PACK_BLOCK)
+
+
+def pack8(x, out: Optional[Packed8] = None) -> Packed8:
+    """x [..., size] f32/bf16 in 8 bits (``sscan_pack8``): along the last dimension, blocks of
+    64 elements share the scale max|x| / 127 (float32), and every element is the nearest
+    whole number of scales.  The leading dimensions may be strided rows of one stride."""
+    lib = load_library()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev, xs = x.device, x.shape
+    if dev.type != "cuda":
+        raise ValueError("sscan.pack8 needs CUDA (HIP) tensors")
+    if x.dtype not in _DT_CODE:
+        raise TypeError("x must be float32 or bfloat16")
+    if not xs:
+        raise ValueError("x needs at least one dimension")
+    _strided(x, "x", dev, x.dtype, xs)
+    stride = _row_stride(xs, x.stride(), len(xs) - 1) if len(xs) > 1 else 0
+    if stride is None:
+        raise ValueError("the leading dimensions of x must collapse to rows of one stride")
+    size, n = xs[-1], _pack_blocks(xs[-1])
+    given = out
+    if out is None:
+        out = Packed8(torch.empty(xs, dtype=torch.int8, device=dev),
+                      torch.empty((*xs[:-1], n), dtype=torch.float32, device=dev))
+    else:
+        _check_packed(out, "out", dev, xs)
+    rows = x.numel() // size if size else 0
+    st = lib.sscan_pack8(x.data_ptr(), stride, rows, size, _DT_CODE[x.dtype], out.q.data_ptr(), out.scale.data_ptr(),
+                         _stream(dev))
+    if st != 0:
+        raise SScanError(st, "sscan_pack8")
+    if given is not None:
+        _written(*given)
+    return out
+
+
+def _check_packed(p, name: str, device, shape):
+    if not isinstance(p, Packed8):
+        raise TypeError(f"{name} must be a Packed8")
+    for t, what in ((p.q, "q"), (p.scale, "scale")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}.{what} must be a torch.Tensor")
+    _check(p.q, name + ".q", device, torch.int8, shape)
+    _check(p.scale, name + ".scale", device, torch.float32, (*shape[:-1], _pack_blocks(shape[-1])))
+
+
+def unpack8(p: Packed8, dtype=torch.float32, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values that ``pack8``'s answer stands for, as ``dtype`` (``sscan_unpack8``)."""
+    lib = load_library()
+    if not isinstance(p, Packed8) or not isinstance(p.q, torch.Tensor):
+        raise TypeError("p must be a Packed8")
+    dev, xs = p.q.device, p.q.shape
+    if dev.type != "cuda":
+        raise ValueError("sscan.unpack8 needs CUDA (HIP) tensors")
+    if dtype not in _DT_CODE:
+        raise TypeError("dtype must be float32 or bfloat16")
+    if not xs:
+        raise ValueError("p.q needs at least one dimension")
+    _check_packed(p, "p", dev, xs)
+    given = out
+    if out is None:
+        out = torch.empty(xs, dtype=dtype, device=dev)
+    else:
+        _check(out, "out", dev, dtype, xs)
+    size = xs[-1]
+    st = lib.sscan_unpack8(p.q.data_ptr(), p.scale.data_ptr(), p.q.numel() // size if size else 0, size, _DT_CODE[dtype],
+                           out.data_ptr(), _stream(dev))
+    if st != 0:
+        raise SScanError(st, "sscan_unpack8")
+    _written(given)
+    return out
+
+
+# ---- the gated recurrence ---------------------------------------------------------
+
+class Kept8(NamedTuple):
+    """A recurrence's inputs in 8 bits (``rec_fwd`` with ``keep``), for ``rec_bwd``; i and z
+    are None where the call has none."""
+    x: Packed8
+    g: Packed8
+    i: Optional[Packed8]
+    z: Optional[Packed8]
+
+
+def _rec_check(what, x, g, i, lam, z, h0, lengths, tokens: bool):
+    """Raises what is wrong with the inputs of a recurrence call (its fast test failed)."""
+    for name, t in (("x", x), ("g", g)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError(f"sscan.{what} needs CUDA (HIP) tensors")
+    if x.dtype not in _DT_CODE:
+        raise TypeError("x, g, i and z must be float32 or bfloat16")
+    if x.dim() != 2 + tokens:
+        raise ValueError("x is [batch, len, dim]" if tokens else "x is [batch, dim]")
+    for name, t in (("x", x), ("g", g), ("i", i), ("z", z)):
+        if t is not None:
+            _strided(t, name, dev, x.dtype, x.shape)
+
+
+def _rec_pack(what, x, g, i, lam, z, h0, lengths, c, reverse, tokens: bool = True):
+    """Checks the inputs of a recurrence call; (packed params, device, (b, L, d), dtype code)."""
+    try:
+        xs, dt, di = x.shape, x.dtype, x.get_device()
+        ok = (dt in _DT_CODE and di >= 0 and len(xs) == 2 + tokens)
+        addr, strides = [], []
+        for t in (x, g, i, z):
+            if t is None and (t is i or t is z):
+                addr.append(0)
+                strides += (0, 0)
+                continue
+            ts = t.stride()
+            ok = ok and t.shape == xs and t.dtype == dt and t.get_device() == di and (ts[-1] == 1 or xs[-1] <= 1)
+            addr.append(t.data_ptr())
+            strides += ts[:2] if tokens else (ts[0], 0)
+    except (AttributeError, IndexError):
+        _rec_check(what, x, g, i, lam, z, h0, lengths, tokens)  # says which of them is no tensor
+        raise
+    if not ok:
+        _rec_check(what, x, g, i, lam, z, h0, lengths, tokens)
+    dev = x.device
+    b, L, d = xs if tokens else (xs[0], 1, xs[1])
+    return _rec_params(dev, addr, strides, (b, L, d), lam, h0, lengths, c, reverse, _DT_CODE[dt]), dev, (b, L, d)
+
+
+def _rec_params(dev, addr, strides, sizes, lam, h0, lengths, c, reverse, code):
+    b, L, d = sizes
+    if lam is not None:
+        _check(lam, "lam", dev, torch.float32, (d,))
+    if h0 is not None:
+        _check(h0, "h0", dev, torch.float32, (b, d))
+    if lengths is not None:
+        _check(lengths, "lengths", dev, torch.int32, (b,))
+    return _REC.pack(*addr, 0 if lam is None else lam.data_ptr(), 0 if lengths is None else lengths.data_ptr(),
+                     0 if h0 is None else h0.data_ptr(), *strides, b, L, d, c, 1 if reverse else 0, code)
+
+
+def _kept_pack(kept: Kept8) -> bytes:
+    return _KEPT.pack(*(0 if p is None else p.q.data_ptr() for p in kept),
+                      *(0 if p is None else p.scale.data_ptr() for p in kept))
+
+
+def _kept_new(dev, sizes, given) -> Kept8:
+    """Room for the inputs that are given (four truth values) in 8 bits."""
+    b, L, d = sizes
+    n = sum(given)
+    parts = [Packed8(q, s) for q, s in zip(torch.empty((n, b, L, d), dtype=torch.int8, device=dev).unbind(0),
+                                           torch.empty((n, b, L, _pack_blocks(d)), device=dev).unbind(0))]
+    return Kept8(*(parts.pop(0) if has else None for has in given))
+
+
+def rec_workspace_bytes(batch: int, length: int, dim: int, io_dtype=torch.bfloat16, backward: bool = False) -> int:
+    lib = load_library()
+    f = lib.sscan_rec_bwd_workspace_bytes if backward else lib.sscan_rec_workspace_bytes
+    return int(f(batch, length, dim, _DT_CODE[io_dtype]))
+
+
+def rec_fwd(x, g, i: Optional[torch.Tensor] = None, lam: Optional[torch.Tensor] = None,
+            z: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+            lengths: Optional[torch.Tensor] = None, c: float = 8.0, reverse: bool = False, keep: bool = False,
+            out: Optional[torch.Tensor] = None, h_last: Optional[torch.Tensor] = None,
+            workspace: Optional[torch.Tensor] = None):
+    """The gated recurrence over whole sequences (``sscan_rec_fwd``), one state per channel:
+    h = a h + w sigmoid(i) x, out = h silu(z), with a = exp(-c softplus(lam) sigmoid(g)) and
+    w = sqrt(1 - a^2), or without ``lam`` a = exp(g) and w = 1.  x, g, i, z: [batch, len, dim]
+    f32/bf16, any strides with the last dimension contiguous (i and z optional); lam: [dim]
+    f32; h0: [batch, dim] f32; lengths: int32 [batch].  Returns (out, h_last); h_last may be
+    given as h0.  With ``keep`` also the inputs in 8 bits, for ``rec_bwd``."""
+    lib = load_library()
+    p, dev, sizes = _rec_pack("rec_fwd", x, g, i, lam, z, h0, lengths, c, reverse)
+    b, L, d = sizes
+    given = out, h_last
+    if out is None:
+        out = torch.empty((b, L, d), dtype=x.dtype, device=dev)
+    else:
+        _check(out, "out", dev, x.dtype, (b, L, d))
+    if h_last is None:
+        h_last = torch.empty((b, d), dtype=torch.float32, device=dev)
+    else:
+        _check(h_last, "h_last", dev, torch.float32, (b, d))
+    kept = _kept_new(dev, sizes, (True, True, i is not None, z is not None)) if keep else None
+    ws, ws_bytes = _workspace(lib.sscan_rec_workspace_bytes(b, L, d, _DT_CODE[x.dtype]), dev, workspace)
+    st = lib.sscan_rec_fwd(p, out.data_ptr(), h_last.data_ptr(), None if kept is None else _kept_pack(kept),
+                           _stream(dev), _ptr(ws), ws_bytes)
+    if st != 0:
+        raise SScanError(st, "sscan_rec_fwd")
+    _written(*given)
+    return (out, h_last, kept) if keep else (out, h_last)
+
+
+def rec_step(state, x, g, i: Optional[torch.Tensor] = None, lam: Optional[torch.Tensor] = None,
+             z: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None, c: float = 8.0,
+             out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token from a stored state (``sscan_rec_step``), updating ``state`` [batch, dim] f32
+    in place.  x, g, i, z: [batch, dim].  Rows of ``lengths`` 0 keep their state and answer 0.
+    Returns [batch, dim] in x's dtype."""
+    lib = load_library()
+    p, dev, (b, _, d) = _rec_pack("rec_step", x, g, i, lam, z, None, lengths, c, False, tokens=False)
+    if state is None:
+        raise ValueError("state is required")
+    _check(state, "state", dev, torch.float32, (b, d))
+    given = out
+    if out is None:
+        out = torch.empty((b, d), dtype=x.dtype, device=dev)
+    else:
+        _check(out, "out", dev, x.dtype, (b, d))
+    st = lib.sscan_rec_step(p, state.data_ptr(), out.data_ptr(), _stream(dev))
+    if st != 0:
+        raise SScanError(st, "sscan_rec_step")
+    _bump(state if given is None else [state, given])
+    return out
+
+
+def rec_bwd(x, g, dout, i=None, lam: Optional[torch.Tensor] = None, z=None, h0: Optional[torch.Tensor] = None,
+            dh_last: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None, c: float = 8.0,
+            reverse: bool = False, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Backward pass of ``rec_fwd`` (``sscan_rec_bwd``): the gradients of sum(dout * out) +
+    sum(dh_last * h_last) as {"dx", "dg", "di", "dz" (dout's dtype), "dlam", "dh0" (f32)},
+    None for an input that was not given (dh0 always); the states are recomputed.  x, g, i
+    and z may be what ``rec_fwd`` kept of them in 8 bits (``Packed8``, all of them): then the
+    gradients are those at the values that the 8 bits stand for."""
+    lib = load_library()
+    if isinstance(x, Packed8):
+        if not isinstance(x.q, torch.Tensor) or not isinstance(dout, torch.Tensor):
+            raise TypeError("x.q and dout must be torch.Tensors")
+        dev, sizes = x.q.device, tuple(x.q.shape)
+        if dev.type != "cuda":
+            raise ValueError("sscan.rec_bwd needs CUDA (HIP) tensors")
+        if len(sizes) != 3:
+            raise ValueError("x is [batch, len, dim]")
+        if dout.dtype not in _DT_CODE:
+            raise TypeError("dout must be float32 or bfloat16")
+        for name, t in (("x", x), ("g", g), ("i", i), ("z", z)):
+            if t is not None or name == "g":
+                _check_packed(t, name, dev, sizes)
+        p = _rec_params(dev, (0,) * 4, (0,) * 8, sizes, lam, h0, lengths, c, reverse, _DT_CODE[dout.dtype])
+        kept = _kept_pack(Kept8(x, g, i, z))
+    else:
+        p, dev, sizes = _rec_pack("rec_bwd", x, g, i, lam, z, h0, lengths, c, reverse)
+        kept = None
+    b, L, d = sizes
+    if dout is None:
+        raise ValueError("dout is required")
+    dt = getattr(dout if kept else x, "dtype", None)
+    _check(dout, "dout", dev, dt, sizes)
+    _check(dh_last, "dh_last", dev, torch.float32, (b, d))
+    r = {n: None if t is None else torch.empty(sizes, dtype=dt, device=dev)
+         for n, t in (("dx", x), ("dg", g), ("di", i), ("dz", z))}
+    r["dlam"] = None if lam is None else torch.empty(d, dtype=torch.float32, device=dev)
+    r["dh0"] = torch.empty((b, d), dtype=torch.float32, device=dev)
+    ws, ws_bytes = _workspace(lib.sscan_rec_bwd_workspace_bytes(b, L, d, _DT_CODE[dt]), dev, workspace)
+    grads = _REC_GRADS.pack(*(0 if r[n] is None else r[n].data_ptr() for n in ("dx", "dg", "di", "dz", "dlam", "dh0")))
+    st = lib.sscan_rec_bwd(p, kept, dout.data_ptr(), _ptr(dh_last), grads, _stream(dev), _ptr(ws), ws_bytes)
+    if st != 0:
+        raise SScanError(st, "sscan_rec_bwd")
+    return r
+
+
+class _RecFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, g, i, lam, z, h0, lengths, c, reverse, checkpoint):
+        ctx.c, ctx.reverse, ctx.checkpoint = c, reverse, checkpoint
+        ctx.set_materialize_grads(False)
+        if not checkpoint:
+            ctx.save_for_backward(x, g, i, z, lam, h0, lengths)
+            return rec_fwd(x, g, i, lam, z, h0, lengths, c, reverse)
+        out, h_last, kept = rec_fwd(x, g, i, lam, z, h0, lengths, c, reverse, keep=True)
+        ctx.dtype = x.dtype
+        flat = [t for p in kept for t in ((None, None) if p is None else p)]
+        ctx.save_for_backward(*flat, lam, h0, lengths)
+        return out, h_last
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, dout, dh_last):
+        if ctx.checkpoint:
+            *flat, lam, h0, lengths = ctx.saved_tensors
+            x, g, i, z = (None if q is None else Packed8(q, s) for q, s in zip(flat[::2], flat[1::2]))
+            like, dt = x.q, ctx.dtype
+        else:
+            x, g, i, z, lam, h0, lengths = ctx.saved_tensors
+            like, dt = x, x.dtype
+        dout = torch.zeros(like.shape, dtype=dt, device=like.device) if dout is None else dout.contiguous()
+        r = rec_bwd(x, g, dout, i, lam, z, h0, None if dh_last is None else dh_last.contiguous(), lengths, ctx.c,
+                    ctx.reverse)
+        return (r["dx"], r["dg"], r["di"], r["dlam"], r["dz"], None if h0 is None else r["dh0"], None, None, None, None)
+
+
+def gated_recurrence(x, g, i: Optional[torch.Tensor] = None, lam: Optional[torch.Tensor] = None,
+                     z: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+                     lengths: Optional[torch.Tensor] = None, c: float = 8.0, reverse: bool = False,
+                     checkpoint: bool = False):
+    """``rec_fwd`` with gradients in x, g, i, lam, z and h0 (``sscan_rec_bwd`` in the backward
+    pass; no second derivatives).  With ``checkpoint`` the backward pass keeps x, g, i and z
+    in 8 bits instead of the tensors themselves (half the memory of bfloat16): gradients are
+    those at the kept values, outputs are as without, and a backward pass with
+    ``create_graph`` raises.  Returns (out, h_last)."""
+    return _RecFn.apply(x, g, i, lam, z, h0, lengths, c, reverse, checkpoint)
+
+
+# ---- layer norm -------------------------------------------------------------------
+
+def _layer_pack(what, x, x_name, residual, residual_dtype, io_dtype, weight, bias, eps):
+    """(packed params, device, (rows, size))"""
+    for name, t in ((x_name, x), ("residual", residual), ("weight", weight), ("bias", bias)):
+        if not isinstance(t, torch.Tensor) and (t is not None or name == x_name):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    dev, xs = x.device, x.shape
+    if dev.type != "cuda":
+        raise ValueError(f"sscan.{what} needs CUDA (HIP) tensors")
+    if x.dtype not in _DT_CODE or residual_dtype not in _DT_CODE or io_dtype not in _DT_CODE:
+        raise TypeError("x and the residual must be float32 or bfloat16")
+    if not xs:
+        raise ValueError(f"{x_name} needs at least one dimension")
+    size = xs[-1]
+    if x.is_contiguous():
+        stride = size
+    else:
+        _strided(x, x_name, dev, x.dtype, xs)
+        stride = _row_stride(xs, x.stride(), len(xs) - 1) if len(xs) > 1 else 0
+        if stride is None:
+            raise ValueError(f"the leading dimensions of {x_name} must collapse to rows of one stride")
+    if residual is not None:
+        _check(residual, "residual", dev, residual_dtype, xs)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _check(t, name, dev, torch.float32, (size,))
+    addr = [0 if t is None else t.data_ptr() for t in (x, residual, weight, bias)]
+    rows = x.numel() // size if size else 0
+    return _LAYER.pack(*addr, stride, rows, size, eps, _DT_CODE[io_dtype], _DT_CODE[residual_dtype]), dev, (rows, size)
+
+
+def layer_norm(x, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, eps: float = 1e-5, residual_dtype=None,
+               out: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None):
+    """Layer norm over the last dimension, of x or of the residual sum (``sscan_layer_norm``):
+    total = residual + x, out = (total - mean) / sqrt(var + eps) * weight + bias.  x: [...,
+    size] f32/bf16, rows of one stride; residual: f32/bf16 of the same shape, contiguous;
+    weight, bias: [size] f32 or None.  Returns (out, total).  Without a residual total is x
+    itself, unless ``residual_dtype`` (or ``residual_out``) asks for it as a residual stream's
+    first entry; ``residual_out`` may be ``residual`` itself."""
+    lib = load_library()
+    stored = residual is not None or residual_dtype is not None or residual_out is not None
+    if residual_dtype is None:
+        residual_dtype = getattr(x if residual is None else residual, "dtype", None)
+    p, dev, _ = _layer_pack("layer_norm", x, "x", residual, residual_dtype, getattr(x, "dtype", None), weight, bias, eps)
+    given = out, residual_out
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _check(out, "out", dev, x.dtype, x.shape)
+    total = residual_out
+    if total is not None:
+        _check(total, "residual_out", dev, residual_dtype, x.shape)
+    elif stored:
+        total = torch.empty(x.shape, dtype=residual_dtype, device=dev)
+    st = lib.sscan_layer_norm(p, out.data_ptr(), 0 if total is None else total.data_ptr(), _stream(dev))
+    if st != 0:
+        raise SScanError(st, "sscan_layer_norm")
+    _written(*given)
+    return out, x if total is None else total
+
+
+def layer_norm_bwd(total, dout, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                   dtotal: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                   workspace: Optional[torch.Tensor] = None) -> dict:
+    """Backward pass of ``layer_norm`` (``sscan_layer_norm_bwd``) from the total it returned
+    and the gradients of both its outputs: {"dx" (dout's dtype), "dresidual" (total's dtype;
+    dx itself where the types agree), "dweight", "dbias" (f32, None for one that was not
+    given)}."""
+    lib = load_library()
+    io = getattr(dout, "dtype", None)
+    if not isinstance(dout, torch.Tensor):
+        raise TypeError("dout must be a torch.Tensor")
+    p, dev, sizes = _layer_pack("layer_norm_bwd", total, "total", None, getattr(total, "dtype", None), io, weight, bias,
+                                eps)
+    _check(dout, "dout", dev, io, total.shape)
+    _check(dtotal, "dtotal", dev, total.dtype, total.shape)
+    dx = torch.empty(total.shape, dtype=io, device=dev)
+    dres = dx if total.dtype == io else torch.empty(total.shape, dtype=total.dtype, device=dev)
+    dw, db = (None if t is None else torch.empty_like(t) for t in (weight, bias))
+    ws, ws_bytes = _workspace(lib.sscan_layer_norm_bwd_workspace_bytes(*sizes), dev, workspace)
+    st = lib.sscan_layer_norm_bwd(p, _ptr(dout), _ptr(dtotal), _ptr(dx), None if dres is dx else _ptr(dres), _ptr(dw),
+                                  _ptr(db), _stream(dev), _ptr(ws), ws_bytes)
+    if st != 0:
+        raise SScanError(st, "sscan_layer_norm_bwd")
+    return dict(dx=dx, dresidual=dres, dweight=dw, dbias=db)
+
+
+class _LayerNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, bias, eps, residual_dtype):
+        out, total = layer_norm(x, weight, bias, residual, eps, residual_dtype)
+        ctx.save_for_backward(total, weight, bias)
+        ctx.eps, ctx.has_residual, ctx.dtype = eps, residual is not None, x.dtype
+        ctx.set_materialize_grads(False)
+        return out, total
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, dout, dtotal):
+        total, weight, bias = ctx.saved_tensors
+        dout = torch.zeros(total.shape, dtype=ctx.dtype, device=total.device) if dout is None else dout.contiguous()
+        r = layer_norm_bwd(total, dout, weight, bias, None if dtotal is None else dtotal.contiguous(), ctx.eps)
+        return r["dx"], r["dresidual"] if ctx.has_residual else None, r["dweight"], r["dbias"], None, None
+
+
+def add_layer_norm(x, residual: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                   bias: Optional[torch.Tensor] = None, eps: float = 1e-5, residual_dtype=None):
+    """``layer_norm`` with gradients in x, residual, weight and bias (no second derivatives).
+    Returns (out, total)."""
+    return _LayerNormFn.apply(x, residual, weight, bias, eps, residual_dtype)
