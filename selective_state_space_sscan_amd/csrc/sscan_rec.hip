@@ -1,66 +1,267 @@
-// sscan_rec.hip -- the gated recurrence over whole sequences and for single tokens: one
-// lane a channel, which walks its row token by token.
-#include "sscan_rec_device.h"
+// sscan_rec.hip -- the gated recurrence over whole sequences and for single tokens.
+#include <type_traits>
+
+#include "sscan_rec_tile.h"
 
 namespace sscan {
 namespace rec {
 
-struct RowWalk {  // the tokens of a row in the order of the scan
-  int64_t n, first, step;
-  __device__ __forceinline__ RowWalk(const RecArgs& a, int64_t b) {
-    n = a.len;
-    if (a.lengths) n = a.lengths[b] < 0 ? 0 : a.lengths[b] < a.len ? a.lengths[b] : a.len;
-    first = a.reverse ? n - 1 : 0;
-    step = a.reverse ? -1 : 1;
+// One segment a block (sscan_rec_tile.h).  A lane first turns its tokens into decays and
+// inputs, which it holds in registers with their map; the waves' maps meet in LDS, wave 0
+// finds the state that enters the segment (from the row's segments before, where there are
+// any) and from it those that enter the waves, and every wave walks its tokens once more,
+// now from its state, and answers.  SPLIT: rows have several segments.  OUT: outputs are
+// wanted, not the states between segments alone.
+template <typename IO, int C, int T, bool GATED, bool IGATE, bool ZGATE, bool SPLIT, bool OUT>
+__global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
+  typedef typename Vec<IO, C>::V V;
+  extern __shared__ float lds[];     // [waves][2][64 C]: A and H; then the waves' entry states in A's place
+  __shared__ unsigned number;
+  const RecArgs& a = p.a;
+  const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  const int waves = int(blockDim.x) >> 6;
+  unsigned unit = blockIdx.x;
+  if (SPLIT) {
+    if (threadIdx.x == 0) number = atomicAdd(p.ticket, 1u);
+    __syncthreads();
+    unit = __builtin_amdgcn_readfirstlane(number);
   }
+  const unsigned rows = unsigned(a.batch) * p.groups;  // below 2^32 / 256, as all of them
+  const int seg = SPLIT ? int(unit / rows) : 0;
+  const int64_t b = unit % rows / p.groups, group = unit % p.groups;
+  const int64_t ch = (group * 64 + lane) * C;
+  const bool on = ch < a.dim;
+  const int64_t at = on ? ch : 0;    // lanes beyond the last channel read the first ones
+  const Span span(a, b, (int64_t(seg) * waves + wave) * T, T);
+
+  float rate[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) rate[c] = GATED ? decay_rate(a.lam, at + c, a.c) : 0.0f;
+
+  const auto load = [&](const RecIn& in, V (&v)[T]) {
+    const IO* row = static_cast<const IO*>(in.p) + b * in.b;
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+      v[j] = *reinterpret_cast<const V*>(row + span.place(j < span.live ? j : span.live - 1) * in.t + at);
+  };
+  float A[T][C], U[T][C];
+  V z[T];
+  if (span.live > 0) {
+    V x[T], g[T], i[T];
+    load(a.x, x);
+    load(a.g, g);
+    if (IGATE) load(a.i, i);
+    if (OUT && ZGATE) load(a.z, z);
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const Decay d = decay<GATED>(part<V, C>(g[j], c), rate[c]);
+        float u = part<V, C>(x[j], c) * d.w;
+        if (IGATE) u *= sigmoid(part<V, C>(i[j], c));
+        const bool live = j < span.live;
+        A[j][c] = live ? d.a : 1.0f;
+        U[j][c] = live ? u : 0.0f;
+      }
+  } else {
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        A[j][c] = 1.0f;
+        U[j][c] = 0.0f;
+      }
+  }
+  float* mine = lds + wave * (2 * 64 * C) + lane;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float P = A[0][c], H = U[0][c];
+#pragma unroll
+    for (int j = 1; j < T; ++j) {
+      P *= A[j][c];
+      H = fmaf(A[j][c], H, U[j][c]);
+    }
+    mine[c * 64] = P;
+    mine[(C + c) * 64] = H;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    const int64_t pitch = int64_t(rows) * (64 * C), place = (b * p.groups + group) * (64 * C) + lane * C;
+    const bool ends_run = SPLIT && seg % kRun == kRun - 1;
+    float h[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) h[c] = a.h0 ? a.h0[b * a.dim + at + c] : 0.0f;
+    if (SPLIT) {
+      if (!ends_run) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          float P = 1.0f, H = 0.0f;
+          for (int v = 0; v < waves; ++v) {
+            const float w = lds[v * (2 * 64 * C) + c * 64 + lane];
+            P *= w;
+            H = fmaf(w, H, lds[v * (2 * 64 * C) + (C + c) * 64 + lane]);
+          }
+          publish(p.maps + seg * pitch + place + c, map_bits(P), H);
+        }
+      }
+      enter<C>(p.maps + place, p.states + place, pitch, seg, h);
+    }
+    for (int v = 0; v < waves; ++v)
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float* w = lds + v * (2 * 64 * C) + c * 64 + lane;
+        const float P = *w;
+        *w = h[c];
+        h[c] = fmaf(P, h[c], w[C * 64]);
+      }
+    if (ends_run) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) publish(p.states + int64_t(seg / kRun) * pitch + place + c, 0, h[c]);
+    }
+    if (OUT && seg == p.nseg - 1 && on) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) a.h_last[b * a.dim + ch + c] = h[c];
+    }
+  }
+  if (!OUT) return;
+  __syncthreads();
+  float h[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) h[c] = mine[c * 64];
+  IO* out = static_cast<IO*>(a.out) + b * a.len * a.dim + ch;
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+    float y[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      h[c] = fmaf(A[j][c], h[c], U[j][c]);
+      y[c] = h[c];
+      if (ZGATE) {
+        const float q = part<V, C>(z[j], c);
+        y[c] *= q * sigmoid(q);
+      }
+      if (j >= span.live) y[c] = 0.0f;
+    }
+    if (on && span.k0 + j < a.len) *reinterpret_cast<V*>(out + span.place(j) * a.dim) = packed<IO, C>(y);
+  }
+}
+
+// One token from a stored state.
+template <typename IO, int C, bool GATED>
+__global__ __launch_bounds__(64) void step_kernel(RecArgs a) {
+  typedef typename Vec<IO, C>::V V;
+  const unsigned groups = unsigned((a.dim + 64 * C - 1) / (64 * C));
+  const int64_t ch = (int64_t(blockIdx.x % groups) * 64 + threadIdx.x) * C, b = blockIdx.x / groups;
+  if (ch >= a.dim) return;
+  const auto load = [&](const RecIn& in) {
+    return *reinterpret_cast<const V*>(static_cast<const IO*>(in.p) + b * in.b + ch);
+  };
+  float* state = a.h_last + b * a.dim + ch;
+  const bool live = !a.lengths || a.lengths[b] > 0;
+  float y[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) y[c] = 0.0f;
+  if (live) {
+    const V x = load(a.x), g = load(a.g), i = a.i.p ? load(a.i) : V{}, z = a.z.p ? load(a.z) : V{};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const Decay d = decay<GATED>(part<V, C>(g, c), GATED ? decay_rate(a.lam, ch + c, a.c) : 0.0f);
+      float u = part<V, C>(x, c) * d.w;
+      if (a.i.p) u *= sigmoid(part<V, C>(i, c));
+      y[c] = fmaf(d.a, state[c], u);
+      state[c] = y[c];
+      if (a.z.p) {
+        const float q = part<V, C>(z, c);
+        y[c] *= q * sigmoid(q);
+      }
+    }
+  }
+  *reinterpret_cast<V*>(static_cast<IO*>(a.out) + b * a.dim + ch) = packed<IO, C>(y);
+}
+
+// The state handed through where there are no tokens.
+__global__ __launch_bounds__(256) void pass_kernel(const float* from, float* to, int64_t n) {
+  const int64_t k = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (k < n) to[k] = from ? from[k] : 0.0f;
+}
+
+constexpr int kT = 16;               // tokens of a wave's tile
+constexpr int kWaves = 8;            // of a block where rows have several segments
+
+int channels_of(int64_t dim) { return dim % 2 == 0 ? 2 : 1; }
+
+struct Plan {
+  int c, waves;
+  int64_t groups, nseg, words;       // bytes of the maps and states
 };
 
-template <typename IO>
-__device__ __forceinline__ float at(const RecIn& in, int64_t b, int64_t t, int64_t ch) {
-  return float(static_cast<const IO*>(in.p)[b * in.b + t * in.t + ch]);
+Plan plan_of(int64_t batch, int64_t len, int64_t dim) {
+  Plan p;
+  p.c = channels_of(dim);
+  p.groups = up(dim, 64 * p.c);
+  const int64_t tiles = up(len, kT);
+  p.waves = tiles <= kMaxWaves ? int(tiles) : kWaves;
+  p.nseg = tiles <= kMaxWaves ? 1 : up(tiles, p.waves);
+  p.words = p.nseg > 1 ? (p.nseg + p.nseg / kRun) * batch * p.groups * 64 * p.c * 8 : 0;
+  return p;
 }
 
-template <typename IO, bool GATED>
-__global__ __launch_bounds__(64) void fwd_kernel(RecArgs a) {
-  const int64_t ch = int64_t(blockIdx.x) * 64 + threadIdx.x, b = blockIdx.y;
-  if (ch >= a.dim) return;
-  const RowWalk row(a, b);
-  const float rate = GATED ? decay_rate(a.lam, ch, a.c) : 0.0f;
-  float h = a.h0 ? a.h0[b * a.dim + ch] : 0.0f;
-  IO* out = static_cast<IO*>(a.out) + b * a.len * a.dim + ch;
-  for (int64_t k = 0; k < row.n; ++k) {
-    const int64_t t = row.first + k * row.step;
-    const Decay d = decay<GATED>(at<IO>(a.g, b, t, ch), rate);
-    float u = at<IO>(a.x, b, t, ch) * d.w;
-    if (a.i.p) u *= sigmoid(at<IO>(a.i, b, t, ch));
-    h = fmaf(d.a, h, u);
-    float y = h;
-    if (a.z.p) {
-      const float z = at<IO>(a.z, b, t, ch);
-      y *= z * sigmoid(z);
-    }
-    out[t * a.dim] = IO(y);
-  }
-  for (int64_t t = row.n; t < a.len; ++t) out[t * a.dim] = IO(0.0f);
-  a.h_last[b * a.dim + ch] = h;
-}
-
-template <typename IO>
-hipError_t fwd(const RecArgs& a, hipStream_t stream) {
-  const dim3 grid(unsigned((a.dim + 63) / 64), unsigned(a.batch));
-  if (a.lam)
-    fwd_kernel<IO, true><<<grid, 64, 0, stream>>>(a);
+template <typename F>
+void by_flag(bool v, F f) {
+  if (v)
+    f(std::true_type());
   else
-    fwd_kernel<IO, false><<<grid, 64, 0, stream>>>(a);
+    f(std::false_type());
+}
+
+template <typename IO, int C>
+hipError_t fwd(const RecArgs& a, const Plan& plan, char* workspace, hipStream_t stream) {
+  uint64_t* words = reinterpret_cast<uint64_t*>(workspace + 256);
+  const TileArgs p{a, words, words + plan.nseg * a.batch * plan.groups * 64 * C, reinterpret_cast<unsigned*>(workspace),
+                   int(plan.nseg), unsigned(plan.groups)};
+  const dim3 grid(unsigned(plan.nseg * a.batch * plan.groups)), block(unsigned(plan.waves * 64));
+  const size_t lds = size_t(plan.waves) * 2 * 64 * C * 4;
+  if (plan.nseg > 1) {
+    const int64_t n = plan.words / 16, blocks = up(n, 256 * 4);
+    clear_kernel<<<dim3(unsigned(blocks < 2048 ? blocks : 2048)), 256, 0, stream>>>(reinterpret_cast<uint4*>(words), n, p.ticket);
+  }
+  by_flag(a.lam != nullptr, [&](auto gated) {
+    by_flag(a.i.p != nullptr, [&](auto igate) {
+      by_flag(a.z.p != nullptr, [&](auto zgate) {
+        by_flag(plan.nseg > 1, [&](auto split) {
+          fwd_kernel<IO, C, kT, decltype(gated)::value, decltype(igate)::value, decltype(zgate)::value,
+                     decltype(split)::value, true><<<grid, block, lds, stream>>>(p);
+        });
+      });
+    });
+  });
+  return hipGetLastError();
+}
+
+template <typename IO, int C>
+hipError_t step(const RecArgs& a, hipStream_t stream) {
+  const dim3 grid(unsigned(up(a.dim, 64 * C) * a.batch));
+  if (a.lam)
+    step_kernel<IO, C, true><<<grid, 64, 0, stream>>>(a);
+  else
+    step_kernel<IO, C, false><<<grid, 64, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace rec
 
-size_t rec_workspace(int64_t, int64_t, int64_t, bool) { return 0; }
+size_t rec_workspace(int64_t batch, int64_t len, int64_t dim, bool) {
+  const rec::Plan p = rec::plan_of(batch, len, dim);
+  return p.nseg > 1 ? size_t(p.words) + 256 : 0;
+}
 
-hipError_t launch_rec_fwd(const RecArgs& a, char*, hipStream_t stream) {
-  if (a.kept.x && a.len > 0) {
+hipError_t launch_rec_fwd(const RecArgs& a, char* workspace, hipStream_t stream) {
+  if (a.len == 0) {
+    const int64_t n = a.batch * a.dim;
+    rec::pass_kernel<<<dim3(unsigned(rec::up(n, 256))), 256, 0, stream>>>(a.h0, a.h_last, n);
+    return hipGetLastError();
+  }
+  if (a.kept.x) {
     const RecIn in[4] = {a.x, a.g, a.i, a.z};
     int8_t* q[4] = {a.kept.x, a.kept.g, a.kept.i, a.kept.z};
     float* s[4] = {a.kept.xs, a.kept.gs, a.kept.is, a.kept.zs};
@@ -71,9 +272,16 @@ hipError_t launch_rec_fwd(const RecArgs& a, char*, hipStream_t stream) {
       if (e != hipSuccess) return e;
     }
   }
-  return a.io_bf16 ? rec::fwd<rec::bf16>(a, stream) : rec::fwd<float>(a, stream);
+  const rec::Plan p = rec::plan_of(a.batch, a.len, a.dim);
+  if (a.io_bf16)
+    return p.c == 2 ? rec::fwd<rec::bf16, 2>(a, p, workspace, stream) : rec::fwd<rec::bf16, 1>(a, p, workspace, stream);
+  return p.c == 2 ? rec::fwd<float, 2>(a, p, workspace, stream) : rec::fwd<float, 1>(a, p, workspace, stream);
 }
 
-hipError_t launch_rec_step(const RecArgs& a, hipStream_t stream) { return launch_rec_fwd(a, nullptr, stream); }
+hipError_t launch_rec_step(const RecArgs& a, hipStream_t stream) {
+  const int c = rec::channels_of(a.dim);
+  if (a.io_bf16) return c == 2 ? rec::step<rec::bf16, 2>(a, stream) : rec::step<rec::bf16, 1>(a, stream);
+  return c == 2 ? rec::step<float, 2>(a, stream) : rec::step<float, 1>(a, stream);
+}
 
 }  // namespace sscan

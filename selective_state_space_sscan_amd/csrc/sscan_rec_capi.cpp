@@ -14,7 +14,7 @@ namespace {
 
 using namespace sscan::check;
 
-constexpr int64_t kMaxLen = int64_t(1) << 30, kMaxDim = int64_t(1) << 24, kMaxTiles = int64_t(1) << 24;
+constexpr int64_t kMaxLen = int64_t(1) << 30, kMaxDim = int64_t(1) << 24, kMaxTiles = int64_t(1) << 22;
 
 int64_t blocks_of(int64_t size) { return (size + sscan::kPackBlock - 1) / sscan::kPackBlock; }
 

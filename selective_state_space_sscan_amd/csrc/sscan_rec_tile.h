@@ -1,0 +1,159 @@
+// sscan_rec_tile.h -- how the recurrence's kernels cut a call into tiles, and how the tiles
+// of a row hand the state on.
+//
+// A wave holds T tokens of 64 C consecutive channels, C of them a lane, and a block's waves
+// hold consecutive tokens: a segment of a row.  A segment maps its entry state to its exit
+// state by h -> A h + H, A the product of its decays and H its exit state from zero.  Where a
+// row has several segments they run at once, and inputs are read once: a segment's block
+// publishes its map as soon as it has one, joins the maps of the segments before it in its
+// run of kRun segments, and applies them to the state that enters the run, which the last
+// segment of the run before publishes.  So a chain over the row has a link for each run
+// only, and every state is computed in one order, whatever the order of arrival.
+//
+// The waits for other blocks have to end whatever the order in which blocks start: a block
+// takes the number of its segment from a counter when it starts, the first segments of all
+// rows first.  Those it waits for have lower numbers, so their blocks run already, and the
+// lowest of them waits for nobody.
+//
+// Maps and states are words of 64 bits, written and read whole (no fence orders them against
+// anything else): the upper half is A's bits, never kEmpty's, the lower half H's or the
+// state's.  A small kernel empties them before.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "sscan_rec_device.h"
+
+namespace sscan {
+namespace rec {
+
+constexpr uint32_t kEmpty = 0xffffffffu;
+constexpr int kRun = 16;             // segments of a run
+constexpr int kMaxWaves = 16;        // of a block
+
+struct TileArgs {
+  RecArgs a;
+  uint64_t* maps;                    // [nseg][batch][groups * 64 C]
+  uint64_t* states;                  // [runs][batch][groups * 64 C]: the state that leaves a run
+  unsigned* ticket;                  // segments handed out
+  int nseg;
+  unsigned groups;                   // of 64 C channels
+};
+
+__device__ __forceinline__ void publish(uint64_t* at, uint32_t hi, float lo) {
+  const uint64_t w = uint64_t(hi) << 32 | __float_as_uint(lo);
+  __hip_atomic_store(at, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ uint32_t map_bits(float a) {
+  const uint32_t u = __float_as_uint(a);
+  return u == kEmpty ? 0x7fc00000u : u;
+}
+
+// Reads n words `pitch` apart, C a lane, in order, as soon as they are there: f(k, c, A, H)
+// for each.  All lanes of a wave go on together; four places are read at once.  A wait of
+// 2^24 reads is many seconds long and cannot happen; it ends, with NaN, instead of never.
+template <int C, typename F>
+__device__ __forceinline__ void read_words(const uint64_t* at, int64_t pitch, int n, F f) {
+  constexpr int kAhead = 4;
+  int done = 0;
+  for (int tries = 0; done < n; ++tries) {
+    uint64_t w[kAhead][C];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        w[k][c] = __hip_atomic_load(at + (done + k < n ? done + k : n - 1) * pitch + c, __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT);
+    const int first = done;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      bool ready = true;
+#pragma unroll
+      for (int c = 0; c < C; ++c) ready = ready && uint32_t(w[k][c] >> 32) != kEmpty;
+      if (done == first + k && done < n && (!__ballot(!ready) || tries > (1 << 24))) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) f(c, __uint_as_float(uint32_t(w[k][c] >> 32)), __uint_as_float(uint32_t(w[k][c])));
+        ++done;
+      }
+    }
+  }
+}
+
+// The state that enters segment `seg`: h holds the row's entry state, and the lane's words
+// lie `pitch` apart from segment to segment (of the maps) and from run to run (of the states).
+template <int C>
+__device__ __forceinline__ void enter(const uint64_t* maps, const uint64_t* states, int64_t pitch, int seg, float (&h)[C]) {
+  const int run = seg / kRun, inside = seg % kRun;
+  float A[C], H[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    A[c] = 1.0f;
+    H[c] = 0.0f;
+  }
+  read_words<C>(maps + int64_t(run) * kRun * pitch, pitch, inside, [&](int c, float a, float b) {
+    A[c] *= a;
+    H[c] = fmaf(a, H[c], b);
+  });
+  if (run > 0) read_words<C>(states + int64_t(run - 1) * pitch, pitch, 1, [&](int c, float, float b) { h[c] = b; });
+#pragma unroll
+  for (int c = 0; c < C; ++c) h[c] = fmaf(A[c], h[c], H[c]);
+}
+
+// Empties the words and sets the counter to 0.
+__global__ __launch_bounds__(256) static void clear_kernel(uint4* words, int64_t n, unsigned* ticket) {
+  for (int64_t k = int64_t(blockIdx.x) * 256 + threadIdx.x; k < n; k += int64_t(gridDim.x) * 256)
+    words[k] = uint4{kEmpty, kEmpty, kEmpty, kEmpty};
+  if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
+}
+
+template <typename IO, int C>
+struct Vec {
+  typedef IO V __attribute__((ext_vector_type(C), aligned(sizeof(IO))));
+};
+template <typename IO>
+struct Vec<IO, 1> {
+  typedef IO V;
+};
+
+template <typename V, int C>
+__device__ __forceinline__ float part(const V& v, int c) {
+  if constexpr (C == 1)
+    return float(v);
+  else
+    return float(v[c]);
+}
+
+template <typename IO, int C>
+__device__ __forceinline__ typename Vec<IO, C>::V packed(const float (&x)[C]) {
+  typename Vec<IO, C>::V v;
+  if constexpr (C == 1) {
+    v = IO(x[0]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c) v[c] = IO(x[c]);
+  }
+  return v;
+}
+
+// The tokens of a wave's tile in the order of the scan, and where a row's tokens lie.
+struct Span {
+  int64_t n, rev, k0;                // tokens of the row, whether it is scanned backwards, the tile's first token
+  int live;                          // tokens of the tile that the row has
+  __device__ __forceinline__ Span(const RecArgs& a, int64_t b, int64_t first, int tokens) : k0(first) {
+    n = a.len;
+    if (a.lengths) n = a.lengths[b] < 0 ? 0 : a.lengths[b] < a.len ? a.lengths[b] : a.len;
+    rev = a.reverse;
+    const int64_t left = n - first;
+    live = left <= 0 ? 0 : left < tokens ? int(left) : tokens;
+  }
+  // where token j of the tile lies; past the row's end, tokens are in their places
+  __device__ __forceinline__ int64_t place(int j) const { return rev && k0 + j < n ? n - 1 - (k0 + j) : k0 + j; }
+};
+
+inline int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace rec
+}  // namespace sscan
