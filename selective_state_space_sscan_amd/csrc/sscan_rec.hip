@@ -1,150 +1,8 @@
 // sscan_rec.hip -- the gated recurrence over whole sequences and for single tokens.
-#include <type_traits>
-
-#include "sscan_rec_tile.h"
+#include "sscan_rec_fwd.h"
 
 namespace sscan {
 namespace rec {
-
-// One segment a block (sscan_rec_tile.h).  A lane first turns its tokens into decays and
-// inputs, which it holds in registers with their map; the waves' maps meet in LDS, wave 0
-// finds the state that enters the segment (from the row's segments before, where there are
-// any) and from it those that enter the waves, and every wave walks its tokens once more,
-// now from its state, and answers.  SPLIT: rows have several segments.  OUT: outputs are
-// wanted, not the states between segments alone.
-template <typename IO, int C, int T, bool GATED, bool IGATE, bool ZGATE, bool SPLIT, bool OUT>
-__global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
-  typedef typename Vec<IO, C>::V V;
-  extern __shared__ float lds[];     // [waves][2][64 C]: A and H; then the waves' entry states in A's place
-  __shared__ unsigned number;
-  const RecArgs& a = p.a;
-  const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-  const int waves = int(blockDim.x) >> 6;
-  unsigned unit = blockIdx.x;
-  if (SPLIT) {
-    if (threadIdx.x == 0) number = atomicAdd(p.ticket, 1u);
-    __syncthreads();
-    unit = __builtin_amdgcn_readfirstlane(number);
-  }
-  const unsigned rows = unsigned(a.batch) * p.groups;  // below 2^32 / 256, as all of them
-  const int seg = SPLIT ? int(unit / rows) : 0;
-  const int64_t b = unit % rows / p.groups, group = unit % p.groups;
-  const int64_t ch = (group * 64 + lane) * C;
-  const bool on = ch < a.dim;
-  const int64_t at = on ? ch : 0;    // lanes beyond the last channel read the first ones
-  const Span span(a, b, (int64_t(seg) * waves + wave) * T, T);
-
-  float rate[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) rate[c] = GATED ? decay_rate(a.lam, at + c, a.c) : 0.0f;
-
-  const auto load = [&](const RecIn& in, V (&v)[T]) {
-    const IO* row = static_cast<const IO*>(in.p) + b * in.b;
-#pragma unroll
-    for (int j = 0; j < T; ++j)
-      v[j] = *reinterpret_cast<const V*>(row + span.place(j < span.live ? j : span.live - 1) * in.t + at);
-  };
-  float A[T][C], U[T][C];
-  V z[T];
-  if (span.live > 0) {
-    V x[T], g[T], i[T];
-    load(a.x, x);
-    load(a.g, g);
-    if (IGATE) load(a.i, i);
-    if (OUT && ZGATE) load(a.z, z);
-#pragma unroll
-    for (int j = 0; j < T; ++j)
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const Decay d = decay<GATED>(part<V, C>(g[j], c), rate[c]);
-        float u = part<V, C>(x[j], c) * d.w;
-        if (IGATE) u *= sigmoid(part<V, C>(i[j], c));
-        const bool live = j < span.live;
-        A[j][c] = live ? d.a : 1.0f;
-        U[j][c] = live ? u : 0.0f;
-      }
-  } else {
-#pragma unroll
-    for (int j = 0; j < T; ++j)
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        A[j][c] = 1.0f;
-        U[j][c] = 0.0f;
-      }
-  }
-  float* mine = lds + wave * (2 * 64 * C) + lane;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    float P = A[0][c], H = U[0][c];
-#pragma unroll
-    for (int j = 1; j < T; ++j) {
-      P *= A[j][c];
-      H = fmaf(A[j][c], H, U[j][c]);
-    }
-    mine[c * 64] = P;
-    mine[(C + c) * 64] = H;
-  }
-  __syncthreads();
-  if (wave == 0) {
-    const int64_t pitch = int64_t(rows) * (64 * C), place = (b * p.groups + group) * (64 * C) + lane * C;
-    const bool ends_run = SPLIT && seg % kRun == kRun - 1;
-    float h[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) h[c] = a.h0 ? a.h0[b * a.dim + at + c] : 0.0f;
-    if (SPLIT) {
-      if (!ends_run) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          float P = 1.0f, H = 0.0f;
-          for (int v = 0; v < waves; ++v) {
-            const float w = lds[v * (2 * 64 * C) + c * 64 + lane];
-            P *= w;
-            H = fmaf(w, H, lds[v * (2 * 64 * C) + (C + c) * 64 + lane]);
-          }
-          publish(p.maps + seg * pitch + place + c, map_bits(P), H);
-        }
-      }
-      enter<C>(p.maps + place, p.states + place, pitch, seg, h);
-    }
-    for (int v = 0; v < waves; ++v)
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        float* w = lds + v * (2 * 64 * C) + c * 64 + lane;
-        const float P = *w;
-        *w = h[c];
-        h[c] = fmaf(P, h[c], w[C * 64]);
-      }
-    if (ends_run) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) publish(p.states + int64_t(seg / kRun) * pitch + place + c, 0, h[c]);
-    }
-    if (OUT && seg == p.nseg - 1 && on) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) a.h_last[b * a.dim + ch + c] = h[c];
-    }
-  }
-  if (!OUT) return;
-  __syncthreads();
-  float h[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) h[c] = mine[c * 64];
-  IO* out = static_cast<IO*>(a.out) + b * a.len * a.dim + ch;
-#pragma unroll
-  for (int j = 0; j < T; ++j) {
-    float y[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      h[c] = fmaf(A[j][c], h[c], U[j][c]);
-      y[c] = h[c];
-      if (ZGATE) {
-        const float q = part<V, C>(z[j], c);
-        y[c] *= q * sigmoid(q);
-      }
-      if (j >= span.live) y[c] = 0.0f;
-    }
-    if (on && span.k0 + j < a.len) *reinterpret_cast<V*>(out + span.place(j) * a.dim) = packed<IO, C>(y);
-  }
-}
 
 // One token from a stored state.
 template <typename IO, int C, bool GATED>
@@ -206,19 +64,11 @@ Plan plan_of(int64_t batch, int64_t len, int64_t dim) {
   return p;
 }
 
-template <typename F>
-void by_flag(bool v, F f) {
-  if (v)
-    f(std::true_type());
-  else
-    f(std::false_type());
-}
-
 template <typename IO, int C>
 hipError_t fwd(const RecArgs& a, const Plan& plan, char* workspace, hipStream_t stream) {
   uint64_t* words = reinterpret_cast<uint64_t*>(workspace + 256);
   const TileArgs p{a, words, words + plan.nseg * a.batch * plan.groups * 64 * C, reinterpret_cast<unsigned*>(workspace),
-                   int(plan.nseg), unsigned(plan.groups)};
+                   nullptr, int(plan.nseg), unsigned(plan.groups)};
   const dim3 grid(unsigned(plan.nseg * a.batch * plan.groups)), block(unsigned(plan.waves * 64));
   const size_t lds = size_t(plan.waves) * 2 * 64 * C * 4;
   if (plan.nseg > 1) {
@@ -230,7 +80,7 @@ hipError_t fwd(const RecArgs& a, const Plan& plan, char* workspace, hipStream_t 
       by_flag(a.z.p != nullptr, [&](auto zgate) {
         by_flag(plan.nseg > 1, [&](auto split) {
           fwd_kernel<IO, C, kT, decltype(gated)::value, decltype(igate)::value, decltype(zgate)::value,
-                     decltype(split)::value, true><<<grid, block, lds, stream>>>(p);
+                     decltype(split)::value, true, false><<<grid, block, lds, stream>>>(p);
         });
       });
     });

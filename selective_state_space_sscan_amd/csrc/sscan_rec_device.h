@@ -39,16 +39,16 @@ __device__ __forceinline__ float decay_loss(float m) {
   return fabsf(m) < 0.25f ? m * p : 1.0f - __builtin_amdgcn_exp2f(m * -kLog2e);
 }
 
-// The decay of a token: a, and with lam also r = sigmoid(g) and w = sqrt(1 - a^2).
+// The decay of a token: a, and with lam also 1 - a and w = sqrt(1 - a^2).
 struct Decay {
-  float a, r, w;
+  float a, loss, w;
 };
 
 template <bool GATED>
 __device__ __forceinline__ Decay decay(float g, float rate) {
   if constexpr (GATED) {
     const float r = sigmoid(g), loss = decay_loss(rate * r);
-    return {1.0f - loss, r, __builtin_amdgcn_sqrtf(loss * (2.0f - loss))};
+    return {1.0f - loss, loss, __builtin_amdgcn_sqrtf(loss * (2.0f - loss))};
   } else {
     // -inf: m = inf, whose series is not taken
     return {fabsf(g) < 0.25f ? 1.0f - decay_loss(-g) : __builtin_amdgcn_exp2f(g * kLog2e), 0.0f, 1.0f};

@@ -23,6 +23,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "sscan_rec_device.h"
 
@@ -38,6 +39,7 @@ struct TileArgs {
   uint64_t* maps;                    // [nseg][batch][groups * 64 C]
   uint64_t* states;                  // [runs][batch][groups * 64 C]: the state that leaves a run
   unsigned* ticket;                  // segments handed out
+  float* entry;                      // [nseg][batch][groups * 64 C]: states that enter the segments (from the second on)
   int nseg;
   unsigned groups;                   // of 64 C channels
 };
@@ -102,11 +104,11 @@ __device__ __forceinline__ void enter(const uint64_t* maps, const uint64_t* stat
   for (int c = 0; c < C; ++c) h[c] = fmaf(A[c], h[c], H[c]);
 }
 
-// Empties the words and sets the counter to 0.
-__global__ __launch_bounds__(256) static void clear_kernel(uint4* words, int64_t n, unsigned* ticket) {
+// Empties the words (n pairs of them) and sets the counters to 0.
+__global__ __launch_bounds__(256) static void clear_kernel(uint4* words, int64_t n, unsigned* tickets) {
   for (int64_t k = int64_t(blockIdx.x) * 256 + threadIdx.x; k < n; k += int64_t(gridDim.x) * 256)
     words[k] = uint4{kEmpty, kEmpty, kEmpty, kEmpty};
-  if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
+  if (blockIdx.x == 0 && threadIdx.x < 2) tickets[threadIdx.x] = 0;
 }
 
 template <typename IO, int C>
@@ -138,6 +140,29 @@ __device__ __forceinline__ typename Vec<IO, C>::V packed(const float (&x)[C]) {
   return v;
 }
 
+// One token's C channels of an input as they are loaded, or of what was kept of it in 8 bits.
+template <typename IO, int C, bool KEPT>
+struct In {
+  typename Vec<IO, C>::V v;
+  __device__ __forceinline__ void load(const RecArgs& a, const RecIn& in, const int8_t*, const float*, int64_t b, int64_t t,
+                                       int64_t ch) {
+    v = *reinterpret_cast<const typename Vec<IO, C>::V*>(static_cast<const IO*>(in.p) + b * in.b + t * in.t + ch);
+  }
+  __device__ __forceinline__ float get(int c) const { return part<typename Vec<IO, C>::V, C>(v, c); }
+};
+template <typename IO, int C>
+struct In<IO, C, true> {
+  typename Vec<int8_t, C>::V v;
+  float scale;
+  __device__ __forceinline__ void load(const RecArgs& a, const RecIn&, const int8_t* q, const float* s, int64_t b, int64_t t,
+                                       int64_t ch) {
+    const int64_t row = b * a.len + t;
+    v = *reinterpret_cast<const typename Vec<int8_t, C>::V*>(q + row * a.dim + ch);
+    scale = s[row * ((a.dim + kPackBlock - 1) / kPackBlock) + ch / kPackBlock];
+  }
+  __device__ __forceinline__ float get(int c) const { return part<typename Vec<int8_t, C>::V, C>(v, c) * scale; }
+};
+
 // The tokens of a wave's tile in the order of the scan, and where a row's tokens lie.
 struct Span {
   int64_t n, rev, k0;                // tokens of the row, whether it is scanned backwards, the tile's first token
@@ -154,6 +179,59 @@ struct Span {
 };
 
 inline int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The segment, row and channels of a block (`number`: shared, for the counter).
+struct Tile {
+  int seg;
+  int64_t b, group;
+  template <bool SPLIT>
+  static __device__ __forceinline__ Tile of(const TileArgs& p, unsigned* number, bool last_first = false) {
+    unsigned unit = blockIdx.x;
+    if (SPLIT) {
+      if (threadIdx.x == 0) *number = atomicAdd(p.ticket, 1u);
+      __syncthreads();
+      unit = __builtin_amdgcn_readfirstlane(*number);
+    }
+    const unsigned rows = unsigned(p.a.batch) * p.groups;  // below 2^24, as all blocks
+    const unsigned row = unit % rows;
+    const int seg = SPLIT ? int(unit / rows) : 0;
+    return {last_first ? p.nseg - 1 - seg : seg, int64_t(row / p.groups), int64_t(row % p.groups)};
+  }
+};
+
+// The map of all the block's waves, one after another: their maps lie in LDS (first: the
+// lane's first), A and H `half` floats apart and a wave's `pitch` after the one before.
+// STEP 1: from the first wave on; -1: from the last.
+template <int STEP>
+__device__ __forceinline__ void join(const float* first, int half, int pitch, int waves, float& A, float& H) {
+  A = 1.0f;
+  H = 0.0f;
+  for (int v = 0; v < waves; ++v) {
+    const float* w = first + (STEP > 0 ? v : waves - 1 - v) * pitch;
+    A *= w[0];
+    H = fmaf(w[0], H, w[half]);
+  }
+}
+
+// From the state h that enters the block: puts every wave's entry state in its A's place and
+// leaves the exit state in h.
+template <int STEP>
+__device__ __forceinline__ void hand_on(float* first, int half, int pitch, int waves, float& h) {
+  for (int v = 0; v < waves; ++v) {
+    float* w = first + (STEP > 0 ? v : waves - 1 - v) * pitch;
+    const float A = w[0];
+    w[0] = h;
+    h = fmaf(A, h, w[half]);
+  }
+}
+
+template <typename F>
+void by_flag(bool v, F f) {
+  if (v)
+    f(std::true_type());
+  else
+    f(std::false_type());
+}
 
 }  // namespace rec
 }  // namespace sscan
