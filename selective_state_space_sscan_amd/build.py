@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsscan.so")
 
-SOURCES = ["sscan_kernels.hip", "sscan_short.hip", "sscan_bwd.hip", "sscan_conv_bwd.hip", "sscan_multi.hip", "sscan_noalloc.hip", "sscan_delta.hip", "sscan_delta_bwd.hip", "sscan_norm.hip", "sscan_rec.hip", "sscan_rec_bwd.hip",
+SOURCES = ["sscan_kernels.hip", "sscan_short.hip", "sscan_bwd.hip", "sscan_conv_bwd.hip", "sscan_multi.hip", "sscan_noalloc.hip", "sscan_delta.hip", "sscan_delta_bwd.hip", "sscan_norm.hip", "sscan_rec.hip", "sscan_rec_keep.hip", "sscan_rec_bwd.hip", "sscan_rec_bwd_kept.hip",
            "sscan_pack8.hip", "sscan_layer_norm.hip", "sscan_capi.cpp",
            "sscan_delta_capi.cpp", "sscan_rec_capi.cpp"]
 

@@ -1,0 +1,34 @@
+// sscan_pack8.h -- a block's scale and its elements in steps of it, for the kernels that keep
+// activations in 8 bits.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "sscan_rec.h"
+
+namespace sscan {
+namespace rec {
+
+typedef __bf16 bf16;
+
+// |x| as a whole number, in the order of the values: infinities above all numbers, NaN above them.
+__device__ __forceinline__ unsigned magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// From the largest magnitude of a block: its scale, and what turns elements into steps.  By
+// float32 divisions, so that whoever repeats them has the same steps.
+struct Scale {
+  float step, per;
+  __device__ __forceinline__ explicit Scale(unsigned m) {
+    const float top = __uint_as_float(m);
+    const bool fine = m < 0x7f800000u && top >= 0x1p-100f;
+    per = fine ? 127.0f / top : 0.0f;
+    step = m >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : fine ? top / 127.0f : 0.0f;
+  }
+  // 0 where the block has no scale
+  __device__ __forceinline__ int steps(float x) const { return int(rintf(per == 0.0f ? 0.0f : x * per)); }
+};
+
+}  // namespace rec
+}  // namespace sscan

@@ -62,12 +62,12 @@ hipError_t launch_rec_step(const RecArgs& a, hipStream_t stream);
 hipError_t launch_rec_bwd(const RecBwdArgs& a, char* workspace, hipStream_t stream);
 
 struct PackArgs {
-  const void* x;                     // [batch, rows, size] by these strides
-  int64_t xb, xr;
-  int8_t* q;                         // [batch, rows, size]
-  float* scale;                      // [batch, rows, ceil(size / 64)]
+  const void* x;                     // [rows, size], rows x_stride apart
+  int64_t x_stride;
+  int8_t* q;                         // [rows, size]
+  float* scale;                      // [rows, ceil(size / 64)]
   void* out;                         // unpack: contiguous
-  int64_t batch, rows, size;
+  int64_t rows, size;
   int io_bf16;
 };
 

@@ -1,288 +1,8 @@
-// sscan_rec_bwd.hip -- gradients of the gated recurrence.  Where rows have several segments,
-// a first kernel leaves the states that enter them (sscan_rec_fwd.h, without its outputs);
-// the kernel below then takes the segments of a row at once, the last ones first, and joins
-// the adjoints between them as the forward pass joins the states.
-#include "sscan_rec_fwd.h"
+// sscan_rec_bwd.hip -- gradients of the gated recurrence (sscan_rec_bwd.h).
+#include "sscan_rec_bwd.h"
 
 namespace sscan {
 namespace rec {
-
-// One segment a block.  The adjoint that passes from token t to t - 1 is c_t = a_t (e_t +
-// c_{t+1}), e_t = dout_t silu(z_t): a map of the adjoint that enters a tile from behind, with
-// the same product of decays as the state's.  A lane holds its tokens' inputs as they were
-// loaded and 1 - a (a itself where it has no rounding to lose), walks them once for both
-// maps, and after the exchange once forwards from the state before them and once back.
-template <typename IO, int C, int T, bool GATED, bool IGATE, bool ZGATE, bool SPLIT, bool KEPT>
-__global__ __launch_bounds__(kMaxWaves * 64) void bwd_kernel(TileArgs p, RecBwdArgs w, float* partial) {
-  typedef typename Vec<IO, C>::V V;
-  extern __shared__ float lds[];     // [waves][4][64 C]: A and H of the states, A and H of the adjoints
-  __shared__ unsigned number;
-  constexpr int kPlane = 64 * C, kPitch = 4 * kPlane;
-  const RecArgs& a = p.a;
-  const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-  const int waves = int(blockDim.x) >> 6;
-  const Tile tile = Tile::of<SPLIT>(p, &number, true);
-  const int seg = tile.seg;
-  const int64_t b = tile.b, group = tile.group;
-  const int64_t ch = (group * 64 + lane) * C;
-  const bool on = ch < a.dim;
-  const int64_t at = on ? ch : 0;
-  const Span span(a, b, (int64_t(seg) * waves + wave) * T, T);
-  const int64_t pitch = a.batch * p.groups * kPlane, place = (b * p.groups + group) * kPlane + lane * C;
-
-  float rate[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) rate[c] = GATED ? decay_rate(a.lam, at + c, a.c) : 0.0f;
-
-  In<IO, C, KEPT> x[T], g[T], i[T], z[T];
-  V d[T];
-  float D[T][C], U[T][C];            // 1 - a (or a) and the token's input; later the state before the token
-  const auto decay_of = [&](float v) { return GATED ? 1.0f - v : v; };
-  float P[C], H[C], M[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    P[c] = 1.0f;
-    H[c] = M[c] = 0.0f;
-  }
-  if (span.live > 0) {
-    const auto load = [&](const RecIn& in, const int8_t* q, const float* s, In<IO, C, KEPT>(&v)[T]) {
-#pragma unroll
-      for (int j = 0; j < T; ++j) v[j].load(a, in, q, s, b, span.place(j < span.live ? j : span.live - 1), at);
-    };
-    load(a.g, a.kept.g, a.kept.gs, g);
-    load(a.x, a.kept.x, a.kept.xs, x);
-    if (IGATE) load(a.i, a.kept.i, a.kept.is, i);
-    const IO* dout = static_cast<const IO*>(w.dout) + b * a.len * a.dim + at;
-#pragma unroll
-    for (int j = 0; j < T; ++j)
-      d[j] = *reinterpret_cast<const V*>(dout + span.place(j < span.live ? j : span.live - 1) * a.dim);
-    if (ZGATE) load(a.z, a.kept.z, a.kept.zs, z);
-#pragma unroll
-    for (int j = 0; j < T; ++j)
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const Decay q = decay<GATED>(g[j].get(c), rate[c]);
-        float u = x[j].get(c) * q.w;
-        if (IGATE) u *= sigmoid(i[j].get(c));
-        const bool live = j < span.live;
-        D[j][c] = live ? (GATED ? q.loss : q.a) : decay_of(1.0f);
-        U[j][c] = live ? u : 0.0f;
-        const float A = decay_of(D[j][c]);
-        P[c] *= A;
-        H[c] = fmaf(A, H[c], U[j][c]);
-      }
-#pragma unroll
-    for (int j = T - 1; j >= 0; --j)
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        float e = part<V, C>(d[j], c);
-        if (ZGATE) {
-          const float v = z[j].get(c);
-          e *= v * sigmoid(v);
-        }
-        M[c] = decay_of(D[j][c]) * (M[c] + (j < span.live ? e : 0.0f));
-      }
-  }
-  float* mine = lds + wave * kPitch + lane;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    mine[c * 64] = mine[2 * kPlane + c * 64] = P[c];
-    mine[kPlane + c * 64] = H[c];
-    mine[3 * kPlane + c * 64] = M[c];
-  }
-  __syncthreads();
-  if (wave == 0) {                   // adjoints, from the last wave on
-    const int back = p.nseg - 1 - seg;
-    const bool ends_run = SPLIT && back % kRun == kRun - 1;
-    float* first = lds + 2 * kPlane + lane;
-    float h[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) h[c] = w.dh_last ? w.dh_last[b * a.dim + at + c] : 0.0f;
-    if (SPLIT) {
-      if (!ends_run) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          float A, B;
-          join<-1>(first + c * 64, kPlane, kPitch, waves, A, B);
-          publish(p.maps + back * pitch + place + c, map_bits(A), B);
-        }
-      }
-      enter<C>(p.maps + place, p.states + place, pitch, back, h);
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) hand_on<-1>(first + c * 64, kPlane, kPitch, waves, h[c]);
-    if (ends_run) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) publish(p.states + int64_t(back / kRun) * pitch + place + c, 0, h[c]);
-    }
-    if (w.dh0 && seg == 0 && on) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) w.dh0[b * a.dim + ch + c] = h[c];
-    }
-  }
-  if (wave == waves - 1) {           // states, from the first wave on
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      float h = seg > 0 ? p.entry[seg * pitch + place + c] : a.h0 ? a.h0[b * a.dim + at + c] : 0.0f;
-      hand_on<1>(lds + c * 64 + lane, kPlane, kPitch, waves, h);
-    }
-  }
-  __syncthreads();
-  float h[C], carry[C], dlam[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    h[c] = mine[c * 64];
-    carry[c] = mine[2 * kPlane + c * 64];
-    dlam[c] = 0.0f;
-  }
-  if (span.live > 0) {
-#pragma unroll
-    for (int j = 0; j < T; ++j)
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const float before = h[c];
-        h[c] = fmaf(decay_of(D[j][c]), h[c], U[j][c]);
-        U[j][c] = before;
-      }
-  }
-  const int64_t base = b * a.len * a.dim + ch;
-  IO *dx = static_cast<IO*>(w.dx) + base, *dg = static_cast<IO*>(w.dg) + base, *di = static_cast<IO*>(w.di) + base,
-     *dz = static_cast<IO*>(w.dz) + base;
-#pragma unroll
-  for (int j = T - 1; j >= 0; --j) {
-    float ox[C], og[C], oi[C], oz[C];
-    const bool live = j < span.live;
-#pragma unroll
-    for (int c = 0; c < C; ++c) ox[c] = og[c] = oi[c] = oz[c] = 0.0f;
-    if (live) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const float A = decay_of(D[j][c]), before = U[j][c];
-        const float v = x[j].get(c), s = IGATE ? sigmoid(i[j].get(c)) : 1.0f;
-        float e = part<V, C>(d[j], c);
-        if (ZGATE) {
-          const float q = z[j].get(c), sq = sigmoid(q);
-          oz[c] = e * h[c] * sq * fmaf(q, 1.0f - sq, 1.0f);
-          e *= q * sq;
-        }
-        h[c] = before;               // the state after the token before
-        const float adj = e + carry[c];
-        carry[c] = A * adj;
-        float dlog = carry[c] * before, wgt = 1.0f;
-        const float sx = s * v;
-        if (GATED) {
-          const float loss = D[j][c], r = sigmoid(g[j].get(c));
-          wgt = __builtin_amdgcn_sqrtf(loss * (2.0f - loss));
-          const float slope = wgt > 0.0f ? A * A * __builtin_amdgcn_rcpf(wgt) : 0.0f;
-          dlog = fmaf(-adj * sx, slope, dlog);
-          og[c] = -dlog * rate[c] * r * (1.0f - r);
-          dlam[c] = fmaf(-dlog, r, dlam[c]);
-        } else {
-          og[c] = dlog;
-        }
-        const float dw = adj * wgt;
-        ox[c] = dw * s;
-        oi[c] = dw * sx * (1.0f - s);
-      }
-    }
-    if (on && span.k0 + j < a.len) {
-      const int64_t o = span.place(j) * a.dim;
-      *reinterpret_cast<V*>(dx + o) = packed<IO, C>(ox);
-      *reinterpret_cast<V*>(dg + o) = packed<IO, C>(og);
-      if (IGATE) *reinterpret_cast<V*>(di + o) = packed<IO, C>(oi);
-      if (ZGATE) *reinterpret_cast<V*>(dz + o) = packed<IO, C>(oz);
-    }
-  }
-  if (GATED && w.dlam) {             // over the block's waves, in order
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < C; ++c) mine[c * 64] = dlam[c];
-    __syncthreads();
-    if (wave == 0 && on) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        float sum = 0.0f;
-        for (int v = 0; v < waves; ++v) sum += lds[v * kPitch + c * 64 + lane];
-        const float l = a.lam[ch + c];
-        partial[(int64_t(seg) * a.batch + b) * a.dim + ch + c] = sum * (a.c / (1.0f + expf(-l)));
-      }
-    }
-  }
-}
-
-constexpr int kBackT = 8, kStateT = 16;  // tokens of a wave's tile, here and in the kernel of the states
-constexpr int kBackWaves = 8;            // of a block where rows have several segments
-
-struct BackPlan {
-  int c, waves;
-  int64_t groups, nseg;
-  int64_t words;                     // words of one set of maps and states
-  size_t off_words, off_entry, off_partial, bytes;
-};
-
-BackPlan back_plan(int64_t batch, int64_t len, int64_t dim) {
-  BackPlan p;
-  p.c = dim % 2 == 0 ? 2 : 1;
-  p.groups = up(dim, 64 * p.c);
-  const int64_t tiles = up(len, kBackT), row = batch * p.groups * 64 * p.c;
-  p.waves = tiles <= kMaxWaves ? int(tiles) : kBackWaves;
-  p.nseg = tiles <= kMaxWaves ? 1 : up(tiles, p.waves);
-  p.words = p.nseg > 1 ? (p.nseg + p.nseg / kRun) * row : 0;
-  p.off_words = 256;
-  p.off_entry = p.off_words + size_t(p.words) * 16;
-  p.off_partial = p.off_entry + (p.nseg > 1 ? size_t(p.nseg * row) * 4 : 0);
-  p.bytes = (p.off_partial + size_t(p.nseg) * size_t(batch) * size_t(dim) * 4 + 255) / 256 * 256;
-  return p;
-}
-
-template <typename IO, int C, bool KEPT>
-hipError_t bwd(const RecBwdArgs& w, const BackPlan& plan, char* workspace, hipStream_t stream) {
-  const RecArgs& a = w.f;
-  const int64_t row = a.batch * plan.groups * 64 * C;
-  uint64_t* words = reinterpret_cast<uint64_t*>(workspace + plan.off_words);
-  unsigned* ticket = reinterpret_cast<unsigned*>(workspace);
-  float* partial = reinterpret_cast<float*>(workspace + plan.off_partial);
-  TileArgs p{a, words, words + plan.nseg * row, ticket, reinterpret_cast<float*>(workspace + plan.off_entry),
-             int(plan.nseg), unsigned(plan.groups)};
-  const bool split = plan.nseg > 1, igate = KEPT ? a.kept.i != nullptr : a.i.p != nullptr,
-             zgate = KEPT ? a.kept.z != nullptr : a.z.p != nullptr;
-  if (split) {
-    const int64_t n = plan.words, blocks = up(n, 256 * 4);
-    clear_kernel<<<dim3(unsigned(blocks < 2048 ? blocks : 2048)), 256, 0, stream>>>(reinterpret_cast<uint4*>(words), n,
-                                                                                    ticket);
-    const int waves = plan.waves * kBackT / kStateT;
-    const dim3 grid(unsigned((plan.nseg - 1) * a.batch * plan.groups));
-    by_flag(a.lam != nullptr, [&](auto gated) {
-      by_flag(igate, [&](auto ig) {
-        fwd_kernel<IO, C, kStateT, decltype(gated)::value, decltype(ig)::value, false, true, false, KEPT>
-            <<<grid, waves * 64, size_t(waves) * 2 * 64 * C * 4, stream>>>(p);
-      });
-    });
-    p.maps += plan.words;
-    p.states += plan.words;
-    ++p.ticket;
-  }
-  const dim3 grid(unsigned(plan.nseg * a.batch * plan.groups));
-  by_flag(a.lam != nullptr, [&](auto gated) {
-    by_flag(igate, [&](auto ig) {
-      by_flag(zgate, [&](auto zg) {
-        by_flag(split, [&](auto sp) {
-          bwd_kernel<IO, C, kBackT, decltype(gated)::value, decltype(ig)::value, decltype(zg)::value, decltype(sp)::value,
-                     KEPT><<<grid, plan.waves * 64, size_t(plan.waves) * 4 * 64 * C * 4, stream>>>(p, w, partial);
-        });
-      });
-    });
-  });
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !w.dlam) return e;
-  float* const out[1] = {w.dlam};
-  return launch_row_sums(partial, out, 1, a.dim, plan.nseg * a.batch, stream);
-}
-
-template <typename IO, int C>
-hipError_t by_source(const RecBwdArgs& w, const BackPlan& plan, char* workspace, hipStream_t stream) {
-  return w.f.kept.x ? bwd<IO, C, true>(w, plan, workspace, stream) : bwd<IO, C, false>(w, plan, workspace, stream);
-}
 
 // Without tokens the adjoint of the last state is that of the entry state.
 __global__ __launch_bounds__(256) void through_kernel(const float* from, float* to, int64_t n, float* zeros, int64_t m) {
@@ -294,7 +14,9 @@ __global__ __launch_bounds__(256) void through_kernel(const float* from, float* 
 }  // namespace rec
 
 size_t rec_bwd_workspace(int64_t batch, int64_t len, int64_t dim, bool) {
-  return len == 0 ? 0 : rec::back_plan(batch, len, dim).bytes;
+  if (len == 0) return 0;
+  // the same words and sums whether the inputs were kept or not
+  return rec::back_plan(batch, len, dim, false).bytes;
 }
 
 hipError_t launch_rec_bwd(const RecBwdArgs& w, char* workspace, hipStream_t stream) {
@@ -304,10 +26,12 @@ hipError_t launch_rec_bwd(const RecBwdArgs& w, char* workspace, hipStream_t stre
     rec::through_kernel<<<dim3(unsigned(rec::up(m, 256))), 256, 0, stream>>>(w.dh_last, w.dh0, n, w.dlam, a.dim);
     return hipGetLastError();
   }
-  const rec::BackPlan p = rec::back_plan(a.batch, a.len, a.dim);
-  if (a.io_bf16)
-    return p.c == 2 ? rec::by_source<rec::bf16, 2>(w, p, workspace, stream) : rec::by_source<rec::bf16, 1>(w, p, workspace, stream);
-  return p.c == 2 ? rec::by_source<float, 2>(w, p, workspace, stream) : rec::by_source<float, 1>(w, p, workspace, stream);
+  const bool kept = a.kept.x != nullptr;
+  const rec::BackPlan p = rec::back_plan(a.batch, a.len, a.dim, kept);
+  if (kept) return rec::launch_bwd_kept(w, p, workspace, stream);
+  return rec::by_lane(p.c, a.io_bf16, [&](auto io, auto c) {
+    return rec::bwd<decltype(io), decltype(c)::value, false>(w, p, workspace, stream);
+  });
 }
 
 }  // namespace sscan

@@ -336,7 +336,7 @@ int sscan_pack8(const void* x, int64_t x_stride, int64_t rows, int64_t size, int
   bool empty = false;
   const int st = check_pack8(x, x_stride, rows, size, io_dtype, q, scale, true, &empty);
   if (st != SSCAN_OK || empty) return st;
-  const sscan::PackArgs a{x, 0, x_stride, q, scale, nullptr, 1, rows, size, io_dtype == SSCAN_BF16};
+  const sscan::PackArgs a{x, x_stride, q, scale, nullptr, rows, size, io_dtype == SSCAN_BF16};
   return status_of(sscan::launch_pack8(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -351,7 +351,7 @@ int sscan_unpack8(const int8_t* q, const float* scale, int64_t rows, int64_t siz
   bool empty = false;
   const int st = check_pack8(out, size, rows, size, io_dtype, q, scale, false, &empty);
   if (st != SSCAN_OK || empty) return st;
-  const sscan::PackArgs a{nullptr, 0, 0, const_cast<int8_t*>(q), const_cast<float*>(scale), out, 1, rows, size,
+  const sscan::PackArgs a{nullptr, 0, const_cast<int8_t*>(q), const_cast<float*>(scale), out, rows, size,
                           io_dtype == SSCAN_BF16};
   return status_of(sscan::launch_unpack8(a, static_cast<hipStream_t>(stream)));
 }

@@ -7,6 +7,10 @@
 
 #include "sscan_rec.h"
 
+// Products and sums are joined only where the code says so: otherwise the kernels, which are
+// built for many combinations of arguments, would round the same token differently.
+#pragma clang fp contract(off)
+
 namespace sscan {
 namespace rec {
 
@@ -20,23 +24,33 @@ __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e));
 }
 
-// A channel's constants: k = c softplus(lam) (with lam), by the library's exp and log1p.
+// A channel's constant c softplus(lam).  softplus(x) = max(x, 0) + log1p(w), w = exp(-|x|)
+// by an exponent in two parts; log1p(w) is the logarithm of the rounded sum s = 1 + w plus
+// the rounding's error w - (s - 1), off by less than a unit in the last place.
 __device__ __forceinline__ float decay_rate(const float* lam, int64_t ch, float c) {
-  const float x = lam[ch];
-  return c * (fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))));
+  const float x = -fabsf(lam[ch]), t = x * kLog2e;
+  const float low = fmaf(x, kLog2e, -t) + x * 1.925963033500e-8f;  // what the product and the constant drop
+  const float e = __builtin_amdgcn_exp2f(t), w = fmaf(e * low, 0.693147181f, e), s = 1.0f + w;
+  return c * (fmaxf(lam[ch], 0.0f) + fmaf(__builtin_amdgcn_logf(s), 0.693147181f, w - (s - 1.0f)));
 }
 
-// 1 - exp(-m): by its series up to m = 1/4 (the next term is below 2^-29 of the sum), where
-// the difference would lose digits.  Decays near 1 are taken as 1 minus this: their
-// rounding is what a long sum of states sees of them.
+// 1 - exp(-m) for |m| < 1/4: by its series (the next term is below 2^-28 of the sum).
+__device__ __forceinline__ float small_loss(float m) {
+  float p = fmaf(m, -1.0f / 5040, 1.0f / 720);
+  p = fmaf(m, -p, 1.0f / 120);
+  p = fmaf(m, p, -1.0f / 24);
+  p = fmaf(m, p, 1.0f / 6);
+  p = fmaf(m, p, -0.5f);
+  return m * fmaf(m, p, 1.0f);
+}
+
+// 1 - exp(-m): where the difference would lose digits by the series.  Decays near 1 are taken
+// as 1 minus this: their rounding is what a long sum of states sees of them.  Both ways are
+// evaluated for every token; a second copy of the code for waves of slow channels only, without
+// the exponential, took longer (8 x 4096 x 4096 forward 330 us, so 289).
 __device__ __forceinline__ float decay_loss(float m) {
-  float p = fmaf(m, -1.0f / 7, 1.0f);
-  p = fmaf(m * (-1.0f / 6), p, 1.0f);
-  p = fmaf(m * (-1.0f / 5), p, 1.0f);
-  p = fmaf(m * (-1.0f / 4), p, 1.0f);
-  p = fmaf(m * (-1.0f / 3), p, 1.0f);
-  p = fmaf(m * (-1.0f / 2), p, 1.0f);
-  return fabsf(m) < 0.25f ? m * p : 1.0f - __builtin_amdgcn_exp2f(m * -kLog2e);
+  const float p = small_loss(m), q = 1.0f - __builtin_amdgcn_exp2f(m * -kLog2e);
+  return fabsf(m) < 0.25f ? p : q;
 }
 
 // The decay of a token: a, and with lam also 1 - a and w = sqrt(1 - a^2).
@@ -47,11 +61,11 @@ struct Decay {
 template <bool GATED>
 __device__ __forceinline__ Decay decay(float g, float rate) {
   if constexpr (GATED) {
-    const float r = sigmoid(g), loss = decay_loss(rate * r);
+    const float loss = decay_loss(rate * sigmoid(g));
     return {1.0f - loss, loss, __builtin_amdgcn_sqrtf(loss * (2.0f - loss))};
   } else {
     // -inf: m = inf, whose series is not taken
-    return {fabsf(g) < 0.25f ? 1.0f - decay_loss(-g) : __builtin_amdgcn_exp2f(g * kLog2e), 0.0f, 1.0f};
+    return {fabsf(g) < 0.25f ? 1.0f - small_loss(-g) : __builtin_amdgcn_exp2f(g * kLog2e), 0.0f, 1.0f};
   }
 }
 

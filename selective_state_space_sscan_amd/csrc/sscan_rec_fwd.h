@@ -2,28 +2,42 @@
 // the states between segments, which the backward pass starts from.
 #pragma once
 
+#include "sscan_pack8.h"
 #include "sscan_rec_tile.h"
 
 namespace sscan {
 namespace rec {
 
+// The largest of a block of 64 channels, C a lane, in all its lanes: sixteen lanes by DPP,
+// rows of sixteen by exchanges.
+template <int C>
+__device__ __forceinline__ unsigned block_max(unsigned m) {
+  m = max(m, unsigned(__builtin_amdgcn_update_dpp(0, int(m), 0xb1, 0xf, 0xf, true)));   // quad_perm 1 0 3 2
+  m = max(m, unsigned(__builtin_amdgcn_update_dpp(0, int(m), 0x4e, 0xf, 0xf, true)));   // quad_perm 2 3 0 1
+  m = max(m, unsigned(__builtin_amdgcn_update_dpp(0, int(m), 0x141, 0xf, 0xf, true)));  // row_half_mirror
+  m = max(m, unsigned(__builtin_amdgcn_update_dpp(0, int(m), 0x140, 0xf, 0xf, true)));  // row_mirror
+#pragma unroll
+  for (int s = 16; s < 64 / C; s *= 2) m = max(m, unsigned(__shfl_xor(int(m), s)));
+  return m;
+}
+
 // One segment a block (sscan_rec_tile.h).  A lane first turns its tokens into decays and
 // inputs, which it holds in registers with their map; the waves' maps meet in LDS, wave 0
 // finds the state that enters the segment (from the row's segments before, where there are
 // any) and from it those that enter the waves, and every wave walks its tokens once more,
-// now from its state, and answers.  SPLIT: rows have several segments.  OUT: outputs are
+// now from its state, and answers.  OUT: outputs are
 // wanted, not the states between segments alone (whose last segment has no block).  KEPT:
-// the inputs come in 8 bits.
-template <typename IO, int C, int T, bool GATED, bool IGATE, bool ZGATE, bool SPLIT, bool OUT, bool KEPT>
+// the inputs come in 8 bits.  KEEP: they are left in 8 bits.
+template <typename IO, int C, int T, bool GATED, bool IGATE, bool ZGATE, bool OUT, bool KEPT, bool KEEP>
 __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
-  typedef typename Vec<IO, C>::V V;
   extern __shared__ float lds[];     // [waves][2][64 C]: A and H; then the waves' entry states in A's place
   __shared__ unsigned number;
   const RecArgs& a = p.a;
   const int lane = int(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   const int waves = int(blockDim.x) >> 6;
-  const Tile tile = Tile::of<SPLIT>(p, &number);
+  const Tile tile = Tile::of(p, &number);
   const int seg = tile.seg;
+  const bool split = p.nseg > 1;     // rows have several segments
   const int64_t b = tile.b, group = tile.group;
   const int64_t ch = (group * 64 + lane) * C;
   const bool on = ch < a.dim;
@@ -34,37 +48,75 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
 #pragma unroll
   for (int c = 0; c < C; ++c) rate[c] = GATED ? decay_rate(a.lam, at + c, a.c) : 0.0f;
 
-  const auto load = [&](const RecIn& in, const int8_t* q, const float* s, In<IO, C, KEPT>(&v)[T]) {
+  const auto keep = [&](const In<IO, C, KEPT>(&v)[T], int8_t* q, float* s) {
+    const int64_t blocks = (a.dim + kPackBlock - 1) / kPackBlock;
 #pragma unroll
-    for (int j = 0; j < T; ++j) v[j].load(a, in, q, s, b, span.place(j < span.live ? j : span.live - 1), at);
+    for (int j = 0; j < T; ++j) {
+      unsigned m = 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c) m = max(m, magnitude(v[j].get(c)));
+      const Scale scale(block_max<C>(on ? m : 0));
+      typename Vec<int8_t, C>::V k;
+      if constexpr (C == 1) {
+        k = int8_t(scale.steps(v[j].get(0)));
+      } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) k[c] = int8_t(scale.steps(v[j].get(c)));
+      }
+      if (j < span.live && on) {
+        const int64_t row = b * a.len + span.place(j);
+        store_any<int8_t, C>(q + row * a.dim + ch, k);
+        if (ch % kPackBlock == 0) s[row * blocks + ch / kPackBlock] = scale.step;
+      }
+    }
   };
   float A[T][C], U[T][C];
   In<IO, C, KEPT> z[T];
   if (span.live > 0) {
     In<IO, C, KEPT> x[T], g[T], i[T];
-    load(a.x, a.kept.x, a.kept.xs, x);
+    const auto load = [&](const RecIn& in, const int8_t* q, const float* s, In<IO, C, KEPT>(&v)[T]) {
+      load_tile<IO, C, T, KEPT>(Walk<IO, C, KEPT>(a, in, q, s, b, span, at), span.live, v);
+    };
     load(a.g, a.kept.g, a.kept.gs, g);
+    load(a.x, a.kept.x, a.kept.xs, x);
     if (IGATE) load(a.i, a.kept.i, a.kept.is, i);
-    if (OUT && ZGATE) load(a.z, a.kept.z, a.kept.zs, z);
+    if (KEEP) {
+      keep(g, a.kept.g, a.kept.gs);
+      keep(x, a.kept.x, a.kept.xs);
+      if (IGATE) keep(i, a.kept.i, a.kept.is);
+      as_loaded(g);
+      as_loaded(x);
+      if (IGATE) as_loaded(i);
+    }
 #pragma unroll
-    for (int j = 0; j < T; ++j)
+    for (int j = 0; j < T; ++j) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const Decay d = decay<GATED>(g[j].get(c), rate[c]);
-        float u = x[j].get(c) * d.w;
+        float u = x[j].get(c);
+        if (GATED) u *= d.w;
         if (IGATE) u *= sigmoid(i[j].get(c));
-        const bool live = j < span.live;
-        A[j][c] = live ? d.a : 1.0f;
-        U[j][c] = live ? u : 0.0f;
+        A[j][c] = d.a;
+        U[j][c] = u;
       }
-  } else {
+      __builtin_amdgcn_sched_barrier(0);  // a token at a time: several would need more registers than there are
+    }
+    // on their way while the state comes; with the others they would not fit the registers
+    if (OUT && ZGATE) load(a.z, a.kept.z, a.kept.zs, z);
+    if (KEEP && ZGATE) {
+      keep(z, a.kept.z, a.kept.zs);
+      as_loaded(z);
+    }
+  }
+  if (span.live < T) {               // tokens past the row's end leave the state alone
 #pragma unroll
     for (int j = 0; j < T; ++j)
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        A[j][c] = 1.0f;
-        U[j][c] = 0.0f;
-      }
+      for (int c = 0; c < C; ++c)
+        if (j >= span.live) {
+          A[j][c] = 1.0f;
+          U[j][c] = 0.0f;
+        }
   }
   float* mine = lds + wave * (2 * 64 * C) + lane;
 #pragma unroll
@@ -81,11 +133,11 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
   __syncthreads();
   if (wave == 0) {
     const int64_t pitch = a.batch * p.groups * (64 * C), place = (b * p.groups + group) * (64 * C) + lane * C;
-    const bool ends_run = SPLIT && seg % kRun == kRun - 1;
+    const bool ends_run = split && seg % kRun == kRun - 1;
     float h[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) h[c] = a.h0 ? a.h0[b * a.dim + at + c] : 0.0f;
-    if (SPLIT) {
+    if (split) {
       if (!ends_run) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -116,9 +168,9 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
   float h[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) h[c] = mine[c * 64];
-  IO* out = static_cast<IO*>(a.out) + b * a.len * a.dim + ch;
-#pragma unroll
-  for (int j = 0; j < T; ++j) {
+  char* row = static_cast<char*>(a.out) + b * a.len * a.dim * int64_t(sizeof(IO));  // the same in all lanes
+  const unsigned place = unsigned(ch) * unsigned(sizeof(IO));
+  const auto answer = [&](int j) {
     float y[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -128,11 +180,86 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
         const float q = z[j].get(c);
         y[c] *= q * sigmoid(q);
       }
-      if (j >= span.live) y[c] = 0.0f;
     }
-    if (on && span.k0 + j < a.len) *reinterpret_cast<V*>(out + span.place(j) * a.dim) = packed<IO, C>(y);
+    return packed<IO, C>(y);
+  };
+  if (span.live == T) {
+    char* to = row + span.place(0) * a.dim * int64_t(sizeof(IO));
+    const int64_t step = (span.rev ? -a.dim : a.dim) * int64_t(sizeof(IO));
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const auto y = answer(j);
+      if (on) store_any<IO, C>(reinterpret_cast<IO*>(to + place), y);
+      to += step;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const auto y = j < span.live ? answer(j) : typename Vec<IO, C>::V{};
+      if (on && span.k0 + j < a.len)
+        store_any<IO, C>(reinterpret_cast<IO*>(row + span.place(j) * a.dim * int64_t(sizeof(IO)) + place), y);
+    }
   }
 }
+
+constexpr int kWaves = 8;            // of a block where rows have several segments
+
+// Channels a lane, and tokens of a wave's tile: what the registers hold without spilling any
+// (the tokens' decays and inputs alone are 2 C T).  The same whether inputs are kept or not:
+// states are joined at the tiles' ends, and outputs are the same bits.
+inline int channels_of(int64_t dim) { return dim % 2 == 0 ? 2 : 1; }
+constexpr int tokens_of(int c, bool io_bf16) { return c == 2 && !io_bf16 ? 8 : 16; }
+
+struct Plan {
+  int c, waves;
+  int64_t groups, nseg, words;       // bytes of the maps and states
+};
+
+inline Plan plan_of(int64_t batch, int64_t len, int64_t dim, bool io_bf16) {
+  Plan p;
+  p.c = channels_of(dim);
+  p.groups = up(dim, 64 * p.c);
+  const int64_t tiles = up(len, tokens_of(p.c, io_bf16));
+  p.waves = tiles <= kMaxWaves ? int(tiles) : kWaves;
+  p.nseg = tiles <= kMaxWaves ? 1 : up(tiles, p.waves);
+  p.words = p.nseg > 1 ? (p.nseg + p.nseg / kRun) * batch * p.groups * 64 * p.c * 8 : 0;
+  return p;
+}
+
+template <typename IO, int C, bool KEEP>
+hipError_t fwd(const RecArgs& a, const Plan& plan, char* workspace, hipStream_t stream) {
+  uint64_t* words = reinterpret_cast<uint64_t*>(workspace + 256);
+  const TileArgs p{a, words, words + plan.nseg * a.batch * plan.groups * 64 * C, reinterpret_cast<unsigned*>(workspace),
+                   nullptr, int(plan.nseg), unsigned(plan.groups)};
+  const dim3 grid(unsigned(plan.nseg * a.batch * plan.groups)), block(unsigned(plan.waves * 64));
+  const size_t lds = size_t(plan.waves) * 2 * 64 * C * 4;
+  if (plan.nseg > 1) {
+    const int64_t n = plan.words / 16, blocks = up(n, 256 * 4);
+    clear_kernel<<<dim3(unsigned(blocks < 2048 ? blocks : 2048)), 256, 0, stream>>>(reinterpret_cast<uint4*>(words), n, p.ticket);
+  }
+  by_flag(a.lam != nullptr, [&](auto gated) {
+    by_flag(a.i.p != nullptr, [&](auto igate) {
+      by_flag(a.z.p != nullptr, [&](auto zgate) {
+        fwd_kernel<IO, C, tokens_of(C, sizeof(IO) == 2), decltype(gated)::value, decltype(igate)::value, decltype(zgate)::value, true,
+                   false, KEEP><<<grid, block, lds, stream>>>(p);
+      });
+    });
+  });
+  return hipGetLastError();
+}
+
+// f(element, channels a lane), as types.
+template <typename F>
+hipError_t by_lane(int c, bool io_bf16, F f) {
+  const auto with = [&](auto io) {
+    return c == 2 ? f(io, std::integral_constant<int, 2>()) : f(io, std::integral_constant<int, 1>());
+  };
+  return io_bf16 ? with(bf16{}) : with(0.0f);
+}
+
+// The forward call whose inputs are left in 8 bits (sscan_rec_keep.hip).
+hipError_t launch_keep(const RecArgs& a, const Plan& plan, char* workspace, hipStream_t stream);
 
 }  // namespace rec
 }  // namespace sscan

@@ -111,17 +111,29 @@ __global__ __launch_bounds__(256) static void clear_kernel(uint4* words, int64_t
   if (blockIdx.x == 0 && threadIdx.x < 2) tickets[threadIdx.x] = 0;
 }
 
+// C elements, and the same at any address that an element can have.
 template <typename IO, int C>
 struct Vec {
-  typedef IO V __attribute__((ext_vector_type(C), aligned(sizeof(IO))));
+  typedef IO V __attribute__((ext_vector_type(C)));
+  typedef V Any __attribute__((aligned(sizeof(IO))));
 };
 template <typename IO>
 struct Vec<IO, 1> {
   typedef IO V;
+  typedef IO Any;
 };
 
-template <typename V, int C>
-__device__ __forceinline__ float part(const V& v, int c) {
+template <typename IO, int C>
+__device__ __forceinline__ typename Vec<IO, C>::V load_any(const IO* p) {
+  return *reinterpret_cast<const typename Vec<IO, C>::Any*>(p);
+}
+template <typename IO, int C>
+__device__ __forceinline__ void store_any(IO* p, typename Vec<IO, C>::V v) {
+  *reinterpret_cast<typename Vec<IO, C>::Any*>(p) = v;
+}
+
+template <int C, typename V>
+__device__ __forceinline__ float part(V v, int c) {
   if constexpr (C == 1)
     return float(v);
   else
@@ -144,24 +156,41 @@ __device__ __forceinline__ typename Vec<IO, C>::V packed(const float (&x)[C]) {
 template <typename IO, int C, bool KEPT>
 struct In {
   typename Vec<IO, C>::V v;
-  __device__ __forceinline__ void load(const RecArgs& a, const RecIn& in, const int8_t*, const float*, int64_t b, int64_t t,
-                                       int64_t ch) {
-    v = *reinterpret_cast<const typename Vec<IO, C>::V*>(static_cast<const IO*>(in.p) + b * in.b + t * in.t + ch);
-  }
-  __device__ __forceinline__ float get(int c) const { return part<typename Vec<IO, C>::V, C>(v, c); }
+  __device__ __forceinline__ float get(int c) const { return part<C>(v, c); }
 };
 template <typename IO, int C>
 struct In<IO, C, true> {
   typename Vec<int8_t, C>::V v;
   float scale;
-  __device__ __forceinline__ void load(const RecArgs& a, const RecIn&, const int8_t* q, const float* s, int64_t b, int64_t t,
-                                       int64_t ch) {
-    const int64_t row = b * a.len + t;
-    v = *reinterpret_cast<const typename Vec<int8_t, C>::V*>(q + row * a.dim + ch);
-    scale = s[row * ((a.dim + kPackBlock - 1) / kPackBlock) + ch / kPackBlock];
+  // four steps at a time become unsigned bytes, which one instruction converts; the product is exact
+  // before the sum, so the value is that of step * scale
+  __device__ __forceinline__ float get(int c) const {
+    if constexpr (C == 4) {
+      const uint32_t u = __builtin_bit_cast(uint32_t, v) ^ 0x80808080u;
+      return fmaf(float(u >> (8 * c) & 0xffu), scale, -128.0f * scale);
+    } else {
+      return part<C>(v, c) * scale;
+    }
   }
-  __device__ __forceinline__ float get(int c) const { return part<typename Vec<int8_t, C>::V, C>(v, c) * scale; }
 };
+
+// What a tile holds is unpacked again where it is used again: the values of the first use,
+// kept as floats, would fill the registers.
+template <typename IO, int C, bool KEPT, int T>
+__device__ __forceinline__ void as_loaded(In<IO, C, KEPT> (&x)[T]) {
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+    if constexpr (sizeof(x[j].v) >= 4) {
+      struct {
+        uint32_t w[sizeof(x[j].v) / 4];
+      } raw;
+      __builtin_memcpy(&raw, &x[j].v, sizeof(raw));
+#pragma unroll
+      for (uint32_t& w : raw.w) asm("" : "+v"(w));
+      __builtin_memcpy(&x[j].v, &raw, sizeof(raw));
+    }  // a single narrow value has no copy to save
+  }
+}
 
 // The tokens of a wave's tile in the order of the scan, and where a row's tokens lie.
 struct Span {
@@ -178,23 +207,78 @@ struct Span {
   __device__ __forceinline__ int64_t place(int j) const { return rev && k0 + j < n ? n - 1 - (k0 + j) : k0 + j; }
 };
 
+// A walk over one input's tokens in the order of the scan: the address of a token is the same
+// in all lanes (scalar registers), a lane adds its channels' offset.
+template <typename IO, int C, bool KEPT>
+struct Walk {
+  const char* p;
+  int64_t step;
+  unsigned lane;
+  __device__ __forceinline__ Walk(const RecArgs& a, const RecIn& in, const int8_t*, const float*, int64_t b, const Span& s,
+                                  int64_t ch)
+      : p(static_cast<const char*>(in.p) + (b * in.b + s.place(0) * in.t) * int64_t(sizeof(IO))),
+        step((s.rev ? -in.t : in.t) * int64_t(sizeof(IO))), lane(unsigned(ch) * unsigned(sizeof(IO))) {}
+  __device__ __forceinline__ In<IO, C, KEPT> load() const {
+    return {load_any<IO, C>(reinterpret_cast<const IO*>(p + lane))};
+  }
+  __device__ __forceinline__ void next(bool more = true) { p += more ? step : 0; }
+};
+template <typename IO, int C>
+struct Walk<IO, C, true> {
+  const int8_t* p;
+  const float* s;
+  int64_t step, sstep;
+  unsigned lane, block;
+  __device__ __forceinline__ Walk(const RecArgs& a, const RecIn&, const int8_t* q, const float* scale, int64_t b,
+                                  const Span& sp, int64_t ch)
+      : lane(unsigned(ch)), block(unsigned(ch) / kPackBlock) {
+    const int64_t blocks = (a.dim + kPackBlock - 1) / kPackBlock, row = b * a.len + sp.place(0);
+    p = q + row * a.dim;
+    s = scale + row * blocks;
+    step = sp.rev ? -a.dim : a.dim;
+    sstep = sp.rev ? -blocks : blocks;
+  }
+  __device__ __forceinline__ In<IO, C, true> load() const { return {load_any<int8_t, C>(p + lane), s[block]}; }
+  __device__ __forceinline__ void next(bool more = true) {
+    p += more ? step : 0;
+    s += more ? sstep : 0;
+  }
+};
+
+// The walk's T tokens; where the tile has fewer, its last one again.
+template <typename IO, int C, int T, bool KEPT>
+__device__ __forceinline__ void load_tile(Walk<IO, C, KEPT> w, int live, In<IO, C, KEPT> (&v)[T]) {
+  if (live == T) {
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      v[j] = w.load();
+      w.next();
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      v[j] = w.load();
+      w.next(j + 1 < live);
+    }
+  }
+}
+
 inline int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The segment, row and channels of a block (`number`: shared, for the counter).
 struct Tile {
   int seg;
   int64_t b, group;
-  template <bool SPLIT>
   static __device__ __forceinline__ Tile of(const TileArgs& p, unsigned* number, bool last_first = false) {
     unsigned unit = blockIdx.x;
-    if (SPLIT) {
+    if (p.nseg > 1) {
       if (threadIdx.x == 0) *number = atomicAdd(p.ticket, 1u);
       __syncthreads();
       unit = __builtin_amdgcn_readfirstlane(*number);
     }
     const unsigned rows = unsigned(p.a.batch) * p.groups;  // below 2^24, as all blocks
     const unsigned row = unit % rows;
-    const int seg = SPLIT ? int(unit / rows) : 0;
+    const int seg = int(unit / rows);
     return {last_first ? p.nseg - 1 - seg : seg, int64_t(row / p.groups), int64_t(row % p.groups)};
   }
 };
