@@ -8,6 +8,8 @@
 
 #include "sscan_rec.h"
 
+#pragma clang fp contract(off)
+
 namespace sscan {
 namespace rec {
 
@@ -29,6 +31,19 @@ struct Scale {
   // 0 where the block has no scale
   __device__ __forceinline__ int steps(float x) const { return int(rintf(per == 0.0f ? 0.0f : x * per)); }
 };
+
+// The same with a scale's `per` alone.  A whole number of steps below 2^22 added to 1.5 2^23
+// stands in the low bits of the sum, which is rounded as rintf is; bfloat16 has no NaN whose
+// low bits are not 0.
+template <typename IO>
+__device__ __forceinline__ int8_t steps_of(float x, float per) {
+  if constexpr (sizeof(IO) == 2) {
+    const float y = x * per;
+    return int8_t(__float_as_uint(y + 12582912.0f) & 0xffu);
+  } else {
+    return int8_t(int(rintf(per == 0.0f ? 0.0f : x * per)));
+  }
+}
 
 }  // namespace rec
 }  // namespace sscan

@@ -9,11 +9,14 @@
 namespace sscan {
 namespace rec {
 
-// A segment has 64 tokens: a wave has as many as the registers hold without spilling any, and
-// a block the waves for the others.
-constexpr int kBackSeg = 64;
-constexpr int kStateTokens = 16;     // of a wave in the kernel of the states
-constexpr int back_tokens(int c, bool kept) { return c == 2 && kept ? 4 : 8; }
+// A segment is eight waves' tiles.  A wave has as many tokens as the registers hold without
+// spilling any; four channels a lane where the inputs come in 8 bits, for whole words of them.
+constexpr int kBackWaves = 8;
+constexpr int back_tokens(bool kept) { return kept ? 4 : 8; }
+inline int back_channels(int64_t dim, bool kept) { return kept && dim % 4 == 0 ? 4 : channels_of(dim); }
+// Of a block in the kernel of the states.
+constexpr int state_tokens(int c, bool kept) { return c == 4 || (c == 2 && kept) ? 8 : 16; }
+constexpr int kStateWaves = 16;
 
 // One segment a block.  The adjoint that passes from token t to t - 1 is c_t = a_t (e_t +
 // c_{t+1}), e_t = dout_t silu(z_t): a map of the adjoint that enters a tile from behind, with
@@ -21,7 +24,7 @@ constexpr int back_tokens(int c, bool kept) { return c == 2 && kept ? 4 : 8; }
 // loaded and 1 - a (a itself where it has no rounding to lose), walks them once for both
 // maps, and after the exchange once forwards from the state before them and once back.
 template <typename IO, int C, int T, bool GATED, bool IGATE, bool ZGATE, bool KEPT>
-__global__ __launch_bounds__(64 * kBackSeg / T) void bwd_kernel(TileArgs p, RecBwdArgs w, float* partial) {
+__global__ __launch_bounds__(64 * kBackWaves) void bwd_kernel(TileArgs p, RecBwdArgs w, float* partial) {
   extern __shared__ float lds[];     // [waves][4][64 C]: A and H of the states, A and H of the adjoints
   __shared__ unsigned number;
   constexpr int kPlane = 64 * C, kPitch = 4 * kPlane;
@@ -54,13 +57,13 @@ __global__ __launch_bounds__(64 * kBackSeg / T) void bwd_kernel(TileArgs p, RecB
   }
   if (span.live > 0) {
     const auto load = [&](const RecIn& in, const int8_t* q, const float* s, In<IO, C, KEPT>(&v)[T]) {
-      load_tile<IO, C, T, KEPT>(Walk<IO, C, KEPT>(a, in, q, s, b, span, at), span.live, v);
+      load_tile<IO, C, T>(a, in, q, s, b, span, at, v);
     };
     load(a.g, a.kept.g, a.kept.gs, g);
     load(a.x, a.kept.x, a.kept.xs, x);
     if (IGATE) load(a.i, a.kept.i, a.kept.is, i);
     const RecIn back{w.dout, a.len * a.dim, a.dim};
-    load_tile<IO, C, T, false>(Walk<IO, C, false>(a, back, nullptr, nullptr, b, span, at), span.live, d);
+    load_tile<IO, C, T>(a, back, nullptr, nullptr, b, span, at, d);
     if (ZGATE) load(a.z, a.kept.z, a.kept.zs, z);
 #pragma unroll
     for (int j = 0; j < T; ++j) {
@@ -177,9 +180,11 @@ __global__ __launch_bounds__(64 * kBackSeg / T) void bwd_kernel(TileArgs p, RecB
       }
   }
   const int64_t row = b * a.len * a.dim * int64_t(sizeof(IO));
-  const unsigned lane_at = unsigned(ch) * unsigned(sizeof(IO));
-  const auto put = [&](void* out, int64_t token, const float (&v)[C]) {  // the token's place is the same in all lanes
-    store_any<IO, C>(reinterpret_cast<IO*>(static_cast<char*>(out) + row + token * a.dim * int64_t(sizeof(IO)) + lane_at),
+  const unsigned step = unsigned(a.dim) * unsigned(sizeof(IO)), lane_at = unsigned(ch) * unsigned(sizeof(IO));
+  const Rows rows(span);
+  const int64_t lowest = row + (span.live > 0 ? rows.lowest(span) : 0) * a.dim * int64_t(sizeof(IO));
+  const auto put = [&](void* out, int j, const float (&v)[C]) {
+    store_any<IO, C>(reinterpret_cast<IO*>(static_cast<char*>(out) + lowest + (rows.at(j) * step + lane_at)),
                      packed<IO, C>(v));
   };
 #pragma unroll
@@ -216,14 +221,26 @@ __global__ __launch_bounds__(64 * kBackSeg / T) void bwd_kernel(TileArgs p, RecB
         oi[c] = dw * sx * (1.0f - s);
       }
     }
-    if (on && span.k0 + j < a.len) {
-      const int64_t token = span.place(j);
-      put(w.dx, token, ox);
-      put(w.dg, token, og);
-      if (IGATE) put(w.di, token, oi);
-      if (ZGATE) put(w.dz, token, oz);
+    if (on && j < span.live) {
+      put(w.dx, j, ox);
+      put(w.dg, j, og);
+      if (IGATE) put(w.di, j, oi);
+      if (ZGATE) put(w.dz, j, oz);
     }
     __builtin_amdgcn_sched_barrier(0);
+  }
+  if (span.live < T) {               // zeros past the row's end
+    for (int j = span.live; j < T; ++j) {
+      if (!on || span.k0 + j >= a.len) continue;
+      const int64_t to = row + (span.k0 + j) * a.dim * int64_t(sizeof(IO)) + lane_at;
+      const auto zero = [&](void* out) {
+        store_any<IO, C>(reinterpret_cast<IO*>(static_cast<char*>(out) + to), typename Vec<IO, C>::V{});
+      };
+      zero(w.dx);
+      zero(w.dg);
+      if (IGATE) zero(w.di);
+      if (ZGATE) zero(w.dz);
+    }
   }
   if (GATED && w.dlam) {             // over the block's waves, in order
     __syncthreads();
@@ -251,11 +268,11 @@ struct BackPlan {
 
 inline BackPlan back_plan(int64_t batch, int64_t len, int64_t dim, bool kept) {
   BackPlan p;
-  p.c = channels_of(dim);
+  p.c = back_channels(dim, kept);
   p.groups = up(dim, 64 * p.c);
-  const int64_t tiles = up(len, back_tokens(p.c, kept)), row = batch * p.groups * 64 * p.c;
-  p.nseg = up(len, kBackSeg);
-  p.waves = p.nseg > 1 ? kBackSeg / back_tokens(p.c, kept) : int(tiles);
+  const int64_t tiles = up(len, back_tokens(kept)), row = batch * p.groups * 64 * p.c;
+  p.nseg = up(tiles, kBackWaves);
+  p.waves = p.nseg > 1 ? kBackWaves : int(tiles);
   p.words = p.nseg > 1 ? (p.nseg + p.nseg / kRun) * row : 0;
   p.off_words = 256;
   p.off_entry = p.off_words + size_t(p.words) * 16;
@@ -272,30 +289,36 @@ hipError_t bwd(const RecBwdArgs& w, const BackPlan& plan, char* workspace, hipSt
   unsigned* ticket = reinterpret_cast<unsigned*>(workspace);
   float* partial = reinterpret_cast<float*>(workspace + plan.off_partial);
   TileArgs p{a, words, words + plan.nseg * row, ticket, reinterpret_cast<float*>(workspace + plan.off_entry),
-             int(plan.nseg), unsigned(plan.groups)};
+             0, int(plan.nseg), unsigned(plan.groups)};
   const bool split = plan.nseg > 1, igate = KEPT ? a.kept.i != nullptr : a.i.p != nullptr,
              zgate = KEPT ? a.kept.z != nullptr : a.z.p != nullptr;
   if (split) {
     const int64_t n = plan.words, blocks = up(n, 256 * 4);
     clear_kernel<<<dim3(unsigned(blocks < 2048 ? blocks : 2048)), 256, 0, stream>>>(reinterpret_cast<uint4*>(words), n,
                                                                                     ticket);
-    const int waves = kBackSeg / kStateTokens;
-    const dim3 grid(unsigned((plan.nseg - 1) * a.batch * plan.groups));
+    // before the last segment only; its maps and states need no more room than the adjoints'
+    const int64_t tokens = (plan.nseg - 1) * kBackWaves * back_tokens(KEPT) + 1, tiles = up(tokens, state_tokens(C, KEPT));
+    const int waves = tiles < kStateWaves ? int(tiles) : kStateWaves;
+    p.nseg = int(up(tiles, waves));
+    p.states = p.maps + p.nseg * row;
+    p.entry_step = kBackWaves * back_tokens(KEPT);
+    const dim3 grid(unsigned(p.nseg * a.batch * plan.groups));
     by_flag(a.lam != nullptr, [&](auto gated) {
       by_flag(igate, [&](auto ig) {
-        fwd_kernel<IO, C, kStateTokens, decltype(gated)::value, decltype(ig)::value, false, false, KEPT, false>
+        fwd_kernel<IO, C, state_tokens(C, KEPT), decltype(gated)::value, decltype(ig)::value, false, false, KEPT, false>
             <<<grid, waves * 64, size_t(waves) * 2 * 64 * C * 4, stream>>>(p);
       });
     });
     p.maps += plan.words;
-    p.states += plan.words;
+    p.states = p.maps + plan.nseg * row;
+    p.nseg = int(plan.nseg);
     ++p.ticket;
   }
   const dim3 grid(unsigned(plan.nseg * a.batch * plan.groups));
   by_flag(a.lam != nullptr, [&](auto gated) {
     by_flag(igate, [&](auto ig) {
       by_flag(zgate, [&](auto zg) {
-        bwd_kernel<IO, C, back_tokens(C, KEPT), decltype(gated)::value, decltype(ig)::value, decltype(zg)::value, KEPT>
+        bwd_kernel<IO, C, back_tokens(KEPT), decltype(gated)::value, decltype(ig)::value, decltype(zg)::value, KEPT>
             <<<grid, plan.waves * 64, size_t(plan.waves) * 4 * 64 * C * 4, stream>>>(p, w, partial);
       });
     });

@@ -15,8 +15,9 @@ __global__ __launch_bounds__(256) void through_kernel(const float* from, float* 
 
 size_t rec_bwd_workspace(int64_t batch, int64_t len, int64_t dim, bool) {
   if (len == 0) return 0;
-  // the same words and sums whether the inputs were kept or not
-  return rec::back_plan(batch, len, dim, false).bytes;
+  // whichever of the inputs themselves and what was kept of them needs more
+  const size_t x = rec::back_plan(batch, len, dim, false).bytes, k = rec::back_plan(batch, len, dim, true).bytes;
+  return x > k ? x : k;
 }
 
 hipError_t launch_rec_bwd(const RecBwdArgs& w, char* workspace, hipStream_t stream) {

@@ -14,6 +14,7 @@ namespace {
 
 using namespace sscan::check;
 
+constexpr int64_t kMaxStride = int64_t(1) << 26;  // elements between tokens: a tile's sixteen stay within 2^32 bytes
 constexpr int64_t kMaxLen = int64_t(1) << 30, kMaxDim = int64_t(1) << 24, kMaxTiles = int64_t(1) << 22;
 
 int64_t blocks_of(int64_t size) { return (size + sscan::kPackBlock - 1) / sscan::kPackBlock; }
@@ -76,8 +77,9 @@ int view_rec(const sscan_rec_params* p, bool kept, RecView* w) {
     if (!aligned(ptr[k], w->esz)) return SSCAN_ERR_ALIGN;
     const int64_t dims[2] = {p->batch, p->len}, e = extent(dims, strides[k], 2, p->dim);
     if (e < 0) return SSCAN_ERR_SHAPE;
+    if (p->len > 1 && strides[k][1] >= kMaxStride) return SSCAN_ERR_UNSUPPORTED;  // a single token's is never used
     w->in[k] = range_of(ptr[k], w->no_rows || w->no_tokens ? 0 : size_t(e) * w->esz);
-    in[k] = sscan::RecIn{ptr[k], strides[k][0], strides[k][1]};
+    in[k] = sscan::RecIn{ptr[k], strides[k][0], p->len > 1 ? strides[k][1] : 0};
   }
   w->lam = range_of(p->lam, w->lam_bytes);
   w->lengths = range_of(p->lengths, size_t(p->batch) * 4);

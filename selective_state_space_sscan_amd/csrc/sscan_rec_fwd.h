@@ -26,7 +26,7 @@ __device__ __forceinline__ unsigned block_max(unsigned m) {
 // finds the state that enters the segment (from the row's segments before, where there are
 // any) and from it those that enter the waves, and every wave walks its tokens once more,
 // now from its state, and answers.  OUT: outputs are
-// wanted, not the states between segments alone (whose last segment has no block).  KEPT:
+// wanted, not the states before every entry_step-th token alone.  KEPT:
 // the inputs come in 8 bits.  KEEP: they are left in 8 bits.
 template <typename IO, int C, int T, bool GATED, bool IGATE, bool ZGATE, bool OUT, bool KEPT, bool KEEP>
 __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
@@ -48,26 +48,39 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
 #pragma unroll
   for (int c = 0; c < C; ++c) rate[c] = GATED ? decay_rate(a.lam, at + c, a.c) : 0.0f;
 
+  // A tensor's tokens in 8 bits.  A block of 64 channels lies in kBlockLanes lanes, which all
+  // have its largest element; lane j of them takes token j's, so that one evaluation gives all
+  // the tile's scales, and hands them back.
   const auto keep = [&](const In<IO, C, KEPT>(&v)[T], int8_t* q, float* s) {
-    const int64_t blocks = (a.dim + kPackBlock - 1) / kPackBlock;
+    constexpr int kBlockLanes = 64 / C;
+    const int first = lane / kBlockLanes * kBlockLanes, nth = lane - first;
+    unsigned top = 0;
 #pragma unroll
     for (int j = 0; j < T; ++j) {
       unsigned m = 0;
 #pragma unroll
       for (int c = 0; c < C; ++c) m = max(m, magnitude(v[j].get(c)));
-      const Scale scale(block_max<C>(on ? m : 0));
+      m = block_max<C>(on ? m : 0);
+      top = nth == j ? m : top;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const Scale scale(top);
+    const int64_t blocks = (a.dim + kPackBlock - 1) / kPackBlock, block = group * C + lane / kBlockLanes;
+    if (nth < span.live && block < blocks) s[(b * a.len + span.place(nth)) * blocks + block] = scale.step;
+    const Rows rows(span);
+    int8_t* to = q + (b * a.len + rows.lowest(span)) * a.dim;  // the same in all lanes
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const float per = __shfl(scale.per, first + j);
       typename Vec<int8_t, C>::V k;
       if constexpr (C == 1) {
-        k = int8_t(scale.steps(v[j].get(0)));
+        k = steps_of<IO>(v[j].get(0), per);
       } else {
 #pragma unroll
-        for (int c = 0; c < C; ++c) k[c] = int8_t(scale.steps(v[j].get(c)));
+        for (int c = 0; c < C; ++c) k[c] = steps_of<IO>(v[j].get(c), per);
       }
-      if (j < span.live && on) {
-        const int64_t row = b * a.len + span.place(j);
-        store_any<int8_t, C>(q + row * a.dim + ch, k);
-        if (ch % kPackBlock == 0) s[row * blocks + ch / kPackBlock] = scale.step;
-      }
+      if (j < span.live && on) store_any<int8_t, C>(to + (rows.at(j) * unsigned(a.dim) + unsigned(ch)), k);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
   float A[T][C], U[T][C];
@@ -75,7 +88,7 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
   if (span.live > 0) {
     In<IO, C, KEPT> x[T], g[T], i[T];
     const auto load = [&](const RecIn& in, const int8_t* q, const float* s, In<IO, C, KEPT>(&v)[T]) {
-      load_tile<IO, C, T, KEPT>(Walk<IO, C, KEPT>(a, in, q, s, b, span, at), span.live, v);
+      load_tile<IO, C, T>(a, in, q, s, b, span, at, v);
     };
     load(a.g, a.kept.g, a.kept.gs, g);
     load(a.x, a.kept.x, a.kept.xs, x);
@@ -154,20 +167,23 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
 #pragma unroll
       for (int c = 0; c < C; ++c) publish(p.states + int64_t(seg / kRun) * pitch + place + c, 0, h[c]);
     }
-    if (!OUT) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) p.entry[(seg + 1) * pitch + place + c] = h[c];
-    }
     if (OUT && seg == p.nseg - 1 && on) {
 #pragma unroll
       for (int c = 0; c < C; ++c) a.h_last[b * a.dim + ch + c] = h[c];
     }
   }
-  if (!OUT) return;
   __syncthreads();
   float h[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) h[c] = mine[c * 64];
+  if (!OUT) {
+    if (span.k0 % p.entry_step == 0 && span.k0 < a.len) {
+      const int64_t pitch = a.batch * p.groups * (64 * C), place = (b * p.groups + group) * (64 * C) + lane * C;
+#pragma unroll
+      for (int c = 0; c < C; ++c) p.entry[span.k0 / p.entry_step * pitch + place + c] = h[c];
+    }
+    return;
+  }
   char* row = static_cast<char*>(a.out) + b * a.len * a.dim * int64_t(sizeof(IO));  // the same in all lanes
   const unsigned place = unsigned(ch) * unsigned(sizeof(IO));
   const auto answer = [&](int j) {
@@ -183,23 +199,22 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
     }
     return packed<IO, C>(y);
   };
-  if (span.live == T) {
-    char* to = row + span.place(0) * a.dim * int64_t(sizeof(IO));
-    const int64_t step = (span.rev ? -a.dim : a.dim) * int64_t(sizeof(IO));
+  if (span.live > 0) {
+    const Rows rows(span);
+    char* to = row + rows.lowest(span) * a.dim * int64_t(sizeof(IO));
+    const unsigned step = unsigned(a.dim) * unsigned(sizeof(IO));
 #pragma unroll
     for (int j = 0; j < T; ++j) {
       const auto y = answer(j);
-      if (on) store_any<IO, C>(reinterpret_cast<IO*>(to + place), y);
-      to += step;
+      if (on && j < span.live) store_any<IO, C>(reinterpret_cast<IO*>(to + (rows.at(j) * step + place)), y);
       __builtin_amdgcn_sched_barrier(0);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < T; ++j) {
-      const auto y = j < span.live ? answer(j) : typename Vec<IO, C>::V{};
+  }
+  if (span.live < T) {               // zeros past the row's end
+    for (int j = span.live; j < T; ++j)
       if (on && span.k0 + j < a.len)
-        store_any<IO, C>(reinterpret_cast<IO*>(row + span.place(j) * a.dim * int64_t(sizeof(IO)) + place), y);
-    }
+        store_any<IO, C>(reinterpret_cast<IO*>(row + (span.k0 + j) * a.dim * int64_t(sizeof(IO)) + place),
+                         typename Vec<IO, C>::V{});
   }
 }
 
@@ -231,7 +246,7 @@ template <typename IO, int C, bool KEEP>
 hipError_t fwd(const RecArgs& a, const Plan& plan, char* workspace, hipStream_t stream) {
   uint64_t* words = reinterpret_cast<uint64_t*>(workspace + 256);
   const TileArgs p{a, words, words + plan.nseg * a.batch * plan.groups * 64 * C, reinterpret_cast<unsigned*>(workspace),
-                   nullptr, int(plan.nseg), unsigned(plan.groups)};
+                   nullptr, 0, int(plan.nseg), unsigned(plan.groups)};
   const dim3 grid(unsigned(plan.nseg * a.batch * plan.groups)), block(unsigned(plan.waves * 64));
   const size_t lds = size_t(plan.waves) * 2 * 64 * C * 4;
   if (plan.nseg > 1) {

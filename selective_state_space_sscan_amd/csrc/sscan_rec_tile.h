@@ -39,7 +39,8 @@ struct TileArgs {
   uint64_t* maps;                    // [nseg][batch][groups * 64 C]
   uint64_t* states;                  // [runs][batch][groups * 64 C]: the state that leaves a run
   unsigned* ticket;                  // segments handed out
-  float* entry;                      // [nseg][batch][groups * 64 C]: states that enter the segments (from the second on)
+  float* entry;                      // [ceil(len / entry_step)][batch][groups * 64 C]: the gradients' entry states
+  int entry_step;
   int nseg;
   unsigned groups;                   // of 64 C channels
 };
@@ -207,59 +208,46 @@ struct Span {
   __device__ __forceinline__ int64_t place(int j) const { return rev && k0 + j < n ? n - 1 - (k0 + j) : k0 + j; }
 };
 
-// A walk over one input's tokens in the order of the scan: the address of a token is the same
-// in all lanes (scalar registers), a lane adds its channels' offset.
-template <typename IO, int C, bool KEPT>
-struct Walk {
-  const char* p;
-  int64_t step;
-  unsigned lane;
-  __device__ __forceinline__ Walk(const RecArgs& a, const RecIn& in, const int8_t*, const float*, int64_t b, const Span& s,
-                                  int64_t ch)
-      : p(static_cast<const char*>(in.p) + (b * in.b + s.place(0) * in.t) * int64_t(sizeof(IO))),
-        step((s.rev ? -in.t : in.t) * int64_t(sizeof(IO))), lane(unsigned(ch) * unsigned(sizeof(IO))) {}
-  __device__ __forceinline__ In<IO, C, KEPT> load() const {
-    return {load_any<IO, C>(reinterpret_cast<const IO*>(p + lane))};
+// One input's tokens of a tile: a scalar address of the lowest of them, and 32-bit offsets from
+// there (the check of the arguments keeps sixteen tokens within 2^32 bytes).  Token j lies
+// at(j) tokens above it; where the tile has fewer, its last one stands for those missing.
+struct Rows {
+  int live, rev;
+  __device__ __forceinline__ explicit Rows(const Span& s) : live(s.live), rev(int(s.rev)) {}
+  __device__ __forceinline__ unsigned at(int j) const {
+    const int k = j < live ? j : live - 1;
+    return unsigned(rev ? live - 1 - k : k);
   }
-  __device__ __forceinline__ void next(bool more = true) { p += more ? step : 0; }
-};
-template <typename IO, int C>
-struct Walk<IO, C, true> {
-  const int8_t* p;
-  const float* s;
-  int64_t step, sstep;
-  unsigned lane, block;
-  __device__ __forceinline__ Walk(const RecArgs& a, const RecIn&, const int8_t* q, const float* scale, int64_t b,
-                                  const Span& sp, int64_t ch)
-      : lane(unsigned(ch)), block(unsigned(ch) / kPackBlock) {
-    const int64_t blocks = (a.dim + kPackBlock - 1) / kPackBlock, row = b * a.len + sp.place(0);
-    p = q + row * a.dim;
-    s = scale + row * blocks;
-    step = sp.rev ? -a.dim : a.dim;
-    sstep = sp.rev ? -blocks : blocks;
-  }
-  __device__ __forceinline__ In<IO, C, true> load() const { return {load_any<int8_t, C>(p + lane), s[block]}; }
-  __device__ __forceinline__ void next(bool more = true) {
-    p += more ? step : 0;
-    s += more ? sstep : 0;
-  }
+  __device__ __forceinline__ int64_t lowest(const Span& s) const { return s.place(rev ? live - 1 : 0); }
 };
 
-// The walk's T tokens; where the tile has fewer, its last one again.
-template <typename IO, int C, int T, bool KEPT>
-__device__ __forceinline__ void load_tile(Walk<IO, C, KEPT> w, int live, In<IO, C, KEPT> (&v)[T]) {
-  if (live == T) {
+template <typename IO, int C, int T>
+__device__ __forceinline__ void load_tile(const RecArgs& a, const RecIn& in, const int8_t*, const float*, int64_t b,
+                                          const Span& s, int64_t ch, In<IO, C, false> (&v)[T]) {
+  const Rows rows(s);
+  const char* p = static_cast<const char*>(in.p) + (b * in.b + rows.lowest(s) * in.t) * int64_t(sizeof(IO));
+  const unsigned step = unsigned(in.t) * unsigned(sizeof(IO)), lane = unsigned(ch) * unsigned(sizeof(IO));
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-      v[j] = w.load();
-      w.next();
-    }
-  } else {
+  for (int j = 0; j < T; ++j) {
+    v[j].v = load_any<IO, C>(reinterpret_cast<const IO*>(p + (rows.at(j) * step + lane)));
+    __builtin_amdgcn_sched_barrier(0);  // in order: the first tokens are wanted first
+  }
+}
+
+template <typename IO, int C, int T>
+__device__ __forceinline__ void load_tile(const RecArgs& a, const RecIn&, const int8_t* q, const float* scale, int64_t b,
+                                          const Span& s, int64_t ch, In<IO, C, true> (&v)[T]) {
+  const Rows rows(s);
+  const int64_t blocks = (a.dim + kPackBlock - 1) / kPackBlock, row = b * a.len + rows.lowest(s);
+  const int8_t* p = q + row * a.dim;
+  const char* at = reinterpret_cast<const char*>(scale + row * blocks);
+  const unsigned lane = unsigned(ch), block = lane / kPackBlock * 4;
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-      v[j] = w.load();
-      w.next(j + 1 < live);
-    }
+  for (int j = 0; j < T; ++j) {
+    const unsigned k = rows.at(j);
+    v[j].v = load_any<int8_t, C>(p + (k * unsigned(a.dim) + lane));
+    v[j].scale = *reinterpret_cast<const float*>(at + (k * unsigned(blocks * 4) + block));
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
