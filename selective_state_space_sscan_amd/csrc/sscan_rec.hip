@@ -23,7 +23,7 @@ __global__ __launch_bounds__(64) void step_kernel(RecArgs a) {
     const V x = load(a.x), g = load(a.g), i = a.i.p ? load(a.i) : V{}, z = a.z.p ? load(a.z) : V{};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const Decay d = decay<GATED>(part<C>(g, c), GATED ? decay_rate(a.lam, ch + c, a.c) : 0.0f);
+      const Decay d = decay<GATED>(part<C>(g, c), GATED ? decay_rate(a.lam, ch + c, a.c) : 0.0f, true);
       float u = part<C>(x, c) * d.w;
       if (a.i.p) u *= sigmoid(part<C>(i, c));
       y[c] = fmaf(d.a, state[c], u);

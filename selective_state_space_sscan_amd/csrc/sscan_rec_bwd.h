@@ -9,11 +9,16 @@
 namespace sscan {
 namespace rec {
 
-// A segment is eight waves' tiles.  A wave has as many tokens as the registers hold without
-// spilling any; four channels a lane where the inputs come in 8 bits, for whole words of them.
-constexpr int kBackWaves = 8;
+// A segment has 64 tokens: a wave as many as the registers hold without spilling any, a block
+// the waves for the others; four channels a lane where the inputs come in 8 bits, for whole
+// words of them.  Segments of 32 tokens spend more on the words between them (4 x 4096 x 2048
+// from 8 bits 301 us a call, so 265).
+constexpr int kBackSegment = 64;
 constexpr int back_tokens(bool kept) { return kept ? 4 : 8; }
-inline int back_channels(int64_t dim, bool kept) { return kept && dim % 4 == 0 ? 4 : channels_of(dim); }
+constexpr int back_waves(bool kept) { return kBackSegment / back_tokens(kept); }
+inline int back_channels(int64_t dim, bool kept, bool io_bf16) {
+  return kept && io_bf16 && dim % 4 == 0 ? 4 : channels_of(dim);
+}
 // Of a block in the kernel of the states.
 constexpr int state_tokens(int c, bool kept) { return c == 4 || (c == 2 && kept) ? 8 : 16; }
 constexpr int kStateWaves = 16;
@@ -24,7 +29,7 @@ constexpr int kStateWaves = 16;
 // loaded and 1 - a (a itself where it has no rounding to lose), walks them once for both
 // maps, and after the exchange once forwards from the state before them and once back.
 template <typename IO, int C, int T, bool GATED, bool IGATE, bool ZGATE, bool KEPT>
-__global__ __launch_bounds__(64 * kBackWaves) void bwd_kernel(TileArgs p, RecBwdArgs w, float* partial) {
+__global__ __launch_bounds__(64 * back_waves(KEPT)) void bwd_kernel(TileArgs p, RecBwdArgs w, float* partial) {
   extern __shared__ float lds[];     // [waves][4][64 C]: A and H of the states, A and H of the adjoints
   __shared__ unsigned number;
   constexpr int kPlane = 64 * C, kPitch = 4 * kPlane;
@@ -44,9 +49,13 @@ __global__ __launch_bounds__(64 * kBackWaves) void bwd_kernel(TileArgs p, RecBwd
   float rate[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) rate[c] = GATED ? decay_rate(a.lam, at + c, a.c) : 0.0f;
+  const bool far = any_far<C>(rate);
 
   In<IO, C, KEPT> x[T], g[T], i[T], z[T];
   In<IO, C, false> d[T];
+  // sigmoid(i) in the place of i, where registers are left (8 bits and their scales take more)
+  constexpr bool kHold = IGATE && !KEPT, kLate = KEPT;
+  float S[kHold ? T : 1][C];
   float D[T][C], U[T][C];            // 1 - a (or a) and the token's input; later the state before the token
   const auto decay_of = [&](float v) { return GATED ? 1.0f - v : v; };
   float P[C], H[C], M[C];
@@ -56,28 +65,49 @@ __global__ __launch_bounds__(64 * kBackWaves) void bwd_kernel(TileArgs p, RecBwd
     H[c] = M[c] = 0.0f;
   }
   if (span.live > 0) {
-    const auto load = [&](const RecIn& in, const int8_t* q, const float* s, In<IO, C, KEPT>(&v)[T]) {
-      load_tile<IO, C, T>(a, in, q, s, b, span, at, v);
-    };
-    load(a.g, a.kept.g, a.kept.gs, g);
-    load(a.x, a.kept.x, a.kept.xs, x);
-    if (IGATE) load(a.i, a.kept.i, a.kept.is, i);
+    const Rows rows(span);
+    const Loader<IO, C, KEPT> gs(a, a.g, a.kept.g, a.kept.gs, b, span, at), xs(a, a.x, a.kept.x, a.kept.xs, b, span, at),
+        is(a, a.i, a.kept.i, a.kept.is, b, span, at), zs(a, a.z, a.kept.z, a.kept.zs, b, span, at);
     const RecIn back{w.dout, a.len * a.dim, a.dim};
-    load_tile<IO, C, T>(a, back, nullptr, nullptr, b, span, at, d);
-    if (ZGATE) load(a.z, a.kept.z, a.kept.zs, z);
+    const Loader<IO, C, false> ds(a, back, nullptr, nullptr, b, span, at);
+    // token by token: the first are computed while the last are on their way
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const unsigned k = rows.at(j);
+      g[j] = gs.row(k);
+      if (IGATE) i[j] = is.row(k);
+      x[j] = xs.row(k);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const auto load_back = [&] {
+#pragma unroll
+      for (int j = T - 1; j >= 0; --j) {
+        const unsigned k = rows.at(j);
+        d[j] = ds.row(k);
+        if (ZGATE) z[j] = zs.row(k);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    if (!kLate) load_back();
 #pragma unroll
     for (int j = 0; j < T; ++j) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const Decay q = decay<GATED>(g[j].get(c), rate[c]);
+        const Decay q = decay<GATED>(g[j].get(c), rate[c], far);
         float u = x[j].get(c);
         if (GATED) u *= q.w;
-        if (IGATE) u *= sigmoid(i[j].get(c));
+        if (IGATE) {
+          const float s = sigmoid(i[j].get(c));
+          u *= s;
+          if (kHold) S[j][c] = s;
+        }
         D[j][c] = GATED ? q.loss : q.a;
         U[j][c] = u;
+        if (C == 4) __builtin_amdgcn_sched_barrier(0);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    if (kLate) load_back();
     if (span.live < T) {             // tokens past the row's end leave state and adjoint alone
 #pragma unroll
       for (int j = 0; j < T; ++j)
@@ -114,7 +144,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void bwd_kernel(TileArgs p, RecBwd
   }
   as_loaded(g);
   as_loaded(x);
-  if (IGATE) as_loaded(i);
+  if (IGATE && !kHold) as_loaded(i);
   as_loaded(d);
   if (ZGATE) as_loaded(z);
   float* mine = lds + wave * kPitch + lane;
@@ -194,7 +224,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void bwd_kernel(TileArgs p, RecBwd
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const float A = decay_of(D[j][c]), before = U[j][c];
-        const float v = x[j].get(c), s = IGATE ? sigmoid(i[j].get(c)) : 1.0f;
+        const float v = x[j].get(c), s = kHold ? S[kHold ? j : 0][c] : IGATE ? sigmoid(i[j].get(c)) : 1.0f;
         float e = d[j].get(c);
         if (ZGATE) {
           const float q = z[j].get(c), sq = sigmoid(q);
@@ -208,9 +238,9 @@ __global__ __launch_bounds__(64 * kBackWaves) void bwd_kernel(TileArgs p, RecBwd
         const float sx = s * v;
         if (GATED) {
           const float loss = D[j][c], r = sigmoid(g[j].get(c));
-          wgt = __builtin_amdgcn_sqrtf(loss * (2.0f - loss));
-          const float slope = wgt > 0.0f ? A * A * __builtin_amdgcn_rcpf(wgt) : 0.0f;
-          dlog = fmaf(-adj * sx, slope, dlog);
+          const float w2 = loss * (2.0f - loss), inv = w2 > 0.0f ? __builtin_amdgcn_rsqf(w2) : 0.0f;  // 1 / w
+          wgt = w2 * inv;
+          dlog = fmaf(-adj * sx, A * A * inv, dlog);
           og[c] = -dlog * rate[c] * r * (1.0f - r);
           dlam[c] = fmaf(-dlog, r, dlam[c]);
         } else {
@@ -219,6 +249,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void bwd_kernel(TileArgs p, RecBwd
         const float dw = adj * wgt;
         ox[c] = dw * s;
         oi[c] = dw * sx * (1.0f - s);
+        if (C == 4) __builtin_amdgcn_sched_barrier(0);  // four channels side by side would spill
       }
     }
     if (on && j < span.live) {
@@ -266,13 +297,13 @@ struct BackPlan {
   size_t off_words, off_entry, off_partial, bytes;
 };
 
-inline BackPlan back_plan(int64_t batch, int64_t len, int64_t dim, bool kept) {
+inline BackPlan back_plan(int64_t batch, int64_t len, int64_t dim, bool kept, bool io_bf16) {
   BackPlan p;
-  p.c = back_channels(dim, kept);
+  p.c = back_channels(dim, kept, io_bf16);
   p.groups = up(dim, 64 * p.c);
   const int64_t tiles = up(len, back_tokens(kept)), row = batch * p.groups * 64 * p.c;
-  p.nseg = up(tiles, kBackWaves);
-  p.waves = p.nseg > 1 ? kBackWaves : int(tiles);
+  p.nseg = up(len, kBackSegment);
+  p.waves = p.nseg > 1 ? back_waves(kept) : int(tiles);
   p.words = p.nseg > 1 ? (p.nseg + p.nseg / kRun) * row : 0;
   p.off_words = 256;
   p.off_entry = p.off_words + size_t(p.words) * 16;
@@ -297,11 +328,11 @@ hipError_t bwd(const RecBwdArgs& w, const BackPlan& plan, char* workspace, hipSt
     clear_kernel<<<dim3(unsigned(blocks < 2048 ? blocks : 2048)), 256, 0, stream>>>(reinterpret_cast<uint4*>(words), n,
                                                                                     ticket);
     // before the last segment only; its maps and states need no more room than the adjoints'
-    const int64_t tokens = (plan.nseg - 1) * kBackWaves * back_tokens(KEPT) + 1, tiles = up(tokens, state_tokens(C, KEPT));
+    const int64_t tokens = (plan.nseg - 1) * kBackSegment + 1, tiles = up(tokens, state_tokens(C, KEPT));
     const int waves = tiles < kStateWaves ? int(tiles) : kStateWaves;
     p.nseg = int(up(tiles, waves));
     p.states = p.maps + p.nseg * row;
-    p.entry_step = kBackWaves * back_tokens(KEPT);
+    p.entry_step = kBackSegment;
     const dim3 grid(unsigned(p.nseg * a.batch * plan.groups));
     by_flag(a.lam != nullptr, [&](auto gated) {
       by_flag(igate, [&](auto ig) {

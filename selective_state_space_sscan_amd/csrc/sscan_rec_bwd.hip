@@ -13,10 +13,10 @@ __global__ __launch_bounds__(256) void through_kernel(const float* from, float* 
 
 }  // namespace rec
 
-size_t rec_bwd_workspace(int64_t batch, int64_t len, int64_t dim, bool) {
+size_t rec_bwd_workspace(int64_t batch, int64_t len, int64_t dim, bool io_bf16) {
   if (len == 0) return 0;
   // whichever of the inputs themselves and what was kept of them needs more
-  const size_t x = rec::back_plan(batch, len, dim, false).bytes, k = rec::back_plan(batch, len, dim, true).bytes;
+  const size_t x = rec::back_plan(batch, len, dim, false, io_bf16).bytes, k = rec::back_plan(batch, len, dim, true, io_bf16).bytes;
   return x > k ? x : k;
 }
 
@@ -28,7 +28,7 @@ hipError_t launch_rec_bwd(const RecBwdArgs& w, char* workspace, hipStream_t stre
     return hipGetLastError();
   }
   const bool kept = a.kept.x != nullptr;
-  const rec::BackPlan p = rec::back_plan(a.batch, a.len, a.dim, kept);
+  const rec::BackPlan p = rec::back_plan(a.batch, a.len, a.dim, kept, a.io_bf16);
   if (kept) return rec::launch_bwd_kept(w, p, workspace, stream);
   return rec::by_lane(p.c, a.io_bf16, [&](auto io, auto c) {
     return rec::bwd<decltype(io), decltype(c)::value, false>(w, p, workspace, stream);

@@ -45,12 +45,13 @@ __device__ __forceinline__ float small_loss(float m) {
 }
 
 // 1 - exp(-m): where the difference would lose digits by the series.  Decays near 1 are taken
-// as 1 minus this: their rounding is what a long sum of states sees of them.  Both ways are
-// evaluated for every token; a second copy of the code for waves of slow channels only, without
-// the exponential, took longer (8 x 4096 x 4096 forward 330 us, so 289).
-__device__ __forceinline__ float decay_loss(float m) {
-  const float p = small_loss(m), q = 1.0f - __builtin_amdgcn_exp2f(m * -kLog2e);
-  return fabsf(m) < 0.25f ? p : q;
+// as 1 minus this: their rounding is what a long sum of states sees of them.  `far`: whether
+// any channel of the wave decays that fast at all (its rate, the largest m of its tokens,
+// reaches 1/4); where none does, the exponential is passed over.
+__device__ __forceinline__ float decay_loss(float m, bool far) {
+  float p = small_loss(m);
+  if (far) p = fabsf(m) < 0.25f ? p : 1.0f - __builtin_amdgcn_exp2f(m * -kLog2e);
+  return p;
 }
 
 // The decay of a token: a, and with lam also 1 - a and w = sqrt(1 - a^2).
@@ -59,14 +60,23 @@ struct Decay {
 };
 
 template <bool GATED>
-__device__ __forceinline__ Decay decay(float g, float rate) {
+__device__ __forceinline__ Decay decay(float g, float rate, bool far) {
   if constexpr (GATED) {
-    const float loss = decay_loss(rate * sigmoid(g));
+    const float loss = decay_loss(rate * sigmoid(g), far);
     return {1.0f - loss, loss, __builtin_amdgcn_sqrtf(loss * (2.0f - loss))};
   } else {
     // -inf: m = inf, whose series is not taken
     return {fabsf(g) < 0.25f ? 1.0f - small_loss(-g) : __builtin_amdgcn_exp2f(g * kLog2e), 0.0f, 1.0f};
   }
+}
+
+// Whether a wave has a channel whose rate reaches 1/4 (or is no number).
+template <int C>
+__device__ __forceinline__ bool any_far(const float (&rate)[C]) {
+  bool far = false;
+#pragma unroll
+  for (int c = 0; c < C; ++c) far = far || !(rate[c] < 0.25f);
+  return __ballot(far) != 0;
 }
 
 }  // namespace rec

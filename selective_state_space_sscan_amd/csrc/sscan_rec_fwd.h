@@ -47,6 +47,7 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
   float rate[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) rate[c] = GATED ? decay_rate(a.lam, at + c, a.c) : 0.0f;
+  const bool far = any_far<C>(rate);
 
   // A tensor's tokens in 8 bits.  A block of 64 channels lies in kBlockLanes lanes, which all
   // have its largest element; lane j of them takes token j's, so that one evaluation gives all
@@ -62,7 +63,6 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
       for (int c = 0; c < C; ++c) m = max(m, magnitude(v[j].get(c)));
       m = block_max<C>(on ? m : 0);
       top = nth == j ? m : top;
-      __builtin_amdgcn_sched_barrier(0);
     }
     const Scale scale(top);
     const int64_t blocks = (a.dim + kPackBlock - 1) / kPackBlock, block = group * C + lane / kBlockLanes;
@@ -87,12 +87,18 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
   In<IO, C, KEPT> z[T];
   if (span.live > 0) {
     In<IO, C, KEPT> x[T], g[T], i[T];
-    const auto load = [&](const RecIn& in, const int8_t* q, const float* s, In<IO, C, KEPT>(&v)[T]) {
-      load_tile<IO, C, T>(a, in, q, s, b, span, at, v);
-    };
-    load(a.g, a.kept.g, a.kept.gs, g);
-    load(a.x, a.kept.x, a.kept.xs, x);
-    if (IGATE) load(a.i, a.kept.i, a.kept.is, i);
+    const Rows rows(span);
+    const Loader<IO, C, KEPT> gs(a, a.g, a.kept.g, a.kept.gs, b, span, at), xs(a, a.x, a.kept.x, a.kept.xs, b, span, at),
+        is(a, a.i, a.kept.i, a.kept.is, b, span, at);
+    // token by token: the first are computed while the last are on their way
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const unsigned k = rows.at(j);
+      g[j] = gs.row(k);
+      if (IGATE) i[j] = is.row(k);
+      x[j] = xs.row(k);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     if (KEEP) {
       keep(g, a.kept.g, a.kept.gs);
       keep(x, a.kept.x, a.kept.xs);
@@ -105,7 +111,7 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
     for (int j = 0; j < T; ++j) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const Decay d = decay<GATED>(g[j].get(c), rate[c]);
+        const Decay d = decay<GATED>(g[j].get(c), rate[c], far);
         float u = x[j].get(c);
         if (GATED) u *= d.w;
         if (IGATE) u *= sigmoid(i[j].get(c));
@@ -115,7 +121,14 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
       __builtin_amdgcn_sched_barrier(0);  // a token at a time: several would need more registers than there are
     }
     // on their way while the state comes; with the others they would not fit the registers
-    if (OUT && ZGATE) load(a.z, a.kept.z, a.kept.zs, z);
+    if (OUT && ZGATE) {
+      const Loader<IO, C, KEPT> zs(a, a.z, a.kept.z, a.kept.zs, b, span, at);
+#pragma unroll
+      for (int j = 0; j < T; ++j) {
+        z[j] = zs.row(rows.at(j));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
     if (KEEP && ZGATE) {
       keep(z, a.kept.z, a.kept.zs);
       as_loaded(z);

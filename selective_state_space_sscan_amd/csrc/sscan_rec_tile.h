@@ -56,11 +56,12 @@ __device__ __forceinline__ uint32_t map_bits(float a) {
 }
 
 // Reads n words `pitch` apart, C a lane, in order, as soon as they are there: f(k, c, A, H)
-// for each.  All lanes of a wave go on together; four places are read at once.  A wait of
+// for each.  All lanes of a wave go on together; four places (two, of
+// four channels) are read at once.  A wait of
 // 2^24 reads is many seconds long and cannot happen; it ends, with NaN, instead of never.
 template <int C, typename F>
 __device__ __forceinline__ void read_words(const uint64_t* at, int64_t pitch, int n, F f) {
-  constexpr int kAhead = 4;
+  constexpr int kAhead = C == 4 ? 2 : 4;
   int done = 0;
   for (int tries = 0; done < n; ++tries) {
     uint64_t w[kAhead][C];
@@ -190,6 +191,7 @@ __device__ __forceinline__ void as_loaded(In<IO, C, KEPT> (&x)[T]) {
       for (uint32_t& w : raw.w) asm("" : "+v"(w));
       __builtin_memcpy(&x[j].v, &raw, sizeof(raw));
     }  // a single narrow value has no copy to save
+    if constexpr (KEPT) asm("" : "+v"(x[j].scale));
   }
 }
 
@@ -221,35 +223,37 @@ struct Rows {
   __device__ __forceinline__ int64_t lowest(const Span& s) const { return s.place(rev ? live - 1 : 0); }
 };
 
-template <typename IO, int C, int T>
-__device__ __forceinline__ void load_tile(const RecArgs& a, const RecIn& in, const int8_t*, const float*, int64_t b,
-                                          const Span& s, int64_t ch, In<IO, C, false> (&v)[T]) {
-  const Rows rows(s);
-  const char* p = static_cast<const char*>(in.p) + (b * in.b + rows.lowest(s) * in.t) * int64_t(sizeof(IO));
-  const unsigned step = unsigned(in.t) * unsigned(sizeof(IO)), lane = unsigned(ch) * unsigned(sizeof(IO));
-#pragma unroll
-  for (int j = 0; j < T; ++j) {
-    v[j].v = load_any<IO, C>(reinterpret_cast<const IO*>(p + (rows.at(j) * step + lane)));
-    __builtin_amdgcn_sched_barrier(0);  // in order: the first tokens are wanted first
+template <typename IO, int C, bool KEPT>
+struct Loader {
+  const char* p;
+  unsigned step, lane;
+  __device__ __forceinline__ Loader(const RecArgs&, const RecIn& in, const int8_t*, const float*, int64_t b, const Span& s,
+                                    int64_t ch)
+      : p(static_cast<const char*>(in.p) + (b * in.b + Rows(s).lowest(s) * in.t) * int64_t(sizeof(IO))),
+        step(unsigned(in.t) * unsigned(sizeof(IO))), lane(unsigned(ch) * unsigned(sizeof(IO))) {}
+  __device__ __forceinline__ In<IO, C, false> row(unsigned k) const {
+    return {load_any<IO, C>(reinterpret_cast<const IO*>(p + (k * step + lane)))};
   }
-}
-
-template <typename IO, int C, int T>
-__device__ __forceinline__ void load_tile(const RecArgs& a, const RecIn&, const int8_t* q, const float* scale, int64_t b,
-                                          const Span& s, int64_t ch, In<IO, C, true> (&v)[T]) {
-  const Rows rows(s);
-  const int64_t blocks = (a.dim + kPackBlock - 1) / kPackBlock, row = b * a.len + rows.lowest(s);
-  const int8_t* p = q + row * a.dim;
-  const char* at = reinterpret_cast<const char*>(scale + row * blocks);
-  const unsigned lane = unsigned(ch), block = lane / kPackBlock * 4;
-#pragma unroll
-  for (int j = 0; j < T; ++j) {
-    const unsigned k = rows.at(j);
-    v[j].v = load_any<int8_t, C>(p + (k * unsigned(a.dim) + lane));
-    v[j].scale = *reinterpret_cast<const float*>(at + (k * unsigned(blocks * 4) + block));
-    __builtin_amdgcn_sched_barrier(0);
+};
+template <typename IO, int C>
+struct Loader<IO, C, true> {
+  const int8_t* p;
+  const char* scale;
+  unsigned step, lane, scale_step, block;
+  __device__ __forceinline__ Loader(const RecArgs& a, const RecIn&, const int8_t* q, const float* s, int64_t b,
+                                    const Span& sp, int64_t ch)
+      : lane(unsigned(ch)) {
+    const int64_t blocks = (a.dim + kPackBlock - 1) / kPackBlock, row = b * a.len + Rows(sp).lowest(sp);
+    p = q + row * a.dim;
+    scale = reinterpret_cast<const char*>(s + row * blocks);
+    step = unsigned(a.dim);
+    scale_step = unsigned(blocks * 4);
+    block = lane / kPackBlock * 4;
   }
-}
+  __device__ __forceinline__ In<IO, C, true> row(unsigned k) const {
+    return {load_any<int8_t, C>(p + (k * step + lane)), *reinterpret_cast<const float*>(scale + (k * scale_step + block))};
+  }
+};
 
 inline int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
