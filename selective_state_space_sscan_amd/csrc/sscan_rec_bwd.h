@@ -15,13 +15,11 @@ namespace rec {
 // from 8 bits 301 us a call, so 265).
 constexpr int kBackSegment = 64;
 constexpr int back_tokens(bool kept) { return kept ? 4 : 8; }
-constexpr int back_waves(bool kept) { return kBackSegment / back_tokens(kept); }
 inline int back_channels(int64_t dim, bool kept, bool io_bf16) {
   return kept && io_bf16 && dim % 4 == 0 ? 4 : channels_of(dim);
 }
-// Of a block in the kernel of the states.
-constexpr int state_tokens(int c, bool kept) { return c == 4 || (c == 2 && kept) ? 8 : 16; }
-constexpr int kStateWaves = 16;
+constexpr int state_tokens(int c, bool kept, bool few) { return few || c == 4 || (c == 2 && kept) ? 8 : 16; }
+constexpr int kStateWaves = 16;      // of a block in the kernel of the states
 
 // One segment a block.  The adjoint that passes from token t to t - 1 is c_t = a_t (e_t +
 // c_{t+1}), e_t = dout_t silu(z_t): a map of the adjoint that enters a tile from behind, with
@@ -29,7 +27,7 @@ constexpr int kStateWaves = 16;
 // loaded and 1 - a (a itself where it has no rounding to lose), walks them once for both
 // maps, and after the exchange once forwards from the state before them and once back.
 template <typename IO, int C, int T, bool GATED, bool IGATE, bool ZGATE, bool KEPT>
-__global__ __launch_bounds__(64 * back_waves(KEPT)) void bwd_kernel(TileArgs p, RecBwdArgs w, float* partial) {
+__global__ __launch_bounds__(64 * kBackSegment / T) void bwd_kernel(TileArgs p, RecBwdArgs w, float* partial) {
   extern __shared__ float lds[];     // [waves][4][64 C]: A and H of the states, A and H of the adjoints
   __shared__ unsigned number;
   constexpr int kPlane = 64 * C, kPitch = 4 * kPlane;
@@ -292,6 +290,7 @@ __global__ __launch_bounds__(64 * back_waves(KEPT)) void bwd_kernel(TileArgs p, 
 
 struct BackPlan {
   int c, waves;
+  bool few;
   int64_t groups, nseg;
   int64_t words;                     // words of one set of maps and states
   size_t off_words, off_entry, off_partial, bytes;
@@ -301,9 +300,10 @@ inline BackPlan back_plan(int64_t batch, int64_t len, int64_t dim, bool kept, bo
   BackPlan p;
   p.c = back_channels(dim, kept, io_bf16);
   p.groups = up(dim, 64 * p.c);
-  const int64_t tiles = up(len, back_tokens(kept)), row = batch * p.groups * 64 * p.c;
+  p.few = few_tiles(batch, len, p.groups);
+  const int64_t row = batch * p.groups * 64 * p.c;
   p.nseg = up(len, kBackSegment);
-  p.waves = p.nseg > 1 ? back_waves(kept) : int(tiles);
+  p.waves = p.nseg > 1 ? kBackSegment / back_tokens(kept) : int(up(len, back_tokens(kept)));
   p.words = p.nseg > 1 ? (p.nseg + p.nseg / kRun) * row : 0;
   p.off_words = 256;
   p.off_entry = p.off_words + size_t(p.words) * 16;
@@ -328,7 +328,8 @@ hipError_t bwd(const RecBwdArgs& w, const BackPlan& plan, char* workspace, hipSt
     clear_kernel<<<dim3(unsigned(blocks < 2048 ? blocks : 2048)), 256, 0, stream>>>(reinterpret_cast<uint4*>(words), n,
                                                                                     ticket);
     // before the last segment only; its maps and states need no more room than the adjoints'
-    const int64_t tokens = (plan.nseg - 1) * kBackSegment + 1, tiles = up(tokens, state_tokens(C, KEPT));
+    const int each = state_tokens(C, KEPT, plan.few);
+    const int64_t tokens = (plan.nseg - 1) * kBackSegment + 1, tiles = up(tokens, each);
     const int waves = tiles < kStateWaves ? int(tiles) : kStateWaves;
     p.nseg = int(up(tiles, waves));
     p.states = p.maps + p.nseg * row;
@@ -336,8 +337,14 @@ hipError_t bwd(const RecBwdArgs& w, const BackPlan& plan, char* workspace, hipSt
     const dim3 grid(unsigned(p.nseg * a.batch * plan.groups));
     by_flag(a.lam != nullptr, [&](auto gated) {
       by_flag(igate, [&](auto ig) {
-        fwd_kernel<IO, C, state_tokens(C, KEPT), decltype(gated)::value, decltype(ig)::value, false, false, KEPT, false>
-            <<<grid, waves * 64, size_t(waves) * 2 * 64 * C * 4, stream>>>(p);
+        const auto with = [&](auto t) {
+          fwd_kernel<IO, C, decltype(t)::value, decltype(gated)::value, decltype(ig)::value, false, false, KEPT, false>
+              <<<grid, waves * 64, size_t(waves) * 2 * 64 * C * 4, stream>>>(p);
+        };
+        if (each == 8)
+          with(std::integral_constant<int, 8>());
+        else if constexpr (state_tokens(C, KEPT, false) == 16)
+          with(std::integral_constant<int, 16>());
       });
     });
     p.maps += plan.words;

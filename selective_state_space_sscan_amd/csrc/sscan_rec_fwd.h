@@ -233,14 +233,19 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
 
 constexpr int kWaves = 8;            // of a block where rows have several segments
 
-// Channels a lane, and tokens of a wave's tile: what the registers hold without spilling any
-// (the tokens' decays and inputs alone are 2 C T).  The same whether inputs are kept or not:
-// states are joined at the tiles' ends, and outputs are the same bits.
+// Channels a lane, and tokens of a wave's tile: sixteen, which the registers hold without
+// spilling any (the tokens' decays and inputs alone are 2 C T); eight of two float32 channels,
+// and where a call has too few tiles to fill the chip, so that each takes half as long (prompts
+// of 77, 384 channels: @A us, so @B; 2 x 700 x 2048: @C and @D).  The same whether inputs are
+// kept or not: states are joined at the tiles' ends, and outputs are the same bits.
 inline int channels_of(int64_t dim) { return dim % 2 == 0 ? 2 : 1; }
-constexpr int tokens_of(int c, bool io_bf16) { return c == 2 && !io_bf16 ? 8 : 16; }
+constexpr int64_t kFewTiles = 2048;  // half of what the chip holds at once
+
+inline bool few_tiles(int64_t batch, int64_t len, int64_t groups) { return batch * groups * up(len, 16) < kFewTiles; }
+inline int tokens_of(int c, bool io_bf16, bool few) { return few || (c == 2 && !io_bf16) ? 8 : 16; }
 
 struct Plan {
-  int c, waves;
+  int c, tokens, waves;
   int64_t groups, nseg, words;       // bytes of the maps and states
 };
 
@@ -248,7 +253,8 @@ inline Plan plan_of(int64_t batch, int64_t len, int64_t dim, bool io_bf16) {
   Plan p;
   p.c = channels_of(dim);
   p.groups = up(dim, 64 * p.c);
-  const int64_t tiles = up(len, tokens_of(p.c, io_bf16));
+  p.tokens = tokens_of(p.c, io_bf16, few_tiles(batch, len, p.groups));
+  const int64_t tiles = up(len, p.tokens);
   p.waves = tiles <= kMaxWaves ? int(tiles) : kWaves;
   p.nseg = tiles <= kMaxWaves ? 1 : up(tiles, p.waves);
   p.words = p.nseg > 1 ? (p.nseg + p.nseg / kRun) * batch * p.groups * 64 * p.c * 8 : 0;
@@ -269,8 +275,18 @@ hipError_t fwd(const RecArgs& a, const Plan& plan, char* workspace, hipStream_t 
   by_flag(a.lam != nullptr, [&](auto gated) {
     by_flag(a.i.p != nullptr, [&](auto igate) {
       by_flag(a.z.p != nullptr, [&](auto zgate) {
-        fwd_kernel<IO, C, tokens_of(C, sizeof(IO) == 2), decltype(gated)::value, decltype(igate)::value, decltype(zgate)::value, true,
-                   false, KEEP><<<grid, block, lds, stream>>>(p);
+        const auto with = [&](auto tokens) {
+          fwd_kernel<IO, C, decltype(tokens)::value, decltype(gated)::value, decltype(igate)::value,
+                     decltype(zgate)::value, true, false, KEEP><<<grid, block, lds, stream>>>(p);
+        };
+        if constexpr (C == 2 && sizeof(IO) == 4) {
+          with(std::integral_constant<int, 8>());
+        } else {
+          if (plan.tokens == 8)
+            with(std::integral_constant<int, 8>());
+          else
+            with(std::integral_constant<int, 16>());
+        }
       });
     });
   });

@@ -1844,7 +1844,7 @@ def rec_fwd(x, g, i: Optional[torch.Tensor] = None, lam: Optional[torch.Tensor] 
     b, L, d = sizes
     given = out, h_last
     if out is None:
-        out = torch.empty((b, L, d), dtype=x.dtype, device=dev)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         _check(out, "out", dev, x.dtype, (b, L, d))
     if h_last is None:
@@ -1874,7 +1874,7 @@ def rec_step(state, x, g, i: Optional[torch.Tensor] = None, lam: Optional[torch.
     _check(state, "state", dev, torch.float32, (b, d))
     given = out
     if out is None:
-        out = torch.empty((b, d), dtype=x.dtype, device=dev)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         _check(out, "out", dev, x.dtype, (b, d))
     st = lib.sscan_rec_step(p, state.data_ptr(), out.data_ptr(), _stream(dev))
@@ -1973,8 +1973,8 @@ def gated_recurrence(x, g, i: Optional[torch.Tensor] = None, lam: Optional[torch
 
 # ---- layer norm -------------------------------------------------------------------
 
-def _layer_pack(what, x, x_name, residual, residual_dtype, io_dtype, weight, bias, eps):
-    """(packed params, device, (rows, size))"""
+def _layer_check(what, x, x_name, residual, residual_dtype, io_dtype, weight, bias):
+    """Raises what is wrong with the inputs of a layer norm call (its fast test failed)."""
     for name, t in ((x_name, x), ("residual", residual), ("weight", weight), ("bias", bias)):
         if not isinstance(t, torch.Tensor) and (t is not None or name == x_name):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -1985,22 +1985,43 @@ def _layer_pack(what, x, x_name, residual, residual_dtype, io_dtype, weight, bia
         raise TypeError("x and the residual must be float32 or bfloat16")
     if not xs:
         raise ValueError(f"{x_name} needs at least one dimension")
-    size = xs[-1]
-    if x.is_contiguous():
-        stride = size
-    else:
-        _strided(x, x_name, dev, x.dtype, xs)
-        stride = _row_stride(xs, x.stride(), len(xs) - 1) if len(xs) > 1 else 0
-        if stride is None:
-            raise ValueError(f"the leading dimensions of {x_name} must collapse to rows of one stride")
+    _strided(x, x_name, dev, x.dtype, xs)
     if residual is not None:
         _check(residual, "residual", dev, residual_dtype, xs)
     for name, t in (("weight", weight), ("bias", bias)):
         if t is not None:
-            _check(t, name, dev, torch.float32, (size,))
-    addr = [0 if t is None else t.data_ptr() for t in (x, residual, weight, bias)]
+            _check(t, name, dev, torch.float32, (xs[-1],))
+
+
+def _layer_pack(what, x, x_name, residual, residual_dtype, io_dtype, weight, bias, eps):
+    """(packed params, device, (rows, size))"""
+    try:
+        xs, di = x.shape, x.get_device()
+        # one test of everything that is wrong only in a wrong call; _layer_check says what
+        ok = len(xs) > 0 and di >= 0 and x.dtype in _DT_CODE and (xs[-1] <= 1 or x.stride(-1) == 1)
+        if residual is not None:
+            ok = ok and (residual.shape == xs and residual.dtype == residual_dtype and residual.is_contiguous()
+                         and residual.get_device() == di)
+        for t in (weight, bias):
+            if t is not None:
+                ok = ok and (t.dtype == torch.float32 and t.dim() == 1 and t.shape[0] == xs[-1] and t.is_contiguous()
+                             and t.get_device() == di)
+        codes = _DT_CODE[io_dtype], _DT_CODE[residual_dtype]
+    except (AttributeError, KeyError):
+        ok = False
+    if not ok:
+        _layer_check(what, x, x_name, residual, residual_dtype, io_dtype, weight, bias)
+    size = xs[-1]
+    if x.is_contiguous():
+        stride = size
+    else:
+        stride = _row_stride(xs, x.stride(), len(xs) - 1) if len(xs) > 1 else 0
+        if stride is None:
+            raise ValueError(f"the leading dimensions of {x_name} must collapse to rows of one stride")
     rows = x.numel() // size if size else 0
-    return _LAYER.pack(*addr, stride, rows, size, eps, _DT_CODE[io_dtype], _DT_CODE[residual_dtype]), dev, (rows, size)
+    return _LAYER.pack(x.data_ptr(), 0 if residual is None else residual.data_ptr(),
+                       0 if weight is None else weight.data_ptr(), 0 if bias is None else bias.data_ptr(), stride, rows,
+                       size, eps, *codes), x.device, (rows, size)
 
 
 def layer_norm(x, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -2019,12 +2040,14 @@ def layer_norm(x, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Te
     p, dev, _ = _layer_pack("layer_norm", x, "x", residual, residual_dtype, getattr(x, "dtype", None), weight, bias, eps)
     given = out, residual_out
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         _check(out, "out", dev, x.dtype, x.shape)
     total = residual_out
     if total is not None:
         _check(total, "residual_out", dev, residual_dtype, x.shape)
+    elif residual is not None:
+        total = torch.empty_like(residual)
     elif stored:
         total = torch.empty(x.shape, dtype=residual_dtype, device=dev)
     st = lib.sscan_layer_norm(p, out.data_ptr(), 0 if total is None else total.data_ptr(), _stream(dev))
