@@ -162,17 +162,14 @@ __global__ __launch_bounds__(64 * kBackSegment / T) void bwd_kernel(TileArgs p, 
     for (int c = 0; c < C; ++c) h[c] = w.dh_last ? w.dh_last[b * a.dim + at + c] : 0.0f;
     if (split) {
       if (!ends_run) {
+        float A[C], B[C];
+        join<-1, C>(first, kPlane, kPitch, waves, A, B);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          float A, B;
-          join<-1>(first + c * 64, kPlane, kPitch, waves, A, B);
-          publish(p.maps + back * pitch + place + c, map_bits(A), B);
-        }
+        for (int c = 0; c < C; ++c) publish(p.maps + back * pitch + place + c, map_bits(A[c]), B[c]);
       }
       enter<C>(p.maps + place, p.states + place, pitch, back, h);
     }
-#pragma unroll
-    for (int c = 0; c < C; ++c) hand_on<-1>(first + c * 64, kPlane, kPitch, waves, h[c]);
+    hand_on<-1, C>(first, kPlane, kPitch, waves, h);
     if (ends_run) {
 #pragma unroll
       for (int c = 0; c < C; ++c) publish(p.states + int64_t(back / kRun) * pitch + place + c, 0, h[c]);
@@ -183,11 +180,11 @@ __global__ __launch_bounds__(64 * kBackSegment / T) void bwd_kernel(TileArgs p, 
     }
   }
   if (wave == waves - 1) {           // states, from the first wave on
+    float h[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      float h = seg > 0 ? p.entry[seg * pitch + place + c] : a.h0 ? a.h0[b * a.dim + at + c] : 0.0f;
-      hand_on<1>(lds + c * 64 + lane, kPlane, kPitch, waves, h);
-    }
+    for (int c = 0; c < C; ++c)
+      h[c] = seg > 0 ? p.entry[seg * pitch + place + c] : a.h0 ? a.h0[b * a.dim + at + c] : 0.0f;
+    hand_on<1, C>(lds + lane, kPlane, kPitch, waves, h);
   }
   __syncthreads();
   float h[C], carry[C], dlam[C];

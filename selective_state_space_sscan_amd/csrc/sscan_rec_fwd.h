@@ -165,17 +165,14 @@ __global__ __launch_bounds__(kMaxWaves * 64) void fwd_kernel(TileArgs p) {
     for (int c = 0; c < C; ++c) h[c] = a.h0 ? a.h0[b * a.dim + at + c] : 0.0f;
     if (split) {
       if (!ends_run) {
+        float P[C], H[C];
+        join<1, C>(lds + lane, C * 64, 2 * 64 * C, waves, P, H);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          float P, H;
-          join<1>(lds + c * 64 + lane, C * 64, 2 * 64 * C, waves, P, H);
-          publish(p.maps + seg * pitch + place + c, map_bits(P), H);
-        }
+        for (int c = 0; c < C; ++c) publish(p.maps + seg * pitch + place + c, map_bits(P[c]), H[c]);
       }
       enter<C>(p.maps + place, p.states + place, pitch, seg, h);
     }
-#pragma unroll
-    for (int c = 0; c < C; ++c) hand_on<1>(lds + c * 64 + lane, C * 64, 2 * 64 * C, waves, h[c]);
+    hand_on<1, C>(lds + lane, C * 64, 2 * 64 * C, waves, h);
     if (ends_run) {
 #pragma unroll
       for (int c = 0; c < C; ++c) publish(p.states + int64_t(seg / kRun) * pitch + place + c, 0, h[c]);

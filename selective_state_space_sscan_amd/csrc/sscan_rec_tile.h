@@ -276,29 +276,45 @@ struct Tile {
 };
 
 // The map of all the block's waves, one after another: their maps lie in LDS (first: the
-// lane's first), A and H `half` floats apart and a wave's `pitch` after the one before.
-// STEP 1: from the first wave on; -1: from the last.  (Four read before the first is used took
-// longer: gradients from 8 bits, 4 x 4096 x 2048, 448 us a training pass, so 418.)
-template <int STEP>
-__device__ __forceinline__ void join(const float* first, int half, int pitch, int waves, float& A, float& H) {
-  A = 1.0f;
-  H = 0.0f;
+// lane's first; channel c is 64 floats after the one before), A and H `half` floats apart and
+// a wave's `pitch` after the one before.  STEP 1: from the first wave on; -1: from the last.
+template <int STEP, int C>
+__device__ __forceinline__ void join(const float* first, int half, int pitch, int waves, float (&A)[C], float (&H)[C]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    A[c] = 1.0f;
+    H[c] = 0.0f;
+  }
+#pragma unroll 1
   for (int v = 0; v < waves; ++v) {
     const float* w = first + (STEP > 0 ? v : waves - 1 - v) * pitch;
-    A *= w[0];
-    H = fmaf(w[0], H, w[half]);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float a = w[c * 64];
+      H[c] = fmaf(a, H[c], w[c * 64 + half]);
+      A[c] *= a;
+    }
   }
 }
 
 // From the state h that enters the block: puts every wave's entry state in its A's place and
 // leaves the exit state in h.
-template <int STEP>
-__device__ __forceinline__ void hand_on(float* first, int half, int pitch, int waves, float& h) {
+template <int STEP, int C>
+__device__ __forceinline__ void hand_on(float* first, int half, int pitch, int waves, float (&h)[C]) {
+#pragma unroll 1
   for (int v = 0; v < waves; ++v) {
     float* w = first + (STEP > 0 ? v : waves - 1 - v) * pitch;
-    const float A = w[0];
-    w[0] = h;
-    h = fmaf(A, h, w[half]);
+    float a[C], b[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      a[c] = w[c * 64];
+      b[c] = w[c * 64 + half];
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      w[c * 64] = h[c];
+      h[c] = fmaf(a[c], h[c], b[c]);
+    }
   }
 }
 
