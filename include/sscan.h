@@ -679,8 +679,8 @@ SSCAN_API int sscan_validate_add_norm_bwd(const sscan_add_norm_params* p, const 
  * [batch]): tokens of each row, clamped to 0..len; later tokens are not read, their outputs
  * and gradients are 0 and they leave the state alone.  With reverse != 0 a row is scanned
  * from its last token to its first.  States and sums are float32; bf16 outputs round to
- * nearest even, once.  len <= 2^30, dim <= 2^24, batch * ceil(dim / 64) * (len / 64 + 1) at
- * most 2^22, token strides below 2^26 elements, c finite and >= 0. */
+ * nearest even, once.  len <= 2^30, dim <= 2^24, batch * ceil(dim / 64) * (len / 64 + 1)
+ * below 2^22, token strides below 2^26 elements, c finite and >= 0. */
 typedef struct sscan_rec_params {
   const void* x;
   const void* g;

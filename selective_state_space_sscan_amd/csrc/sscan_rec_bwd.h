@@ -19,7 +19,9 @@ inline int back_channels(int64_t dim, bool kept, bool io_bf16) {
   return kept && io_bf16 && dim % 4 == 0 ? 4 : channels_of(dim);
 }
 constexpr int state_tokens(int c, bool kept, bool few) { return few || c == 4 || (c == 2 && kept) ? 8 : 16; }
-constexpr int kStateWaves = 16;      // of a block in the kernel of the states
+// Waves of a block in the kernel of the states: gradients of 8 x 4096 x 2048 bf16 with sixteen
+// 414 us, with eight 402.
+constexpr int kStateWaves = 8;
 
 // One segment a block.  The adjoint that passes from token t to t - 1 is c_t = a_t (e_t +
 // c_{t+1}), e_t = dout_t silu(z_t): a map of the adjoint that enters a tile from behind, with
@@ -158,9 +160,10 @@ __global__ __launch_bounds__(64 * kBackSegment / T) void bwd_kernel(TileArgs p, 
     const bool ends_run = split && back % kRun == kRun - 1;
     float* first = lds + 2 * kPlane + lane;
     float h[C];
+    if (back == 0) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) h[c] = w.dh_last ? w.dh_last[b * a.dim + at + c] : 0.0f;
-    if (split) {
+      for (int c = 0; c < C; ++c) h[c] = w.dh_last ? w.dh_last[b * a.dim + at + c] : 0.0f;
+    } else {
       if (!ends_run) {
         float A[C], B[C];
         join<-1, C>(first, kPlane, kPitch, waves, A, B);
@@ -170,9 +173,10 @@ __global__ __launch_bounds__(64 * kBackSegment / T) void bwd_kernel(TileArgs p, 
       enter<C>(p.maps + place, p.states + place, pitch, back, h);
     }
     hand_on<-1, C>(first, kPlane, kPitch, waves, h);
-    if (ends_run) {
+    if (split && (back == 0 || ends_run)) {
+      uint64_t* to = ends_run ? p.states + int64_t(back / kRun) * pitch : p.maps;
 #pragma unroll
-      for (int c = 0; c < C; ++c) publish(p.states + int64_t(back / kRun) * pitch + place + c, 0, h[c]);
+      for (int c = 0; c < C; ++c) publish(to + place + c, 0, h[c]);
     }
     if (w.dh0 && seg == 0 && on) {
 #pragma unroll

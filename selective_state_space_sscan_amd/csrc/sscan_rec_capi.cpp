@@ -60,7 +60,7 @@ int view_rec(const sscan_rec_params* p, bool kept, RecView* w) {
   if (p->len > kMaxLen || p->dim > kMaxDim) return SSCAN_ERR_SHAPE;
   const int64_t n = product({p->batch, p->len, p->dim}), ns = product({p->batch, p->dim}),
                 tiles = product({p->batch, (p->dim + 63) / 64, p->len / 64 + 1});
-  if (n < 0 || ns < 0 || tiles < 0 || tiles > kMaxTiles) return SSCAN_ERR_SHAPE;
+  if (n < 0 || ns < 0 || tiles < 0 || tiles >= kMaxTiles) return SSCAN_ERR_SHAPE;
   w->bytes = size_t(n) * w->esz;
   w->state_bytes = size_t(ns) * 4;
   w->lam_bytes = size_t(p->dim) * 4;

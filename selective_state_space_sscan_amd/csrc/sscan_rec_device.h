@@ -28,10 +28,11 @@ __device__ __forceinline__ float sigmoid(float x) {
 // by an exponent in two parts; log1p(w) is the logarithm of the rounded sum s = 1 + w plus
 // the rounding's error w - (s - 1), off by less than a unit in the last place.
 __device__ __forceinline__ float decay_rate(const float* lam, int64_t ch, float c) {
-  const float x = -fabsf(lam[ch]), t = x * kLog2e;
+  // far out w is 0 and not the difference of infinities; a NaN stays one
+  const float l = lam[ch], x = l < -200.0f || l > 200.0f ? -200.0f : -fabsf(l), t = x * kLog2e;
   const float low = fmaf(x, kLog2e, -t) + x * 1.925963033500e-8f;  // what the product and the constant drop
   const float e = __builtin_amdgcn_exp2f(t), w = fmaf(e * low, 0.693147181f, e), s = 1.0f + w;
-  return c * (fmaxf(lam[ch], 0.0f) + fmaf(__builtin_amdgcn_logf(s), 0.693147181f, w - (s - 1.0f)));
+  return c * (fmaxf(l, 0.0f) + fmaf(__builtin_amdgcn_logf(s), 0.693147181f, w - (s - 1.0f)));
 }
 
 // 1 - exp(-m) for |m| < 1/4: by its series (the next term is below 2^-28 of the sum).

@@ -166,6 +166,44 @@ def test_pieces_and_states_in_place(l):
     within(h, want["h_last"], "state")
 
 
+@pytest.mark.parametrize("d", [2, 65])
+@pytest.mark.parametrize("l", [200, 300, 1000, 5000])
+def test_state_in_place_of_many_segments(l, d):
+    """The exit state written over the entry state, which the row's first segment alone reads."""
+    t = draw(3, l, d, torch.float32, seed=21)
+    t["lam"].fill_(-12.0)  # decays near 1: every token sees the entry state
+    want = forward(t)
+    for _ in range(10):
+        h = t["h0"].clone()
+        out, last = forward(dict(t, h0=h), h_last=h)
+        assert last is h and torch.equal(out, want[0]) and torch.equal(last, want[1])
+
+
+def test_infinite_parameters():
+    """lam of -inf: no decay and no input; of +inf: a state of one token."""
+    t = draw(2, 300, 4, torch.float32, seed=22)
+    t["lam"][:] = torch.tensor([-float("inf"), float("inf"), 1e30, float("nan")])
+    out, last = forward(t)
+    assert torch.equal(last[:, 0], t["h0"][:, 0])
+    one = sscan.rec_fwd(*(t[k] if k == "lam" else t[k][:, -1:] for k in FWD[:5]))
+    for c in (1, 2):
+        assert torch.equal(out[:, -1:, c], one[0][..., c]) and torch.isfinite(out[..., c]).all()
+    assert torch.isnan(out[..., 3]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_kept_blocks_that_are_not_finite(dtype):
+    t = draw(1, 40, 130, dtype, seed=23)
+    t["x"][0, 3, 5], t["g"][0, 20, 70], t["z"][0, 39, 129] = float("nan"), float("inf"), -float("inf")
+    t["i"][0, 7, :64] = 0.0
+    _, _, kept = forward(t, keep=True)
+    for k, p in zip(("x", "g", "i", "z"), kept):
+        q, scale, _ = rec_ref.eight(t[k].cpu())
+        assert torch.equal(p.q.cpu(), q), k
+        assert torch.equal(torch.isnan(p.scale.cpu()), torch.isnan(scale))
+        assert torch.equal(torch.nan_to_num(p.scale.cpu()), torch.nan_to_num(scale)), k
+
+
 def test_resets_and_far_values():
     """Log decays of -inf start a row anew; gates far out; no channel leaks into another."""
     t = draw(1, 400, 130, torch.float32, seed=10, gated=False)

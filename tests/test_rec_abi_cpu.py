@@ -51,6 +51,9 @@ BOTH = [
     (dict(batch=1 << 25, len=1, dim=1), ESHAPE), (dict(io_dtype=7), EUNSUP), (dict(reverse=2), EUNSUP),
     (dict(c=float("nan")), EUNSUP), (dict(c=float("inf")), EUNSUP), (dict(c=-1.0), EUNSUP),
     (dict(x=(1 << 40) + 1), EALIGN), (dict(lam=(1 << 40) + 2), EALIGN), (dict(h0=(1 << 41) + 2), EALIGN),
+    (dict(batch=1 << 22, len=1, dim=64), ESHAPE), (dict(b=(1 << 22) - 1, L=1, d=1), OK),
+    (dict(z_stride=I2(0, 1 << 26)), EUNSUP), (dict(z=1 << 50, z_stride=I2(0, (1 << 26) - 1)), OK),
+    (dict(L=1, len=1, z_stride=I2(0, 1 << 40)), OK),
     (dict(lengths=(1 << 41) + 2), EALIGN), (dict(x_stride=I2(-1, 96)), ESHAPE), (dict(z_stride=I2(1 << 60, 96)), ESHAPE),
 ]
 
