@@ -1,7 +1,9 @@
 // sscan_layer_norm.hip -- layer norm fused with the residual sum in front of it, and its
 // gradients.  Rows are held in registers as in the RMS norms (sscan_norm_device.h): every
 // input is read once and every output written once.  The variance is that of the values
-// minus their mean, both sums in float32 over registers.
+// minus their mean, both sums in float32 over registers.  Bound by HBM: gradients of 16384 x
+// 1536 bf16 with a float32 residual take 85 us, sum over blocks included, where a large copy
+// would move their bytes in 79.
 #include "sscan_norm_device.h"
 #include "sscan_rec.h"
 

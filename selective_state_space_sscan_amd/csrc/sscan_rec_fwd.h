@@ -1,5 +1,7 @@
 // sscan_rec_fwd.h -- the recurrence over a segment of a row: the forward's kernel, and that of
-// the states between segments, which the backward pass starts from.
+// the states between segments, which the backward pass starts from.  Long rows are bound by HBM
+// (262144 x 1536 bf16 804 us, 5.0 TB/s; a large copy 5.1), a few rounds of blocks by loads and
+// arithmetic that take turns (4 x 2048 x 2560 59 us, 3.5 TB/s).
 #pragma once
 
 #include "sscan_pack8.h"
