@@ -679,7 +679,9 @@ SSCAN_API int sscan_validate_add_norm_bwd(const sscan_add_norm_params* p, const 
  * [batch]): tokens of each row, clamped to 0..len; later tokens are not read, their outputs
  * and gradients are 0 and they leave the state alone.  With reverse != 0 a row is scanned
  * from its last token to its first.  States and sums are float32; bf16 outputs round to
- * nearest even, once.  len <= 2^30, dim <= 2^24, batch * ceil(dim / 64) * (len / 64 + 1)
+ * nearest even, once.  Rows are joined by products of their decays: where those overflow
+ * (g > 0) or a state is infinite, results can be NaN where single steps give an infinity
+ * or a number.  len <= 2^30, dim <= 2^24, batch * ceil(dim / 64) * (len / 64 + 1)
  * below 2^22, token strides below 2^26 elements, c finite and >= 0. */
 typedef struct sscan_rec_params {
   const void* x;

@@ -1,7 +1,7 @@
 // sscan_pack8.hip -- activations in 8 bits: blocks of 64 elements of a row, each with the
 // scale max|x| / 127.  Eight lanes take a block, eight elements a lane, by 16-byte accesses
-// at whatever alignment the rows have.  Bound by HBM: 16384 x 1536 bf16 there and back 30 us
-// (5.2 TB/s); one lane an element took 128.
+// at whatever alignment the rows have.  Bound by memory: 16384 x 1536 bf16 there and back 30
+// us (5.2 TB/s; the tensors fit the last cache); one element a lane took 128.
 #include "sscan_pack8.h"
 
 #include "sscan_norm_device.h"
