@@ -742,8 +742,9 @@ SSCAN_API int sscan_rec_step(const sscan_rec_params* p, float* state, void* out,
  * contiguous; dh_last optional).  The forward states are recomputed; no atomics on sums:
  * results are bitwise reproducible.  With kept the inputs are read from there (x, g, i and z
  * of p must be NULL) and the gradients are those at the values that the 8 bits stand for.
- * Where a decay rounds to 1 (w_t = 0) the slope of w_t is taken as 0.  Outputs must not
- * overlap each other, any input or the workspace (sscan_rec_bwd_workspace_bytes). */
+ * Where w_t is below 2^-56 (a_t rounds to 1) it and its slope may be taken as 0, forward too.
+ * Outputs must not overlap each other, any input or the workspace
+ * (sscan_rec_bwd_workspace_bytes). */
 SSCAN_API int sscan_rec_bwd(const sscan_rec_params* p, const sscan_rec_kept* kept, const void* dout,
                   const float* dh_last, const sscan_rec_grads* grads, void* stream, void* workspace,
                   size_t workspace_bytes);

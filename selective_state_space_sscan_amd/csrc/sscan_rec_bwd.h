@@ -239,7 +239,8 @@ __global__ __launch_bounds__(64 * kBackSegment / T) void bwd_kernel(TileArgs p, 
         const float sx = s * v;
         if (GATED) {
           const float loss = D[j][c], r = sigmoid(g[j].get(c));
-          const float w2 = loss * (2.0f - loss), inv = w2 > 0.0f ? __builtin_amdgcn_rsqf(w2) : 0.0f;  // 1 / w
+          // 1 / w; the instruction answers infinity for what is no normal number, whose w is taken as 0
+          const float w2 = loss * (2.0f - loss), inv = w2 >= 0x1p-126f ? __builtin_amdgcn_rsqf(w2) : 0.0f;
           wgt = w2 * inv;
           dlog = fmaf(-adj * sx, A * A * inv, dlog);
           og[c] = -dlog * rate[c] * r * (1.0f - r);

@@ -399,3 +399,41 @@ def test_refusals():
     for dout in (x[:1], x.bfloat16()):
         with pytest.raises((ValueError, TypeError)):
             sscan.rec_bwd(x, g, dout)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kept", [False, True])
+def test_decays_that_round_to_one(kept, dtype):
+    """w^2 = 1 - a^2 on both sides of 2^-126, the smallest number that the hardware's square root
+    and its reciprocal take: w may count as 0 there."""
+    pairs = [(-30.0, -61.0), (-5.0, -86.0), (-60.0, -35.0), (-85.0, -6.0), (-30.0, -60.0), (-30.0, -59.0), (-86.0, -1.0),
+             (-87.0, 0.0), (-88.0, 2.0), (-20.0, -70.0),
+             (30.0, -88.0)]
+    d = 64 * len(pairs)  # a block of 64 channels for each: the 8 bits hold its one value of g exactly
+    t = draw(2, 150, d, dtype, seed=24)
+    for k, (lam, g) in enumerate(pairs):
+        t["lam"][64 * k:64 * k + 64] = lam
+        t["g"][..., 64 * k:64 * k + 64] = g
+    src, args = dict(t), [t[k] for k in ("x", "g", "i", "z")]
+    if kept:
+        args = forward(t, keep=True)[2]
+        src.update((k, rec_ref.eight(t[k].cpu())[2].to(DEV)) for k in ("x", "g", "i", "z"))
+    x, g, i, z = args
+    got = sscan.rec_bwd(x, g, t["dout"], i, t["lam"], z, t["h0"], t["dh_last"])
+    want = rec_ref.rec_bwd(src["x"], src["g"], t["dout"], src["i"], t["lam"], src["z"], t["h0"], t["dh_last"])
+    out, h_last = forward(t)
+    states = rec_ref.rec(*(t[k] for k in FWD))
+    # a w below 2^-56 may count as 0: that much of |D s x|, |D s| or |s x| for each token (the slope
+    # of w has 1 / w, but times c softplus(lam) r = w^2 / 2).  |D| is at most the sum over the row of
+    # |dout silu(z)| and |dh_last|; states that lack an input reach dlog a, dz and out with such factors.
+    x, dout, z = (src[k].double().abs() for k in ("x", "dout", "z"))
+    D = (dout * (1 + z)).sum(1, keepdim=True) + t["dh_last"].double().abs()[:, None]
+    add = 2.0 ** -56 * 150 * (1 + D) * (1 + x.amax(1, keepdim=True)) * (1 + z.amax())
+    for name in ("dx", "dg", "di", "dz", "dh0"):
+        v, bound = want[name]
+        within(got[name], (v, 1.25 * bound + (add if v.dim() == 3 else add[:, 0])), name)
+    v, bound = want["dlam"]
+    within(got["dlam"], (v, 1.25 * bound + 150 * add.sum((0, 1))), "dlam")
+    for name, v in (("out", out), ("h_last", h_last)):
+        value, bound = states[name]
+        within(v, (value, bound + (add if value.dim() == 3 else add[:, 0])), name)
