@@ -1817,8 +1817,9 @@ def _kept_new(dev, sizes, given) -> Kept8:
     """Room for the inputs that are given (four truth values) in 8 bits."""
     b, L, d = sizes
     n = sum(given)
-    parts = [Packed8(q, s) for q, s in zip(torch.empty((n, b, L, d), dtype=torch.int8, device=dev).unbind(0),
-                                           torch.empty((n, b, L, _pack_blocks(d)), device=dev).unbind(0))]
+    q = torch.empty((n, b, L, d), dtype=torch.int8, device=dev)
+    scale = torch.empty((n, b, L, _pack_blocks(d)), dtype=torch.float32, device=dev)
+    parts = [Packed8(*p) for p in zip(q.unbind(0), scale.unbind(0))]
     return Kept8(*(parts.pop(0) if has else None for has in given))
 
 
