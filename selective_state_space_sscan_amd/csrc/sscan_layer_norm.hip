@@ -106,7 +106,8 @@ __global__ __launch_bounds__(threads<TPR>()) void layer_norm_bwd_kernel(LayerNor
     }
     group_sum<TPR>(dots, lds, turn);
     turn ^= 1;
-    const float r = 1.0f / sqrtf(dots[0] * inv + a.eps), dot = dots[1] * inv * (r * r);
+    // a group past the last row holds zeros, and leaves the sums alone where eps is 0 too
+    const float r = kGroups > 1 && !size ? 0.0f : 1.0f / sqrtf(dots[0] * inv + a.eps), dot = dots[1] * inv * (r * r);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       dw[j] += d[j] * (x[j] * r);

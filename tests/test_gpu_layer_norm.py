@@ -171,3 +171,13 @@ def test_refusals():
     for args in ((x, x[:2]), (x, x.half()), (x, 3), (x, x, w, w, x[:1])):
         with pytest.raises((ValueError, TypeError)):
             sscan.layer_norm_bwd(*args)
+
+
+@pytest.mark.parametrize("size", [2, 5, 64, 120, 128, 200, 513, 1000])
+@pytest.mark.parametrize("n", [5, 17, 700])
+def test_without_eps(n, size):
+    """eps = 0 with fewer rows than a block's threads take, whose idle ones add nothing."""
+    x, dout, dtotal = rand(n, size, seed=1), rand(n, size, seed=2), rand(n, size, seed=3)
+    x[:, 0] += 4.0  # no two elements next to each other in a row of two
+    x[:, 1] -= 4.0
+    check(x, None, 1 + rand(size, seed=4, scale=0.2), rand(size, seed=5), dout, dtotal, eps=0.0)
