@@ -150,7 +150,8 @@ __global__ __launch_bounds__(threads<TPR>()) void gated_norm_bwd_kernel(GatedNor
     }
     group_sum<TPR>(sum, lds, turn);
     turn ^= 1;
-    const float r = 1.0f / sqrtf(sum[0] * inv + a.eps), mean = sum[1] * inv;
+    // a group past the last unit holds zeros, and leaves the sums alone where eps is 0 too
+    const float r = kGroups > 1 && !size ? 0.0f : 1.0f / sqrtf(sum[0] * inv + a.eps), mean = sum[1] * inv;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float gate = z[j] * sig[j], slope = sig[j] * (1.0f + z[j] * (1.0f - sig[j]));
@@ -287,8 +288,10 @@ __global__ __launch_bounds__(threads<TPR>()) void add_norm_bwd_kernel(AddNormArg
     }
     group_sum<TPR>(sum, lds, turn);
     turn ^= 1;
-    const float r = 1.0f / sqrtf(sum[0] * inv + a.eps), mean = sum[1] * inv;
-    const float rx = POST ? 1.0f / sqrtf(sum[2] * inv + a.eps) : 1.0f;
+    // a group past the last row holds zeros, and leaves the sums alone where eps is 0 too
+    const bool idle = kGroups > 1 && !size;
+    const float r = idle ? 0.0f : 1.0f / sqrtf(sum[0] * inv + a.eps), mean = sum[1] * inv;
+    const float rx = !POST ? 1.0f : idle ? 0.0f : 1.0f / sqrtf(sum[2] * inv + a.eps);
     float dot[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {

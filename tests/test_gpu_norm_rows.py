@@ -127,3 +127,26 @@ def test_the_gate_is_as_exact_as_stated():
     ref = zd / (1 + torch.exp(-zd)) / (1 + EPS) ** 0.5
     err = (y - ref).abs() / ((1.25 * zd.abs() + 10) * 2.0 ** -24 * ref.abs() + 1e-45)
     assert float(err.max()) <= 1.0
+
+
+# threads of 16 to 128 a row, so sixteen to two rows a block, the last one not full
+@pytest.mark.parametrize("n,size", [(5, 64), (17, 120), (5, 200), (7, 500), (701, 513), (9, 1000)])
+def test_without_eps(n, size):
+    """eps = 0: threads of a block without a row of their own add nothing to a weight's gradient."""
+    x, z, dout = (rand(n, size, seed=s) for s in (1, 2, 3))
+    w = 1 + rand(size, seed=4, scale=0.2)
+    for gate_first in (False, True):
+        got = sscan.gated_norm_bwd(*on(x, z, dout, w), eps=0.0, gate_first=gate_first)
+        ins = [t.double().requires_grad_(True) for t in (x, z, w)]
+        want = torch.autograd.grad(delta_ref.gated_norm(*ins, 0.0, gate_first), ins, dout.double())
+        for k, v in zip(("dx", "dz", "dweight"), want):
+            close(got[k], v, k, delta_ref.norm_terms(x, dout.double(), 0.0) if k != "dweight" else 0.0)
+    residual, dres, p = rand(n, size, seed=5), rand(n, size, seed=6), 1 + rand(size, seed=7, scale=0.2)
+    for post in (None, p):
+        _, total = sscan.add_norm(*on(x, residual, w), post_weight=on(post)[0], eps=0.0)
+        got = sscan.add_norm_bwd(*on(x), total, *on(dout, w), dresidual_out=on(dres)[0], post_weight=on(post)[0], eps=0.0)
+        ins = [t.double().requires_grad_(True) for t in (x, residual, w, *(() if post is None else (p,)))]
+        outs = delta_ref.add_norm(ins[0], ins[1], ins[2], None, ins[3] if post is not None else None, 0.0, torch.float64)
+        want = torch.autograd.grad(outs, ins, [dout.double(), dres.double()])
+        for k, v in zip(("dx", "dresidual", "dweight", "dpost_weight"), want):
+            close(got[k], v, k, delta_ref.norm_terms(total.cpu(), dout.double(), 0.0) if k[:2] != "dw" else 0.0)
