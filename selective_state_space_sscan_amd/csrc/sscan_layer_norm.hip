@@ -107,10 +107,11 @@ __global__ __launch_bounds__(threads<TPR>()) void layer_norm_bwd_kernel(LayerNor
     group_sum<TPR>(dots, lds, turn);
     turn ^= 1;
     // a group past the last row holds zeros, and leaves the sums alone where eps is 0 too
-    const float r = kGroups > 1 && !size ? 0.0f : 1.0f / sqrtf(dots[0] * inv + a.eps), dot = dots[1] * inv * (r * r);
+    const float r = kGroups > 1 && !size ? 0.0f : 1.0f / sqrtf(dots[0] * inv + a.eps), dot = dots[1] * inv * r;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      dw[j] += d[j] * (x[j] * r);
+      x[j] *= r;
+      dw[j] += d[j] * x[j];
       db[j] += d[j];
       e[j] += r * (d[j] * w[j] - dmean - x[j] * dot);
     }

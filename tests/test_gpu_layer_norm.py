@@ -181,3 +181,20 @@ def test_without_eps(n, size):
     x[:, 0] += 4.0  # no two elements next to each other in a row of two
     x[:, 1] -= 4.0
     check(x, None, 1 + rand(size, seed=4, scale=0.2), rand(size, seed=5), dout, dtotal, eps=0.0)
+
+
+def test_small_rows_without_eps():
+    """Rows of 2e-20 with eps = 0: 1 / sd is 5e19, whose square is beyond float32."""
+    x, dout, w = rand(30, 200, seed=1, scale=2e-20), rand(30, 200, seed=2), 1 + rand(200, seed=3, scale=0.2)
+    out, _ = sscan.layer_norm(x, w, None, eps=0.0)
+    got = sscan.layer_norm_bwd(x, dout, w, eps=0.0)
+    want = rec_ref.layer_norm(x, w, None, 0.0, dout)
+    # squares of 4e-40 are rounded to multiples of 2^-149: off by 2^-150 each, so the deviation by
+    # 2^-150 / 4e-40 / 2 = 9e-7 of itself, 15 U, and as much again in n and in the gradients' factors
+    v, bound = want["out"]
+    within(out, (v, bound + 15 * U * v.abs()), "out")
+    v, bound = want["dweight"]
+    within(got["dweight"], (v, bound + 15 * U * (dout.double() * want["out"][0] / w.double()).abs().sum(0)), "dweight")
+    v, bound = want["dx"]
+    size = (dout * w).double().abs() * (1 + want["out"][0].abs())
+    within(got["dx"], (v, bound + 60 * U / 2e-20 * (size + size.mean(-1, keepdim=True) * (1 + want["out"][0].abs()))), "dx")
