@@ -1,7 +1,7 @@
 // sscan_layer_norm.hip -- layer norm fused with the residual sum in front of it, and its
 // gradients.  Rows are held in registers as in the RMS norms (sscan_norm_device.h): every
-// input is read once and every output written once.  The variance is that of the values
-// minus their mean, both sums in float32 over registers.  Bound by HBM: gradients of 16384 x
+// input is read once and every output written once.  Mean and variance are by two sums in
+// float32 over registers.  Bound by HBM: gradients of 16384 x
 // 1536 bf16 with a float32 residual take 85 us, sum over blocks included, where a large copy
 // would move their bytes in 79.
 #include "sscan_norm_device.h"
@@ -11,6 +11,13 @@ namespace sscan {
 namespace norm {
 
 constexpr int kMaxLayerBlocks = 8192, kMaxLayerBackBlocks = 1024;
+
+// The mean of the squares around a mean that is off by `off`.  The mean is the quotient of a
+// rounded sum, off by up to 17 U of the values' size (U = 2^-24), which rows of nearly equal
+// values would show as a deviation: so the deviations' own mean is summed along with their
+// squares and taken out.  Rows of one value then have none at all: their deviations are the
+// same few steps, whose sum and quotient are exact.
+__device__ __forceinline__ float variance(float squares, float off) { return fmaxf(squares - off * off, 0.0f); }
 
 // total = residual + x (stored as RES where wanted), out = (total - mean) / sqrt(var + eps) * weight + bias
 template <typename IO, typename RES, int TPR, bool whole>
@@ -34,7 +41,7 @@ __global__ __launch_bounds__(threads<TPR>()) void layer_norm_kernel(LayerNormArg
   for (int64_t u0 = int64_t(blockIdx.x) * kGroups; u0 < a.rows; u0 += step) {
     const int64_t u = u0 + grp, flat = u * a.size;
     const int size = u < a.rows ? int(a.size) : 0;
-    float x[8], sum[1] = {0.0f}, ss[1] = {0.0f};
+    float x[8], sum[1] = {0.0f}, dev[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       x[j] = next_y[j] + next_x[j];
@@ -45,18 +52,19 @@ __global__ __launch_bounds__(threads<TPR>()) void layer_norm_kernel(LayerNormArg
     if (a.total) store<whole>(static_cast<RES*>(a.total) + flat, size, t, x);
     group_sum<TPR>(sum, lds, turn);
     turn ^= 1;
-    const float mean = sum[0] / float(a.size);  // a row of equal values has no deviation
+    const float mean = sum[0] / float(a.size);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       // places that hold no element of their own count for nothing
       x[j] = j >= at.dup && at.off + j < size ? x[j] - mean : 0.0f;
-      ss[0] += x[j] * x[j];
+      dev[0] += x[j];
+      dev[1] += x[j] * x[j];
     }
-    group_sum<TPR>(ss, lds, turn);
+    group_sum<TPR>(dev, lds, turn);
     turn ^= 1;
-    const float r = 1.0f / sqrtf(ss[0] * inv + a.eps);
+    const float off = dev[0] / float(a.size), r = 1.0f / sqrtf(variance(dev[1] * inv, off) + a.eps);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j] + c[j];
+    for (int j = 0; j < 8; ++j) x[j] = (x[j] - off) * r * w[j] + c[j];
     store<whole>(static_cast<IO*>(a.out) + flat, size, t, x);
   }
 }
@@ -85,7 +93,7 @@ __global__ __launch_bounds__(threads<TPR>()) void layer_norm_bwd_kernel(LayerNor
   for (int64_t u0 = int64_t(blockIdx.x) * kGroups; u0 < a.rows; u0 += step) {
     const int64_t u = u0 + grp, flat = u * a.size;
     const int size = u < a.rows ? int(a.size) : 0;
-    float x[8], d[8], e[8], sum[2] = {0.0f, 0.0f}, dots[2] = {0.0f, 0.0f};
+    float x[8], d[8], e[8], sum[2] = {0.0f, 0.0f}, dev[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       x[j] = next_x[j];
@@ -101,16 +109,18 @@ __global__ __launch_bounds__(threads<TPR>()) void layer_norm_bwd_kernel(LayerNor
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       x[j] = j >= at.dup && at.off + j < size ? x[j] - mean : 0.0f;
-      dots[0] += x[j] * x[j];
-      dots[1] += d[j] * w[j] * x[j];
+      dev[0] += x[j];
+      dev[1] += x[j] * x[j];
+      dev[2] += d[j] * w[j] * x[j];
     }
-    group_sum<TPR>(dots, lds, turn);
+    group_sum<TPR>(dev, lds, turn);
     turn ^= 1;
     // a group past the last row holds zeros, and leaves the sums alone where eps is 0 too
-    const float r = kGroups > 1 && !size ? 0.0f : 1.0f / sqrtf(dots[0] * inv + a.eps), dot = dots[1] * inv * r;
+    const float off = dev[0] / float(a.size), var = variance(dev[1] * inv, off);
+    const float r = kGroups > 1 && !size ? 0.0f : 1.0f / sqrtf(var + a.eps), dot = (dev[2] * inv - off * dmean) * r;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      x[j] *= r;
+      x[j] = (x[j] - off) * r;
       dw[j] += d[j] * x[j];
       db[j] += d[j];
       e[j] += r * (d[j] * w[j] - dmean - x[j] * dot);

@@ -198,3 +198,52 @@ def test_small_rows_without_eps():
     v, bound = want["dx"]
     size = (dout * w).double().abs() * (1 + want["out"][0].abs())
     within(got["dx"], (v, bound + 60 * U / 2e-20 * (size + size.mean(-1, keepdim=True) * (1 + want["out"][0].abs()))), "dx")
+
+
+@pytest.mark.parametrize("size", [2, 3, 7, 64, 333, 768, 1536, 2001, 4096, 8191])
+def test_rows_of_equal_values(size):
+    """Whole rows of one value, whose sum is not exact, have no deviation."""
+    value = 1.0 + 9999.0 * torch.rand(50, 1, generator=torch.Generator().manual_seed(size))
+    value[:3, 0] = torch.tensor([1234.567, -0.1, 1e-3])
+    x, c = value.expand(50, size).contiguous().to(DEV), rand(size, seed=1)
+    out, _ = sscan.layer_norm(x, 1 + rand(size, seed=2), c)
+    assert torch.equal(out, c.expand(50, size))
+    dout = rand(50, size, seed=3)
+    got = sscan.layer_norm_bwd(x, dout, torch.ones(size, device=DEV), c)
+    assert not got["dweight"].any()
+    # with no deviation dx = (dout - mean(dout)) / sqrt(eps): the mean within 20 U of the mean magnitude,
+    # the quotient by four roundings
+    d = dout.double()
+    want, r = (d - d.mean(-1, keepdim=True)) / 1e-5 ** 0.5, 1e-5 ** -0.5
+    within(got["dx"], (want, r * U * (20 * d.abs().mean(-1, keepdim=True) + 5 * d.abs())), "dx")
+
+
+@pytest.mark.parametrize("size", [64, 333, 1536, 8191])
+@pytest.mark.parametrize("shift", [100.0, 3e4])
+def test_deviations_far_below_the_mean(shift, size):
+    """The mean's own rounding, up to 17 U of its size, is taken out again."""
+    x, dout = rand(40, size, seed=1, shift=shift), rand(40, size, seed=2)
+    w = 1 + rand(size, seed=3, scale=0.2)
+    out, _ = sscan.layer_norm(x, w, None)
+    y = x.double() - x.double().mean(-1, keepdim=True)
+    sd = (y.square().mean(-1, keepdim=True) + 1e-5).sqrt()
+    # x - m for a rounded mean m: off by U of its size, which is |y| + |m - mean|, 17 U of the shift;
+    # the mean of these by sixteen additions in a row and a quotient; the difference
+    gap = 17 * U * (shift + 1)
+    E = (2 * U * (y.abs() + gap) + 19 * U * (y.abs() + gap).mean(-1, keepdim=True)) / sd
+    n = y / sd
+    value = n * w.double()
+    bound = w.double().abs() * (E + n.abs() * (2 * E.amax(-1, keepdim=True) + 26 * U))
+    within(out, (value, bound), "out")
+    # gradients at the same rounding of n: their own sums add 24 U of the mean magnitudes
+    got = sscan.layer_norm_bwd(x, dout, w)
+    d = dout.double()
+    dn = d * w.double()
+    m1, m2 = dn.mean(-1, keepdim=True), (dn * n).mean(-1, keepdim=True)
+    a1, a2 = dn.abs().mean(-1, keepdim=True), (dn * n).abs().mean(-1, keepdim=True)
+    Em = E.amax(-1, keepdim=True)
+    dy = E + n.abs() * (2 * Em + 26 * U)
+    err = dn.abs() * 4 * U + 20 * U * a1 + n.abs() * (30 * U * a2 + (dn.abs() * dy).mean(-1, keepdim=True)) + dy * a2
+    err = (err + (dn.abs() + a1 + n.abs() * a2) * (2 * Em + 30 * U)) / sd
+    within(got["dx"], ((dn - m1 - n * m2) / sd, err), "dx")
+    within(got["dweight"], ((d * n).sum(0), (d.abs() * dy).sum(0) + 101 * U * (d * n).abs().sum(0)), "dweight")
