@@ -169,16 +169,9 @@ template <typename IO, int C>
 struct In<IO, C, true> {
   typename Vec<int8_t, C>::V v;
   float scale;
-  // four steps at a time become unsigned bytes, which one instruction converts; the product is exact
-  // before the sum, so the value is that of step * scale
-  __device__ __forceinline__ float get(int c) const {
-    if constexpr (C == 4) {
-      const uint32_t u = __builtin_bit_cast(uint32_t, v) ^ 0x80808080u;
-      return fmaf(float(u >> (8 * c) & 0xffu), scale, -128.0f * scale);
-    } else {
-      return part<C>(v, c) * scale;
-    }
-  }
+  // a product alone: unsigned bytes and a sum with -128 scales, as fast (gradients of 4 x 4096 x
+  // 2048 268 us either way), overflow for a block that holds bfloat16's lowest value
+  __device__ __forceinline__ float get(int c) const { return part<C>(v, c) * scale; }
 };
 
 // What a tile holds is unpacked again where it is used again: the values of the first use,

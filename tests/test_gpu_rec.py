@@ -437,3 +437,22 @@ def test_decays_that_round_to_one(kept, dtype):
     for name, v in (("out", out), ("h_last", h_last)):
         value, bound = states[name]
         within(v, (value, bound + (add if value.dim() == 3 else add[:, 0])), name)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d", [128, 130, 65])
+def test_gates_shut_by_the_lowest_value(d, dtype):
+    """Gates of some tokens shut by their type's lowest value, in the gradients from 8 bits too:
+    the other elements of its blocks are then below half a step, 0."""
+    t = draw(2, 100, d, dtype, seed=25)
+    low = torch.finfo(dtype).min
+    t["g"][0, 10, 3], t["i"][0, 20, 5], t["g"][1, 30, 64], t["i"][1, 99, :7] = low, low, low, low
+    if dtype == torch.bfloat16:  # float32's lowest value is read back from 8 bits as an infinity
+        t["z"][1, 40, 0] = low
+    _, _, kept = forward(t, keep=True)
+    back = dict(t, **{k: rec_ref.eight(t[k].cpu())[2].to(DEV) for k in ("x", "g", "i", "z")})
+    assert not back["g"][0, 10, 4:64].any() and back["g"][0, 10, 3] < -3e38
+    got = sscan.rec_bwd(kept.x, kept.g, t["dout"], kept.i, t["lam"], kept.z, t["h0"], t["dh_last"])
+    want = rec_ref.rec_bwd(back["x"], back["g"], t["dout"], back["i"], t["lam"], back["z"], t["h0"], t["dh_last"])
+    for k, v in want.items():
+        within(got[k], (v[0], v[1] * 1.25), k)
