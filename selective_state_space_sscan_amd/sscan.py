@@ -1969,6 +1969,9 @@ def gated_recurrence(x, g, i: Optional[torch.Tensor] = None, lam: Optional[torch
     in 8 bits instead of the tensors themselves (half the memory of bfloat16): gradients are
     those at the kept values, outputs are as without, and a backward pass with
     ``create_graph`` raises.  Returns (out, h_last)."""
+    # where no gradient can be asked for nothing is kept: the forward that keeps does twice the work
+    checkpoint = bool(checkpoint) and torch.is_grad_enabled() and any(
+        getattr(t, "requires_grad", False) for t in (x, g, i, lam, z, h0))
     return _RecFn.apply(x, g, i, lam, z, h0, lengths, c, reverse, checkpoint)
 
 

@@ -456,3 +456,23 @@ def test_gates_shut_by_the_lowest_value(d, dtype):
     want = rec_ref.rec_bwd(back["x"], back["g"], t["dout"], back["i"], t["lam"], back["z"], t["h0"], t["dh_last"])
     for k, v in want.items():
         within(got[k], (v[0], v[1] * 1.25), k)
+
+
+def test_nothing_is_kept_without_a_backward_pass(monkeypatch):
+    """checkpoint=True where no gradient can be asked for: the plain forward, with the same bits."""
+    t = draw(2, 200, 130, torch.bfloat16, seed=26)
+    args = [t[k] for k in FWD[:5]]
+    made, new = [], sscan._kept_new
+    monkeypatch.setattr(sscan, "_kept_new", lambda *a: made.append(a) or new(*a))
+    want = forward(t)
+    for got in (sscan.gated_recurrence(*args, h0=t["h0"], checkpoint=True),):
+        assert not made and all(torch.equal(p, q) for p, q in zip(got, want))
+    t["lam"].requires_grad_(True)
+    with torch.no_grad():
+        got = sscan.gated_recurrence(*args, h0=t["h0"], checkpoint=True)
+    assert not made and all(torch.equal(p, q) for p, q in zip(got, want)) and not got[0].requires_grad
+    with torch.inference_mode():
+        sscan.gated_recurrence(*args, h0=t["h0"], checkpoint=True)
+    assert not made
+    got = sscan.gated_recurrence(*args, h0=t["h0"], checkpoint=True)
+    assert len(made) == 1 and all(torch.equal(p, q) for p, q in zip(got, want)) and got[0].requires_grad
