@@ -1778,7 +1778,7 @@ def _rec_pack(what, x, g, i, lam, z, h0, lengths, c, reverse, tokens: bool = Tru
         ok = (dt in _DT_CODE and di >= 0 and len(xs) == 2 + tokens)
         addr, strides = [], []
         for t in (x, g, i, z):
-            if t is None and (t is i or t is z):
+            if t is None and g is not None:
                 addr.append(0)
                 strides += (0, 0)
                 continue

@@ -476,3 +476,21 @@ def test_nothing_is_kept_without_a_backward_pass(monkeypatch):
     assert not made
     got = sscan.gated_recurrence(*args, h0=t["h0"], checkpoint=True)
     assert len(made) == 1 and all(torch.equal(p, q) for p, q in zip(got, want)) and got[0].requires_grad
+
+
+@pytest.mark.parametrize("l", [0, 6])
+def test_a_missing_gate_is_refused(l):
+    """x and g are required, with i given or not, with tokens or without."""
+    t = draw(2, l, 8, torch.float32, seed=27)
+    for i in (None, t["i"]):
+        for x, g in ((t["x"], None), (None, t["g"]), (None, None)):
+            with pytest.raises(TypeError, match="must be a torch.Tensor"):
+                sscan.rec_fwd(x, g, i)
+            with pytest.raises(TypeError, match="must be a torch.Tensor"):
+                sscan.rec_bwd(x, g, t["dout"], i)
+            with pytest.raises(TypeError, match="must be a torch.Tensor"):
+                sscan.gated_recurrence(x, g, i)
+            if l:
+                with pytest.raises(TypeError, match="must be a torch.Tensor"):
+                    sscan.rec_step(t["h0"].clone(), None if x is None else x[:, 0], None if g is None else g[:, 0],
+                                   None if i is None else i[:, 0])
