@@ -398,6 +398,11 @@ def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]):
 
 
 def _stream(device) -> ctypes.c_void_p:
+    """The current stream of the tensors' device, which has to be the current one: the library
+    launches there, where the others' memory may be out of reach."""
+    if device.index not in (None, torch._C._cuda_getDevice()):
+        raise ValueError(f"the tensors are on {device} and the current device is cuda:{torch._C._cuda_getDevice()}: "
+                         "call under torch.cuda.device(...)")
     if device.index is None:
         return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
     # the handle alone, without a Stream object: 2 us less a call
