@@ -3,6 +3,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 
 #include "sscan_rec.h"
@@ -32,7 +33,8 @@ __device__ __forceinline__ float decay_rate(const float* lam, int64_t ch, float 
   const float l = lam[ch], x = l < -200.0f || l > 200.0f ? -200.0f : -fabsf(l), t = x * kLog2e;
   const float low = fmaf(x, kLog2e, -t) + x * 1.925963033500e-8f;  // what the product and the constant drop
   const float e = __builtin_amdgcn_exp2f(t), w = fmaf(e * low, 0.693147181f, e), s = 1.0f + w;
-  return c * (fmaxf(l, 0.0f) + fmaf(__builtin_amdgcn_logf(s), 0.693147181f, w - (s - 1.0f)));
+  const float rate = c * (fmaxf(l, 0.0f) + fmaf(__builtin_amdgcn_logf(s), 0.693147181f, w - (s - 1.0f)));
+  return rate > FLT_MAX ? FLT_MAX : rate;  // decays to 0 as well, and its product with a slope of 0 is 0
 }
 
 // 1 - exp(-m) for |m| < 1/4: by its series (the next term is below 2^-28 of the sum).

@@ -494,3 +494,25 @@ def test_a_missing_gate_is_refused(l):
                 with pytest.raises(TypeError, match="must be a torch.Tensor"):
                     sscan.rec_step(t["h0"].clone(), None if x is None else x[:, 0], None if g is None else g[:, 0],
                                    None if i is None else i[:, 0])
+
+
+@pytest.mark.parametrize("kept", [False, True])
+def test_gradients_at_infinite_parameters(kept):
+    """lam of +inf (and beyond where c softplus(lam) fits float32): every state is its own token's
+    input, so dg, dlam and dh0 are 0 and the others are those of h = sigmoid(i) x.  lam of -inf: no
+    decay and no input."""
+    t = draw(2, 150, 256, torch.float32, seed=28)
+    t["lam"][:128], t["lam"][64:128], t["lam"][128:] = float("inf"), 3e38, -float("inf")
+    args = forward(t, keep=True)[2] if kept else [t[k] for k in ("x", "g", "i", "z")]
+    src = {k: rec_ref.eight(t[k].cpu())[2].to(DEV) if kept else t[k].double() for k in ("x", "g", "i", "z")}
+    x, g, i, z = args
+    got = sscan.rec_bwd(x, g, t["dout"], i, t["lam"], z, t["h0"], t["dh_last"])
+    # the same at a rate of 8e4, whose decays are 0 too in float64
+    near = dict(t, lam=t["lam"].clamp(-1e5, 1e4))
+    want = rec_ref.rec_bwd(src["x"], src["g"], t["dout"], src["i"], near["lam"], src["z"], t["h0"], t["dh_last"])
+    for k, (v, bound) in want.items():
+        within(got[k], (v, 1.25 * bound), k)
+    assert not got["dg"].any() and not got["dlam"].any() and not got["dh0"][:, :128].any()
+    # a gate so far shut that it is 0 keeps the state
+    t["g"].fill_(-1e4)
+    assert torch.equal(forward(t)[1], t["h0"])
