@@ -729,8 +729,8 @@ typedef struct sscan_rec_grads {
 /* Whole sequences.  h_last (required) receives the state after each row's last scanned
  * token; it may be h0 itself.  kept (optional) receives the inputs in 8 bits; tokens past a
  * row's length are not written there.  Outputs must not overlap each other, any other input
- * or the workspace (sscan_rec_workspace_bytes(...) bytes, 256-byte aligned).  len == 0
- * copies the entry state (or zeros) to h_last. */
+ * or the workspace (sscan_rec_workspace_bytes(...) bytes, 256-byte aligned), nor may that
+ * overlap an input.  len == 0 copies the entry state (or zeros) to h_last. */
 SSCAN_API int sscan_rec_fwd(const sscan_rec_params* p, void* out, float* h_last, const sscan_rec_kept* kept,
                   void* stream, void* workspace, size_t workspace_bytes);
 
@@ -743,8 +743,8 @@ SSCAN_API int sscan_rec_step(const sscan_rec_params* p, float* state, void* out,
  * results are bitwise reproducible.  With kept the inputs are read from there (x, g, i and z
  * of p must be NULL) and the gradients are those at the values that the 8 bits stand for.
  * Where w_t is below 2^-56 (a_t rounds to 1) it and its slope may be taken as 0, forward too.
- * Outputs must not overlap each other, any input or the workspace
- * (sscan_rec_bwd_workspace_bytes). */
+ * Outputs and the workspace (sscan_rec_bwd_workspace_bytes) must not overlap each other or
+ * any input. */
 SSCAN_API int sscan_rec_bwd(const sscan_rec_params* p, const sscan_rec_kept* kept, const void* dout,
                   const float* dh_last, const sscan_rec_grads* grads, void* stream, void* workspace,
                   size_t workspace_bytes);
@@ -801,7 +801,7 @@ SSCAN_API int sscan_layer_norm(const sscan_layer_norm_params* p, void* out, void
  * total that the forward stored (or x, where residual_dtype is io_dtype): dx (io_dtype) and
  * the same gradient in residual_dtype as dresidual (optional; may be dtotal itself), and
  * the optional float32 dweight and dbias [size].  Sums run in a fixed order.  Workspace:
- * sscan_layer_norm_bwd_workspace_bytes, 16-byte aligned. */
+ * sscan_layer_norm_bwd_workspace_bytes, 16-byte aligned, apart from all of these. */
 SSCAN_API int sscan_layer_norm_bwd(const sscan_layer_norm_params* p, const void* dout, const void* dtotal, void* dx,
                          void* dresidual, float* dweight, float* dbias, void* stream, void* workspace,
                          size_t workspace_bytes);

@@ -105,7 +105,7 @@ int check_rec_fwd(const sscan_rec_params* p, const void* out, const float* h_las
   if (st != SSCAN_OK) return st;
   const Range o = range_of(out, w->bytes), s = range_of(h_last, w->state_bytes), ws = range_of(workspace, need);
   if (clash_inputs(o, *w) || clash(o, {w->h0, s, ws}) || clash_inputs(s, *w) || overlap(s, ws) ||
-      (h_last != p->h0 && overlap(s, w->h0)))
+      (h_last != p->h0 && overlap(s, w->h0)) || clash_inputs(ws, *w) || overlap(ws, w->h0))
     return SSCAN_ERR_ALIAS;
   for (int i = 0; i < 8; ++i) {
     if (clash_inputs(w->kept[i], *w) || clash(w->kept[i], {w->h0, o, s, ws})) return SSCAN_ERR_ALIAS;
@@ -147,6 +147,9 @@ int check_rec_bwd(const sscan_rec_params* p, const sscan_rec_kept* kept, const v
   const Range outs[6] = {range_of(g.dx, w->bytes), range_of(g.dg, w->bytes),       range_of(g.di, w->bytes),
                          range_of(g.dz, w->bytes), range_of(g.dlam, w->lam_bytes), range_of(g.dh0, w->state_bytes)};
   const Range d = range_of(dout, w->bytes), dh = range_of(dh_last, w->state_bytes), ws = range_of(workspace, need);
+  if (clash_inputs(ws, *w) || clash(ws, {w->h0, d, dh})) return SSCAN_ERR_ALIAS;
+  for (int m = 0; m < 8; ++m)
+    if (overlap(ws, w->kept[m])) return SSCAN_ERR_ALIAS;
   for (int n = 0; n < 6; ++n) {
     if (clash_inputs(outs[n], *w) || clash(outs[n], {w->h0, d, dh, ws})) return SSCAN_ERR_ALIAS;
     for (int m = 0; m < 8; ++m)
@@ -258,6 +261,7 @@ int check_layer_bwd(const sscan_layer_norm_params* p, const void* dout, const vo
   const Range d = range_of(dout, w->bytes), dt = range_of(dtotal, w->res_bytes), ws = range_of(workspace, need);
   const Range outs[4] = {range_of(dx, w->bytes), range_of(dresidual, w->res_bytes), range_of(dweight, w->vec_bytes),
                          range_of(dbias, w->vec_bytes)};
+  if (clash(ws, {w->x, w->weight, w->bias, d, dt})) return SSCAN_ERR_ALIAS;
   for (int i = 0; i < 4; ++i) {
     if (clash(outs[i], {w->x, w->weight, w->bias, d, ws})) return SSCAN_ERR_ALIAS;
     if (!(i == 1 && dresidual == dtotal) && overlap(outs[i], dt)) return SSCAN_ERR_ALIAS;

@@ -206,3 +206,23 @@ def test_validate_layer_norm_outputs(lib):  # noqa: F811
     assert lib.sscan_validate_layer_norm(None, 0, 0) == ENULL
     for n, size in ((0, 5), (5, 0), (5, 8193), (-1, 5)):
         assert lib.sscan_layer_norm_bwd_workspace_bytes(n, size) == 0
+
+
+def test_validate_workspace_apart_from_inputs(lib):  # noqa: F811
+    """A workspace over an input would be emptied before the input is read."""
+    many = dict(b=8, L=5000)
+    p, r = rec(**many)
+    for call in (fwd, bwd):
+        for at in (p.x, p.g, p.i, p.z, p.lam, p.lengths, p.h0):
+            assert call(lib, ws=at, **many) == EALIAS
+        assert call(lib, **many) == OK
+    n = lib.sscan_rec_workspace_bytes(8, 5000, D, 1)
+    assert fwd(lib, ws=p.x - n, **many) == OK and fwd(lib, ws=p.x - n + 256, **many) == EALIAS
+    for at in (r["dout"], r["dh"]):
+        assert bwd(lib, ws=at, **many) == EALIAS
+    p, r = rec()
+    for name in KEPT:
+        assert bwd(lib, kept=True, ws=r[name]) == EALIAS
+    p, r = layer(n=3000)
+    for at in (p.x, p.weight, p.bias, r["dout"], r["dtotal"]):
+        assert lbwd(lib, n=3000, ws=at) == EALIAS
