@@ -681,7 +681,10 @@ SSCAN_API int sscan_validate_add_norm_bwd(const sscan_add_norm_params* p, const 
  * from its last token to its first.  States and sums are float32; bf16 outputs round to
  * nearest even, once.  Rows are joined by products of their decays: where those overflow
  * (g > 0) or a state is infinite, results can be NaN where single steps give an infinity
- * or a number.  len <= 2^30, dim <= 2^24, batch * ceil(dim / 64) * (len / 64 + 1)
+ * or a number.  How a row is cut, and with it the last bits of its results, depends on batch,
+ * len, dim and io_dtype.  With lam no g resets the state inside a row (a_t >= exp(-c softplus(lam)))
+ * and every input is weighted by w_t: several sequences are rows of their own, or calls.
+ * len <= 2^30, dim <= 2^24, batch * ceil(dim / 64) * (len / 64 + 1)
  * below 2^22, token strides below 2^26 elements, c finite and >= 0. */
 typedef struct sscan_rec_params {
   const void* x;
@@ -767,7 +770,8 @@ SSCAN_API int sscan_validate_rec_bwd(const sscan_rec_params* p, const sscan_rec_
  * zeros (scale 0); one that holds an infinity or a NaN has scale NaN and is read back as
  * NaN.  x [rows, size] io_dtype with a stride between rows (elements, >= 0); q [rows, size]
  * and scale [rows, ceil(size / 64)] contiguous.  An element is read back as q * scale, off
- * by at most half a scale (and the rounding to io_dtype). */
+ * by at most half a scale (and the rounding to io_dtype); one within 2^-23 of float32's largest
+ * value can be read back as an infinity. */
 SSCAN_API int sscan_pack8(const void* x, int64_t x_stride, int64_t rows, int64_t size, int io_dtype, int8_t* q,
                 float* scale, void* stream);
 SSCAN_API int sscan_unpack8(const int8_t* q, const float* scale, int64_t rows, int64_t size, int io_dtype, void* out,

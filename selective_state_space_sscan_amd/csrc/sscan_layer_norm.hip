@@ -1,9 +1,9 @@
 // sscan_layer_norm.hip -- layer norm fused with the residual sum in front of it, and its
 // gradients.  Rows are held in registers as in the RMS norms (sscan_norm_device.h): every
-// input is read once and every output written once.  Mean and variance are by two sums in
-// float32 over registers.  Bound by HBM: gradients of 16384 x
-// 1536 bf16 with a float32 residual take 85 us, sum over blocks included, where a large copy
-// would move their bytes in 79.
+// input is read once and every output written once.  Mean and variance are by two rounds of
+// sums in float32 over registers.  Bound by HBM: 16384 x 1536 bf16 with a float32 residual take
+// 57 us, where a large copy would move their bytes in 59 (part stays in the last cache), their
+// gradients 85, sum over blocks included (79); 8192 x 4096 71 (79) and 117 (105).
 #include "sscan_norm_device.h"
 #include "sscan_rec.h"
 
@@ -16,7 +16,9 @@ constexpr int kMaxLayerBlocks = 8192, kMaxLayerBackBlocks = 1024;
 // rounded sum, off by up to 17 U of the values' size (U = 2^-24), which rows of nearly equal
 // values would show as a deviation: so the deviations' own mean is summed along with their
 // squares and taken out.  Rows of one value then have none at all: their deviations are the
-// same few steps, whose sum and quotient are exact.
+// same few steps, whose sum and quotient are exact.  The sum more costs 1% to 2% up to sizes of
+// 4096, in rows of 8192, which a block of 1024 threads holds, 4% and 5% (2048 x 8192 f32 46.1 ->
+// 47.9 us, gradients 80.6 -> 84.9).
 __device__ __forceinline__ float variance(float squares, float off) { return fmaxf(squares - off * off, 0.0f); }
 
 // total = residual + x (stored as RES where wanted), out = (total - mean) / sqrt(var + eps) * weight + bias

@@ -1,8 +1,8 @@
 // sscan_rec_bwd.h -- gradients of the gated recurrence.  Where rows have several segments, a
 // first kernel leaves the states that enter them (sscan_rec_fwd.h, without its outputs); the
 // kernel below then takes the segments of a row at once, the last ones first, and joins the
-// adjoints between them as the forward pass joins the states.  2 x 4096 x 2560 bf16 takes 152 us;
-// in a trace, which adds to both, the states take 51 and the gradients 105 (vector units 61%
+// adjoints between them as the forward pass joins the states.  2 x 4096 x 2560 bf16 takes 149 us;
+// in a trace, which adds to both, the states take 51 and the gradients 104 (vector units 63%
 // busy, 3.6 TB/s).
 #pragma once
 

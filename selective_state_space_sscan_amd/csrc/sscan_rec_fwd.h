@@ -1,6 +1,6 @@
 // sscan_rec_fwd.h -- the recurrence over a segment of a row: the forward's kernel, and that of
 // the states between segments, which the backward pass starts from.  Long rows are bound by HBM
-// (262144 x 1536 bf16 804 us, 5.0 TB/s; a large copy 5.1), a few rounds of blocks by loads and
+// (262144 x 1536 bf16 795 us, 5.1 TB/s; a large copy 5.1), a few rounds of blocks by loads and
 // arithmetic that take turns (4 x 2048 x 2560 59 us, 3.5 TB/s).
 #pragma once
 
@@ -235,9 +235,11 @@ constexpr int kWaves = 8;            // of a block where rows have several segme
 
 // Channels a lane, and tokens of a wave's tile: sixteen, which the registers hold without
 // spilling any (the tokens' decays and inputs alone are 2 C T); eight of two float32 channels,
-// and where a call has too few tiles to fill the chip, so that each takes half as long (the
-// kernel for prompts of 77, 384 channels: 11.3 us, so 8.6).  The same whether inputs are kept
-// or not: states are joined at the tiles' ends, and outputs are the same bits.
+// and where a call has too few tiles to fill the chip, so that each takes half as long (calls
+// from a graph: 3 x 77 x 384 bf16 7.4 us, with sixteen 8.9; 1 x 200 x 2048 10.1, 14.0; 4 x 1000 x
+// 384 13.1, 14.6; 1 x 2048 x 1024 15.5, 15.5).  Rows that are long as well lose: twice the segments
+// make twice the links between runs (1 x 16384 of 64 channels 46 us, with sixteen 30).  The same
+// whether inputs are kept or not: states are joined at the tiles' ends, and outputs are the same bits.
 inline int channels_of(int64_t dim) { return dim % 2 == 0 ? 2 : 1; }
 constexpr int64_t kFewTiles = 2048;  // half of what the chip holds at once
 

@@ -169,8 +169,9 @@ template <typename IO, int C>
 struct In<IO, C, true> {
   typename Vec<int8_t, C>::V v;
   float scale;
-  // a product alone: unsigned bytes and a sum with -128 scales, as fast (gradients of 4 x 4096 x
-  // 2048 268 us either way), overflow for a block that holds bfloat16's lowest value
+  // a product alone: unsigned bytes and a sum with -128 scales are 2% to 4% faster (gradients of
+  // 4 x 4096 x 2048 257 us, so 262; 65536 x 1536 868, so 902), but overflow for a block that
+  // holds bfloat16's lowest value
   __device__ __forceinline__ float get(int c) const { return part<C>(v, c) * scale; }
 };
 

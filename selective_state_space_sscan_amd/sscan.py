@@ -1844,7 +1844,9 @@ def rec_fwd(x, g, i: Optional[torch.Tensor] = None, lam: Optional[torch.Tensor] 
     w = sqrt(1 - a^2), or without ``lam`` a = exp(g) and w = 1.  x, g, i, z: [batch, len, dim]
     f32/bf16, any strides with the last dimension contiguous (i and z optional); lam: [dim]
     f32; h0: [batch, dim] f32; lengths: int32 [batch].  Returns (out, h_last); h_last may be
-    given as h0.  With ``keep`` also the inputs in 8 bits, for ``rec_bwd``."""
+    given as h0.  With ``keep`` also the inputs in 8 bits (``Kept8``), for ``rec_bwd``; what they
+    hold past a row's length is not written.  Without ``lam`` g = -inf starts a row anew inside
+    it; with ``lam`` nothing does."""
     lib = load_library()
     p, dev, sizes = _rec_pack("rec_fwd", x, g, i, lam, z, h0, lengths, c, reverse)
     b, L, d = sizes
