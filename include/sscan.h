@@ -28,8 +28,9 @@
  * Ownership: every data pointer is a DEVICE pointer owned by the caller.  The
  * library allocates no memory on these calls and keeps no state after return.
  * Work is enqueued on `stream` (a hipStream_t of the current device, where the data has
- * to be; NULL = its default stream) and the call returns; y is valid once the stream reaches that point, and inputs must stay
- * alive until then.  y must not overlap any input.  Calls take a caller-provided
+ * to be; NULL = its default stream) and the call returns; y is valid once the stream
+ * reaches that point, and inputs must stay alive until then.  y must not overlap any
+ * input.  Calls take a caller-provided
  * device workspace of sscan_workspace_bytes(...) bytes, 16-byte aligned (B/C re-laid token-major;
  * for long sequences the segment chains; for one-segment bidirectional sequences
  * over 64 tokens the two directions' meeting buffers; NULL is allowed when that

@@ -19,7 +19,8 @@ constexpr int kMaxLayerBlocks = 8192, kMaxLayerBackBlocks = 1024;
 // same few steps, whose sum and quotient are exact.  The sum more costs 1% to 2% up to sizes of
 // 4096, in rows of 8192, which a block of 1024 threads holds, 4% and 5% (2048 x 8192 f32 46.1 ->
 // 47.9 us, gradients 80.6 -> 84.9).
-__device__ __forceinline__ float variance(float squares, float off) { return fmaxf(squares - off * off, 0.0f); }
+// The product is not rounded by itself: squares beyond float32 stay an infinity.
+__device__ __forceinline__ float variance(float squares, float off) { return fmaxf(fmaf(-off, off, squares), 0.0f); }
 
 // total = residual + x (stored as RES where wanted), out = (total - mean) / sqrt(var + eps) * weight + bias
 template <typename IO, typename RES, int TPR, bool whole>

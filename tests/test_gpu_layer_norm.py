@@ -247,3 +247,16 @@ def test_deviations_far_below_the_mean(shift, size):
     err = (err + (dn.abs() + a1 + n.abs() * a2) * (2 * Em + 30 * U)) / sd
     within(got["dx"], ((dn - m1 - n * m2) / sd, err), "dx")
     within(got["dweight"], ((d * n).sum(0), (d.abs() * dy).sum(0) + 101 * U * (d * n).abs().sum(0)), "dweight")
+
+
+@pytest.mark.parametrize("size", [64, 333, 2001, 8192])
+@pytest.mark.parametrize("shift", [0.0, 1e30])
+def test_rows_whose_squares_overflow(size, shift):
+    """Deviations whose squares are beyond float32 count as infinitely far apart: 1 / sd is 0."""
+    x, c, dout, dtotal = rand(20, size, seed=1, scale=1e26, shift=shift), rand(size, seed=2), rand(20, size, seed=3), \
+        rand(20, size, seed=4)
+    w = 1 + rand(size, seed=5, scale=0.2)
+    out, _ = sscan.layer_norm(x, w, c)
+    assert torch.equal(out, c.expand(20, size))
+    got = sscan.layer_norm_bwd(x, dout, w, c, dtotal)
+    assert torch.equal(got["dx"], dtotal) and not got["dweight"].any()
